@@ -1,0 +1,84 @@
+// Paged key-value cache: the arguments its kernels share and their lookup.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace lf {
+
+// The pools of one layer and one call's page table.  Strides are in bytes.
+struct PagedPool {
+  char* k;
+  char* v;
+  int64_t page_stride, head_stride, token_stride;
+  int page_size, page_shift;  // page_shift: log2(page_size), or -1 when it is no power of two
+  int num_pages, kv_heads;
+  const int32_t* table;       // [batch][max_pages]
+  const int32_t* lens;        // [batch]
+  int batch, max_pages;
+  int32_t* err;               // may be null
+};
+
+struct PagedAppendArgs {
+  PagedPool pool;
+  const char* k_new;
+  const char* v_new;
+  const int32_t* new_start;   // [batch + 1], or null: one token per sequence
+  int total_new, tokens_per_block, row_bytes;  // row_bytes: one head's row
+};
+
+struct PagedDecodeArgs {
+  PagedPool pool;
+  const void* q;
+  const char* k_new;          // null: the new token is in the pages already
+  const char* v_new;
+  void* out;
+  float* lse;                 // may be null
+  int q_heads, group, window, sinks;
+  float scale_log2;           // log2(e) / sqrt(head_dim)
+  int whole_units;            // 1: CTA i takes unit i alone (no join); 0: level ranges
+  float* part_o;              // level ranges: [2 grid][group][head_dim] partial outputs
+  float* part_ml;             // [2 grid][group][2] their max and sum
+  int32_t* part_unit;         // [grid] the unit a CTA's range starts inside, or -1
+};
+
+struct PagedPromptArgs {
+  PagedPool pool;
+  const void* q;
+  const int32_t* q_start;     // [batch + 1]
+  void* out;
+  float* lse;                 // may be null
+  int q_heads, group, window, sinks, total_q, max_q;
+  float scale_log2;
+};
+
+// Occupied tokens of sequence b, kept inside its row of the page table.
+__device__ __forceinline__ int paged_len(const PagedPool& p, int b) {
+  const int n = p.lens[b];
+  const int64_t most = (int64_t)p.max_pages * p.page_size;
+  return n < 0 ? 0 : (n > most ? (int)most : n);
+}
+
+// Page index in the row and slot in the page of a position.
+__device__ __forceinline__ void paged_split(const PagedPool& p, int pos, int* page, int* slot) {
+  if (p.page_shift >= 0) {
+    *page = pos >> p.page_shift;
+    *slot = pos & (p.page_size - 1);
+  } else {
+    *page = (int)((unsigned)pos / (unsigned)p.page_size);
+    *slot = pos - *page * p.page_size;
+  }
+}
+
+// Launches (one translation unit each).  They return the launch's error.
+cudaError_t paged_append_launch(const PagedAppendArgs& a, cudaStream_t stream);
+// elem: bytes of an element (2 bf16, 4 fp32).  `grid`: CTAs of the attention kernel.
+cudaError_t paged_decode_launch(const PagedDecodeArgs& a, int elem, int head_dim, int grid,
+                                cudaStream_t stream);
+cudaError_t paged_prompt_launch(const PagedPromptArgs& a, int elem, int head_dim,
+                                cudaStream_t stream);
+
+// Tokens that one CTA of the decode kernel takes in one sweep of its warps.
+int paged_decode_sweep(int elem, int head_dim);
+
+}  // namespace lf

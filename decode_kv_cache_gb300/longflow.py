@@ -29,6 +29,8 @@ __all__ = [
     "lf_abi_version",
     "lf_prefill_fill_noalloc", "lf_rkv_compress", "lf_launch_plan", "lf_launch_plan_for",
     "LFCache",
+    "LFPages", "lf_paged_append", "lf_paged_decode", "lf_paged_decode_workspace", "lf_paged_prompt",
+    "LFPagedCache",
 ]
 
 LF_OK, LF_ERR_ARG, LF_ERR_OOM, LF_ERR_CUDA, LF_ERR_DEVICE, LF_ERR_UNSUPPORTED = 0, -1, -2, -3, -5, -7
@@ -75,6 +77,13 @@ class LFLayout(ctypes.Structure):
         (n, ctypes.c_int) for n in ("rkv_buffer", "rkv_alpha", "rkv_beta")] + [
         ("rkv_lambda", ctypes.c_float), ("rkv_tau", ctypes.c_float),
         ("split_units", ctypes.c_int), ("split_cnt", ctypes.c_void_p)]
+
+
+class LFPages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "dtype", "kv_heads", "head_dim", "page_size", "num_pages")] + [
+        (n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")] + [
+        (n, ctypes.c_void_p) for n in ("k", "v", "err")]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -126,6 +135,16 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.lf_prefill_fill_noalloc.restype = I
     lib.lf_prefill_fill_noalloc.argtypes = [ctypes.POINTER(LFLayout), I, VP, VP,
                                             ctypes.POINTER(ctypes.c_int32), I, VP]
+    PG = ctypes.POINTER(LFPages)
+    lib.lf_paged_append.restype = I
+    lib.lf_paged_append.argtypes = [PG, I, VP, I, VP, VP, VP, VP, I, VP]
+    lib.lf_paged_decode.restype = I
+    lib.lf_paged_decode.argtypes = [PG, I, VP, I, VP, I, VP, VP, VP, VP, VP, I, I, VP,
+                                    ctypes.c_size_t, VP]
+    lib.lf_paged_decode_workspace.restype = I
+    lib.lf_paged_decode_workspace.argtypes = [PG, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
+    lib.lf_paged_prompt.restype = I
+    lib.lf_paged_prompt.argtypes = [PG, I, VP, I, VP, I, VP, VP, I, I, VP, VP, I, I, VP]
     _lib = lib
     return lib
 
@@ -280,6 +299,36 @@ def lf_cache_layout(handle) -> LFLayout:
     return lay
 
 
+def lf_paged_append(pages: LFPages, batch, page_table, max_pages, lens, k_new, v_new, new_start,
+                    total_new, stream=None) -> int:
+    return _check(load_library().lf_paged_append(
+        ctypes.byref(pages), batch, _ptr(page_table), max_pages, _ptr(lens), _ptr(k_new), _ptr(v_new),
+        _ptr(new_start), total_new, _stream(stream)))
+
+
+def lf_paged_decode(pages: LFPages, batch, page_table, max_pages, lens, q_heads, q, k_new, v_new, out,
+                    lse, window, sinks, workspace, workspace_bytes, stream=None) -> int:
+    return _check(load_library().lf_paged_decode(
+        ctypes.byref(pages), batch, _ptr(page_table), max_pages, _ptr(lens), q_heads, _ptr(q),
+        _ptr(k_new), _ptr(v_new), _ptr(out), _ptr(lse), window, sinks, _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def lf_paged_decode_workspace(pages: LFPages, batch, max_pages, q_heads, window=0, sinks=0) -> int:
+    """Bytes of the workspace that such lf_paged_decode calls need (0: none)."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().lf_paged_decode_workspace(ctypes.byref(pages), batch, max_pages, q_heads,
+                                                    window, sinks, ctypes.byref(n)))
+    return int(n.value)
+
+
+def lf_paged_prompt(pages: LFPages, batch, page_table, max_pages, lens, q_heads, q, q_start, total_q,
+                    max_q, out, lse, window, sinks, stream=None) -> int:
+    return _check(load_library().lf_paged_prompt(
+        ctypes.byref(pages), batch, _ptr(page_table), max_pages, _ptr(lens), q_heads, _ptr(q),
+        _ptr(q_start), total_q, max_q, _ptr(out), _ptr(lse), window, sinks, _stream(stream)))
+
+
 # ---- convenience owner ------------------------------------------------------
 
 class _DevArray:
@@ -400,3 +449,173 @@ class LFCache:
             "split_cnt": (_view(lay.split_cnt, (lay.split_units, 2), torch.int32, self.device)
                           if lay.split_cnt else None),
         }
+
+
+class LFPagedCache:
+    """Paged K and V pools of a model's layers, and the calls that use them.
+
+    ``LFPagedCache(layers, num_pages, page_size, kv_heads, head_dim)`` allocates pools
+    ``[layers][num_pages][kv_heads][page_size][head_dim]`` (uninitialised); ``over(k, v)`` takes
+    tensors that the caller owns, of that shape in any stride order with contiguous rows.  The
+    caller hands out pages: ``page_table`` int32 ``[batch][max_pages]`` and ``lens`` int32
+    ``[batch]`` (lengths including the call's own tokens) are contiguous tensors on the device.
+    """
+
+    def __init__(self, layers, num_pages, page_size, kv_heads, head_dim, dtype="bf16", device=None):
+        device = torch.device("cuda", torch.cuda.current_device() if device is None
+                              else torch.device(device).index or 0)
+        if min(layers, num_pages, page_size, kv_heads, head_dim) < 1:
+            raise LFError(LF_ERR_ARG, "layers, num_pages, page_size, kv_heads and head_dim must be >= 1")
+        if dtype not in _DTYPE:
+            raise LFError(LF_ERR_ARG, f"dtype must be one of {sorted(_DTYPE)}")
+        shape = (layers, num_pages, kv_heads, page_size, head_dim)
+        t = _TORCH_DTYPE[_DTYPE[dtype]]
+        self._take(torch.empty(shape, dtype=t, device=device), torch.empty(shape, dtype=t, device=device))
+
+    @classmethod
+    def over(cls, k: torch.Tensor, v: torch.Tensor) -> "LFPagedCache":
+        """A cache on the caller's pools k, v [layers][num_pages][kv_heads][page_size][head_dim]."""
+        self = cls.__new__(cls)
+        self._take(k, v)
+        return self
+
+    def _take(self, k, v):
+        types = {t: n for n, t in _TORCH_DTYPE.items()}
+        for name, t in (("k", k), ("v", v)):
+            if not isinstance(t, torch.Tensor) or t.dim() != 5 or not t.is_cuda or t.dtype not in types:
+                raise LFError(LF_ERR_ARG, f"{name}: expected a bf16 or fp32 CUDA tensor [layers][num_pages]"
+                                          "[kv_heads][page_size][head_dim]")
+        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or k.stride() != v.stride():
+            raise LFError(LF_ERR_ARG, "k and v must agree in shape, strides, dtype and device")
+        if k.numel() == 0 or (k.shape[4] > 1 and k.stride(4) != 1):
+            raise LFError(LF_ERR_ARG, "the pools must not be empty and their rows must be contiguous")
+        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.layers, self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._index = k.device.index
+        self._pages = []
+        for i in range(self.layers):
+            p = LFPages(types[k.dtype], self.kv_heads, self.head_dim, self.page_size, self.num_pages,
+                        k.stride(1), k.stride(2), k.stride(3), k[i].data_ptr(), v[i].data_ptr(),
+                        self.err.data_ptr())
+            self._pages.append(p)
+        self._bytes = {}
+
+    def _layer(self, layer) -> LFPages:
+        if not 0 <= layer < self.layers:
+            raise LFError(LF_ERR_ARG, f"layer {layer} outside [0, {self.layers})")
+        return self._pages[layer]
+
+    def _bad(self, t, name, dtype, shape):
+        got = (tuple(t.shape), t.dtype, str(t.device)) if isinstance(t, torch.Tensor) else type(t)
+        return LFError(LF_ERR_ARG, f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}, "
+                                   f"got {got}")
+
+    def _expect(self, t, name, dtype, *shape):
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape \
+                or t.device != self.device or not t.is_contiguous():
+            raise self._bad(t, name, dtype, shape)
+
+    def _sequences(self, page_table, lens):
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise self._bad(page_table, "page_table", torch.int32, ("batch", "max_pages"))
+        batch, width = page_table.shape
+        self._expect(page_table, "page_table", torch.int32, batch, width)
+        self._expect(lens, "lens", torch.int32, batch)
+        return batch, width
+
+    def _heads(self, q, rows):
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise self._bad(q, "q", self.dtype, (rows, "q_heads", self.head_dim))
+        rows = q.shape[0] if rows is None else rows
+        self._expect(q, "q", self.dtype, rows, q.shape[1], self.head_dim)
+        return q.shape[1]
+
+    def _outputs(self, q, out, lse):
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._expect(out, "out", self.dtype, *q.shape)
+        if lse is not None:
+            self._expect(lse, "lse", torch.float32, q.shape[0], q.shape[1])
+        return out
+
+    def _run(self, stream, call):
+        """call(stream handle) with this cache's device and `stream` current, so that
+        what it allocates belongs to that stream."""
+        if stream is None:
+            if torch.cuda.current_device() == self._index:
+                return call(torch.cuda.current_stream().cuda_stream)
+            with torch.cuda.device(self._index):
+                return call(torch.cuda.current_stream().cuda_stream)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        with torch.cuda.device(self._index), torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+    def append(self, layer, k_new, v_new, page_table, lens, new_start=None, stream=None):
+        """lf_paged_append: k_new, v_new [tokens][kv_heads][head_dim] go to their pages;
+        new_start int32 [batch + 1], or None: one token per sequence."""
+        pages = self._layer(layer)
+        batch, width = self._sequences(page_table, lens)
+        if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
+            raise self._bad(k_new, "k_new", self.dtype, ("tokens", self.kv_heads, self.head_dim))
+        n = batch if new_start is None else k_new.shape[0]
+        self._expect(k_new, "k_new", self.dtype, n, self.kv_heads, self.head_dim)
+        self._expect(v_new, "v_new", self.dtype, n, self.kv_heads, self.head_dim)
+        if new_start is not None:
+            self._expect(new_start, "new_start", torch.int32, batch + 1)
+        self._run(stream, lambda st: lf_paged_append(pages, batch, page_table, width, lens, k_new, v_new,
+                                                     new_start, n, st))
+
+    def decode(self, layer, q, page_table, lens, k_new=None, v_new=None, window=0, sinks=0, out=None,
+               lse=None, stream=None):
+        """lf_paged_decode: q [batch][q_heads][head_dim] -> out of that shape.  With k_new and v_new
+        [batch][kv_heads][head_dim] the call stores the new token too."""
+        pages = self._layer(layer)
+        batch, width = self._sequences(page_table, lens)
+        q_heads = self._heads(q, batch)
+        if k_new is not None or v_new is not None:
+            self._expect(k_new, "k_new", self.dtype, batch, self.kv_heads, self.head_dim)
+            self._expect(v_new, "v_new", self.dtype, batch, self.kv_heads, self.head_dim)
+
+        def call(st):
+            key = (batch, width, q_heads, window, sinks)
+            need = self._bytes.get(key)
+            if need is None:
+                need = self._bytes[key] = lf_paged_decode_workspace(pages, batch, width, q_heads, window,
+                                                                    sinks)
+            o = self._outputs(q, out, lse)
+            # a workspace of this call's own: calls on other streams and graphs cannot meet in it
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+            lf_paged_decode(pages, batch, page_table, width, lens, q_heads, q, k_new, v_new, o, lse,
+                            window, sinks, ws, need, st)
+            return o
+
+        return self._run(stream, call)
+
+    def prompt(self, layer, q, page_table, lens, q_start, max_q, window=0, sinks=0, out=None, lse=None,
+               stream=None):
+        """lf_paged_prompt: q [rows][q_heads][head_dim] -> out of that shape; q_start int32
+        [batch + 1], max_q at least every sequence's number of rows."""
+        pages = self._layer(layer)
+        batch, width = self._sequences(page_table, lens)
+        q_heads = self._heads(q, None)
+        self._expect(q_start, "q_start", torch.int32, batch + 1)
+
+        def call(st):
+            o = self._outputs(q, out, lse)
+            lf_paged_prompt(pages, batch, page_table, width, lens, q_heads, q, q_start, q.shape[0], max_q,
+                            o, lse, window, sinks, st)
+            return o
+
+        return self._run(stream, call)
+
+    def check(self, stream=None) -> int:
+        """The device error bits since the last check (0 when clean); synchronises the stream."""
+        def call(_):
+            bits = int(self.err.item())
+            if bits:
+                self.err.zero_()
+            return bits
+        return self._run(stream, call)

@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define LF_ABI_VERSION 6
+#define LF_ABI_VERSION 7
 
 typedef struct lf_cache lf_cache; /* opaque; owns the slab */
 
@@ -363,6 +363,107 @@ int lf_launch_plan_for(const int32_t* occupancy, int units, int cluster, int clu
 int lf_prefill_fill_noalloc(const lf_layout* dst, int layer, const void* k, const void* v,
                             const int32_t* prompt_len, int max_prompt, lf_stream_t stream);
 
+/*
+ * Paged key-value cache.  (No counterpart on the pages: a sequence that keeps
+ * every token, or a window of them, grows page by page instead of holding a slab.)
+ *
+ * The caller owns everything: the pools of one layer, described by lf_pages, and
+ * for each call a page table and lengths, all device memory.  Page x of KV head g
+ * holds page_size tokens; slot s of it starts at element
+ *   x * page_stride + g * head_stride + s * token_stride
+ * of the K pool and of the V pool, head_dim elements in a row.  Any order of
+ * pages, heads and tokens goes, also K and V interleaved in one allocation, as
+ * long as every row starts on 16 bytes.  Row b of page_table [batch][max_pages]
+ * lists the pages of sequence b in order of position: position p is slot
+ * p % page_size of page page_table[b][p / page_size].  Sequences may share pages
+ * that no call writes.  Entries past a sequence's last token are not read.
+ *
+ * lens[b] is sequence b's length INCLUDING the tokens of the call that gets it: all
+ * layers of one step share one page table and one lens.  Lengths, tables and row
+ * starts are read on the device, so a captured graph follows their contents.
+ *
+ * Errors found on the device are OR-ed into *err where err is not NULL:
+ * LF_DEVERR_STATE for a page index outside [0, num_pages), a length outside [0,
+ * max_pages * page_size] or row starts outside the rows (such tokens are not
+ * stored or read as zeros; outputs of that sequence are unspecified, no other is
+ * touched), LF_DEVERR_NONFINITE for a softmax sum that is not finite,
+ * LF_DEVERR_TIMEOUT for an expired on-chip wait (that call's outputs are
+ * unspecified).  The caller reads and clears the word.
+ *
+ * Query head h reads KV head floor(h / G), G = q_heads / kv_heads in {1, 2, 4, 8};
+ * head_dim in {16, 32, 64, 128}; logits are scaled by 1 / sqrt(head_dim).  With
+ * window = W > 0 the query at position p sees positions p - W + 1 .. p and the
+ * positions below `sinks`; window = 0: all of 0 .. p (sinks must be 0 too).  A
+ * query that sees nothing gives zeros and a log-sum-exp of -inf.  lse may be
+ * NULL.  Softmax statistics and sums are fp32, outputs are rounded once (RNE).
+ * Values of tokens behind a sequence's end or outside the window never reach an
+ * output, whatever they hold (NaN included).
+ *
+ * Calls are stream-ordered, run on the current device, allocate nothing, do not
+ * synchronise the host and can be captured in a CUDA graph.
+ */
+typedef struct lf_pages {
+  int dtype;            /* LF_BF16 or LF_F32: type of the pools, q, k_new, v_new, out */
+  int kv_heads, head_dim;
+  int page_size;        /* tokens of a page, >= 1 */
+  int num_pages;        /* pages of the pools */
+  int64_t page_stride, head_stride, token_stride; /* elements; multiples of 16 bytes */
+  void* k;              /* 16-byte aligned */
+  void* v;
+  int32_t* err;         /* device error word, or NULL */
+} lf_pages;
+
+/*
+ * Write a call's new tokens to their pages.  Sequence b's tokens are rows
+ * new_start[b] .. new_start[b + 1] - 1 of k_new and v_new
+ * [total_new][kv_heads][head_dim] (contiguous, 16-byte aligned), its last ones:
+ * the first of n goes to position lens[b] - n.  Rows from new_start[batch] on
+ * belong to no sequence and are not read.  new_start [batch + 1] may be NULL: one
+ * token for each sequence, total_new = batch.  A page that is written belongs to
+ * one sequence of the call.
+ */
+int lf_paged_append(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
+                    const int32_t* lens, const void* k_new, const void* v_new,
+                    const int32_t* new_start, int total_new, lf_stream_t stream);
+
+/*
+ * Attention of each sequence's last token (position lens[b] - 1) over its pages.
+ *   q, out        [batch][q_heads][head_dim], contiguous, 16-byte aligned
+ *   k_new, v_new  [batch][kv_heads][head_dim]: that token's key and value, which the
+ *                 call writes to their page as lf_paged_append does; both NULL: they
+ *                 are in the pages already
+ *   lse           fp32 [batch][q_heads], or NULL: log sum exp of the scaled logits
+ *   workspace     lf_paged_decode_workspace bytes, 16-byte aligned, contents of no
+ *                 meaning before and after the call; not shared by calls that may run
+ *                 at the same time (two streams, two graphs)
+ * Results do not depend on how the work is split.  Up to two launches.
+ */
+int lf_paged_decode(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
+                    const int32_t* lens, int q_heads, const void* q, const void* k_new,
+                    const void* v_new, void* out, float* lse, int window, int sinks,
+                    void* workspace, size_t workspace_bytes, lf_stream_t stream);
+
+/* Bytes of the workspace of lf_paged_decode calls with these arguments on the
+ * current device; 0 when they need none. */
+int lf_paged_decode_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads,
+                              int window, int sinks, size_t* bytes);
+
+/*
+ * Causal attention of the last tokens of every sequence over its pages, which hold
+ * their keys and values already (lf_paged_append): whole prompts, or chunks behind
+ * tokens that are cached.  Sequence b's queries are rows q_start[b] .. q_start[b +
+ * 1] - 1 of q and out [total_q][q_heads][head_dim] (contiguous, 16-byte aligned);
+ * the first of n is at position lens[b] - n.  Rows from q_start[batch] on are left as
+ * they are.
+ *   q_start   device [batch + 1]
+ *   max_q     no sequence has more rows (more: LF_DEVERR_STATE, the rest is left)
+ *   lse       fp32 [total_q][q_heads], or NULL
+ */
+int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
+                    const int32_t* lens, int q_heads, const void* q, const int32_t* q_start,
+                    int total_q, int max_q, void* out, float* lse, int window, int sinks,
+                    lf_stream_t stream);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* lf_last_error(void);
 
@@ -371,7 +472,7 @@ const char* lf_last_error(void);
  * LF_ERR_UNSUPPORTED, LF_ERR_OOM (the slab does not fit in device memory) or
  * LF_ERR_CUDA.  It keeps its value until the next failure, or until one of
  * lf_cache_create*, lf_cache_destroy, lf_prefill_fill, lf_prefill_fill_noalloc,
- * lf_cache_check and lf_cache_layout resets it (with the message) on entry. */
+ * lf_cache_check, lf_cache_layout and lf_paged_* resets it (with the message) on entry. */
 int lf_last_status(void);
 
 /* LF_ABI_VERSION of the loaded library. */
