@@ -78,6 +78,11 @@ cudaError_t paged_decode_launch(const PagedDecodeArgs& a, int elem, int head_dim
 cudaError_t paged_prompt_launch(const PagedPromptArgs& a, int elem, int head_dim,
                                 cudaStream_t stream);
 
+// The tensor-core kernel for bf16: false, and nothing launched, where it is not built
+// (head_dim 16 and 32, pages that do not divide its key tiles); else *err is the
+// launch's error.
+bool paged_prompt_tc_launch(const PagedPromptArgs& a, int head_dim, cudaStream_t stream, cudaError_t* err);
+
 // Tokens that one CTA of the decode kernel takes in one sweep of its warps.
 int paged_decode_sweep(int elem, int head_dim);
 

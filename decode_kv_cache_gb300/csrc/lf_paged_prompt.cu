@@ -260,6 +260,8 @@ cudaError_t launch_dim(const PagedPromptArgs& a, int head_dim, cudaStream_t stre
 }  // namespace
 
 cudaError_t paged_prompt_launch(const PagedPromptArgs& a, int elem, int head_dim, cudaStream_t stream) {
+  cudaError_t e;
+  if (elem == 2 && paged_prompt_tc_launch(a, head_dim, stream, &e)) return e;
   return elem == 2 ? launch_dim<__nv_bfloat16>(a, head_dim, stream) : launch_dim<float>(a, head_dim, stream);
 }
 

@@ -1,0 +1,591 @@
+// Causal attention of the last tokens of every sequence over a paged bf16 cache
+// on the tensor cores (tcgen05), head_dim 64 and 128, with an optional sliding
+// window and sinks.  The formula is lf_paged_prompt.cu's.
+//
+// Work.  A CTA takes 256 rows of one KV head's queries, (token, head of the group)
+// pairs with the head inner, as two tiles of 128: every key and value it loads
+// serves both tiles and all heads of the group.  Key tiles of 128 tokens that no
+// row sees are not visited.  CTAs with the most keys start first.
+//
+// Roles (11 warps):
+//   loader   gathers K and V tiles by page with TMA (one box per page and 64
+//            columns, one lane each; a page past the end is a box outside the
+//            tensor, which the hardware fills with zeros) into a ring;
+//   scrubber where some row does not see some key of a tile, a weight of 0 must
+//            take nothing of the value, but 0 * NaN is NaN on the tensor cores: it
+//            zeroes the rows behind the last key that a row of the CTA sees and
+//            looks for values that are not finite in the others.  If it finds any,
+//            the CTA's rows are computed again, one by one, at the end;
+//   MMA      S_t = Q_t K^T into tensor memory, then O_t += P_t V with P_t read from
+//            tensor memory; the two tiles take turns, so that one's softmax runs
+//            under the other's products;
+//   softmax  two groups of four warps, a thread per row: S from tensor memory, the
+//            running maximum, P = 2^(s - m) rounded to bf16 back over S, the sum in
+//            fp32.  O is scaled down only when a row's maximum has grown by more
+//            than 2^8 (P and the sum stay far from fp32's range, and the division
+//            at the end makes any m right), so nearly never after the first tiles.
+//
+// Rounding P to bf16 (half a step is 2^-8 of a weight) is what the tensor cores
+// take; a second product for the remainder would double the P V work.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "lf_device.cuh"
+#include "lf_paged.h"
+#include "longflow.h"
+
+namespace lf {
+
+namespace {
+
+constexpr int kTile = 128;                 // rows of a query tile, tokens of a key tile
+constexpr int kBlk = kTile * 128;          // a tile's 64 columns in shared memory (128-byte swizzle)
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kScrubWarp = 10;
+constexpr int kThreadsTc = 352;
+constexpr float kGrow = 8.f;               // log2 growth of a maximum that is let pass
+constexpr float kNegInfTc = -INFINITY;
+
+struct PromptTcArgs {
+  CUtensorMap q, k, v;
+  PagedPromptArgs a;
+  int box_rows;      // tokens of one TMA box: min(page_size, 128)
+  int group_shift;
+};
+
+template <int D>
+struct TcPlan {
+  static constexpr int kTileBytes = D / 64 * kBlk;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffQ = 1024;
+  static constexpr int kOffRing = kOffQ + 2 * kTileBytes;
+  static constexpr int kSmem = kOffRing + kStages * kTileBytes + 1024;   // + alignment slack
+  static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ float ex2t(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] x B[smem desc], bf16 inputs, fp32 accumulation.
+__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// This warp's 32 lanes, 32 consecutive 32-bit columns of tensor memory.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The key tiles that a CTA visits: [0, sink) and [from, to).
+struct Tiles {
+  int sink, from, to;
+  __device__ int count() const { return sink + to - from; }
+  __device__ int at(int j) const { return j < sink ? j : from + j - sink; }
+};
+
+// One row by the definition, a warp at a time: for CTAs whose tiles held values
+// that are not finite where some row does not look.
+template <int D>
+__device__ __noinline__ void row_by_hand(const PagedPromptArgs& a, int b, int g, int64_t row, int pos,
+                                         int lane) {
+  constexpr int E = D / 32;
+  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + row * D + lane * E;
+  float qv[E], acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    qv[e] = to_f32(q[e]);
+    acc[e] = 0.f;
+  }
+  float m = kNegInfTc, l = 0.f;
+  for (int p = 0; p <= pos; ++p) {
+    if (a.window > 0 && p >= a.sinks && p <= pos - a.window) p = pos - a.window + 1;
+    int pi, slot;
+    paged_split(a.pool, p, &pi, &slot);
+    const int page = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
+    if (page < 0 || page >= a.pool.num_pages) continue;
+    const int64_t off = page * a.pool.page_stride + slot * a.pool.token_stride + g * a.pool.head_stride;
+    const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(a.pool.k + off) + lane * E;
+    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.pool.v + off) + lane * E;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(qv[e], to_f32(k[e]), s);
+    s = warp_sum(s) * a.scale_log2;
+    const float mn = fmaxf(m, s), mu = mn == kNegInfTc ? 0.f : mn;
+    const float f = ex2t(m - mu), w = ex2t(s - mu);
+    m = mn;
+    l = l * f + w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + w * to_f32(v[e]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + row * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) from_f32(l == 0.f ? 0.f : acc[e] * inv, out + e);
+  if (lane == 0) {
+    if (a.lse) a.lse[row] = l == 0.f ? kNegInfTc : (m + log2f(l)) * 0.6931471805599453f;
+    if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __grid_constant__ PromptTcArgs ta) {
+  using P = TcPlan<D>;
+  constexpr int S = P::kStages;
+  const PagedPromptArgs& a = ta.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.group, gs = ta.group_shift;
+  const int b = blockIdx.x / a.pool.kv_heads, g = blockIdx.x - b * a.pool.kv_heads;
+
+  const int q0 = a.q_start[b], n = a.q_start[b + 1] - q0;
+  const bool head_block = blockIdx.y == 0 && g == 0 && tid == 0;
+  if (q0 < 0 || n < 0 || n > a.total_q - q0) {   // not rows of q
+    if (head_block && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+    return;
+  }
+  const int len = paged_len(a.pool, b);
+  if (head_block && a.pool.err && (n > a.max_q || len != a.pool.lens[b] || n > len))
+    atomicOr(a.pool.err, LF_DEVERR_STATE);
+  const int64_t rows = (int64_t)n << gs;
+  const int64_t r0 = (int64_t)(gridDim.y - 1 - blockIdx.y) * (2 * kTile);
+  if (r0 >= rows) return;
+  const int first_pos = len - n;
+  const int p_lo = first_pos + (int)(r0 >> gs);
+  const int p_hi = first_pos + (int)((min(r0 + 2 * kTile, rows) - 1) >> gs);
+  Tiles tiles = {0, 0, 0};
+  if (p_hi >= 0) {
+    tiles.to = p_hi / kTile + 1;
+    if (a.window > 0) {
+      tiles.from = (int)max((int64_t)0, (int64_t)p_lo - a.window + 1) / kTile;
+      tiles.sink = min((int)(((int64_t)a.sinks + kTile - 1) / kTile), tiles.from);
+    }
+  }
+  const int nt = tiles.count();
+  // Does some row of the CTA not see some key of the tile at k0?
+  auto masked = [&](int k0) {
+    return k0 + kTile - 1 > p_lo ||
+           (a.window > 0 && k0 + kTile > a.sinks && (int64_t)k0 <= (int64_t)p_hi - a.window);
+  };
+
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);   // [S] a tile is ready for the MMAs
+  uint64_t* empty = full + S;                           // [S] the MMAs have read it
+  uint64_t* raw = empty + S;                            // [S] V landed, to be scrubbed
+  uint64_t* qfull = raw + S;
+  uint64_t* sfull = qfull + 1;                          // [2] S_t ready (and every MMA before it done)
+  uint64_t* pfull = sfull + 2;                          // [2] P_t written, O_t scaled
+  uint64_t* ofull = pfull + 2;                          // [2] O_t final
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + 528);   // [0] a wait expired, [1] by hand
+  unsigned char* qs = smem + P::kOffQ;
+  unsigned char* ring = smem + P::kOffRing;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+      mbar_init(&raw[i], 1);
+    }
+    mbar_init(qfull, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sfull[t], 1);
+      mbar_init(&pfull[t], 4);
+      mbar_init(&ofull[t], 1);
+    }
+    fence_mbar_init();
+    misc[0] = misc[1] = 0;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tmem_slot;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!misc[0] && mbar_wait_bounded(bar, parity)) return true;
+    misc[0] = 1;
+    return false;
+  };
+
+  float m = kNegInfTc, l = 0.f;   // softmax threads: their row's maximum (log2) and sum
+
+  if (warp == kLoadWarp) {
+    // ---- loader ---------------------------------------------------------------------
+    const int boxes = kTile / ta.box_rows;
+    const int box = lane % boxes, blk = lane / boxes;
+    const bool mine = lane < boxes * (D / 64);
+    auto page_of = [&](int tile, int* slot) {   // of this lane's box; num_pages: zeros
+      const int p = tile * kTile + box * ta.box_rows;
+      *slot = 0;
+      if (!mine || p > p_hi) return a.pool.num_pages;
+      int pi;
+      paged_split(a.pool, p, &pi, slot);
+      const int page = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
+      if (page >= 0 && page < a.pool.num_pages) return page;
+      if (a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+      return a.pool.num_pages;
+    };
+    if (lane == 0 && nt > 0) {
+      mbar_arrive_expect_tx(qfull, 2 * P::kTileBytes);
+      for (int t = 0; t < 2; ++t)
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(qs + t * P::kTileBytes + c * kBlk, &ta.q, c * 64, g * G,
+                      q0 + (int)(r0 >> gs) + t * (kTile >> gs), qfull);
+    }
+    int slot = 0, page = nt > 0 ? page_of(tiles.at(0), &slot) : 0;
+    int issued = 0;
+    bool ok = true;
+    for (int j = 0; j < nt && ok; ++j) {
+      const int cur_page = page, cur_slot = slot;
+      if (j + 1 < nt) page = page_of(tiles.at(j + 1), &slot);
+      const bool scrub = masked(tiles.at(j) * kTile);
+      for (int kv = 0; kv < 2 && ok; ++kv) {
+        const int i = 2 * j + kv, st = i % S;
+        if (i >= S) ok = wait(&empty[st], (uint32_t)((i / S - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint64_t* bar = kv == 1 && scrub ? &raw[st] : &full[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, P::kTileBytes);
+        __syncwarp();
+        if (mine)
+          tma_load_4d(ring + st * P::kTileBytes + blk * kBlk + box * ta.box_rows * 128,
+                      kv ? &ta.v : &ta.k, blk * 64, cur_slot, g, cur_page, bar);
+        issued = i + 1;
+      }
+    }
+    // Every copy issued lands before the CTA may exit: the last ones of the ring
+    // here where the MMAs may not have waited for them.
+    if (!ok && lane == 0) {
+      (void)mbar_wait_bounded(qfull, 0);
+      // Per stage only its last copy can be in flight; its bytes arrive on full or
+      // raw, of which the other has no bytes to wait for: give the copies a second.
+      const unsigned long long t0 = global_ns();
+      while (issued > 0 && global_ns() - t0 < kWaitLimitNs) {}
+    }
+    __syncwarp();
+  } else if (warp == kScrubWarp) {
+    // ---- scrubber -------------------------------------------------------------------
+    uint32_t phase = 0;   // a bit per stage: its raw barrier's next parity
+    for (int j = 0; j < nt; ++j) {
+      const int k0 = tiles.at(j) * kTile;
+      if (!masked(k0)) continue;
+      const int st = (2 * j + 1) % S;
+      const bool ok = wait(&raw[st], (phase >> st) & 1u);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      phase ^= 1u << st;
+      unsigned char* v = ring + st * P::kTileBytes;
+      const int valid = min(kTile, p_hi + 1 - k0);
+      __nv_bfloat162 bad = __float2bfloat162_rn(0.f);
+      const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint4* rows4 = reinterpret_cast<uint4*>(v + c * kBlk);   // eight chunks per row
+#pragma unroll 8
+        for (int i = lane; i < valid * 8; i += 32) {
+          const uint4 x = rows4[i];
+          // 0 * x is 0, or NaN where x is not finite
+          bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, bad);
+          bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, bad);
+          bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, bad);
+          bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, bad);
+        }
+        for (int i = valid * 8 + lane; i < kTile * 8; i += 32) rows4[i] = make_uint4(0, 0, 0, 0);
+      }
+      const float2 f = __bfloat1622float2(bad);
+      if (__any_sync(0xffffffffu, !(f.x == 0.f) || !(f.y == 0.f)) && lane == 0) misc[1] = 1;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- MMA ------------------------------------------------------------------------
+    if (lane == 0 && nt > 0) {
+      constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
+      const uint32_t qa = smem_u32(qs), ra = smem_u32(ring);
+      auto mma_s = [&](int t, int st) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (uint32_t)((kk >> 2) * kBlk + (kk & 3) * 32);
+          tc_mma_bf16(tm + t * 128, sw128_desc(qa + t * P::kTileBytes + o, 16, 1024),
+                      sw128_desc(ra + st * P::kTileBytes + o, 16, 1024), kIdS, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&sfull[t]);
+      };
+      auto mma_o = [&](int t, int st, bool first) {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          tc_mma_bf16_ta(tm + 256 + t * D, tm + t * 128 + kk * 8,
+                         sw128_desc(ra + st * P::kTileBytes + kk * 2048, kBlk, 1024), kIdO,
+                         first && kk == 0 ? 0u : 1u);
+      };
+      bool ok = wait(qfull, 0) && wait(&full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        mma_s(0, 0);
+        mma_s(1, 0);
+        tc_commit(&empty[0]);
+      }
+      for (int j = 0; j < nt && ok; ++j) {
+        const int iv = 2 * j + 1, sv = iv % S, ik = iv + 1, sk = ik % S;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (t == 0) ok = wait(&full[sv], (uint32_t)((iv / S) & 1));
+          ok = ok && wait(&pfull[t], (uint32_t)(j & 1));
+          if (!ok) break;
+          tc_fence_after();
+          mma_o(t, sv, j == 0);
+          if (t == 1) tc_commit(&empty[sv]);
+          if (j + 1 == nt) {
+            tc_commit(&ofull[t]);
+            continue;
+          }
+          if (t == 0) {
+            ok = wait(&full[sk], (uint32_t)((ik / S) & 1));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          mma_s(t, sk);
+          if (t == 1) tc_commit(&empty[sk]);
+        }
+      }
+      if (!ok) {   // MMAs in flight end before the tensor memory is given back
+        tc_commit(qfull);
+        (void)mbar_wait_bounded(qfull, 1);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax ----------------------------------------------------------------------
+    const int t = warp >> 2;
+    const int64_t r = r0 + t * kTile + (warp & 3) * 32 + lane;
+    const int pos = r < rows ? first_pos + (int)(r >> gs) : -1;
+    const uint32_t ts = tm + t * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t to = tm + 256 + t * D + ((uint32_t)((warp & 3) * 32) << 16);
+    const float c = a.scale_log2;
+    for (int j = 0; j < nt; ++j) {
+      const int k0 = tiles.at(j) * kTile;
+      if (!__all_sync(0xffffffffu, wait(&sfull[t], (uint32_t)(j & 1)))) break;
+      tc_fence_after();
+      float x[kTile];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
+      tmem_wait_ld();
+      if (masked(k0)) {
+        const int hi = pos - k0, sk = a.sinks - k0;
+        const int lo = a.window > 0 && pos >= 0 ? pos - a.window + 1 - k0 : -1;
+#pragma unroll
+        for (int i = 0; i < kTile; ++i)
+          if (!(i <= hi && (i >= lo || i < sk))) x[i] = kNegInfTc;
+      }
+      float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int i = 4; i < kTile; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+      // O_t holds no product yet at j = 0; later, every product before S_t is done.
+      if (__any_sync(0xffffffffu, mx > m + kGrow || (m == kNegInfTc && mx > m))) {
+        const float mn = fmaxf(m, mx);
+        const float f = mn == kNegInfTc ? 1.f : ex2t(m - mn);
+        m = mn;
+        l *= f;
+        if (j > 0) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            float o[32];
+            tmem_ld32(to + 32 * i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tmem_st32(to + 32 * i, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+      }
+      const float mu = m == kNegInfTc ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float u = ex2t(fmaf(x[64 * h + 2 * i], c, -mu));
+          const float w = ex2t(fmaf(x[64 * h + 2 * i + 1], c, -mu));
+          sum[(2 * i) & 3] += u;
+          sum[(2 * i + 1) & 3] += w;
+          p[i] = pack2(u, w);
+        }
+        tmem_st32(ts + 32 * h, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[t]);
+    }
+    if (nt > 0) {
+      (void)wait(&ofull[t], 0);
+      tc_fence_after();
+    }
+  }
+  __syncthreads();
+
+  // ---- rows out ------------------------------------------------------------------------
+  if (warp < kMmaWarp) {
+    const int t = warp >> 2;
+    const int64_t r = r0 + t * kTile + (warp & 3) * 32 + lane;
+    const bool live = r < rows;
+    const int64_t row = live ? (int64_t)(q0 + (r >> gs)) * a.q_heads + g * G + (r & (G - 1)) : 0;
+    if (misc[0]) {
+      if (tid == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
+    } else if (misc[1]) {
+      for (int i = 0; i < 32; ++i) {
+        const int64_t ri = r - lane + i;
+        if (ri >= rows) break;
+        const int64_t rowi = (int64_t)(q0 + (ri >> gs)) * a.q_heads + g * G + (ri & (G - 1));
+        row_by_hand<D>(a, b, g, rowi, first_pos + (int)(ri >> gs), lane);
+      }
+    } else {
+      const uint32_t to = tm + 256 + t * D + ((uint32_t)((warp & 3) * 32) << 16);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + row * D);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        float o[32];
+        if (nt > 0) {
+          tmem_ld32(to + 32 * i, o);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            out[4 * i + e] = make_uint4(pack2(o[8 * e], o[8 * e + 1]), pack2(o[8 * e + 2], o[8 * e + 3]),
+                                        pack2(o[8 * e + 4], o[8 * e + 5]), pack2(o[8 * e + 6], o[8 * e + 7]));
+        }
+      }
+      if (live) {
+        if (a.lse) a.lse[row] = l == 0.f ? kNegInfTc : (m + log2f(l)) * 0.6931471805599453f;
+        if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                             CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static std::atomic<void*> fn{nullptr};
+  void* p = fn.load();
+  if (!p) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess || q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      return nullptr;
+    }
+    fn.store(p);
+  }
+  return reinterpret_cast<EncodeFn>(p);
+}
+
+bool encode(EncodeFn fn, CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const PromptTcArgs& ta, dim3 grid, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(paged_prompt_tc_kernel<D>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, TcPlan<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  paged_prompt_tc_kernel<D><<<grid, kThreadsTc, TcPlan<D>::kSmem, stream>>>(ta);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool paged_prompt_tc_launch(const PagedPromptArgs& a, int head_dim, cudaStream_t stream, cudaError_t* err) {
+  const int ps = a.pool.page_size;
+  // A key tile is whole boxes of whole pages (or a page is whole tiles), and a box
+  // is whole groups of the eight rows that the swizzle repeats over.
+  const bool pages = ps >= 8 && (ps < kTile ? kTile % ps == 0 : ps % kTile == 0);
+  const int64_t row_tiles = ((int64_t)a.max_q * a.group + 2 * kTile - 1) / (2 * kTile);
+  const int64_t heads = (int64_t)a.pool.batch * a.pool.kv_heads;
+  if ((head_dim != 64 && head_dim != 128) || !pages || row_tiles > 65535 || heads > 0x7fffffff) return false;
+  EncodeFn fn = encoder();
+  if (!fn) return false;
+  PromptTcArgs ta;
+  ta.a = a;
+  ta.box_rows = ps < kTile ? ps : kTile;
+  ta.group_shift = a.group == 1 ? 0 : a.group == 2 ? 1 : a.group == 4 ? 2 : 3;
+  const cuuint64_t qd[3] = {(cuuint64_t)head_dim, (cuuint64_t)a.q_heads, (cuuint64_t)a.total_q};
+  const cuuint64_t qst[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)a.q_heads * head_dim * 2};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(kTile / a.group)};
+  const cuuint64_t kd[4] = {(cuuint64_t)head_dim, (cuuint64_t)ps, (cuuint64_t)a.pool.kv_heads,
+                            (cuuint64_t)a.pool.num_pages};
+  // a dimension of one entry has no use for its stride, which must still be a legal one
+  auto legal = [](int64_t s, cuuint64_t n) { return n == 1 && s < 16 ? (cuuint64_t)16 : (cuuint64_t)s; };
+  const cuuint64_t kst[3] = {legal(a.pool.token_stride, kd[1]), legal(a.pool.head_stride, kd[2]),
+                             legal(a.pool.page_stride, kd[3])};
+  const cuuint32_t kb[4] = {64, (cuuint32_t)ta.box_rows, 1, 1};
+  // What a tensor map cannot describe (a stride of zero or from 2^40 bytes on) is the other kernel's.
+  if (!encode(fn, &ta.q, a.q, 3, qd, qst, qb) || !encode(fn, &ta.k, a.pool.k, 4, kd, kst, kb) ||
+      !encode(fn, &ta.v, a.pool.v, 4, kd, kst, kb))
+    return false;
+  const dim3 grid((unsigned)heads, (unsigned)row_tiles, 1);
+  *err = head_dim == 64 ? launch<64>(ta, grid, stream) : launch<128>(ta, grid, stream);
+  return true;
+}
+
+}  // namespace lf
