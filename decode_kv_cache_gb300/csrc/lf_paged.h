@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace lf {
 
 // The pools of one layer and one call's page table.  Strides are in bytes.
@@ -68,6 +70,19 @@ __device__ __forceinline__ void paged_split(const PagedPool& p, int pos, int* pa
     *page = (int)((unsigned)pos / (unsigned)p.page_size);
     *slot = pos - *page * p.page_size;
   }
+}
+
+// Opt-in shared memory of a kernel, asked for once per device: `done` has a bit per
+// device (the first 64; further ones ask each time).
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Launches (one translation unit each).  They return the launch's error.

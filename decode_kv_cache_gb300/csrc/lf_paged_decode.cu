@@ -809,8 +809,8 @@ cudaError_t launch(const PagedDecodeArgs& a, int grid, cudaStream_t stream) {
   using T = typename C::T;
   constexpr int kSmem = C::kWarps * warp_bytes<C, D, G>();
   static_assert(kSmem + (2 * C::kWarps * (int)sizeof(Part) + 127) / 128 * 128 <= 232448, "shared memory of one CTA");
-  cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<C, D, G>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_decode_kernel<C, D, G>), kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -239,8 +239,8 @@ __global__ void __launch_bounds__(kThreadsP) paged_prompt_simt_kernel(const __gr
 template <typename T, int D>
 cudaError_t launch(const PagedPromptArgs& a, cudaStream_t stream) {
   constexpr int kSmem = prompt_smem<T, D>();
-  const cudaError_t e = cudaFuncSetAttribute(paged_prompt_simt_kernel<T, D>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_prompt_simt_kernel<T, D>), kSmem, done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)a.max_q * a.group + kRows - 1) / kRows;
   paged_prompt_simt_kernel<T, D><<<dim3((unsigned)tiles, a.pool.kv_heads, a.pool.batch), kThreadsP, kSmem, stream>>>(a);

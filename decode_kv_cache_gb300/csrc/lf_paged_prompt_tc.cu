@@ -99,7 +99,40 @@ __device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem,
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// This warp's 32 lanes, 32 consecutive 32-bit columns of tensor memory.
+// The largest of three; a NaN among them is passed over.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two floats in a register pair, for the instructions that take both at once.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float* x, float* y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// This warp's 32 lanes, 16 / 32 consecutive 32-bit columns of tensor memory.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -170,7 +203,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   using P = TcPlan<D>;
   constexpr int S = P::kStages;
   const PagedPromptArgs& a = ta.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform for the compiler too
   const int G = a.group, gs = ta.group_shift;
   const int b = blockIdx.x / a.pool.kv_heads, g = blockIdx.x - b * a.pool.kv_heads;
 
@@ -211,8 +245,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   uint64_t* raw = empty + S;                            // [S] V landed, to be scrubbed
   uint64_t* qfull = raw + S;
   uint64_t* sfull = qfull + 1;                          // [2] S_t ready (and every MMA before it done)
-  uint64_t* pfull = sfull + 2;                          // [2] P_t written, O_t scaled
-  uint64_t* ofull = pfull + 2;                          // [2] O_t final
+  uint64_t* pfull = sfull + 2;                          // [2][2] half of P_t written (O_t scaled)
+  uint64_t* ofull = pfull + 4;                          // [2] O_t final
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
   volatile int* misc = reinterpret_cast<volatile int*>(smem + 528);   // [0] a wait expired, [1] by hand
   unsigned char* qs = smem + P::kOffQ;
@@ -227,7 +261,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     mbar_init(qfull, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
-      mbar_init(&pfull[t], 4);
+      mbar_init(&pfull[2 * t], 4);
+      mbar_init(&pfull[2 * t + 1], 4);
       mbar_init(&ofull[t], 1);
     }
     fence_mbar_init();
@@ -240,7 +275,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = *tmem_slot;
+  const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!misc[0] && mbar_wait_bounded(bar, parity)) return true;
     misc[0] = 1;
@@ -339,56 +374,69 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     }
   } else if (warp == kMmaWarp) {
     // ---- MMA ------------------------------------------------------------------------
-    if (lane == 0 && nt > 0) {
+    // The whole warp walks the tiles, so that descriptors stay in uniform registers;
+    // lane 0 issues.
+    if (nt > 0) {
       constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
-      const uint32_t qa = smem_u32(qs), ra = smem_u32(ring);
+      // Descriptors of an operand differ in their start address alone (16-byte units).
+      const uint64_t dq = sw128_desc(smem_u32(qs), 16, 1024);
+      const uint64_t dk = sw128_desc(smem_u32(ring), 16, 1024);
+      const uint64_t dv = sw128_desc(smem_u32(ring), kBlk, 1024);
+      const bool leader = lane == 0;
       auto mma_s = [&](int t, int st) {
+        const uint64_t qd = dq + (uint64_t)(t * (P::kTileBytes >> 4));
+        const uint64_t kd = dk + (uint64_t)(st * (P::kTileBytes >> 4));
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (uint32_t)((kk >> 2) * kBlk + (kk & 3) * 32);
-          tc_mma_bf16(tm + t * 128, sw128_desc(qa + t * P::kTileBytes + o, 16, 1024),
-                      sw128_desc(ra + st * P::kTileBytes + o, 16, 1024), kIdS, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t o = (uint64_t)(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4);
+            tc_mma_bf16(tm + t * 128, qd + o, kd + o, kIdS, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&sfull[t]);
         }
-        tc_commit(&sfull[t]);
       };
-      auto mma_o = [&](int t, int st, bool first) {
+      auto mma_o = [&](int t, int st, int half, uint32_t acc) {
+        const uint64_t vd = dv + (uint64_t)(st * (P::kTileBytes >> 4));
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          tc_mma_bf16_ta(tm + 256 + t * D, tm + t * 128 + kk * 8,
-                         sw128_desc(ra + st * P::kTileBytes + kk * 2048, kBlk, 1024), kIdO,
-                         first && kk == 0 ? 0u : 1u);
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16_ta(tm + 256 + t * D, tm + t * 128 + half * 32 + kk * 8,
+                           vd + (uint64_t)((half * 4 + kk) * 128), kIdO, kk > 0 ? 1u : acc);
+        }
       };
-      bool ok = wait(qfull, 0) && wait(&full[0], 0);
+      bool ok = __all_sync(0xffffffffu, wait(qfull, 0) && wait(&full[0], 0));
       if (ok) {
         tc_fence_after();
         mma_s(0, 0);
         mma_s(1, 0);
-        tc_commit(&empty[0]);
+        if (leader) tc_commit(&empty[0]);
       }
       for (int j = 0; j < nt && ok; ++j) {
         const int iv = 2 * j + 1, sv = iv % S, ik = iv + 1, sk = ik % S;
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (t == 0) ok = wait(&full[sv], (uint32_t)((iv / S) & 1));
-          ok = ok && wait(&pfull[t], (uint32_t)(j & 1));
+        const bool last = j + 1 == nt;
+        ok = __all_sync(0xffffffffu, wait(&full[sv], (uint32_t)((iv / S) & 1)));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          ok = ok && __all_sync(0xffffffffu, wait(&pfull[2 * t], (uint32_t)(j & 1)));
           if (!ok) break;
           tc_fence_after();
-          mma_o(t, sv, j == 0);
-          if (t == 1) tc_commit(&empty[sv]);
-          if (j + 1 == nt) {
-            tc_commit(&ofull[t]);
-            continue;
+          mma_o(t, sv, 0, j > 0 ? 1u : 0u);
+          if (t == 0 && !last) ok = __all_sync(0xffffffffu, wait(&full[sk], (uint32_t)((ik / S) & 1)));
+          ok = ok && __all_sync(0xffffffffu, wait(&pfull[2 * t + 1], (uint32_t)(j & 1)));
+          if (!ok) break;
+          tc_fence_after();
+          mma_o(t, sv, 1, 1u);
+          if (leader && t == 1) tc_commit(&empty[sv]);
+          if (last) {
+            if (leader) tc_commit(&ofull[t]);
+          } else {
+            mma_s(t, sk);
+            if (leader && t == 1) tc_commit(&empty[sk]);
           }
-          if (t == 0) {
-            ok = wait(&full[sk], (uint32_t)((ik / S) & 1));
-            if (!ok) break;
-            tc_fence_after();
-          }
-          mma_s(t, sk);
-          if (t == 1) tc_commit(&empty[sk]);
         }
       }
-      if (!ok) {   // MMAs in flight end before the tensor memory is given back
+      if (!ok && leader) {   // MMAs in flight end before the tensor memory is given back
         tc_commit(qfull);
         (void)mbar_wait_bounded(qfull, 1);
       }
@@ -419,46 +467,54 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
       }
       float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int i = 4; i < kTile; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+      for (int i = 4; i < kTile; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e + 4 < kTile) top[e] = max3(top[e], x[i + e], x[i + e + 4]);
+          else top[e] = fmaxf(top[e], x[i + e]);
       const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
       // O_t holds no product yet at j = 0; later, every product before S_t is done.
-      if (__any_sync(0xffffffffu, mx > m + kGrow || (m == kNegInfTc && mx > m))) {
+      if (__any_sync(0xffffffffu, mx > m + kGrow)) {
         const float mn = fmaxf(m, mx);
         const float f = mn == kNegInfTc ? 1.f : ex2t(m - mn);
         m = mn;
         l *= f;
         if (j > 0) {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            float o[32];
-            tmem_ld32(to + 32 * i, o);
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i) {
+            float o[16];
+            tmem_ld16(to + 16 * i, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(to + 32 * i, reinterpret_cast<const uint32_t*>(o));
+            for (int e = 0; e < 16; ++e) o[e] *= f;
+            tmem_st16(to + 16 * i, reinterpret_cast<const uint32_t*>(o));
           }
         }
       }
       const float mu = m == kNegInfTc ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t cc = pair(c, c), mm = pair(-mu, -mu);
+      uint64_t sum[2] = {0ull, 0ull};   // two pairs of zeros
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t p[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float u = ex2t(fmaf(x[64 * h + 2 * i], c, -mu));
-          const float w = ex2t(fmaf(x[64 * h + 2 * i + 1], c, -mu));
-          sum[(2 * i) & 3] += u;
-          sum[(2 * i + 1) & 3] += w;
+          float u, w;
+          unpair(fma_pair(pair(x[64 * h + 2 * i], x[64 * h + 2 * i + 1]), cc, mm), &u, &w);
+          u = ex2t(u);
+          w = ex2t(w);
+          sum[i & 1] = add_pair(sum[i & 1], pair(u, w));
           p[i] = pack2(u, w);
         }
         tmem_st32(ts + 32 * h, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[2 * t + h]);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pfull[t]);
+      float u, w;
+      unpair(add_pair(sum[0], sum[1]), &u, &w);
+      l += u + w;
     }
     if (nt > 0) {
       (void)wait(&ofull[t], 0);
@@ -546,8 +602,8 @@ bool encode(EncodeFn fn, CUtensorMap* m, const void* base, int rank, const cuuin
 
 template <int D>
 cudaError_t launch(const PromptTcArgs& ta, dim3 grid, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(paged_prompt_tc_kernel<D>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, TcPlan<D>::kSmem);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_prompt_tc_kernel<D>), TcPlan<D>::kSmem, done);
   if (e != cudaSuccess) return e;
   paged_prompt_tc_kernel<D><<<grid, kThreadsTc, TcPlan<D>::kSmem, stream>>>(ta);
   return cudaGetLastError();

@@ -487,86 +487,79 @@ class LFPagedCache:
                                           "[kv_heads][page_size][head_dim]")
         if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or k.stride() != v.stride():
             raise LFError(LF_ERR_ARG, "k and v must agree in shape, strides, dtype and device")
-        if k.numel() == 0 or (k.shape[4] > 1 and k.stride(4) != 1):
+        strides = k.stride()
+        if k.numel() == 0 or (k.shape[4] > 1 and strides[4] != 1):
             raise LFError(LF_ERR_ARG, "the pools must not be empty and their rows must be contiguous")
         self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
         self.layers, self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self._index = k.get_device()
+        self._row = (self.kv_heads, self.head_dim)
+        # the device error word, as a tensor of one int32
         self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self._index = k.device.index
-        self._pages = []
-        for i in range(self.layers):
-            p = LFPages(types[k.dtype], self.kv_heads, self.head_dim, self.page_size, self.num_pages,
-                        k.stride(1), k.stride(2), k.stride(3), k[i].data_ptr(), v[i].data_ptr(),
-                        self.err.data_ptr())
-            self._pages.append(p)
-        self._bytes = {}
+        step, pk, pv = strides[0] * k.element_size(), k.data_ptr(), v.data_ptr()
+        self._pages = [LFPages(types[k.dtype], self.kv_heads, self.head_dim, self.page_size, self.num_pages,
+                               strides[1], strides[2], strides[3], pk + i * step, pv + i * step,
+                               self.err.data_ptr()) for i in range(self.layers)]
+        self._need = {}   # workspace bytes by the shape of a decode call
+        self._lib = load_library()
 
     def _layer(self, layer) -> LFPages:
         if not 0 <= layer < self.layers:
             raise LFError(LF_ERR_ARG, f"layer {layer} outside [0, {self.layers})")
         return self._pages[layer]
 
-    def _bad(self, t, name, dtype, shape):
-        got = (tuple(t.shape), t.dtype, str(t.device)) if isinstance(t, torch.Tensor) else type(t)
-        return LFError(LF_ERR_ARG, f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}, "
-                                   f"got {got}")
-
-    def _expect(self, t, name, dtype, *shape):
+    def _expect(self, t, name, dtype, shape):
         if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape \
-                or t.device != self.device or not t.is_contiguous():
-            raise self._bad(t, name, dtype, shape)
+                or t.get_device() != self._index or not t.is_contiguous():
+            got = (tuple(t.shape), t.dtype, str(t.device)) if isinstance(t, torch.Tensor) else type(t)
+            raise LFError(LF_ERR_ARG, f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}, "
+                                      f"got {got}")
+
+    def _sizes(self, t, name, dims):
+        """The shape of a tensor of so many dimensions; a wrong one fails the check that follows."""
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            raise LFError(LF_ERR_ARG, f"{name}: expected a tensor of {dims} dimensions, got "
+                                      f"{tuple(t.shape) if isinstance(t, torch.Tensor) else type(t)}")
+        return t.shape
 
     def _sequences(self, page_table, lens):
-        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-            raise self._bad(page_table, "page_table", torch.int32, ("batch", "max_pages"))
-        batch, width = page_table.shape
-        self._expect(page_table, "page_table", torch.int32, batch, width)
-        self._expect(lens, "lens", torch.int32, batch)
-        return batch, width
-
-    def _heads(self, q, rows):
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise self._bad(q, "q", self.dtype, (rows, "q_heads", self.head_dim))
-        rows = q.shape[0] if rows is None else rows
-        self._expect(q, "q", self.dtype, rows, q.shape[1], self.head_dim)
-        return q.shape[1]
+        shape = self._sizes(page_table, "page_table", 2)
+        self._expect(page_table, "page_table", torch.int32, shape)
+        self._expect(lens, "lens", torch.int32, shape[:1])
+        return shape
 
     def _outputs(self, q, out, lse):
-        if out is None:
-            out = torch.empty_like(q)
-        else:
-            self._expect(out, "out", self.dtype, *q.shape)
+        if out is not None:
+            self._expect(out, "out", self.dtype, q.shape)
         if lse is not None:
-            self._expect(lse, "lse", torch.float32, q.shape[0], q.shape[1])
-        return out
+            self._expect(lse, "lse", torch.float32, q.shape[:2])
 
-    def _run(self, stream, call):
-        """call(stream handle) with this cache's device and `stream` current, so that
+    def _run(self, stream, call, *args):
+        """call(stream handle, *args) with this cache's device and `stream` current, so that
         what it allocates belongs to that stream."""
-        if stream is None:
-            if torch.cuda.current_device() == self._index:
-                return call(torch.cuda.current_stream().cuda_stream)
-            with torch.cuda.device(self._index):
-                return call(torch.cuda.current_stream().cuda_stream)
+        if stream is None and torch.cuda.current_device() == self._index:
+            return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
         with torch.cuda.device(self._index), torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
 
     def append(self, layer, k_new, v_new, page_table, lens, new_start=None, stream=None):
         """lf_paged_append: k_new, v_new [tokens][kv_heads][head_dim] go to their pages;
         new_start int32 [batch + 1], or None: one token per sequence."""
         pages = self._layer(layer)
         batch, width = self._sequences(page_table, lens)
-        if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
-            raise self._bad(k_new, "k_new", self.dtype, ("tokens", self.kv_heads, self.head_dim))
-        n = batch if new_start is None else k_new.shape[0]
-        self._expect(k_new, "k_new", self.dtype, n, self.kv_heads, self.head_dim)
-        self._expect(v_new, "v_new", self.dtype, n, self.kv_heads, self.head_dim)
+        n = batch if new_start is None else self._sizes(k_new, "k_new", 3)[0]
+        self._expect(k_new, "k_new", self.dtype, (n, *self._row))
+        self._expect(v_new, "v_new", self.dtype, (n, *self._row))
         if new_start is not None:
-            self._expect(new_start, "new_start", torch.int32, batch + 1)
-        self._run(stream, lambda st: lf_paged_append(pages, batch, page_table, width, lens, k_new, v_new,
-                                                     new_start, n, st))
+            self._expect(new_start, "new_start", torch.int32, (batch + 1,))
+        self._run(stream, self._append, pages, batch, width, page_table, lens, k_new, v_new, new_start, n)
+
+    def _append(self, st, pages, batch, width, page_table, lens, k_new, v_new, new_start, n):
+        _check(self._lib.lf_paged_append(
+            pages, batch, page_table.data_ptr(), width, lens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+            None if new_start is None else new_start.data_ptr(), n, st))
 
     def decode(self, layer, q, page_table, lens, k_new=None, v_new=None, window=0, sinks=0, out=None,
                lse=None, stream=None):
@@ -574,25 +567,29 @@ class LFPagedCache:
         [batch][kv_heads][head_dim] the call stores the new token too."""
         pages = self._layer(layer)
         batch, width = self._sequences(page_table, lens)
-        q_heads = self._heads(q, batch)
+        q_heads = self._sizes(q, "q", 3)[1]
+        self._expect(q, "q", self.dtype, (batch, q_heads, self.head_dim))
         if k_new is not None or v_new is not None:
-            self._expect(k_new, "k_new", self.dtype, batch, self.kv_heads, self.head_dim)
-            self._expect(v_new, "v_new", self.dtype, batch, self.kv_heads, self.head_dim)
+            self._expect(k_new, "k_new", self.dtype, (batch, *self._row))
+            self._expect(v_new, "v_new", self.dtype, (batch, *self._row))
+        self._outputs(q, out, lse)
+        return self._run(stream, self._decode, pages, batch, width, q_heads, page_table, lens, q, k_new,
+                         v_new, out, lse, window, sinks)
 
-        def call(st):
-            key = (batch, width, q_heads, window, sinks)
-            need = self._bytes.get(key)
-            if need is None:
-                need = self._bytes[key] = lf_paged_decode_workspace(pages, batch, width, q_heads, window,
-                                                                    sinks)
-            o = self._outputs(q, out, lse)
-            # a workspace of this call's own: calls on other streams and graphs cannot meet in it
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-            lf_paged_decode(pages, batch, page_table, width, lens, q_heads, q, k_new, v_new, o, lse,
-                            window, sinks, ws, need, st)
-            return o
-
-        return self._run(stream, call)
+    def _decode(self, st, pages, batch, width, q_heads, page_table, lens, q, k_new, v_new, out, lse, window,
+                sinks):
+        key = (batch, width, q_heads, window, sinks)
+        need = self._need.get(key)
+        if need is None:
+            need = self._need[key] = lf_paged_decode_workspace(pages, *key)
+        if out is None:
+            out = torch.empty_like(q)
+        # a workspace of this call's own: calls on other streams and graphs cannot meet in it
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        _check(self._lib.lf_paged_decode(
+            pages, batch, page_table.data_ptr(), width, lens.data_ptr(), q_heads, q.data_ptr(), _ptr(k_new),
+            _ptr(v_new), out.data_ptr(), _ptr(lse), window, sinks, _ptr(ws), need, st))
+        return out
 
     def prompt(self, layer, q, page_table, lens, q_start, max_q, window=0, sinks=0, out=None, lse=None,
                stream=None):
@@ -600,22 +597,28 @@ class LFPagedCache:
         [batch + 1], max_q at least every sequence's number of rows."""
         pages = self._layer(layer)
         batch, width = self._sequences(page_table, lens)
-        q_heads = self._heads(q, None)
-        self._expect(q_start, "q_start", torch.int32, batch + 1)
+        rows, q_heads, _ = self._sizes(q, "q", 3)
+        self._expect(q, "q", self.dtype, (rows, q_heads, self.head_dim))
+        self._expect(q_start, "q_start", torch.int32, (batch + 1,))
+        self._outputs(q, out, lse)
+        return self._run(stream, self._prompt, pages, batch, width, q_heads, page_table, lens, q, q_start,
+                         rows, max_q, out, lse, window, sinks)
 
-        def call(st):
-            o = self._outputs(q, out, lse)
-            lf_paged_prompt(pages, batch, page_table, width, lens, q_heads, q, q_start, q.shape[0], max_q,
-                            o, lse, window, sinks, st)
-            return o
-
-        return self._run(stream, call)
+    def _prompt(self, st, pages, batch, width, q_heads, page_table, lens, q, q_start, rows, max_q, out, lse,
+                window, sinks):
+        if out is None:
+            out = torch.empty_like(q)
+        _check(self._lib.lf_paged_prompt(
+            pages, batch, page_table.data_ptr(), width, lens.data_ptr(), q_heads, q.data_ptr(),
+            q_start.data_ptr(), rows, max_q, out.data_ptr(), _ptr(lse), window, sinks, st))
+        return out
 
     def check(self, stream=None) -> int:
         """The device error bits since the last check (0 when clean); synchronises the stream."""
-        def call(_):
-            bits = int(self.err.item())
-            if bits:
-                self.err.zero_()
-            return bits
-        return self._run(stream, call)
+        return self._run(stream, self._take_bits)
+
+    def _take_bits(self, _):
+        bits = int(self.err.item())
+        if bits:
+            self.err.zero_()
+        return bits
