@@ -43,8 +43,9 @@ namespace {
 
 constexpr int kTile = 128;                 // rows of a query tile, tokens of a key tile
 constexpr int kBlk = kTile * 128;          // a tile's 64 columns in shared memory (128-byte swizzle)
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kScrubWarp = 10;
-constexpr int kThreadsTc = 352;
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kScrubWarp = 2, kSoftWarp = 4;  // softmax: 4 .. 11 (3 rests)
+constexpr int kThreadsTc = 384;
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 constexpr float kGrow = 8.f;               // log2 growth of a maximum that is let pass
 constexpr float kNegInfTc = -INFINITY;
 
@@ -58,10 +59,11 @@ struct PromptTcArgs {
 template <int D>
 struct TcPlan {
   static constexpr int kTileBytes = D / 64 * kBlk;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kOffQ = 1024;
   static constexpr int kOffRing = kOffQ + 2 * kTileBytes;
-  static constexpr int kSmem = kOffRing + kStages * kTileBytes + 1024;   // + alignment slack
+  static constexpr int kOffOut = kOffRing + kStages * kTileBytes;        // 4 KB per softmax warp
+  static constexpr int kSmem = kOffOut + 8 * 4096 + 1024;                // + alignment slack
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
@@ -90,13 +92,27 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
-// D[tmem] (+)= A[tmem] x B[smem desc], bf16 inputs, fp32 accumulation.
-__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                               uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A x B, bf16 inputs, fp32 accumulation, by the lane whose `lead` is set.
+// The predicate is on the instruction, not on a branch around it: in straight code the
+// descriptors stay in uniform registers, where the instruction wants them.
+// Of a descriptor only the low word changes; the high one is the same for all
+// operands here (1024 bytes between groups of eight rows, version 1, 128-byte swizzle).
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint32_t adesc, uint32_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(adesc), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead), "n"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead), "n"(kDescHigh)
       : "memory");
 }
 // The largest of three; a NaN among them is passed over.
@@ -154,6 +170,18 @@ struct Tiles {
   __device__ int at(int j) const { return j < sink ? j : from + j - sink; }
 };
 
+// Wait on, up to kWaitLimitNs or until another wait has expired (`expired`).
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* expired) {
+  const unsigned long long t0 = global_ns();
+  while (!*expired) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitLimitNs) *expired = 1;
+  }
+  return false;
+}
+
 // One row by the definition, a warp at a time: for CTAs whose tiles held values
 // that are not finite where some row does not look.
 template <int D>
@@ -208,6 +236,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   const int G = a.group, gs = ta.group_shift;
   const int b = blockIdx.x / a.pool.kv_heads, g = blockIdx.x - b * a.pool.kv_heads;
 
+  // The loader's lookups for the first key tile, before it is known whether that is
+  // tile 0 (it is unless a window without sinks starts behind it).
+  const int boxes = kTile / ta.box_rows, box = lane % boxes, blk = lane / boxes;
+  int guess = -1;
+  if (warp == kLoadWarp) {
+    if (lane < 3) tma_prefetch_desc(lane == 0 ? &ta.q : lane == 1 ? &ta.k : &ta.v);
+    int pi, slot;
+    paged_split(a.pool, box * ta.box_rows, &pi, &slot);
+    if (pi < a.pool.max_pages) guess = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
+  }
   const int q0 = a.q_start[b], n = a.q_start[b + 1] - q0;
   const bool head_block = blockIdx.y == 0 && g == 0 && tid == 0;
   if (q0 < 0 || n < 0 || n > a.total_q - q0) {   // not rows of q
@@ -241,32 +279,71 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);   // [S] a tile is ready for the MMAs
-  uint64_t* empty = full + S;                           // [S] the MMAs have read it
-  uint64_t* raw = empty + S;                            // [S] V landed, to be scrubbed
+  uint64_t* raw = full + S;                             // [S] V landed, to be scrubbed
   uint64_t* qfull = raw + S;
-  uint64_t* sfull = qfull + 1;                          // [2] S_t ready (and every MMA before it done)
-  uint64_t* pfull = sfull + 2;                          // [2][2] half of P_t written (O_t scaled)
+  uint64_t* sfull = qfull + 1;                          // [t][j & 3] S_t of key tile j ready, and
+                                                        // every MMA before it done
+  uint64_t* pfull = sfull + 8;                          // [2][2] half of P_t written (O_t scaled)
   uint64_t* ofull = pfull + 4;                          // [2] O_t final
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
   volatile int* misc = reinterpret_cast<volatile int*>(smem + 528);   // [0] a wait expired, [1] by hand
   unsigned char* qs = smem + P::kOffQ;
   unsigned char* ring = smem + P::kOffRing;
 
-  if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-      mbar_init(&raw[i], 1);
+  // The loader sets up the barriers and starts on the queries and the first key tile
+  // at once; the others meet it behind.
+  auto page_of = [&](int tile, int first, int* slot) {   // of this lane's box; num_pages: zeros
+    const int p = tile * kTile + box * ta.box_rows;
+    *slot = 0;
+    if (lane >= boxes * (D / 64) || p > p_hi) return a.pool.num_pages;
+    int pi;
+    paged_split(a.pool, p, &pi, slot);
+    const int page = tile == 0 ? first : a.pool.table[(int64_t)b * a.pool.max_pages + pi];
+    if (page >= 0 && page < a.pool.num_pages) return page;
+    if (a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+    return a.pool.num_pages;
+  };
+  auto load = [&](int i, bool scrub, int page, int slot) {   // K (i even) or V of key tile i / 2
+    const int st = i % S;
+    uint64_t* bar = (i & 1) && scrub ? &raw[st] : &full[st];
+    if (lane == 0) mbar_arrive_expect_tx(bar, P::kTileBytes);
+    __syncwarp();
+    if (lane < boxes * (D / 64))
+      tma_load_4d(ring + st * P::kTileBytes + blk * kBlk + box * ta.box_rows * 128, (i & 1) ? &ta.v : &ta.k,
+                  blk * 64, slot, g, page, bar);
+  };
+  int page = 0, slot = 0;
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < S; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&raw[i], 1);
+      }
+      mbar_init(qfull, 1);
+      for (int t = 0; t < 2; ++t) {
+        for (int i = 0; i < 4; ++i) mbar_init(&sfull[4 * t + i], 1);
+        mbar_init(&pfull[2 * t], 4);
+        mbar_init(&pfull[2 * t + 1], 4);
+        mbar_init(&ofull[t], 1);
+      }
+      fence_mbar_init();
+      misc[0] = misc[1] = 0;
     }
-    mbar_init(qfull, 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&sfull[t], 1);
-      mbar_init(&pfull[2 * t], 4);
-      mbar_init(&pfull[2 * t + 1], 4);
-      mbar_init(&ofull[t], 1);
+    __syncwarp();
+    if (nt > 0) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(qfull, 2 * P::kTileBytes);
+        for (int t = 0; t < 2; ++t)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(qs + t * P::kTileBytes + c * kBlk, &ta.q, c * 64, g * G,
+                        q0 + (int)(r0 >> gs) + t * (kTile >> gs), qfull);
+      }
+      const bool scrub = masked(tiles.at(0) * kTile);
+      page = page_of(tiles.at(0), guess, &slot);
+      load(0, scrub, page, slot);
+      load(1, scrub, page, slot);
+      if (nt > 1) page = page_of(tiles.at(1), guess, &slot);
     }
-    fence_mbar_init();
-    misc[0] = misc[1] = 0;
   }
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, 512);
@@ -276,66 +353,38 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  // The first try costs a few tens of clocks, which the MMA warp's products hide; the
+  // limit and the flag that ends everyone's waits come after it.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!misc[0] && mbar_wait_bounded(bar, parity)) return true;
-    misc[0] = 1;
-    return false;
+    return mbar_try_wait(bar, parity) || wait_longer(bar, parity, misc);
   };
 
   float m = kNegInfTc, l = 0.f;   // softmax threads: their row's maximum (log2) and sum
 
   if (warp == kLoadWarp) {
     // ---- loader ---------------------------------------------------------------------
-    const int boxes = kTile / ta.box_rows;
-    const int box = lane % boxes, blk = lane / boxes;
-    const bool mine = lane < boxes * (D / 64);
-    auto page_of = [&](int tile, int* slot) {   // of this lane's box; num_pages: zeros
-      const int p = tile * kTile + box * ta.box_rows;
-      *slot = 0;
-      if (!mine || p > p_hi) return a.pool.num_pages;
-      int pi;
-      paged_split(a.pool, p, &pi, slot);
-      const int page = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
-      if (page >= 0 && page < a.pool.num_pages) return page;
-      if (a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
-      return a.pool.num_pages;
-    };
-    if (lane == 0 && nt > 0) {
-      mbar_arrive_expect_tx(qfull, 2 * P::kTileBytes);
-      for (int t = 0; t < 2; ++t)
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(qs + t * P::kTileBytes + c * kBlk, &ta.q, c * 64, g * G,
-                      q0 + (int)(r0 >> gs) + t * (kTile >> gs), qfull);
-    }
-    int slot = 0, page = nt > 0 ? page_of(tiles.at(0), &slot) : 0;
-    int issued = 0;
     bool ok = true;
-    for (int j = 0; j < nt && ok; ++j) {
+    for (int j = 1; j < nt && ok; ++j) {
       const int cur_page = page, cur_slot = slot;
-      if (j + 1 < nt) page = page_of(tiles.at(j + 1), &slot);
+      if (j + 1 < nt) page = page_of(tiles.at(j + 1), guess, &slot);   // a tile ahead
       const bool scrub = masked(tiles.at(j) * kTile);
-      for (int kv = 0; kv < 2 && ok; ++kv) {
-        const int i = 2 * j + kv, st = i % S;
-        if (i >= S) ok = wait(&empty[st], (uint32_t)((i / S - 1) & 1));
+      for (int i = 2 * j; i < 2 * j + 2; ++i) {
+        // The stage held load i - S, K or V of key tile u: K_u has been read once S_1
+        // of tile u is there, V_u once S_1 of tile u + 1 is.  (u >= j - 4, and S_1 of
+        // tile j waits for this load: of four barriers in turn none is a lap ahead.)
+        const int u = (i - S + 1) >> 1;
+        static_assert(S <= 8, "sfull barriers");
+        if (i >= S) ok = wait(&sfull[4 + (u & 3)], (uint32_t)((u >> 2) & 1));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        uint64_t* bar = kv == 1 && scrub ? &raw[st] : &full[st];
-        if (lane == 0) mbar_arrive_expect_tx(bar, P::kTileBytes);
-        __syncwarp();
-        if (mine)
-          tma_load_4d(ring + st * P::kTileBytes + blk * kBlk + box * ta.box_rows * 128,
-                      kv ? &ta.v : &ta.k, blk * 64, cur_slot, g, cur_page, bar);
-        issued = i + 1;
+        load(i, scrub, cur_page, cur_slot);
       }
     }
-    // Every copy issued lands before the CTA may exit: the last ones of the ring
-    // here where the MMAs may not have waited for them.
-    if (!ok && lane == 0) {
-      (void)mbar_wait_bounded(qfull, 0);
-      // Per stage only its last copy can be in flight; its bytes arrive on full or
-      // raw, of which the other has no bytes to wait for: give the copies a second.
+    // The MMAs wait for every copy, so none is in flight when the CTA exits, unless a
+    // wait ran out: then give the copies a second.
+    if (!ok) {
       const unsigned long long t0 = global_ns();
-      while (issued > 0 && global_ns() - t0 < kWaitLimitNs) {}
+      while (global_ns() - t0 < kWaitLimitNs) {}
     }
     __syncwarp();
   } else if (warp == kScrubWarp) {
@@ -374,77 +423,82 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     }
   } else if (warp == kMmaWarp) {
     // ---- MMA ------------------------------------------------------------------------
-    // The whole warp walks the tiles, so that descriptors stay in uniform registers;
-    // lane 0 issues.
+    // The tensor cores take an instruction every 64 clocks, so what stands between
+    // two of them counts: the warp walks the tiles together, one lane's predicate is
+    // on the instructions, descriptors are uniform values, and the two commits of a
+    // key tile serve the softmax and the loader both.
     if (nt > 0) {
       constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, false, false);
       constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
+      const uint32_t lead = lane == 0;
       // Descriptors of an operand differ in their start address alone (16-byte units).
-      const uint64_t dq = sw128_desc(smem_u32(qs), 16, 1024);
-      const uint64_t dk = sw128_desc(smem_u32(ring), 16, 1024);
-      const uint64_t dv = sw128_desc(smem_u32(ring), kBlk, 1024);
-      const bool leader = lane == 0;
-      auto mma_s = [&](int t, int st) {
-        const uint64_t qd = dq + (uint64_t)(t * (P::kTileBytes >> 4));
-        const uint64_t kd = dk + (uint64_t)(st * (P::kTileBytes >> 4));
-        if (leader) {
+      const uint32_t dq = (uint32_t)sw128_desc(smem_u32(qs), 16, 1024);
+      const uint32_t dk = (uint32_t)sw128_desc(smem_u32(ring), 16, 1024);
+      const uint32_t dv = (uint32_t)sw128_desc(smem_u32(ring), kBlk, 1024);
+      auto all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+      auto mma_s = [&](int t, int j, int st) {
+        const uint32_t qd = dq + (uint32_t)(t * (P::kTileBytes >> 4));
+        const uint32_t kd = dk + (uint32_t)(st * (P::kTileBytes >> 4));
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t o = (uint64_t)(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4);
-            tc_mma_bf16(tm + t * 128, qd + o, kd + o, kIdS, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(&sfull[t]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (uint32_t)(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4);
+          mma_ss(lead, tm + t * 128, qd + o, kd + o, kIdS, kk > 0 ? 1u : 0u);
         }
+        if (lead) tc_commit(&sfull[4 * t + (j & 3)]);
       };
       auto mma_o = [&](int t, int st, int half, uint32_t acc) {
-        const uint64_t vd = dv + (uint64_t)(st * (P::kTileBytes >> 4));
-        if (leader) {
+        const uint32_t vd = dv + (uint32_t)(st * (P::kTileBytes >> 4));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16_ta(tm + 256 + t * D, tm + t * 128 + half * 32 + kk * 8,
-                           vd + (uint64_t)((half * 4 + kk) * 128), kIdO, kk > 0 ? 1u : acc);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts(lead, tm + 256 + t * D, tm + t * 128 + half * 32 + kk * 8,
+                 vd + (uint32_t)((half * 4 + kk) * 128), kIdO, kk > 0 ? 1u : acc);
       };
-      bool ok = __all_sync(0xffffffffu, wait(qfull, 0) && wait(&full[0], 0));
+      bool ok = all(qfull, 0) && all(&full[0], 0);
       if (ok) {
         tc_fence_after();
-        mma_s(0, 0);
-        mma_s(1, 0);
-        if (leader) tc_commit(&empty[0]);
+        mma_s(0, 0, 0);
+        mma_s(1, 0, 0);
       }
+      int sv = 1 % S, sk = 2 % S;           // stages of V_j and K_(j+1)
+      uint32_t pv = 0, pk = 2 / S;          // and their parities
       for (int j = 0; j < nt && ok; ++j) {
-        const int iv = 2 * j + 1, sv = iv % S, ik = iv + 1, sk = ik % S;
         const bool last = j + 1 == nt;
-        ok = __all_sync(0xffffffffu, wait(&full[sv], (uint32_t)((iv / S) & 1)));
+        const uint32_t pj = (uint32_t)(j & 1);
+        ok = all(&full[sv], pv);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          ok = ok && __all_sync(0xffffffffu, wait(&pfull[2 * t], (uint32_t)(j & 1)));
+          ok = ok && all(&pfull[2 * t], pj);
           if (!ok) break;
           tc_fence_after();
           mma_o(t, sv, 0, j > 0 ? 1u : 0u);
-          if (t == 0 && !last) ok = __all_sync(0xffffffffu, wait(&full[sk], (uint32_t)((ik / S) & 1)));
-          ok = ok && __all_sync(0xffffffffu, wait(&pfull[2 * t + 1], (uint32_t)(j & 1)));
+          if (t == 0 && !last) ok = all(&full[sk], pk);
+          ok = ok && all(&pfull[2 * t + 1], pj);
           if (!ok) break;
           tc_fence_after();
           mma_o(t, sv, 1, 1u);
-          if (leader && t == 1) tc_commit(&empty[sv]);
-          if (last) {
-            if (leader) tc_commit(&ofull[t]);
-          } else {
-            mma_s(t, sk);
-            if (leader && t == 1) tc_commit(&empty[sk]);
-          }
+          if (!last) mma_s(t, j + 1, sk);
+          else if (lead) tc_commit(&ofull[t]);
+        }
+        sv += 2;
+        if (sv >= S) {
+          sv -= S;
+          pv ^= 1u;
+        }
+        sk += 2;
+        if (sk >= S) {
+          sk -= S;
+          pk ^= 1u;
         }
       }
-      if (!ok && leader) {   // MMAs in flight end before the tensor memory is given back
+      if (!ok && lead) {   // MMAs in flight end before the tensor memory is given back
         tc_commit(qfull);
         (void)mbar_wait_bounded(qfull, 1);
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp >= kSoftWarp) {
     // ---- softmax ----------------------------------------------------------------------
-    const int t = warp >> 2;
+    const int t = (warp - kSoftWarp) >> 2;
     const int64_t r = r0 + t * kTile + (warp & 3) * 32 + lane;
     const int pos = r < rows ? first_pos + (int)(r >> gs) : -1;
     const uint32_t ts = tm + t * 128 + ((uint32_t)((warp & 3) * 32) << 16);
@@ -452,7 +506,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     const float c = a.scale_log2;
     for (int j = 0; j < nt; ++j) {
       const int k0 = tiles.at(j) * kTile;
-      if (!__all_sync(0xffffffffu, wait(&sfull[t], (uint32_t)(j & 1)))) break;
+      if (!__all_sync(0xffffffffu, wait(&sfull[4 * t + (j & 3)], (uint32_t)((j >> 2) & 1)))) break;
       tc_fence_after();
       float x[kTile];
 #pragma unroll
@@ -524,13 +578,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   __syncthreads();
 
   // ---- rows out ------------------------------------------------------------------------
-  if (warp < kMmaWarp) {
-    const int t = warp >> 2;
+  if (warp >= kSoftWarp) {
+    const int t = (warp - kSoftWarp) >> 2;
     const int64_t r = r0 + t * kTile + (warp & 3) * 32 + lane;
     const bool live = r < rows;
     const int64_t row = live ? (int64_t)(q0 + (r >> gs)) * a.q_heads + g * G + (r & (G - 1)) : 0;
     if (misc[0]) {
-      if (tid == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
+      if (tid == kSoftWarp * 32 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
     } else if (misc[1]) {
       for (int i = 0; i < 32; ++i) {
         const int64_t ri = r - lane + i;
@@ -541,21 +595,36 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     } else {
       const uint32_t to = tm + 256 + t * D + ((uint32_t)((warp & 3) * 32) << 16);
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + row * D);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        float o[32];
-        if (nt > 0) {
-          tmem_ld32(to + 32 * i, o);
+      unsigned char* stage = smem + P::kOffOut + (warp - kSoftWarp) * 4096;   // 32 rows x 64 columns
+      const int64_t first = r - lane;
+#pragma unroll 1
+      for (int h = 0; h < D / 64; ++h) {   // through shared memory: whole lines of global memory
+        __syncwarp();   // the half before has been read
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          float o[32];   // (without keys nothing is there; l is 0 then)
+          tmem_ld32(to + 64 * h + 32 * q, o);
           tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              y[i] = l == 0.f ? 0u : pack2(o[8 * e + 2 * i] * inv, o[8 * e + 2 * i + 1] * inv);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + e) ^ (lane & 7)) << 4)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+          }
         }
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e] * inv;
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            out[4 * i + e] = make_uint4(pack2(o[8 * e], o[8 * e + 1]), pack2(o[8 * e + 2], o[8 * e + 3]),
-                                        pack2(o[8 * e + 4], o[8 * e + 5]), pack2(o[8 * e + 6], o[8 * e + 7]));
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3);
+          const int64_t ri = first + rr;
+          if (ri < rows)
+            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
+                                      ((int64_t)(q0 + (ri >> gs)) * a.q_heads + g * G + (ri & (G - 1))) * D +
+                                      h * 64 + (lane & 7) * 8) =
+                *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
         }
       }
       if (live) {
