@@ -342,7 +342,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
       page = page_of(tiles.at(0), guess, &slot);
       load(0, scrub, page, slot);
       load(1, scrub, page, slot);
-      if (nt > 1) page = page_of(tiles.at(1), guess, &slot);
     }
   }
   if (warp == kMmaWarp) {
@@ -364,6 +363,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   if (warp == kLoadWarp) {
     // ---- loader ---------------------------------------------------------------------
     bool ok = true;
+    if (nt > 1) page = page_of(tiles.at(1), guess, &slot);
     for (int j = 1; j < nt && ok; ++j) {
       const int cur_page = page, cur_slot = slot;
       if (j + 1 < nt) page = page_of(tiles.at(j + 1), guess, &slot);   // a tile ahead
@@ -500,13 +500,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     // ---- softmax ----------------------------------------------------------------------
     const int t = (warp - kSoftWarp) >> 2;
     const int64_t r = r0 + t * kTile + (warp & 3) * 32 + lane;
-    const int pos = r < rows ? first_pos + (int)(r >> gs) : -1;
+    const bool live = r < rows;
+    const int pos = live ? first_pos + (int)(r >> gs) : -1;
     const uint32_t ts = tm + t * 128 + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t to = tm + 256 + t * D + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = a.scale_log2;
+    bool ok = true;
     for (int j = 0; j < nt; ++j) {
       const int k0 = tiles.at(j) * kTile;
-      if (!__all_sync(0xffffffffu, wait(&sfull[4 * t + (j & 3)], (uint32_t)((j >> 2) & 1)))) break;
+      ok = __all_sync(0xffffffffu, wait(&sfull[4 * t + (j & 3)], (uint32_t)((j >> 2) & 1)));
+      if (!ok) break;
       tc_fence_after();
       float x[kTile];
 #pragma unroll
@@ -516,8 +519,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
         const int hi = pos - k0, sk = a.sinks - k0;
         const int lo = a.window > 0 && pos >= 0 ? pos - a.window + 1 - k0 : -1;
 #pragma unroll
-        for (int i = 0; i < kTile; ++i)
-          if (!(i <= hi && (i >= lo || i < sk))) x[i] = kNegInfTc;
+        for (int c0 = 0; c0 < kTile; c0 += 32)   // 32 keys that all rows of the warp see stay as they are
+          if (__any_sync(0xffffffffu, !(c0 + 31 <= hi && (c0 >= lo || c0 + 31 < sk)))) {
+#pragma unroll
+            for (int i = c0; i < c0 + 32; ++i)
+              if (!(i <= hi && (i >= lo || i < sk))) x[i] = kNegInfTc;
+          }
       }
       float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -570,21 +577,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
       unpair(add_pair(sum[0], sum[1]), &u, &w);
       l += u + w;
     }
-    if (nt > 0) {
-      (void)wait(&ofull[t], 0);
-      tc_fence_after();
-    }
-  }
-  __syncthreads();
 
-  // ---- rows out ------------------------------------------------------------------------
-  if (warp >= kSoftWarp) {
-    const int t = (warp - kSoftWarp) >> 2;
-    const int64_t r = r0 + t * kTile + (warp & 3) * 32 + lane;
-    const bool live = r < rows;
-    const int64_t row = live ? (int64_t)(q0 + (r >> gs)) * a.q_heads + g * G + (r & (G - 1)) : 0;
-    if (misc[0]) {
-      if (tid == kSoftWarp * 32 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
+    // ---- rows out --------------------------------------------------------------------
+    ok = ok && (nt == 0 || __all_sync(0xffffffffu, wait(&ofull[t], 0)));
+    tc_fence_after();
+    if (!ok) {
+      // nothing is right: leave the rows
     } else if (misc[1]) {
       for (int i = 0; i < 32; ++i) {
         const int64_t ri = r - lane + i;
@@ -593,10 +591,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
         row_by_hand<D>(a, b, g, rowi, first_pos + (int)(ri >> gs), lane);
       }
     } else {
-      const uint32_t to = tm + 256 + t * D + ((uint32_t)((warp & 3) * 32) << 16);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       unsigned char* stage = smem + P::kOffOut + (warp - kSoftWarp) * 4096;   // 32 rows x 64 columns
+      // Row rr of the warp's 32 is head rr % G of token rr / G from its first.
       const int64_t first = r - lane;
+      const int left = (int)min((int64_t)32, rows - first);
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) +
+                           ((int64_t)(q0 + (first >> gs)) * a.q_heads + g * G) * D + (lane & 7) * 8;
+      const int64_t token = (int64_t)a.q_heads * D;
 #pragma unroll 1
       for (int h = 0; h < D / 64; ++h) {   // through shared memory: whole lines of global memory
         __syncwarp();   // the half before has been read
@@ -619,25 +621,24 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int rr = 4 * i + (lane >> 3);
-          const int64_t ri = first + rr;
-          if (ri < rows)
-            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                      ((int64_t)(q0 + (ri >> gs)) * a.q_heads + g * G + (ri & (G - 1))) * D +
-                                      h * 64 + (lane & 7) * 8) =
+          if (rr < left)
+            *reinterpret_cast<uint4*>(out + (rr >> gs) * token + (rr & (G - 1)) * D + h * 64) =
                 *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
         }
       }
       if (live) {
+        const int64_t row = (int64_t)(q0 + (r >> gs)) * a.q_heads + g * G + (r & (G - 1));
         if (a.lse) a.lse[row] = l == 0.f ? kNegInfTc : (m + log2f(l)) * 0.6931471805599453f;
         if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
       }
     }
-    tc_fence_before();
   }
+  tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tm, 512);
+    if (lane == 0 && misc[0] && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
   }
 }
 
