@@ -27,70 +27,12 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "lf_device.cuh"
-#include "lf_paged.h"
+#include "lf_paged.cuh"
 #include "longflow.h"
 
 namespace lf {
 
 namespace {
-
-constexpr float kNegInf = -INFINITY;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 16 bytes global -> shared, or 16 zero bytes when `valid` is 0 (nothing is read then).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int valid) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Two floats as packed bf16 (x in the low half), rounded to nearest even.
-__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
-  return r;
-}
-
-// Shared-memory chunk of (row, 16-byte chunk c) in a tile of rows of NC chunks:
-// the low bits of c are XORed with the row's place among the rows that share
-// its banks, so that eight rows' equal chunks fall into eight bank groups.
-template <int NC>
-__device__ __forceinline__ int tile_chunk(int row, int c) {
-  if constexpr (NC >= 8) return row * NC + (c ^ (row & 7));
-  else return row * NC + (c ^ ((row / (8 / NC)) & (NC - 1)));
-}
 
 // 1 / l; 0 for a row that saw nothing (l = 0), so that its output is zeros.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }

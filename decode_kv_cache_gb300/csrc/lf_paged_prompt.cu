@@ -1,268 +1,525 @@
 // Causal attention of the last tokens of every sequence over a paged key-value
-// cache, with an optional sliding window and sinks: the CUDA-core kernel.
+// cache, with an optional sliding window and sinks:
 //
 //   out_i = sum_j 2^(s_ij - m_i) v_j / sum_j 2^(s_ij - m_i),  s = q . k log2(e) / sqrt(d)
 //
 // over j <= i and (no window, or j > i - window, or j < sinks), in one pass over
-// the keys with the running maximum m_i and sum of every row.
-//
-// A CTA takes 64 rows, (token, head of the group) pairs with the head inner: every
-// key and value it loads serves all heads of the group.  Keys and values pass
-// through shared memory in tiles of 64 tokens, gathered by page; key tiles that no
-// row sees are not visited.  A thread holds a 4 x 4 piece of S and 4 rows x d/16
-// columns of O.
+// the keys with the running maximum m_i and sum of every row.  bf16 with head_dim 64
+// and 128 has a kernel of its own (lf_paged_prompt_tc.cu); here are the others:
+//   - bf16 on the legacy matrix instructions, for short heads and for pages that a
+//     tensor map's boxes do not divide into;
+//   - fp32 on the CUDA cores: a tf32 product drops 13 bits of each factor, and three
+//     of them in place of one lose to the tensor cores' truncating sums what fp32
+//     callers keep.
+// A CTA takes some rows of one KV head's queries, (token, head of the group) pairs
+// with the head inner: every key and value it loads serves all heads of the group.
+// Keys and values pass through shared memory in tiles of 64 tokens, 16-byte chunks
+// gathered by page; key tiles that no row sees are not visited.  Blocks with the most
+// keys start first.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <type_traits>
 
-#include "lf_device.cuh"
-#include "lf_paged.h"
-#include "longflow.h"
+#include "lf_paged.cuh"
 
 namespace lf {
 
 namespace {
 
-constexpr int kRows = 64, kKeys = 64, kThreadsP = 256;
-constexpr float kNegInfP = -INFINITY;
+constexpr int kKeys = 64;
 
-__device__ __forceinline__ float ex2p(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+// A block's rows r0 .. of `rows` and what they see.
+struct Piece {
+  int b, g, q0, first_pos, p_lo, p_hi;
+  int64_t r0, rows;
+};
 
-template <typename T, int D>
-constexpr int prompt_smem() {
-  return (2 * 64 * (D + 4) + kKeys * (kRows + 4)) * 4;
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreadsP) paged_prompt_simt_kernel(const __grid_constant__ PagedPromptArgs a) {
-  constexpr int LD = D + 4;           // row stride in floats: eight rows' equal chunks differ in bank
-  constexpr int CW = D / 16;          // columns of O per thread
-  constexpr int VW = CW < 4 ? CW : 4; // .. in runs of
-  constexpr int PER = 16 / sizeof(T); // elements of a 16-byte chunk
-  extern __shared__ __align__(16) float sm[];
-  float* sq = sm;                     // [kRows][LD]
-  float* skv = sm + kRows * LD;       // [kKeys][LD]
-  float* sp = skv + kKeys * LD;       // [kKeys][kRows + 4], transposed weights
-  __shared__ int64_t s_off[kKeys];
-
-  const int b = blockIdx.z, g = blockIdx.y, tid = threadIdx.x;
-  const int G = a.group;
-  const int q0 = a.q_start[b], n = a.q_start[b + 1] - q0;
-  const bool head_block = blockIdx.x == 0 && g == 0 && tid == 0;
-  if (q0 < 0 || n < 0 || n > a.total_q - q0) {   // not rows of q
-    if (head_block && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
-    return;
+// False: no rows for this block.
+__device__ __forceinline__ bool take_piece(const PagedPromptArgs& a, int per_block, Piece* p) {
+  const int64_t heads = (int64_t)a.pool.batch * a.pool.kv_heads;
+  const int hb = (int)(blockIdx.x % heads);
+  const int64_t tile = (gridDim.x - 1 - blockIdx.x) / heads;   // the last rows first
+  p->b = hb / a.pool.kv_heads;
+  p->g = hb - p->b * a.pool.kv_heads;
+  p->q0 = a.q_start[p->b];
+  const int n = a.q_start[p->b + 1] - p->q0;
+  const bool first = blockIdx.x < heads && p->g == 0 && threadIdx.x == 0;
+  if (p->q0 < 0 || n < 0 || n > a.total_q - p->q0) {   // not rows of q
+    if (first && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+    return false;
   }
-  const int len = paged_len(a.pool, b);
-  if (head_block && a.pool.err && (n > a.max_q || len != a.pool.lens[b] || n > len))
+  const int len = paged_len(a.pool, p->b);
+  if (first && a.pool.err && (n > a.max_q || len != a.pool.lens[p->b] || n > len))
     atomicOr(a.pool.err, LF_DEVERR_STATE);
-  // The last rows see the most keys: they start first.
-  const int64_t r0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * kRows;
-  const int64_t rows = (int64_t)n * G;
-  if (r0 >= rows) return;
-  const int first_pos = len - n;      // may be negative: those rows see nothing
-  const int p_lo = first_pos + (int)(r0 / G);
-  const int p_hi = first_pos + (int)((min(r0 + kRows, rows) - 1) / G);
+  p->r0 = tile * per_block;
+  p->rows = (int64_t)n * a.group;
+  if (p->r0 >= p->rows) return false;
+  p->first_pos = len - n;      // may be negative: those rows see nothing
+  p->p_lo = p->first_pos + (int)(p->r0 / a.group);
+  p->p_hi = p->first_pos + (int)((min(p->r0 + per_block, p->rows) - 1) / a.group);
+  return true;
+}
 
-  for (int i = tid; i < kRows * (D / PER); i += kThreadsP) {
-    const int r = i / (D / PER), c = i - r * (D / PER);
-    float x[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) x[e] = 0.f;
-    if (r0 + r < rows) {
-      const int64_t t = q0 + (r0 + r) / G, h = g * G + (r0 + r) % G;
-      load16_f32(reinterpret_cast<const T*>(a.q) + (t * a.q_heads + h) * D + c * PER, x);
-    }
-#pragma unroll
-    for (int e = 0; e < PER; e += 4)
-      *reinterpret_cast<float4*>(sq + r * LD + c * PER + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-  }
+// Row r (of the sequence's token and head pairs) as a row of q and out.
+__device__ __forceinline__ int64_t row_of(const PagedPromptArgs& a, const Piece& p, int64_t r) {
+  return (p.q0 + r / a.group) * a.q_heads + p.g * a.group + r % a.group;
+}
 
-  const int rg = tid >> 4, cg = tid & 15;
-  int pos[4];
-  float m[4], l[4], o[4][CW];
+// Byte offset in the pools of the piece's position `pos`, -1: nothing to read.
+__device__ __forceinline__ int64_t offset_of(const PagedPromptArgs& a, const Piece& p, int pos) {
+  if (pos > p.p_hi) return -1;
+  int pi, slot;
+  paged_split(a.pool, pos, &pi, &slot);
+  const int page = a.pool.table[(int64_t)p.b * a.pool.max_pages + pi];
+  if (page >= 0 && page < a.pool.num_pages)
+    return page * a.pool.page_stride + slot * a.pool.token_stride + p.g * a.pool.head_stride;
+  if (a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+  return -1;
+}
+
+__device__ __forceinline__ bool sees(const PagedPromptArgs& a, int pos, int key) {
+  return key <= pos && (a.window == 0 || key > pos - a.window || key < a.sinks);
+}
+
+__device__ __forceinline__ void write_row_stats(const PagedPromptArgs& a, int64_t row, float m, float l) {
+  if (a.lse) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
+  if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
+}
+
+// ---- bf16: m16n8k16 ------------------------------------------------------------------
+//
+// Four warps of 16 rows, two stages of K and V tiles.  The queries stay in registers as
+// A operands, S comes out as the C operand whose layout is the A operand of P.V, so P
+// (rounded to bf16: half a step is 2^-8 of a weight) never leaves the registers either.
+
+constexpr int kMmaThreads = 128, kMmaRows = 64;
+
+template <int D>
+__global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __grid_constant__ PagedPromptArgs a) {
+  constexpr int NC = D / 8;                // 16-byte chunks of a row
+  constexpr int kTileBytes = kKeys * NC * 16;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_off[2][kKeys];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Piece p;
+  if (!take_piece(a, kMmaRows, &p)) return;
+  const Tiles tiles(a, p.p_lo, p.p_hi, kKeys);
+  const int nt = tiles.count();
+  const uint32_t ring = smem_u32(smem);
+
+  auto look_up = [&](int j) {
+    if (tid < kKeys) s_off[j & 1][tid] = offset_of(a, p, tiles.at(j) * kKeys + tid);
+  };
+  auto issue = [&](int j) {
+    const uint32_t kd = ring + (j & 1) * 2 * kTileBytes, vd = kd + kTileBytes;
+    constexpr int kStep = kMmaThreads / NC;   // rows that the block covers at once
+    const int c = tid % NC;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = r0 + rg * 4 + i;
-    pos[i] = r < rows ? first_pos + (int)(r / G) : -1;
-    m[i] = kNegInfP;
-    l[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < CW; ++c) o[i][c] = 0.f;
-  }
-  auto load_rows = [&](const char* pool) {   // a tile of keys or values, zeros where nothing is read
-    for (int i = tid; i < kKeys * (D / PER); i += kThreadsP) {
-      const int r = i / (D / PER), c = i - r * (D / PER);
-      float x[PER];
-#pragma unroll
-      for (int e = 0; e < PER; ++e) x[e] = 0.f;
-      if (s_off[r] >= 0)
-        load16_f32(reinterpret_cast<const T*>(pool + s_off[r] + g * a.pool.head_stride) + c * PER, x);
-#pragma unroll
-      for (int e = 0; e < PER; e += 4)
-        *reinterpret_cast<float4*>(skv + r * LD + c * PER + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+    for (int i = 0; i < (kKeys + kStep - 1) / kStep; ++i) {
+      const int r = i * kStep + tid / NC;
+      if (kKeys % kStep == 0 || r < kKeys) {
+        const int64_t off = s_off[j & 1][r];
+        const uint32_t d = 16 * tile_chunk<NC>(r, c);
+        cp_async16(kd + d, a.pool.k + (off >= 0 ? off + c * 16 : 0), off >= 0);
+        cp_async16(vd + d, a.pool.v + (off >= 0 ? off + c * 16 : 0), off >= 0);
+      }
     }
   };
 
-  for (int k0 = 0; k0 <= p_hi; k0 += kKeys) {
-    if (a.window > 0 && k0 >= a.sinks) {   // past the sinks: on to the window of the first row
-      const int64_t lo = (int64_t)p_lo - a.window + 1;
-      if (lo > k0) k0 = max(k0, (int)lo / kKeys * kKeys);
+  const int64_t ra = p.r0 + warp * 16 + (lane >> 2);   // and ra + 8
+  uint32_t qa[D / 16][4];
+  int pos[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r = ra + 8 * i;
+    const bool live = r < p.rows;
+    pos[i] = live ? p.first_pos + (int)(r / a.group) : -1;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + (live ? row_of(a, p, r) * (D / 2) : 0) + (lane & 3);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      qa[kk][i] = live ? q[8 * kk] : 0u;
+      qa[kk][2 + i] = live ? q[8 * kk + 4] : 0u;
     }
+  }
+  float o[D / 8][4], m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+  __nv_bfloat162 bad = __float2bfloat162_rn(0.f);
+
+  if (nt > 0) {
+    look_up(0);
     __syncthreads();
-    if (tid < kKeys) {
-      const int p = k0 + tid;
-      int64_t off = -1;
-      if (p <= p_hi) {
-        int pi, slot;
-        paged_split(a.pool, p, &pi, &slot);
-        const int page = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
-        if (page >= 0 && page < a.pool.num_pages)
-          off = page * a.pool.page_stride + slot * a.pool.token_stride;
-        else if (a.pool.err)
-          atomicOr(a.pool.err, LF_DEVERR_STATE);
+    issue(0);
+    cp_async_commit();
+    if (nt > 1) look_up(1);
+  }
+#pragma unroll 1
+  for (int j = 0; j < nt; ++j) {
+    __syncthreads();   // the other stage has been read, its new offsets are there
+    if (j + 1 < nt) issue(j + 1);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncthreads();
+    if (j + 2 < nt) look_up(j + 2);
+    const uint32_t ks = ring + (j & 1) * 2 * kTileBytes, vs = ks + kTileBytes;
+    const int k0 = tiles.at(j) * kKeys;
+    const bool hidden = some_hidden(a, p.p_lo, p.p_hi, k0, kKeys);
+    if (hidden) {   // a weight of 0 must take nothing: are there values that are not finite?
+      const uint4* v = reinterpret_cast<const uint4*>(smem + (j & 1) * 2 * kTileBytes + kTileBytes);
+      const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+      for (int i = tid; i < kKeys * NC; i += kMmaThreads) {
+        const uint4 x = v[i];
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, bad);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, bad);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, bad);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, bad);
       }
-      s_off[tid] = off;
     }
-    __syncthreads();
-    load_rows(a.pool.k);
-    __syncthreads();
-    float s[4][4];
+    float s[8][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int n = 0; n < 8; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-      float4 x[4], y[4];
+      for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(sq + (rg * 4 + i) * LD + d);
+    for (int n = 0; n < 8; ++n) {
+      if constexpr (D >= 32) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(skv + (cg + 16 * j) * LD + d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
-          s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
-          s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
-          s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+        for (int c = 0; c < NC; c += 4) {
+          uint32_t kb[4];
+          ldmatrix4(ks + 16 * tile_chunk<NC>(8 * n + (lane & 7), c + (lane >> 3)), kb);
+          mma16816(s[n], qa[c / 2][0], qa[c / 2][1], qa[c / 2][2], qa[c / 2][3], kb[0], kb[1]);
+          mma16816(s[n], qa[c / 2 + 1][0], qa[c / 2 + 1][1], qa[c / 2 + 1][2], qa[c / 2 + 1][3], kb[2], kb[3]);
         }
+      } else if ((n & 1) == 0) {
+        uint32_t kb[4];
+        ldmatrix4(ks + 16 * tile_chunk<NC>(8 * n + (lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1), kb);
+        mma16816(s[n], qa[0][0], qa[0][1], qa[0][2], qa[0][3], kb[0], kb[1]);
+        mma16816(s[n + 1], qa[0][0], qa[0][1], qa[0][2], qa[0][3], kb[2], kb[3]);
+      }
     }
+    if (hidden) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!sees(a, pos[i >> 1], k0 + 8 * n + 2 * (lane & 3) + (i & 1))) s[n][i] = kNegInf;
+    }
+    float top[2] = {kNegInf, kNegInf};
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
+    bool up = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2)) * a.scale_log2;
+      up |= top[i] > m[i];
+    }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mn = fmaxf(m[i], top[i]);
+        const float f = mn == kNegInf ? 1.f : ex2(m[i] - mn);
+        m[i] = mn;
+        l[i] *= f;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][2 * i] *= f;
+          o[n][2 * i + 1] *= f;
+        }
+      }
+    }
+    const float mu[2] = {m[0] == kNegInf ? 0.f : m[0], m[1] == kNegInf ? 0.f : m[1]};
+    uint32_t pa[8][2];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float x = ex2(fmaf(s[n][2 * i], a.scale_log2, -mu[i]));
+        const float y = ex2(fmaf(s[n][2 * i + 1], a.scale_log2, -mu[i]));
+        l[i] += x + y;
+        pa[n][i] = pack_bf16(x, y);
+      }
+#pragma unroll
+    for (int kk = 0; kk < kKeys / 16; ++kk) {
+      const int row = 16 * kk + (lane & 7) + 8 * ((lane >> 3) & 1);
+#pragma unroll
+      for (int c = 0; c < NC; c += 2) {
+        uint32_t vb[4];
+        ldmatrix4_trans(vs + 16 * tile_chunk<NC>(row, c + (lane >> 4)), vb);
+        mma16816(o[c], pa[2 * kk][0], pa[2 * kk][1], pa[2 * kk + 1][0], pa[2 * kk + 1][1], vb[0], vb[1]);
+        mma16816(o[c + 1], pa[2 * kk][0], pa[2 * kk][1], pa[2 * kk + 1][0], pa[2 * kk + 1][1], vb[2], vb[3]);
+      }
+    }
+  }
+
+  const float2 f = __bfloat1622float2(bad);
+  if (__syncthreads_or(!(f.x == 0.f) || !(f.y == 0.f))) {
+    for (int i = 0; i < 16; ++i) {
+      const int64_t r = p.r0 + warp * 16 + i;
+      if (r < p.rows)
+        row_by_hand<__nv_bfloat16, D>(a, p.b, p.g, row_of(a, p, r), p.first_pos + (int)(r / a.group), lane);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float ls = l[i] + __shfl_xor_sync(0xffffffffu, l[i], 1);
+    ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+    const int64_t r = ra + 8 * i;
+    if (r >= p.rows) continue;
+    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    const int64_t row = row_of(a, p, r);
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out) + row * (D / 2) + (lane & 3);
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) out[4 * n] = pack_bf16(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+    if ((lane & 3) == 0) write_row_stats(a, row, m[i], ls);
+  }
+}
+
+// ---- fp32: CUDA cores -----------------------------------------------------------------
+//
+// Two floats per multiply-add instruction.  A thread holds an 8 x 4 piece of S (sums over
+// even and over odd columns of d) and 8 rows x d/16 columns of O, which makes one
+// shared-memory instruction for 16 of them.  V is on its way while S is computed; P,
+// transposed, goes where K was.
+
+template <int D, int R>
+constexpr int fma_smem() {
+  constexpr int LD = D + 4, LP = R + 4;   // eight rows' equal chunks fall into different banks
+  return (R * LD + kKeys * (LD > LP ? LD : LP) + kKeys * LD) * 4;
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_constant__ PagedPromptArgs a) {
+  constexpr int kThreads = 2 * R;
+  constexpr int LD = D + 4, LP = R + 4;
+  constexpr int NC = D / 4;
+  constexpr int CW = D / 16;            // columns of O per thread
+  constexpr int VW = CW < 4 ? CW : 4;   // .. in runs of
+  constexpr int CP = (CW + 1) / 2;      // .. in pairs
+  extern __shared__ __align__(16) float sm[];
+  float* sq = sm;                                  // [R][LD]
+  float* sk = sm + R * LD;                         // [kKeys][LD], then P^T [kKeys][LP]
+  float* sv = sk + kKeys * (LD > LP ? LD : LP);    // [kKeys][LD]
+  __shared__ int64_t s_off[kKeys];
+  const int tid = threadIdx.x;
+  Piece p;
+  if (!take_piece(a, R, &p)) return;
+  const Tiles tiles(a, p.p_lo, p.p_hi, kKeys);
+  const int nt = tiles.count();
+
+  auto look_up = [&](int j) {
+    if (tid < kKeys) s_off[tid] = offset_of(a, p, tiles.at(j) * kKeys + tid);
+  };
+  auto issue = [&](float* dst, const char* pool) {
+#pragma unroll 4
+    for (int i = tid; i < kKeys * NC; i += kThreads) {
+      const int r = i / NC, c = i - r * NC;
+      const int64_t off = s_off[r];
+      cp_async16(smem_u32(dst + r * LD + c * 4), pool + (off >= 0 ? off + c * 16 : 0), off >= 0);
+    }
+    cp_async_commit();
+  };
+  if (nt > 0) look_up(0);
+  for (int i = tid; i < R * NC; i += kThreads) {
+    const int r = i / NC, c = i - r * NC;
+    const bool live = p.r0 + r < p.rows;
+    const float* q = reinterpret_cast<const float*>(a.q) + (live ? row_of(a, p, p.r0 + r) * D + c * 4 : 0);
+    *reinterpret_cast<float4*>(sq + r * LD + c * 4) =
+        live ? *reinterpret_cast<const float4*>(q) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  if (nt > 0) issue(sk, a.pool.k);
+
+  const int rg = tid >> 4, cg = tid & 15;
+  int pos[8];
+  float m[8], l[8];
+  uint64_t o[8][CP];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = p.r0 + rg * 8 + i;
+    pos[i] = r < p.rows ? p.first_pos + (int)(r / a.group) : -1;
+    m[i] = kNegInf;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CP; ++c) o[i][c] = 0ull;
+  }
+
+#pragma unroll 1
+  for (int j = 0; j < nt; ++j) {
+    const int k0 = tiles.at(j) * kKeys;
+    const bool hidden = some_hidden(a, p.p_lo, p.p_hi, k0, kKeys);
+    issue(sv, a.pool.v);
+    cp_async_wait<1>();
+    __syncthreads();
+    uint64_t s2[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) s2[i][n] = 0ull;
+#pragma unroll 2
+    for (int d = 0; d < D; d += 4) {
+      ulonglong2 y[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) y[n] = *reinterpret_cast<const ulonglong2*>(sk + (cg + 16 * n) * LD + d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sq + (rg * 8 + i) * LD + d);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          s2[i][n] = fma_pair(x.x, y[n].x, s2[i][n]);
+          s2[i][n] = fma_pair(x.y, y[n].y, s2[i][n]);
+        }
+      }
+    }
+    float w[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
       float top = m[i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int p = k0 + cg + 16 * j;
-        const bool see = p <= pos[i] && (a.window == 0 || p > pos[i] - a.window || p < a.sinks);
-        s[i][j] = see ? s[i][j] * a.scale_log2 : kNegInfP;
-        top = fmaxf(top, s[i][j]);
+      for (int n = 0; n < 4; ++n) {
+        float x, y;
+        unpair(s2[i][n], &x, &y);
+        w[i][n] = (x + y) * a.scale_log2;
+        if (hidden && !sees(a, pos[i], k0 + cg + 16 * n)) w[i][n] = kNegInf;
+        top = fmaxf(top, w[i][n]);
       }
 #pragma unroll
       for (int x = 1; x < 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float mu = top == kNegInfP ? 0.f : top;
-      const float f = ex2p(m[i] - mu);
+      const float mu = top == kNegInf ? 0.f : top;
+      const float f = ex2(m[i] - mu);
       m[i] = top;
       l[i] *= f;
 #pragma unroll
-      for (int c = 0; c < CW; ++c) o[i][c] *= f;
+      for (int c = 0; c < CP; ++c) o[i][c] = fma_pair(o[i][c], pair(f, f), 0ull);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = ex2p(s[i][j] - mu);
-        l[i] += s[i][j];
+      for (int n = 0; n < 4; ++n) {
+        w[i][n] = ex2(w[i][n] - mu);
+        l[i] += w[i][n];
       }
     }
+    __syncthreads();   // K has been read
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<float4*>(sp + (cg + 16 * j) * (kRows + 4) + rg * 4) =
-          make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
-    __syncthreads();
-    load_rows(a.pool.v);
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        *reinterpret_cast<float4*>(sk + (cg + 16 * n) * LP + rg * 8 + i) =
+            make_float4(w[i][n], w[i + 1][n], w[i + 2][n], w[i + 3][n]);
+    if (j + 1 < nt) look_up(j + 1);
+    cp_async_wait<0>();
     __syncthreads();
     // Where some row does not see some key of the tile, a weight of zero takes
     // nothing of the value, which may hold anything there.
-    const bool masked = k0 + kKeys - 1 > p_lo || p_lo < 0 ||
-                        (a.window > 0 && k0 + kKeys > a.sinks && k0 <= p_hi - a.window);
     auto accumulate = [&](auto part) {
-#pragma unroll 4
+#pragma unroll 2
       for (int k = 0; k < kKeys; ++k) {
-        const float4 p = *reinterpret_cast<const float4*>(sp + k * (kRows + 4) + rg * 4);
-        const float pi[4] = {p.x, p.y, p.z, p.w};
+        const float4 pa = *reinterpret_cast<const float4*>(sk + k * LP + rg * 8);
+        const float4 pb = *reinterpret_cast<const float4*>(sk + k * LP + rg * 8 + 4);
+        const float pi[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+        uint64_t v[CP];
 #pragma unroll
         for (int c = 0; c < CW; c += VW) {
-          float v[VW];
-          const float* src = skv + k * LD + (c / VW) * 16 * VW + cg * VW;
-          if constexpr (VW == 4) load16_f32(src, v);
-          else if constexpr (VW == 2) {
-            const float2 t = *reinterpret_cast<const float2*>(src);
-            v[0] = t.x;
-            v[1] = t.y;
-          } else v[0] = *src;
+          const float* src = sv + k * LD + (c / VW) * 16 * VW + cg * VW;
+          if constexpr (VW == 4) {
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(src);
+            v[c / 2] = t.x;
+            v[c / 2 + 1] = t.y;
+          } else if constexpr (VW == 2) {
+            v[0] = *reinterpret_cast<const uint64_t*>(src);
+          } else {
+            v[0] = pair(*src, 0.f);
+          }
+        }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i) {
+          if (part.value && pi[i] == 0.f) continue;
+          const uint64_t pp = pair(pi[i], pi[i]);
 #pragma unroll
-            for (int e = 0; e < VW; ++e)
-              if (!part.value || pi[i] != 0.f) o[i][c + e] = fmaf(pi[i], v[e], o[i][c + e]);
+          for (int c = 0; c < CP; ++c) o[i][c] = fma_pair(pp, v[c], o[i][c]);
         }
       }
     };
-    if (masked) accumulate(std::true_type{});
+    if (hidden) accumulate(std::true_type{});
     else accumulate(std::false_type{});
+    __syncthreads();   // P and V have been read
+    if (j + 1 < nt) issue(sk, a.pool.k);
   }
 
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     float ls = l[i];
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-    const int64_t r = r0 + rg * 4 + i;
-    if (r >= rows) continue;
+    const int64_t r = p.r0 + rg * 8 + i;
+    if (r >= p.rows) continue;
     const float inv = ls == 0.f ? 0.f : 1.f / ls;
-    const int64_t row = (q0 + r / G) * a.q_heads + g * G + r % G;
-    T* out = reinterpret_cast<T*>(a.out) + row * D;
+    const int64_t row = row_of(a, p, r);
+    float* out = reinterpret_cast<float*>(a.out) + row * D;
 #pragma unroll
-    for (int c = 0; c < CW; ++c)
-      from_f32(o[i][c] * inv, out + (c / VW) * 16 * VW + cg * VW + c % VW);
-    if (cg == 0) {
-      if (a.lse) a.lse[row] = ls == 0.f ? kNegInfP : (m[i] + log2f(ls)) * 0.6931471805599453f;
-      if (a.pool.err && !(ls <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
+    for (int c = 0; c < CP; ++c) {
+      float x, y;
+      unpair(o[i][c], &x, &y);
+      float* dst = out + (2 * c / VW) * 16 * VW + cg * VW + 2 * c % VW;
+      if constexpr (VW >= 2) *reinterpret_cast<float2*>(dst) = make_float2(x * inv, y * inv);
+      else *dst = x * inv;
     }
+    if (cg == 0) write_row_stats(a, row, m[i], ls);
   }
 }
 
-template <typename T, int D>
-cudaError_t launch(const PagedPromptArgs& a, cudaStream_t stream) {
-  constexpr int kSmem = prompt_smem<T, D>();
+// Blocks for pieces of `per_block` rows; 0: more than a grid holds.
+unsigned blocks_for(const PagedPromptArgs& a, int per_block) {
+  const int64_t tiles = ((int64_t)a.max_q * a.group + per_block - 1) / per_block;
+  const int64_t heads = (int64_t)a.pool.batch * a.pool.kv_heads;
+  return tiles > 0x7fffffff / heads ? 0u : (unsigned)(tiles * heads);
+}
+
+template <int D>
+cudaError_t launch_mma(const PagedPromptArgs& a, cudaStream_t stream) {
+  constexpr int kSmem = 4 * kKeys * D * 2;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_prompt_simt_kernel<T, D>), kSmem, done);
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = ((int64_t)a.max_q * a.group + kRows - 1) / kRows;
-  paged_prompt_simt_kernel<T, D><<<dim3((unsigned)tiles, a.pool.kv_heads, a.pool.batch), kThreadsP, kSmem, stream>>>(a);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_prompt_mma_kernel<D>), kSmem, done);
+  const unsigned blocks = blocks_for(a, kMmaRows);
+  if (e != cudaSuccess || blocks == 0) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
+  paged_prompt_mma_kernel<D><<<blocks, kMmaThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_dim(const PagedPromptArgs& a, int head_dim, cudaStream_t stream) {
-  switch (head_dim) {
-    case 16: return launch<T, 16>(a, stream);
-    case 32: return launch<T, 32>(a, stream);
-    case 64: return launch<T, 64>(a, stream);
-    default: return launch<T, 128>(a, stream);
-  }
+template <int D, int R>
+cudaError_t launch_fma(const PagedPromptArgs& a, cudaStream_t stream) {
+  constexpr int kSmem = fma_smem<D, R>();
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_prompt_fma_kernel<D, R>), kSmem, done);
+  const unsigned blocks = blocks_for(a, R);
+  if (e != cudaSuccess || blocks == 0) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
+  paged_prompt_fma_kernel<D, R><<<blocks, 2 * R, kSmem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t paged_prompt_launch(const PagedPromptArgs& a, int elem, int head_dim, cudaStream_t stream) {
   cudaError_t e;
-  if (elem == 2 && paged_prompt_tc_launch(a, head_dim, stream, &e)) return e;
-  return elem == 2 ? launch_dim<__nv_bfloat16>(a, head_dim, stream) : launch_dim<float>(a, head_dim, stream);
+  if (elem == 2) {
+    if (paged_prompt_tc_launch(a, head_dim, stream, &e)) return e;
+    switch (head_dim) {
+      case 16: return launch_mma<16>(a, stream);
+      case 32: return launch_mma<32>(a, stream);
+      case 64: return launch_mma<64>(a, stream);
+      default: return launch_mma<128>(a, stream);
+    }
+  }
+  switch (head_dim) {
+    case 16: return launch_fma<16, 64>(a, stream);
+    case 32: return launch_fma<32, 64>(a, stream);
+    case 64: return launch_fma<64, 64>(a, stream);
+    default: return launch_fma<128, 64>(a, stream);
+  }
 }
 
 }  // namespace lf

@@ -33,8 +33,7 @@
 
 #include <atomic>
 
-#include "lf_device.cuh"
-#include "lf_paged.h"
+#include "lf_paged.cuh"
 #include "longflow.h"
 
 namespace lf {
@@ -47,7 +46,6 @@ constexpr int kMmaWarp = 0, kLoadWarp = 1, kScrubWarp = 2, kSoftWarp = 4;  // so
 constexpr int kThreadsTc = 384;
 constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 constexpr float kGrow = 8.f;               // log2 growth of a maximum that is let pass
-constexpr float kNegInfTc = -INFINITY;
 
 struct PromptTcArgs {
   CUtensorMap q, k, v;
@@ -67,16 +65,6 @@ struct TcPlan {
   static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
 
-__device__ __forceinline__ float ex2t(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -121,25 +109,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Two floats in a register pair, for the instructions that take both at once.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float* x, float* y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(p));
-}
-__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // This warp's 32 lanes, 16 / 32 consecutive 32-bit columns of tensor memory.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -163,13 +132,6 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// The key tiles that a CTA visits: [0, sink) and [from, to).
-struct Tiles {
-  int sink, from, to;
-  __device__ int count() const { return sink + to - from; }
-  __device__ int at(int j) const { return j < sink ? j : from + j - sink; }
-};
-
 // Wait on, up to kWaitLimitNs or until another wait has expired (`expired`).
 __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* expired) {
   const unsigned long long t0 = global_ns();
@@ -180,50 +142,6 @@ __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatil
     if (global_ns() - t0 > kWaitLimitNs) *expired = 1;
   }
   return false;
-}
-
-// One row by the definition, a warp at a time: for CTAs whose tiles held values
-// that are not finite where some row does not look.
-template <int D>
-__device__ __noinline__ void row_by_hand(const PagedPromptArgs& a, int b, int g, int64_t row, int pos,
-                                         int lane) {
-  constexpr int E = D / 32;
-  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + row * D + lane * E;
-  float qv[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = to_f32(q[e]);
-    acc[e] = 0.f;
-  }
-  float m = kNegInfTc, l = 0.f;
-  for (int p = 0; p <= pos; ++p) {
-    if (a.window > 0 && p >= a.sinks && p <= pos - a.window) p = pos - a.window + 1;
-    int pi, slot;
-    paged_split(a.pool, p, &pi, &slot);
-    const int page = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
-    if (page < 0 || page >= a.pool.num_pages) continue;
-    const int64_t off = page * a.pool.page_stride + slot * a.pool.token_stride + g * a.pool.head_stride;
-    const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(a.pool.k + off) + lane * E;
-    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.pool.v + off) + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qv[e], to_f32(k[e]), s);
-    s = warp_sum(s) * a.scale_log2;
-    const float mn = fmaxf(m, s), mu = mn == kNegInfTc ? 0.f : mn;
-    const float f = ex2t(m - mu), w = ex2t(s - mu);
-    m = mn;
-    l = l * f + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + w * to_f32(v[e]);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + row * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) from_f32(l == 0.f ? 0.f : acc[e] * inv, out + e);
-  if (lane == 0) {
-    if (a.lse) a.lse[row] = l == 0.f ? kNegInfTc : (m + log2f(l)) * 0.6931471805599453f;
-    if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
-  }
 }
 
 template <int D>
@@ -261,20 +179,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   const int first_pos = len - n;
   const int p_lo = first_pos + (int)(r0 >> gs);
   const int p_hi = first_pos + (int)((min(r0 + 2 * kTile, rows) - 1) >> gs);
-  Tiles tiles = {0, 0, 0};
-  if (p_hi >= 0) {
-    tiles.to = p_hi / kTile + 1;
-    if (a.window > 0) {
-      tiles.from = (int)max((int64_t)0, (int64_t)p_lo - a.window + 1) / kTile;
-      tiles.sink = min((int)(((int64_t)a.sinks + kTile - 1) / kTile), tiles.from);
-    }
-  }
+  const Tiles tiles(a, p_lo, p_hi, kTile);
   const int nt = tiles.count();
   // Does some row of the CTA not see some key of the tile at k0?
-  auto masked = [&](int k0) {
-    return k0 + kTile - 1 > p_lo ||
-           (a.window > 0 && k0 + kTile > a.sinks && (int64_t)k0 <= (int64_t)p_hi - a.window);
-  };
+  auto masked = [&](int k0) { return some_hidden(a, p_lo, p_hi, k0, kTile); };
 
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -358,7 +266,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     return mbar_try_wait(bar, parity) || wait_longer(bar, parity, misc);
   };
 
-  float m = kNegInfTc, l = 0.f;   // softmax threads: their row's maximum (log2) and sum
+  float m = kNegInf, l = 0.f;   // softmax threads: their row's maximum (log2) and sum
 
   if (warp == kLoadWarp) {
     // ---- loader ---------------------------------------------------------------------
@@ -523,7 +431,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
           if (__any_sync(0xffffffffu, !(c0 + 31 <= hi && (c0 >= lo || c0 + 31 < sk)))) {
 #pragma unroll
             for (int i = c0; i < c0 + 32; ++i)
-              if (!(i <= hi && (i >= lo || i < sk))) x[i] = kNegInfTc;
+              if (!(i <= hi && (i >= lo || i < sk))) x[i] = kNegInf;
           }
       }
       float top[4] = {x[0], x[1], x[2], x[3]};
@@ -537,7 +445,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
       // O_t holds no product yet at j = 0; later, every product before S_t is done.
       if (__any_sync(0xffffffffu, mx > m + kGrow)) {
         const float mn = fmaxf(m, mx);
-        const float f = mn == kNegInfTc ? 1.f : ex2t(m - mn);
+        const float f = mn == kNegInf ? 1.f : ex2(m - mn);
         m = mn;
         l *= f;
         if (j > 0) {
@@ -552,7 +460,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
           }
         }
       }
-      const float mu = m == kNegInfTc ? 0.f : m;
+      const float mu = m == kNegInf ? 0.f : m;
       const uint64_t cc = pair(c, c), mm = pair(-mu, -mu);
       uint64_t sum[2] = {0ull, 0ull};   // two pairs of zeros
 #pragma unroll
@@ -562,10 +470,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
         for (int i = 0; i < 32; ++i) {
           float u, w;
           unpair(fma_pair(pair(x[64 * h + 2 * i], x[64 * h + 2 * i + 1]), cc, mm), &u, &w);
-          u = ex2t(u);
-          w = ex2t(w);
+          u = ex2(u);
+          w = ex2(w);
           sum[i & 1] = add_pair(sum[i & 1], pair(u, w));
-          p[i] = pack2(u, w);
+          p[i] = pack_bf16(u, w);
         }
         tmem_st32(ts + 32 * h, p);
         tmem_wait_st();
@@ -588,7 +496,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
         const int64_t ri = r - lane + i;
         if (ri >= rows) break;
         const int64_t rowi = (int64_t)(q0 + (ri >> gs)) * a.q_heads + g * G + (ri & (G - 1));
-        row_by_hand<D>(a, b, g, rowi, first_pos + (int)(ri >> gs), lane);
+        row_by_hand<__nv_bfloat16, D>(a, b, g, rowi, first_pos + (int)(ri >> gs), lane);
       }
     } else {
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -612,7 +520,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
             uint32_t y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              y[i] = l == 0.f ? 0u : pack2(o[8 * e + 2 * i] * inv, o[8 * e + 2 * i + 1] * inv);
+              y[i] = l == 0.f ? 0u : pack_bf16(o[8 * e + 2 * i] * inv, o[8 * e + 2 * i + 1] * inv);
             *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + e) ^ (lane & 7)) << 4)) =
                 make_uint4(y[0], y[1], y[2], y[3]);
           }
@@ -628,7 +536,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
       }
       if (live) {
         const int64_t row = (int64_t)(q0 + (r >> gs)) * a.q_heads + g * G + (r & (G - 1));
-        if (a.lse) a.lse[row] = l == 0.f ? kNegInfTc : (m + log2f(l)) * 0.6931471805599453f;
+        if (a.lse) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
         if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
       }
     }
