@@ -200,6 +200,16 @@ int take_window(const lf::PagedPool& p, int window, int sinks, int* w, int* s) {
   return LF_OK;
 }
 
+// The rows of a prompt call fit a grid (every kernel takes at least 32 rows per block).
+int take_rows(const lf::PagedPool& p, int group, int max_q) {
+  if (max_q < 0) return fail(LF_ERR_ARG, "max_q < 0");
+  const int64_t tiles = ((int64_t)max_q * group + 31) / 32;
+  if ((int64_t)max_q * group > INT_MAX - 256 || tiles * 32 / 256 > 65535 ||
+      (int64_t)p.batch * p.kv_heads > INT_MAX || tiles > INT_MAX / ((int64_t)p.batch * p.kv_heads))
+    return fail(LF_ERR_ARG, "max_q * group must be at most 2^24 - 256, and times batch * kv_heads / 32 below 2^31");
+  return LF_OK;
+}
+
 // Streaming multiprocessors of the current device.
 int sm_count(int* sms) {
   int dev = 0;
@@ -323,10 +333,29 @@ int lf_paged_decode(const lf_pages* pages, int batch, const int32_t* page_table,
   return e == cudaSuccess ? LF_OK : cuda_fail(e, "paged decode launch");
 }
 
+int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int max_q,
+                              int window, int sinks, size_t* bytes) {
+  lf::clear_last_error();
+  if (!pages || !bytes) return fail(LF_ERR_ARG, "null pages or bytes");
+  lf::PagedPool pool;
+  static const int32_t any = 0;  // only the shape counts here
+  int group = 0, sms = 0;
+  int rc = take_pool(pages, batch, &any, max_pages, &any, &pool);
+  if (rc != LF_OK || (rc = take_heads(pages, q_heads, &group)) != LF_OK ||
+      (rc = take_window(pool, window, sinks, &window, &sinks)) != LF_OK ||
+      (rc = take_rows(pool, group, max_q)) != LF_OK)
+    return rc;
+  *bytes = 0;
+  if (max_q == 0) return LF_OK;
+  if ((rc = sm_count(&sms)) != LF_OK) return rc;
+  *bytes = lf::paged_prompt_plan(pool, elem_bytes(pages), pages->head_dim, group, max_q, window, sinks, sms).bytes;
+  return LF_OK;
+}
+
 int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
                     const int32_t* lens, int q_heads, const void* q, const int32_t* q_start,
                     int total_q, int max_q, void* out, float* lse, int window, int sinks,
-                    lf_stream_t stream) {
+                    void* workspace, size_t workspace_bytes, lf_stream_t stream) {
   lf::clear_last_error();
   lf::PagedPromptArgs a;
   int rc = take_pool(pages, batch, page_table, max_pages, lens, &a.pool);
@@ -337,8 +366,7 @@ int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table,
     return fail(LF_ERR_ARG, "need 0 <= max_q <= total_q");
   if (!q_start) return fail(LF_ERR_ARG, "null q_start");
   if (total_q == 0 || max_q == 0) return LF_OK;
-  if ((int64_t)max_q * a.group > INT_MAX - 256)
-    return fail(LF_ERR_ARG, "max_q * group must be below 2^31 - 256");
+  if ((rc = take_rows(a.pool, a.group, max_q)) != LF_OK) return rc;
   if (!q || !out || !aligned16(q) || !aligned16(out))
     return fail(LF_ERR_ARG, "q and out must be non-null and 16-byte aligned");
   a.q = q;
@@ -349,7 +377,20 @@ int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table,
   a.total_q = total_q;
   a.max_q = max_q;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)pages->head_dim));
-  const cudaError_t e = lf::paged_prompt_launch(a, elem_bytes(pages), pages->head_dim,
+  int sms = 0;
+  if ((rc = sm_count(&sms)) != LF_OK) return rc;
+  const lf::PromptPlan plan =
+      lf::paged_prompt_plan(a.pool, elem_bytes(pages), pages->head_dim, a.group, max_q, a.window, a.sinks, sms);
+  a.splits = plan.splits;
+  a.part_o = a.part_ml = nullptr;
+  if (plan.bytes > 0) {
+    if (!workspace || !aligned16(workspace) || workspace_bytes < plan.bytes)
+      return fail(LF_ERR_ARG, "workspace: need %zu bytes, 16-byte aligned "
+                  "(lf_paged_prompt_workspace), got %zu", plan.bytes, workspace_bytes);
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.off_ml);
+  }
+  const cudaError_t e = lf::paged_prompt_launch(a, plan, elem_bytes(pages), pages->head_dim,
                                                 static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LF_OK : cuda_fail(e, "paged prompt launch");
 }

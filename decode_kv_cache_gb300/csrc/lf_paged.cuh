@@ -86,20 +86,86 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// A piece of work: rows r0 .. of `rows` of a sequence's queries, and what they see.
+struct Piece {
+  int b, g, q0, first_pos, p_lo, p_hi;
+  int64_t r0, rows, id;
+};
+
+// Piece `tile` of sequence and KV head number `head`; false: it has no rows.  `tell`: this
+// thread reports what is wrong with the sequence.
+__device__ __forceinline__ bool take_piece(const PagedPromptArgs& a, int head, int tile, int per_piece, bool tell,
+                                           Piece* p) {
+  p->id = (int64_t)tile * a.pool.batch * a.pool.kv_heads + head;
+  p->b = head / a.pool.kv_heads;
+  p->g = head - p->b * a.pool.kv_heads;
+  p->q0 = a.q_start[p->b];
+  const int n = a.q_start[p->b + 1] - p->q0;
+  const bool first = tell && tile == 0 && p->g == 0;
+  if (p->q0 < 0 || n < 0 || n > a.total_q - p->q0) {   // not rows of q
+    if (first && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+    return false;
+  }
+  const int len = paged_len(a.pool, p->b);
+  if (first && a.pool.err && (n > a.max_q || len != a.pool.lens[p->b] || n > len))
+    atomicOr(a.pool.err, LF_DEVERR_STATE);
+  p->r0 = (int64_t)tile * per_piece;
+  p->rows = (int64_t)n * a.group;
+  if (p->r0 >= p->rows) return false;
+  p->first_pos = len - n;      // may be negative: those rows see nothing
+  p->p_lo = p->first_pos + (int)(p->r0 / a.group);
+  p->p_hi = p->first_pos + (int)((min(p->r0 + per_piece, p->rows) - 1) / a.group);
+  return true;
+}
+
+// Row r (of the sequence's token and head pairs) as a row of q and out.
+__device__ __forceinline__ int64_t row_of(const PagedPromptArgs& a, const Piece& p, int64_t r) {
+  return (p.q0 + r / a.group) * a.q_heads + p.g * a.group + r % a.group;
+}
+
+// Byte offset in the pools of the piece's position `pos`, -1: nothing to read.
+__device__ __forceinline__ int64_t offset_of(const PagedPromptArgs& a, const Piece& p, int pos) {
+  if (pos > p.p_hi) return -1;
+  int pi, slot;
+  paged_split(a.pool, pos, &pi, &slot);
+  const int page = a.pool.table[(int64_t)p.b * a.pool.max_pages + pi];
+  if (page >= 0 && page < a.pool.num_pages)
+    return page * a.pool.page_stride + slot * a.pool.token_stride + p.g * a.pool.head_stride;
+  if (a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+  return -1;
+}
+
+__device__ __forceinline__ bool sees(const PagedPromptArgs& a, int pos, int key) {
+  return key <= pos && (a.window == 0 || key > pos - a.window || key < a.sinks);
+}
+
+__device__ __forceinline__ void write_row_stats(const PagedPromptArgs& a, int64_t row, float m, float l) {
+  if (a.lse) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
+  if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
+}
+
 // The key tiles of `size` tokens that queries at positions p_lo .. p_hi visit: [0, sink)
-// and [from, to).
+// and [from, to); with splits, a block takes its share of them.
 struct Tiles {
-  int sink, from, to;
-  __device__ Tiles(const PagedPromptArgs& a, int p_lo, int p_hi, int size) : sink(0), from(0), to(0) {
+  int sink, gap, first, last;   // tile j of them is number j below `sink`, else j + gap
+  __device__ Tiles(const PagedPromptArgs& a, int p_lo, int p_hi, int size, int share)
+      : sink(0), gap(0), first(0), last(0) {
     if (p_hi < 0) return;
-    to = p_hi / size + 1;
+    last = p_hi / size + 1;
     if (a.window > 0) {
-      from = (int)max((int64_t)0, (int64_t)p_lo - a.window + 1) / size;
+      const int from = (int)max((int64_t)0, (int64_t)p_lo - a.window + 1) / size;
       sink = min((int)(((int64_t)a.sinks + size - 1) / size), from);
+      gap = from - sink;
+      last -= gap;
+    }
+    if (a.splits > 1) {   // this block's share
+      const unsigned n = last;
+      first = n * (unsigned)share / (unsigned)a.splits;
+      last = n * (unsigned)(share + 1) / (unsigned)a.splits;
     }
   }
-  __device__ int count() const { return sink + to - from; }
-  __device__ int at(int j) const { return j < sink ? j : from + j - sink; }
+  __device__ int count() const { return last - first; }
+  __device__ int at(int j) const { return first + j < sink ? first + j : first + j + gap; }
 };
 
 // Does some query at positions p_lo .. p_hi not see some of the `size` keys from k0 on?
@@ -108,13 +174,27 @@ __device__ __forceinline__ bool some_hidden(const PagedPromptArgs& a, int p_lo, 
          (a.window > 0 && k0 + size > a.sinks && (int64_t)k0 <= (int64_t)p_hi - a.window);
 }
 
-// One row by the definition, a warp at a time: for CTAs whose tiles held values
-// that are not finite where some row does not look (0 * NaN is NaN).
+// Where a block puts row rr of its piece when its keys are a share of the row's.
+template <int D>
+__device__ __forceinline__ float* part_row(const PagedPromptArgs& a, int64_t id, int share, int per_piece, int rr,
+                                           float m, float l, bool write_ml) {
+  const int64_t i = (id * a.splits + share) * per_piece + rr;
+  if (write_ml) {
+    a.part_ml[2 * i] = m;
+    a.part_ml[2 * i + 1] = l;
+  }
+  return a.part_o + i * D;
+}
+
+// Row rr of a piece by the definition, a warp at a time: for blocks whose tiles held
+// values that are not finite where some row does not look (0 * NaN is NaN).
 template <typename T, int D>
-__device__ __noinline__ void row_by_hand(const PagedPromptArgs& a, int b, int g, int64_t row, int pos,
-                                         int lane) {
+__device__ __forceinline__ void row_by_hand(const PagedPromptArgs& a, const Piece& p, const Tiles& tiles, int share,
+                                            int size, int per_piece, int rr, int lane) {
   constexpr int E = D >= 32 ? D / 32 : 1;
   const bool mine = lane * E < D;   // lanes past a short row take nothing
+  const int64_t row = row_of(a, p, p.r0 + rr);
+  const int pos = p.first_pos + (int)((p.r0 + rr) / a.group);
   const T* q = reinterpret_cast<const T*>(a.q) + row * D + lane * E;
   float qv[E], acc[E];
 #pragma unroll
@@ -123,35 +203,54 @@ __device__ __noinline__ void row_by_hand(const PagedPromptArgs& a, int b, int g,
     acc[e] = 0.f;
   }
   float m = kNegInf, l = 0.f;
-  for (int p = 0; p <= pos; ++p) {
-    if (a.window > 0 && p >= a.sinks && p <= pos - a.window) p = pos - a.window + 1;
-    int pi, slot;
-    paged_split(a.pool, p, &pi, &slot);
-    const int page = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
-    if (page < 0 || page >= a.pool.num_pages) continue;
-    const int64_t off = page * a.pool.page_stride + slot * a.pool.token_stride + g * a.pool.head_stride;
-    const T* k = reinterpret_cast<const T*>(a.pool.k + off) + lane * E;
-    const T* v = reinterpret_cast<const T*>(a.pool.v + off) + lane * E;
-    float s = 0.f;
+  const int n = tiles.count();
+  for (int j = 0; j < n; ++j) {
+    const int k0 = tiles.at(j) * size;
+    for (int key = k0; key < k0 + size; ++key) {
+      if (!sees(a, pos, key)) continue;
+      const int64_t off = offset_of(a, p, key);
+      if (off < 0) continue;
+      const T* k = reinterpret_cast<const T*>(a.pool.k + off) + lane * E;
+      const T* v = reinterpret_cast<const T*>(a.pool.v + off) + lane * E;
+      float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) if (mine) s = fmaf(qv[e], to_f32(k[e]), s);
-    s = warp_sum(s) * a.scale_log2;
-    const float mn = fmaxf(m, s), mu = mn == kNegInf ? 0.f : mn;
-    const float f = ex2(m - mu), w = ex2(s - mu);
-    m = mn;
-    l = l * f + w;
+      for (int e = 0; e < E; ++e)
+        if (mine) s = fmaf(qv[e], to_f32(k[e]), s);
+      s = warp_sum(s) * a.scale_log2;
+      const float mn = fmaxf(m, s), mu = mn == kNegInf ? 0.f : mn;
+      const float f = ex2(m - mu), w = ex2(s - mu);
+      m = mn;
+      l = l * f + w;
 #pragma unroll
-    for (int e = 0; e < E; ++e) if (mine) acc[e] = acc[e] * f + w * to_f32(v[e]);
+      for (int e = 0; e < E; ++e)
+        if (mine) acc[e] = acc[e] * f + w * to_f32(v[e]);
+    }
+  }
+  if (a.splits > 1) {
+    float* o = part_row<D>(a, p.id, share, per_piece, rr, m, l, lane == 0) + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (mine) o[e] = acc[e];
+    return;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* out = reinterpret_cast<T*>(a.out) + row * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; ++e)
     if (mine) from_f32(l == 0.f ? 0.f : acc[e] * inv, out + e);
-  if (lane == 0) {
-    if (a.lse) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
-    if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
-  }
+  if (lane == 0) write_row_stats(a, row, m, l);
+}
+
+// Rows rr .. rr + n - 1 of a piece.  What describes it is worked out again, so that the
+// usual path keeps none of it in registers for this one.
+template <typename T, int D>
+__device__ __noinline__ void rows_by_hand(const PagedPromptArgs& a, int head, int tile, int share, int size,
+                                          int per_piece, int rr, int n, int lane) {
+  Piece p;
+  if (!take_piece(a, head, tile, per_piece, false, &p)) return;
+  const Tiles tiles(a, p.p_lo, p.p_hi, size, share);
+  for (int i = rr; i < rr + n && p.r0 + i < p.rows; ++i)
+    row_by_hand<T, D>(a, p, tiles, share, size, per_piece, i, lane);
 }
 
 }  // namespace lf

@@ -52,7 +52,21 @@ struct PagedPromptArgs {
   float* lse;                 // may be null
   int q_heads, group, window, sinks, total_q, max_q;
   float scale_log2;
+  int splits;                 // blocks that share a piece's keys; 1: no join
+  float* part_o;              // [pieces][splits][rows][head_dim] partial outputs
+  float* part_ml;             // [pieces][splits][rows][2] their max and sum
 };
+
+// How a prompt call is spread over the GPU.  A piece of work is `rows` rows (token and
+// head of the group) of one KV head's queries of one sequence.
+struct PromptPlan {
+  enum { kTensor, kMatrix, kFma } kernel;
+  int rows, splits;
+  int64_t pieces;
+  size_t off_ml, bytes;       // workspace: part_o, part_ml
+};
+PromptPlan paged_prompt_plan(const PagedPool& pool, int elem, int head_dim, int group, int max_q,
+                             int window, int sinks, int sms);
 
 // Occupied tokens of sequence b, kept inside its row of the page table.
 __device__ __forceinline__ int paged_len(const PagedPool& p, int b) {
@@ -90,13 +104,12 @@ cudaError_t paged_append_launch(const PagedAppendArgs& a, cudaStream_t stream);
 // elem: bytes of an element (2 bf16, 4 fp32).  `grid`: CTAs of the attention kernel.
 cudaError_t paged_decode_launch(const PagedDecodeArgs& a, int elem, int head_dim, int grid,
                                 cudaStream_t stream);
-cudaError_t paged_prompt_launch(const PagedPromptArgs& a, int elem, int head_dim,
+cudaError_t paged_prompt_launch(const PagedPromptArgs& a, const PromptPlan& plan, int elem, int head_dim,
                                 cudaStream_t stream);
-
-// The tensor-core kernel for bf16: false, and nothing launched, where it is not built
-// (head_dim 16 and 32, pages that do not divide its key tiles); else *err is the
-// launch's error.
-bool paged_prompt_tc_launch(const PagedPromptArgs& a, int head_dim, cudaStream_t stream, cudaError_t* err);
+// Its tensor-core kernel: whether that takes such a cache, and its launch.
+bool paged_prompt_tc_takes(const PagedPool& pool, int head_dim);
+cudaError_t paged_prompt_tc_launch(const PagedPromptArgs& a, const PromptPlan& plan, int head_dim,
+                                   cudaStream_t stream);
 
 // Tokens that one CTA of the decode kernel takes in one sweep of its warps.
 int paged_decode_sweep(int elem, int head_dim);

@@ -29,64 +29,6 @@ namespace {
 
 constexpr int kKeys = 64;
 
-// A block's rows r0 .. of `rows` and what they see.
-struct Piece {
-  int b, g, q0, first_pos, p_lo, p_hi;
-  int64_t r0, rows;
-};
-
-// False: no rows for this block.
-__device__ __forceinline__ bool take_piece(const PagedPromptArgs& a, int per_block, Piece* p) {
-  const int64_t heads = (int64_t)a.pool.batch * a.pool.kv_heads;
-  const int hb = (int)(blockIdx.x % heads);
-  const int64_t tile = (gridDim.x - 1 - blockIdx.x) / heads;   // the last rows first
-  p->b = hb / a.pool.kv_heads;
-  p->g = hb - p->b * a.pool.kv_heads;
-  p->q0 = a.q_start[p->b];
-  const int n = a.q_start[p->b + 1] - p->q0;
-  const bool first = blockIdx.x < heads && p->g == 0 && threadIdx.x == 0;
-  if (p->q0 < 0 || n < 0 || n > a.total_q - p->q0) {   // not rows of q
-    if (first && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
-    return false;
-  }
-  const int len = paged_len(a.pool, p->b);
-  if (first && a.pool.err && (n > a.max_q || len != a.pool.lens[p->b] || n > len))
-    atomicOr(a.pool.err, LF_DEVERR_STATE);
-  p->r0 = tile * per_block;
-  p->rows = (int64_t)n * a.group;
-  if (p->r0 >= p->rows) return false;
-  p->first_pos = len - n;      // may be negative: those rows see nothing
-  p->p_lo = p->first_pos + (int)(p->r0 / a.group);
-  p->p_hi = p->first_pos + (int)((min(p->r0 + per_block, p->rows) - 1) / a.group);
-  return true;
-}
-
-// Row r (of the sequence's token and head pairs) as a row of q and out.
-__device__ __forceinline__ int64_t row_of(const PagedPromptArgs& a, const Piece& p, int64_t r) {
-  return (p.q0 + r / a.group) * a.q_heads + p.g * a.group + r % a.group;
-}
-
-// Byte offset in the pools of the piece's position `pos`, -1: nothing to read.
-__device__ __forceinline__ int64_t offset_of(const PagedPromptArgs& a, const Piece& p, int pos) {
-  if (pos > p.p_hi) return -1;
-  int pi, slot;
-  paged_split(a.pool, pos, &pi, &slot);
-  const int page = a.pool.table[(int64_t)p.b * a.pool.max_pages + pi];
-  if (page >= 0 && page < a.pool.num_pages)
-    return page * a.pool.page_stride + slot * a.pool.token_stride + p.g * a.pool.head_stride;
-  if (a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
-  return -1;
-}
-
-__device__ __forceinline__ bool sees(const PagedPromptArgs& a, int pos, int key) {
-  return key <= pos && (a.window == 0 || key > pos - a.window || key < a.sinks);
-}
-
-__device__ __forceinline__ void write_row_stats(const PagedPromptArgs& a, int64_t row, float m, float l) {
-  if (a.lse) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
-  if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
-}
-
 // ---- bf16: m16n8k16 ------------------------------------------------------------------
 //
 // Four warps of 16 rows, two stages of K and V tiles.  The queries stay in registers as
@@ -103,8 +45,10 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
   __shared__ int64_t s_off[2][kKeys];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Piece p;
-  if (!take_piece(a, kMmaRows, &p)) return;
-  const Tiles tiles(a, p.p_lo, p.p_hi, kKeys);
+  const int share = blockIdx.y, heads = a.pool.batch * a.pool.kv_heads;
+  const int id = gridDim.x - 1 - blockIdx.x, tile = id / heads;   // the last rows first
+  if (!take_piece(a, id - tile * heads, tile, kMmaRows, tid == 0 && share == 0, &p)) return;
+  const Tiles tiles(a, p.p_lo, p.p_hi, kKeys, share);
   const int nt = tiles.count();
   const uint32_t ring = smem_u32(smem);
 
@@ -259,11 +203,7 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
 
   const float2 f = __bfloat1622float2(bad);
   if (__syncthreads_or(!(f.x == 0.f) || !(f.y == 0.f))) {
-    for (int i = 0; i < 16; ++i) {
-      const int64_t r = p.r0 + warp * 16 + i;
-      if (r < p.rows)
-        row_by_hand<__nv_bfloat16, D>(a, p.b, p.g, row_of(a, p, r), p.first_pos + (int)(r / a.group), lane);
-    }
+    rows_by_hand<__nv_bfloat16, D>(a, id - tile * heads, tile, share, kKeys, kMmaRows, warp * 16, 16, lane);
     return;
   }
 #pragma unroll
@@ -272,6 +212,13 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
     ls += __shfl_xor_sync(0xffffffffu, ls, 2);
     const int64_t r = ra + 8 * i;
     if (r >= p.rows) continue;
+    if (a.splits > 1) {
+      float* part = part_row<D>(a, p.id, share, kMmaRows, (int)(r - p.r0), m[i], ls, (lane & 3) == 0) + 2 * (lane & 3);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(part + 8 * n) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+      continue;
+    }
     const float inv = ls == 0.f ? 0.f : 1.f / ls;
     const int64_t row = row_of(a, p, r);
     uint32_t* out = reinterpret_cast<uint32_t*>(a.out) + row * (D / 2) + (lane & 3);
@@ -283,9 +230,8 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
 
 // ---- fp32: CUDA cores -----------------------------------------------------------------
 //
-// Two floats per multiply-add instruction.  A thread holds an 8 x 4 piece of S (sums over
-// even and over odd columns of d) and 8 rows x d/16 columns of O, which makes one
-// shared-memory instruction for 16 of them.  V is on its way while S is computed; P,
+// Two floats per multiply-add instruction.  A thread holds an M x 4 piece of S (sums over
+// even and over odd columns of d) and M rows x d/16 columns of O.  V is on its way while S is computed; P,
 // transposed, goes where K was.
 
 template <int D, int R>
@@ -294,9 +240,10 @@ constexpr int fma_smem() {
   return (R * LD + kKeys * (LD > LP ? LD : LP) + kKeys * LD) * 4;
 }
 
-template <int D, int R>
-__global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_constant__ PagedPromptArgs a) {
-  constexpr int kThreads = 2 * R;
+template <int D, int R, int M>
+__global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __grid_constant__ PagedPromptArgs a) {
+  constexpr int kThreads = 16 * R / M;
+  static_assert(kThreads >= kKeys && M % 4 == 0, "one thread looks up a key");
   constexpr int LD = D + 4, LP = R + 4;
   constexpr int NC = D / 4;
   constexpr int CW = D / 16;            // columns of O per thread
@@ -309,8 +256,10 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
   __shared__ int64_t s_off[kKeys];
   const int tid = threadIdx.x;
   Piece p;
-  if (!take_piece(a, R, &p)) return;
-  const Tiles tiles(a, p.p_lo, p.p_hi, kKeys);
+  const int share = blockIdx.y, heads = a.pool.batch * a.pool.kv_heads;
+  const int id = gridDim.x - 1 - blockIdx.x, tile = id / heads;   // the last rows first
+  if (!take_piece(a, id - tile * heads, tile, R, tid == 0 && share == 0, &p)) return;
+  const Tiles tiles(a, p.p_lo, p.p_hi, kKeys, share);
   const int nt = tiles.count();
 
   auto look_up = [&](int j) {
@@ -337,12 +286,12 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
   if (nt > 0) issue(sk, a.pool.k);
 
   const int rg = tid >> 4, cg = tid & 15;
-  int pos[8];
-  float m[8], l[8];
-  uint64_t o[8][CP];
+  int pos[M];
+  float m[M], l[M];
+  uint64_t o[M][CP];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = p.r0 + rg * 8 + i;
+  for (int i = 0; i < M; ++i) {
+    const int64_t r = p.r0 + rg * M + i;
     pos[i] = r < p.rows ? p.first_pos + (int)(r / a.group) : -1;
     m[i] = kNegInf;
     l[i] = 0.f;
@@ -357,9 +306,9 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
     issue(sv, a.pool.v);
     cp_async_wait<1>();
     __syncthreads();
-    uint64_t s2[8][4];
+    uint64_t s2[M][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < M; ++i)
 #pragma unroll
       for (int n = 0; n < 4; ++n) s2[i][n] = 0ull;
 #pragma unroll 2
@@ -368,8 +317,8 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
 #pragma unroll
       for (int n = 0; n < 4; ++n) y[n] = *reinterpret_cast<const ulonglong2*>(sk + (cg + 16 * n) * LD + d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sq + (rg * 8 + i) * LD + d);
+      for (int i = 0; i < M; ++i) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sq + (rg * M + i) * LD + d);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           s2[i][n] = fma_pair(x.x, y[n].x, s2[i][n]);
@@ -377,9 +326,9 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
         }
       }
     }
-    float w[8][4];
+    float w[M][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < M; ++i) {
       float top = m[i];
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
@@ -407,8 +356,8 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int i = 0; i < 8; i += 4)
-        *reinterpret_cast<float4*>(sk + (cg + 16 * n) * LP + rg * 8 + i) =
+      for (int i = 0; i < M; i += 4)
+        *reinterpret_cast<float4*>(sk + (cg + 16 * n) * LP + rg * M + i) =
             make_float4(w[i][n], w[i + 1][n], w[i + 2][n], w[i + 3][n]);
     if (j + 1 < nt) look_up(j + 1);
     cp_async_wait<0>();
@@ -418,9 +367,9 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
     auto accumulate = [&](auto part) {
 #pragma unroll 2
       for (int k = 0; k < kKeys; ++k) {
-        const float4 pa = *reinterpret_cast<const float4*>(sk + k * LP + rg * 8);
-        const float4 pb = *reinterpret_cast<const float4*>(sk + k * LP + rg * 8 + 4);
-        const float pi[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+        float pi[M];
+#pragma unroll
+        for (int i = 0; i < M; i += 4) load16_f32(sk + k * LP + rg * M + i, pi + i);
         uint64_t v[CP];
 #pragma unroll
         for (int c = 0; c < CW; c += VW) {
@@ -436,7 +385,7 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
           }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < M; ++i) {
           if (part.value && pi[i] == 0.f) continue;
           const uint64_t pp = pair(pi[i], pi[i]);
 #pragma unroll
@@ -451,15 +400,17 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
   }
 
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < M; ++i) {
     float ls = l[i];
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-    const int64_t r = p.r0 + rg * 8 + i;
+    const int64_t r = p.r0 + rg * M + i;
     if (r >= p.rows) continue;
-    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    // the row's output, or its share of it
+    const float inv = a.splits > 1 ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
     const int64_t row = row_of(a, p, r);
-    float* out = reinterpret_cast<float*>(a.out) + row * D;
+    float* out = a.splits > 1 ? part_row<D>(a, p.id, share, R, (int)(r - p.r0), m[i], ls, cg == 0)
+                              : reinterpret_cast<float*>(a.out) + row * D;
 #pragma unroll
     for (int c = 0; c < CP; ++c) {
       float x, y;
@@ -468,58 +419,166 @@ __global__ void __launch_bounds__(2 * R) paged_prompt_fma_kernel(const __grid_co
       if constexpr (VW >= 2) *reinterpret_cast<float2*>(dst) = make_float2(x * inv, y * inv);
       else *dst = x * inv;
     }
-    if (cg == 0) write_row_stats(a, row, m[i], ls);
+    if (cg == 0 && a.splits == 1) write_row_stats(a, row, m[i], ls);
   }
 }
 
-// Blocks for pieces of `per_block` rows; 0: more than a grid holds.
-unsigned blocks_for(const PagedPromptArgs& a, int per_block) {
-  const int64_t tiles = ((int64_t)a.max_q * a.group + per_block - 1) / per_block;
-  const int64_t heads = (int64_t)a.pool.batch * a.pool.kv_heads;
-  return tiles > 0x7fffffff / heads ? 0u : (unsigned)(tiles * heads);
+// ---- joining the shares of rows whose keys several blocks took -----------------------
+//
+// A warp per row: lane i reads share i's maximum and sum, then all lanes add up the
+// shares' outputs in their order.
+constexpr int kJoinWarps = 8, kMaxSplits = 32;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_prompt_join_kernel(const __grid_constant__ PagedPromptArgs a, int per_piece) {
+  constexpr int E = D >= 32 ? D / 32 : 1;
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int rr = (int)(i % per_piece);
+  Piece p;
+  const int id = (int)(i / per_piece), heads = a.pool.batch * a.pool.kv_heads;
+  if (!take_piece(a, id % heads, id / heads, per_piece, false, &p) || p.r0 + rr >= p.rows) return;
+  const int64_t part = p.id * a.splits * per_piece + rr;   // share s: + s * per_piece
+  float m = kNegInf, l = 0.f;
+  if (lane < a.splits) {
+    m = a.part_ml[2 * (part + (int64_t)lane * per_piece)];
+    l = a.part_ml[2 * (part + (int64_t)lane * per_piece) + 1];
+  }
+  const float top = warp_max(m), mu = top == kNegInf ? 0.f : top;
+  const float f = ex2(m - mu);
+  const float sum = warp_sum(l * f);
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const int col = (lane * E) % D;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float fs = __shfl_sync(0xffffffffu, f, s);
+    const float* o = a.part_o + (part + (int64_t)s * per_piece) * D + col;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], fs, acc[e]);
+  }
+  const int64_t row = row_of(a, p, p.r0 + rr);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* out = reinterpret_cast<T*>(a.out) + row * D;
+  if (lane * E < D) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) from_f32(sum == 0.f ? 0.f : acc[e] * inv, out + col + e);
+  }
+  if (lane == 0) write_row_stats(a, row, top, sum);
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const PagedPromptArgs& a, const PromptPlan& plan, cudaStream_t stream) {
+  const int64_t rows = plan.pieces * plan.rows;   // few: splits are for few pieces
+  paged_prompt_join_kernel<T, D><<<(unsigned)((rows + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, stream>>>(a, plan.rows);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_join_dim(const PagedPromptArgs& a, const PromptPlan& plan, int head_dim, cudaStream_t stream) {
+  switch (head_dim) {
+    case 16: return launch_join<T, 16>(a, plan, stream);
+    case 32: return launch_join<T, 32>(a, plan, stream);
+    case 64: return launch_join<T, 64>(a, plan, stream);
+    default: return launch_join<T, 128>(a, plan, stream);
+  }
+}
+
+int64_t pieces_of(const PagedPool& pool, int group, int max_q, int rows) {
+  return ((int64_t)max_q * group + rows - 1) / rows * pool.batch * pool.kv_heads;
 }
 
 template <int D>
-cudaError_t launch_mma(const PagedPromptArgs& a, cudaStream_t stream) {
+cudaError_t launch_mma(const PagedPromptArgs& a, const PromptPlan& plan, cudaStream_t stream) {
   constexpr int kSmem = 4 * kKeys * D * 2;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_prompt_mma_kernel<D>), kSmem, done);
-  const unsigned blocks = blocks_for(a, kMmaRows);
-  if (e != cudaSuccess || blocks == 0) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
-  paged_prompt_mma_kernel<D><<<blocks, kMmaThreads, kSmem, stream>>>(a);
+  if (e != cudaSuccess) return e;
+  paged_prompt_mma_kernel<D><<<dim3((unsigned)plan.pieces, plan.splits), kMmaThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
-template <int D, int R>
-cudaError_t launch_fma(const PagedPromptArgs& a, cudaStream_t stream) {
+template <int D, int R, int M>
+cudaError_t launch_fma(const PagedPromptArgs& a, const PromptPlan& plan, cudaStream_t stream) {
   constexpr int kSmem = fma_smem<D, R>();
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_prompt_fma_kernel<D, R>), kSmem, done);
-  const unsigned blocks = blocks_for(a, R);
-  if (e != cudaSuccess || blocks == 0) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
-  paged_prompt_fma_kernel<D, R><<<blocks, 2 * R, kSmem, stream>>>(a);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_prompt_fma_kernel<D, R, M>), kSmem, done);
+  if (e != cudaSuccess) return e;
+  paged_prompt_fma_kernel<D, R, M><<<dim3((unsigned)plan.pieces, plan.splits), 16 * R / M, kSmem, stream>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_kernel(const PagedPromptArgs& a, const PromptPlan& plan, int head_dim, cudaStream_t stream) {
+  if (plan.kernel == PromptPlan::kTensor) return paged_prompt_tc_launch(a, plan, head_dim, stream);
+  if (plan.kernel == PromptPlan::kMatrix) {
+    switch (head_dim) {
+      case 16: return launch_mma<16>(a, plan, stream);
+      case 32: return launch_mma<32>(a, plan, stream);
+      case 64: return launch_mma<64>(a, plan, stream);
+      default: return launch_mma<128>(a, plan, stream);
+    }
+  }
+  switch (head_dim) {
+    case 16: return launch_fma<16, 32, 4>(a, plan, stream);
+    case 32: return launch_fma<32, 32, 4>(a, plan, stream);
+    case 64: return launch_fma<64, 32, 4>(a, plan, stream);
+    default: return plan.rows == 64 ? launch_fma<128, 64, 8>(a, plan, stream) : launch_fma<128, 32, 4>(a, plan, stream);
+  }
 }
 
 }  // namespace
 
-cudaError_t paged_prompt_launch(const PagedPromptArgs& a, int elem, int head_dim, cudaStream_t stream) {
-  cudaError_t e;
-  if (elem == 2) {
-    if (paged_prompt_tc_launch(a, head_dim, stream, &e)) return e;
-    switch (head_dim) {
-      case 16: return launch_mma<16>(a, stream);
-      case 32: return launch_mma<32>(a, stream);
-      case 64: return launch_mma<64>(a, stream);
-      default: return launch_mma<128>(a, stream);
-    }
+PromptPlan paged_prompt_plan(const PagedPool& pool, int elem, int head_dim, int group, int max_q,
+                             int window, int sinks, int sms) {
+  PromptPlan plan;
+  int keys = kKeys, room = 3 * sms;   // keys of a tile, blocks that run at once
+  if (elem == 2 && paged_prompt_tc_takes(pool, head_dim)) {
+    plan.kernel = PromptPlan::kTensor;
+    plan.rows = 256;
+    keys = 128;
+    room = sms;
+  } else if (elem == 2) {
+    plan.kernel = PromptPlan::kMatrix;
+    plan.rows = kMmaRows;
+  } else {
+    // Pieces of 32 rows in 4 x 4 shares: more blocks, each done sooner.  Heads of 128
+    // read more per multiply-add than that feeds, so where the blocks fill the GPU all
+    // the same they take 64 rows in 8 x 4 shares.  (Eight heads of 128: three prompts of
+    // 500 to 1000 tokens 92 us against 130, three of 2000 tokens 722 against 636.
+    // Shorter heads gain nothing from it: heads of 64, three of 2000 tokens, 362 against
+    // 425.)
+    plan.kernel = PromptPlan::kFma;
+    plan.rows = head_dim == 128 && pieces_of(pool, group, max_q, 64) >= 4 * (int64_t)sms ? 64 : 32;
   }
-  switch (head_dim) {
-    case 16: return launch_fma<16, 64>(a, stream);
-    case 32: return launch_fma<32, 64>(a, stream);
-    case 64: return launch_fma<64, 64>(a, stream);
-    default: return launch_fma<128, 64>(a, stream);
+  plan.pieces = pieces_of(pool, group, max_q, plan.rows);
+  // Where the pieces leave half of the GPU idle and their keys may be many, several
+  // blocks share a piece's keys: at least four tiles for each of them.
+  const int64_t all = (int64_t)pool.max_pages * pool.page_size;
+  const int64_t most = window > 0 ? (int64_t)window + sinks + plan.rows + 2 * keys : all;
+  const int64_t tiles = ((most < all ? most : all) + keys - 1) / keys;
+  int64_t splits = 1;
+  if (plan.pieces <= room / 2 && tiles >= 16) {
+    splits = room / plan.pieces;
+    if (splits > tiles / 4) splits = tiles / 4;
+    if (splits > kMaxSplits) splits = kMaxSplits;
   }
+  plan.splits = (int)splits;
+  plan.off_ml = plan.bytes = 0;
+  if (splits > 1) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    plan.off_ml = up((size_t)plan.pieces * splits * plan.rows * head_dim * 4);
+    plan.bytes = plan.off_ml + up((size_t)plan.pieces * splits * plan.rows * 2 * 4);
+  }
+  return plan;
+}
+
+cudaError_t paged_prompt_launch(const PagedPromptArgs& a, const PromptPlan& plan, int elem, int head_dim,
+                                cudaStream_t stream) {
+  const cudaError_t e = launch_kernel(a, plan, head_dim, stream);
+  if (e != cudaSuccess || plan.splits == 1) return e;
+  return elem == 2 ? launch_join_dim<__nv_bfloat16>(a, plan, head_dim, stream)
+                   : launch_join_dim<float>(a, plan, head_dim, stream);
 }
 
 }  // namespace lf

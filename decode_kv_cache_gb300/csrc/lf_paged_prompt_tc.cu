@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform for the compiler too
   const int G = a.group, gs = ta.group_shift;
-  const int b = blockIdx.x / a.pool.kv_heads, g = blockIdx.x - b * a.pool.kv_heads;
+  const int b = blockIdx.x / a.pool.kv_heads;
 
   // The loader's lookups for the first key tile, before it is known whether that is
   // tile 0 (it is unless a window without sinks starts behind it).
@@ -164,22 +164,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     paged_split(a.pool, box * ta.box_rows, &pi, &slot);
     if (pi < a.pool.max_pages) guess = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
   }
-  const int q0 = a.q_start[b], n = a.q_start[b + 1] - q0;
-  const bool head_block = blockIdx.y == 0 && g == 0 && tid == 0;
-  if (q0 < 0 || n < 0 || n > a.total_q - q0) {   // not rows of q
-    if (head_block && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
-    return;
-  }
-  const int len = paged_len(a.pool, b);
-  if (head_block && a.pool.err && (n > a.max_q || len != a.pool.lens[b] || n > len))
-    atomicOr(a.pool.err, LF_DEVERR_STATE);
-  const int64_t rows = (int64_t)n << gs;
-  const int64_t r0 = (int64_t)(gridDim.y - 1 - blockIdx.y) * (2 * kTile);
-  if (r0 >= rows) return;
-  const int first_pos = len - n;
-  const int p_lo = first_pos + (int)(r0 >> gs);
-  const int p_hi = first_pos + (int)((min(r0 + 2 * kTile, rows) - 1) >> gs);
-  const Tiles tiles(a, p_lo, p_hi, kTile);
+  Piece piece;
+  // The last rows see the most keys: they start first.
+  if (!take_piece(a, blockIdx.x, gridDim.y - 1 - blockIdx.y, 2 * kTile, tid == 0 && blockIdx.z == 0, &piece)) return;
+  const int g = piece.g, q0 = piece.q0, first_pos = piece.first_pos, p_lo = piece.p_lo, p_hi = piece.p_hi;
+  const int64_t r0 = piece.r0, rows = piece.rows;
+  const Tiles tiles(a, p_lo, p_hi, kTile, blockIdx.z);
   const int nt = tiles.count();
   // Does some row of the CTA not see some key of the tile at k0?
   auto masked = [&](int k0) { return some_hidden(a, p_lo, p_hi, k0, kTile); };
@@ -492,11 +482,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     if (!ok) {
       // nothing is right: leave the rows
     } else if (misc[1]) {
-      for (int i = 0; i < 32; ++i) {
-        const int64_t ri = r - lane + i;
-        if (ri >= rows) break;
-        const int64_t rowi = (int64_t)(q0 + (ri >> gs)) * a.q_heads + g * G + (ri & (G - 1));
-        row_by_hand<__nv_bfloat16, D>(a, b, g, rowi, first_pos + (int)(ri >> gs), lane);
+      rows_by_hand<__nv_bfloat16, D>(a, blockIdx.x, gridDim.y - 1 - blockIdx.y, blockIdx.z, kTile, 2 * kTile,
+                                     t * kTile + (warp & 3) * 32, 32, lane);
+    } else if (a.splits > 1) {   // a share of the row: few rows, stored as they lie
+      const int64_t id = (int64_t)(gridDim.y - 1 - blockIdx.y) * gridDim.x + blockIdx.x;
+      float* part = part_row<D>(a, id, blockIdx.z, 2 * kTile, t * kTile + (warp & 3) * 32 + lane, m, l, live);
+#pragma unroll 1
+      for (int i = 0; i < D / 32; ++i) {
+        float o[32];
+        tmem_ld32(to + 32 * i, o);
+        tmem_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + 32 * i + e) =
+                nt > 0 ? make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       }
     } else {
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -535,9 +536,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
         }
       }
       if (live) {
-        const int64_t row = (int64_t)(q0 + (r >> gs)) * a.q_heads + g * G + (r & (G - 1));
-        if (a.lse) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
-        if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
+        write_row_stats(a, (int64_t)(q0 + (r >> gs)) * a.q_heads + g * G + (r & (G - 1)), m, l);
       }
     }
   }
@@ -589,16 +588,26 @@ cudaError_t launch(const PromptTcArgs& ta, dim3 grid, cudaStream_t stream) {
 
 }  // namespace
 
-bool paged_prompt_tc_launch(const PagedPromptArgs& a, int head_dim, cudaStream_t stream, cudaError_t* err) {
-  const int ps = a.pool.page_size;
+// A dimension of one entry has no use for its stride, which must still be a legal one.
+cuuint64_t legal_stride(int64_t s, int64_t n) { return n == 1 && s < 16 ? 16 : (cuuint64_t)s; }
+
+bool paged_prompt_tc_takes(const PagedPool& pool, int head_dim) {
   // A key tile is whole boxes of whole pages (or a page is whole tiles), and a box
   // is whole groups of the eight rows that the swizzle repeats over.
+  const int ps = pool.page_size;
   const bool pages = ps >= 8 && (ps < kTile ? kTile % ps == 0 : ps % kTile == 0);
-  const int64_t row_tiles = ((int64_t)a.max_q * a.group + 2 * kTile - 1) / (2 * kTile);
-  const int64_t heads = (int64_t)a.pool.batch * a.pool.kv_heads;
-  if ((head_dim != 64 && head_dim != 128) || !pages || row_tiles > 65535 || heads > 0x7fffffff) return false;
+  // A tensor map has no stride of zero, and none from 2^40 bytes on.
+  const cuuint64_t st[3] = {legal_stride(pool.token_stride, ps), legal_stride(pool.head_stride, pool.kv_heads),
+                            legal_stride(pool.page_stride, pool.num_pages)};
+  for (cuuint64_t x : st)
+    if (x < 16 || x >= 1ull << 40) return false;
+  return (head_dim == 64 || head_dim == 128) && pages;
+}
+
+cudaError_t paged_prompt_tc_launch(const PagedPromptArgs& a, const PromptPlan& plan, int head_dim, cudaStream_t stream) {
+  const int ps = a.pool.page_size;
   EncodeFn fn = encoder();
-  if (!fn) return false;
+  if (!fn) return cudaErrorNotSupported;
   PromptTcArgs ta;
   ta.a = a;
   ta.box_rows = ps < kTile ? ps : kTile;
@@ -608,18 +617,15 @@ bool paged_prompt_tc_launch(const PagedPromptArgs& a, int head_dim, cudaStream_t
   const cuuint32_t qb[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(kTile / a.group)};
   const cuuint64_t kd[4] = {(cuuint64_t)head_dim, (cuuint64_t)ps, (cuuint64_t)a.pool.kv_heads,
                             (cuuint64_t)a.pool.num_pages};
-  // a dimension of one entry has no use for its stride, which must still be a legal one
-  auto legal = [](int64_t s, cuuint64_t n) { return n == 1 && s < 16 ? (cuuint64_t)16 : (cuuint64_t)s; };
-  const cuuint64_t kst[3] = {legal(a.pool.token_stride, kd[1]), legal(a.pool.head_stride, kd[2]),
-                             legal(a.pool.page_stride, kd[3])};
+  const cuuint64_t kst[3] = {legal_stride(a.pool.token_stride, ps), legal_stride(a.pool.head_stride, a.pool.kv_heads),
+                             legal_stride(a.pool.page_stride, a.pool.num_pages)};
   const cuuint32_t kb[4] = {64, (cuuint32_t)ta.box_rows, 1, 1};
-  // What a tensor map cannot describe (a stride of zero or from 2^40 bytes on) is the other kernel's.
   if (!encode(fn, &ta.q, a.q, 3, qd, qst, qb) || !encode(fn, &ta.k, a.pool.k, 4, kd, kst, kb) ||
       !encode(fn, &ta.v, a.pool.v, 4, kd, kst, kb))
-    return false;
-  const dim3 grid((unsigned)heads, (unsigned)row_tiles, 1);
-  *err = head_dim == 64 ? launch<64>(ta, grid, stream) : launch<128>(ta, grid, stream);
-  return true;
+    return cudaErrorInvalidValue;
+  const unsigned heads = (unsigned)a.pool.batch * a.pool.kv_heads;
+  const dim3 grid(heads, (unsigned)(plan.pieces / heads), plan.splits);
+  return head_dim == 64 ? launch<64>(ta, grid, stream) : launch<128>(ta, grid, stream);
 }
 
 }  // namespace lf

@@ -30,6 +30,7 @@ __all__ = [
     "lf_prefill_fill_noalloc", "lf_rkv_compress", "lf_launch_plan", "lf_launch_plan_for",
     "LFCache",
     "LFPages", "lf_paged_append", "lf_paged_decode", "lf_paged_decode_workspace", "lf_paged_prompt",
+    "lf_paged_prompt_workspace",
     "LFPagedCache",
 ]
 
@@ -144,7 +145,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.lf_paged_decode_workspace.restype = I
     lib.lf_paged_decode_workspace.argtypes = [PG, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
     lib.lf_paged_prompt.restype = I
-    lib.lf_paged_prompt.argtypes = [PG, I, VP, I, VP, I, VP, VP, I, I, VP, VP, I, I, VP]
+    lib.lf_paged_prompt.argtypes = [PG, I, VP, I, VP, I, VP, VP, I, I, VP, VP, I, I, VP,
+                                    ctypes.c_size_t, VP]
+    lib.lf_paged_prompt_workspace.restype = I
+    lib.lf_paged_prompt_workspace.argtypes = [PG, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
     _lib = lib
     return lib
 
@@ -323,10 +327,19 @@ def lf_paged_decode_workspace(pages: LFPages, batch, max_pages, q_heads, window=
 
 
 def lf_paged_prompt(pages: LFPages, batch, page_table, max_pages, lens, q_heads, q, q_start, total_q,
-                    max_q, out, lse, window, sinks, stream=None) -> int:
+                    max_q, out, lse, window, sinks, workspace, workspace_bytes, stream=None) -> int:
     return _check(load_library().lf_paged_prompt(
         ctypes.byref(pages), batch, _ptr(page_table), max_pages, _ptr(lens), q_heads, _ptr(q),
-        _ptr(q_start), total_q, max_q, _ptr(out), _ptr(lse), window, sinks, _stream(stream)))
+        _ptr(q_start), total_q, max_q, _ptr(out), _ptr(lse), window, sinks, _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def lf_paged_prompt_workspace(pages: LFPages, batch, max_pages, q_heads, max_q, window=0, sinks=0) -> int:
+    """Bytes of the workspace that such lf_paged_prompt calls need (0: none)."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().lf_paged_prompt_workspace(ctypes.byref(pages), batch, max_pages, q_heads, max_q,
+                                                    window, sinks, ctypes.byref(n)))
+    return int(n.value)
 
 
 # ---- convenience owner ------------------------------------------------------
@@ -500,7 +513,7 @@ class LFPagedCache:
         self._pages = [LFPages(types[k.dtype], self.kv_heads, self.head_dim, self.page_size, self.num_pages,
                                strides[1], strides[2], strides[3], pk + i * step, pv + i * step,
                                self.err.data_ptr()) for i in range(self.layers)]
-        self._need = {}   # workspace bytes by the shape of a decode call
+        self._need = {}   # workspace bytes by the shape of a decode or prompt call
         self._lib = load_library()
 
     def _layer(self, layer) -> LFPages:
@@ -606,11 +619,16 @@ class LFPagedCache:
 
     def _prompt(self, st, pages, batch, width, q_heads, page_table, lens, q, q_start, rows, max_q, out, lse,
                 window, sinks):
+        key = (batch, width, q_heads, max_q, window, sinks)
+        need = self._need.get(key)
+        if need is None:
+            need = self._need[key] = lf_paged_prompt_workspace(pages, *key)
         if out is None:
             out = torch.empty_like(q)
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         _check(self._lib.lf_paged_prompt(
             pages, batch, page_table.data_ptr(), width, lens.data_ptr(), q_heads, q.data_ptr(),
-            q_start.data_ptr(), rows, max_q, out.data_ptr(), _ptr(lse), window, sinks, st))
+            q_start.data_ptr(), rows, max_q, out.data_ptr(), _ptr(lse), window, sinks, _ptr(ws), need, st))
         return out
 
     def check(self, stream=None) -> int:

@@ -458,11 +458,18 @@ int lf_paged_decode_workspace(const lf_pages* pages, int batch, int max_pages, i
  *   q_start   device [batch + 1]
  *   max_q     no sequence has more rows (more: LF_DEVERR_STATE, the rest is left)
  *   lse       fp32 [total_q][q_heads], or NULL
+ *   workspace lf_paged_prompt_workspace bytes, as lf_paged_decode's
+ * Up to two launches: the keys of few rows are shared by several blocks and joined.
  */
 int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
                     const int32_t* lens, int q_heads, const void* q, const int32_t* q_start,
                     int total_q, int max_q, void* out, float* lse, int window, int sinks,
-                    lf_stream_t stream);
+                    void* workspace, size_t workspace_bytes, lf_stream_t stream);
+
+/* Bytes of the workspace of lf_paged_prompt calls with these arguments on the current
+ * device; 0 when they need none. */
+int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int max_q,
+                              int window, int sinks, size_t* bytes);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* lf_last_error(void);

@@ -266,6 +266,30 @@ def test_prompt_longer(kind, d):
     run_prompt(kind, 1, 8, d, 32, [1500], [37], seed=4)
 
 
+@pytest.mark.parametrize("kind,d,page", [("bf16", 128, 16), ("bf16", 64, 128), ("bf16", 32, 16), ("bf16", 128, 24),
+                                         ("f32", 64, 16), ("f32", 128, 64)])
+def test_prompt_few_rows_over_a_long_axis(kind, d, page):
+    """Several blocks share the keys of few rows, and their parts are joined."""
+    assert lf.lf_paged_prompt_workspace(Paged(kind, 2, d, page, [1]).cache._pages[0], 3, 6000 // page, 8, 5) > 0
+    run_prompt(kind, 2, 4, d, page, [5000, 0, 77], [3, 1, 5], seed=d)
+    run_prompt(kind, 1, 8, d, page, [6000], [1], seed=d + 1)
+    run_prompt(kind, 2, 1, d, page, [5000, 300], [40, 0], 3000, 200, seed=d + 2)
+    run_prompt(kind, 1, 2, d, page, [0, 4000], [140, 130], seed=d + 3)
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 32), ("f32", 64)])
+def test_prompt_shared_keys_and_values_that_are_not_finite(kind, d):
+    """As below, where blocks share the keys: a block whose keys hold a NaN computes its share by hand."""
+    p = Paged(kind, 1, d, 16, [4100], seed=23)
+    q = p.randn(60, 2, d)
+    st = torch.tensor([0, 60], dtype=torch.int32, device="cuda")
+    x, s = int(p.np_table[0, 4070 // 16]), 4070 % 16
+    p.v[x, 0, s] = math.nan
+    out = p.cache.prompt(0, q, p.table, p.t_lens, st, 60)
+    assert torch.isnan(out[30:].float()).all()
+    p.check(0, q[:30], 4040, out[:30], None, weight_step=2.0 ** -8 if kind == "bf16" else 0.0)
+
+
 def test_prompt_sharp_and_flat_logits():
     run_prompt("bf16", 2, 4, 128, 16, [0], [300], scale=6.0)
     run_prompt("f32", 2, 4, 128, 16, [0], [300], scale=6.0)
@@ -409,12 +433,40 @@ def test_streams_and_graphs_do_not_meet():
         with torch.cuda.graph(g):
             o = p.cache.decode(0, q, p.table, p.t_lens)
         graphs.append((g, o))
+    for p, q in ((a, qa), (b, qb)):           # few rows: prompts that share keys and join
+        st = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+        ref = p.cache.prompt(0, q, p.table, p.t_lens, st, 1)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = p.cache.prompt(0, q, p.table, p.t_lens, st, 1)
+        graphs.append((g, o, ref, st))
     for _ in range(10):
-        for (g, o), s in zip(graphs, (s1, s2)):
+        for (g, *_), s in zip(graphs, (s1, s2, s1, s2)):
             with torch.cuda.stream(s):
                 g.replay()
     torch.cuda.synchronize()
     assert torch.equal(graphs[0][1], ref_a) and torch.equal(graphs[1][1], ref_b)
+    assert torch.equal(graphs[2][1], graphs[2][2]) and torch.equal(graphs[3][1], graphs[3][2])
+
+
+def test_workspaces_are_asked_for():
+    p = Paged("bf16", 2, 128, 16, [4000, 5000], seed=51)
+    pages, q = p.cache._pages[0], p.randn(2, 8, 128)
+    out, st = torch.empty_like(q), torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    n = lf.lf_paged_decode_workspace(pages, 2, p.width, 8)
+    m = lf.lf_paged_prompt_workspace(pages, 2, p.width, 8, 1)
+    assert n > 0 and m > 0
+    ws = torch.empty(max(n, m) + 16, dtype=torch.uint8, device="cuda")
+    for w, size in ((None, n), (ws, n - 1), (ws.data_ptr() + 8, n)):
+        with pytest.raises(lf.LFError, match="workspace"):
+            lf.lf_paged_decode(pages, 2, p.table, p.width, p.t_lens, 8, q, None, None, out, None, 0, 0, w, size)
+    for w, size in ((None, m), (ws, m - 1), (ws.data_ptr() + 8, m)):
+        with pytest.raises(lf.LFError, match="workspace"):
+            lf.lf_paged_prompt(pages, 2, p.table, p.width, p.t_lens, 8, q, st, 2, 1, out, None, 0, 0, w, size)
+    lf.lf_paged_decode(pages, 2, p.table, p.width, p.t_lens, 8, q, None, None, out, None, 0, 0, ws, n)
+    p.check(0, q[:1], 3999, out[:1], None, weight_step=2.0 ** -17)
+    lf.lf_paged_prompt(pages, 2, p.table, p.width, p.t_lens, 8, q, st, 2, 1, out, None, 0, 0, ws, m)
+    p.check(1, q[1:], 4999, out[1:], None, weight_step=2.0 ** -8)
 
 
 def test_bad_tensors_are_refused():

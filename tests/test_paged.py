@@ -88,9 +88,9 @@ def decode(lib, p, batch=4, table=C, width=1000, lens=D, hq=32, q=E, k=E, v=E, o
 
 
 def prompt(lib, p, batch=4, table=C, width=10, lens=D, hq=32, q=E, start=D, total=7, most=3, out=E, lse=None,
-           window=0, sinks=0):
+           window=0, sinks=0, ws=E, nbytes=1 << 40):
     return lib.lf_paged_prompt(None if p is None else ctypes.byref(p), batch, table, width, lens, hq, q,
-                               start, total, most, out, lse, window, sinks, None)
+                               start, total, most, out, lse, window, sinks, ws, nbytes, None)
 
 
 BAD_POOLS = [
@@ -149,6 +149,13 @@ def test_bad_prompt_calls_are_refused(lib):
         assert msg in lf.lf_last_error(), kw
     assert prompt(lib, pages(), total=0, most=0) == lf.LF_OK
     assert prompt(lib, pages(), most=0) == lf.LF_OK
+    n = ctypes.c_size_t(7)
+    call = lib.lf_paged_prompt_workspace
+    assert call(None, 1, 1, 8, 1, 0, 0, ctypes.byref(n)) == lf.LF_ERR_ARG
+    assert call(ctypes.byref(pages()), 1, 1, 8, 1, 0, 0, None) == lf.LF_ERR_ARG
+    assert call(ctypes.byref(pages()), 1, 1, 8, -1, 0, 0, ctypes.byref(n)) == lf.LF_ERR_ARG
+    assert call(ctypes.byref(pages()), 1, 1, 24, 1, 0, 0, ctypes.byref(n)) == lf.LF_ERR_UNSUPPORTED
+    assert call(ctypes.byref(pages()), 1, 1, 8, 0, 0, 0, ctypes.byref(n)) == lf.LF_OK and n.value == 0
 
 
 def test_bad_decode_calls_are_refused(lib):
