@@ -226,21 +226,22 @@ struct DecodeShape {
   size_t off_ml, off_unit, bytes;
 };
 
-// A CTA takes a whole unit (one sequence's KV head) where no unit can be longer
-// than a few sweeps of its warps; else every SM takes an equal range of tokens.
+// A CTA takes a whole unit (one sequence's KV head), and no second launch is needed,
+// where the units fit on the GPU at once and none can be long: some sweeps of a CTA's
+// warps, more of them where the units are about as many as the SMs.  Else every SM
+// takes an equal range of all units' tokens.
 int decode_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int window, int sinks,
                  DecodeShape* s) {
   const int64_t most = window > 0 ? (int64_t)window + sinks : (int64_t)pool.max_pages * pool.page_size;
   const int64_t units = (int64_t)pool.batch * pool.kv_heads;
-  const int sweep = lf::paged_decode_sweep(elem_bytes(p), p->head_dim);
-  s->whole_units = most <= 4 * sweep && units <= INT_MAX;
-  if (s->whole_units) {
-    s->grid = (int)units;
-    s->off_ml = s->off_unit = s->bytes = 0;
-    return LF_OK;
-  }
-  const int rc = sm_count(&s->grid);
+  int sms = 0;
+  const int rc = sm_count(&sms);
   if (rc != LF_OK) return rc;
+  const int sweeps = 4 * units >= 3 * (int64_t)sms ? 10 : 4;
+  s->whole_units = units <= sms && most <= sweeps * (int64_t)lf::paged_decode_sweep(elem_bytes(p), p->head_dim);
+  s->grid = s->whole_units ? (int)units : sms;
+  s->off_ml = s->off_unit = s->bytes = 0;
+  if (s->whole_units) return LF_OK;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   s->off_ml = up((size_t)s->grid * 2 * group * p->head_dim * 4);
   s->off_unit = s->off_ml + up((size_t)s->grid * 2 * group * 2 * 4);

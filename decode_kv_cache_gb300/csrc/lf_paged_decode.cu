@@ -443,13 +443,6 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) paged_decode_kernel(const _
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  auto write_nothing_seen = [&](int64_t row, int rows) {
-    T* out = reinterpret_cast<T*>(a.out) + row * D;
-    for (int i = tid; i < rows * D; i += W * 32) from_f32(0.f, out + i);
-    if (a.lse)
-      for (int i = tid; i < rows; i += W * 32) a.lse[row + i] = kNegInf;
-  };
-
   // ---- this warp's range of the list: `left` tiles from place `at` -----------------
   Place at;
   long long left = 0;
@@ -459,9 +452,6 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) paged_decode_kernel(const _
     at.s = seen_of<TT>(a, at.b);
     at.t = (int)((long long)at.s.tiles * warp / W);
     left = (int)((long long)at.s.tiles * (warp + 1) / W) - at.t;
-    if (at.s.tiles == 0) write_nothing_seen((int64_t)at.b * a.q_heads + at.g * G, G);
-    if (tid == 0 && at.g == 0 && a.pool.err && a.pool.lens[at.b] != at.s.len)
-      atomicOr(a.pool.err, LF_DEVERR_STATE);
   } else {
     // Tiles (of one head) before each thread's sequences, a scan over the CTA; it
     // borrows the rings' memory.
@@ -508,21 +498,9 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) paged_decode_kernel(const _
       p.g = (int)(r / p.s.tiles);
       p.t = (int)(r - (long long)p.g * p.s.tiles);
     };
-    if (left > 0) place(x0, at);
-    if (tid == 0) {  // for the join: the unit that this CTA's range starts inside
-      int unit = -1;
-      if (c0 < c1) {
-        Place p;
-        place(c0, p);
-        if (p.t > 0) unit = p.b * H + p.g;
-      }
-      a.part_unit[blockIdx.x] = unit;
-    }
-    for (int b = blockIdx.x; b < a.pool.batch; b += gridDim.x) {  // no tile, no owner
-      const Seen s = seen_of<TT>(a, b);
-      if (s.tiles == 0) write_nothing_seen((int64_t)b * a.q_heads, a.q_heads);
-      if (tid == 0 && a.pool.err && a.pool.lens[b] != s.len) atomicOr(a.pool.err, LF_DEVERR_STATE);
-    }
+    if (left > 0 || (warp == 0 && c0 < c1)) place(x0, at);
+    // For the join: the unit that this CTA's range starts inside.
+    if (tid == 0) a.part_unit[blockIdx.x] = c0 < c1 && at.t > 0 ? at.b * H + at.g : -1;
     __syncthreads();  // the scan's memory becomes the rings
   }
 
@@ -646,6 +624,25 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) paged_decode_kernel(const _
   }
   cp_async_wait<0>();
   __syncthreads();
+
+  // ---- sequences that see nothing have no tile and give zeros -----------------------------
+  auto nothing_seen = [&](int b, int first_head, int heads) {
+    const Seen s = seen_of<TT>(a, b);
+    const int64_t row = (int64_t)b * a.q_heads + first_head;
+    if (s.tiles == 0) {
+      T* out = reinterpret_cast<T*>(a.out) + row * D;
+      for (int i = tid; i < heads * D; i += W * 32) from_f32(0.f, out + i);
+      if (a.lse)
+        for (int i = tid; i < heads; i += W * 32) a.lse[row + i] = kNegInf;
+    }
+    if (tid == 0 && first_head == 0 && a.pool.err && a.pool.lens[b] != s.len) atomicOr(a.pool.err, LF_DEVERR_STATE);
+  };
+  if (a.whole_units) {
+    const int b = blockIdx.x / H;
+    nothing_seen(b, (blockIdx.x - b * H) * G, G);
+  } else {
+    for (int b = blockIdx.x; b < a.pool.batch; b += gridDim.x) nothing_seen(b, 0, a.q_heads);
+  }
 
   // ---- join the warps' parts -----------------------------------------------------------
   // In order of position the parts are warp 0's first and last, warp 1's, ..; a

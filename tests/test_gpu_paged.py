@@ -456,6 +456,9 @@ def test_workspaces_are_asked_for():
     n = lf.lf_paged_decode_workspace(pages, 2, p.width, 8)
     m = lf.lf_paged_prompt_workspace(pages, 2, p.width, 8, 1)
     assert n > 0 and m > 0
+    # few short sequences need none, by the table's width or by the window
+    assert lf.lf_paged_decode_workspace(pages, 2, 4, 8) == 0
+    assert lf.lf_paged_decode_workspace(pages, 2, 1000, 8, window=60, sinks=4) == 0
     ws = torch.empty(max(n, m) + 16, dtype=torch.uint8, device="cuda")
     for w, size in ((None, n), (ws, n - 1), (ws.data_ptr() + 8, n)):
         with pytest.raises(lf.LFError, match="workspace"):

@@ -168,9 +168,6 @@ def test_bad_decode_calls_are_refused(lib):
     assert lib.lf_paged_decode_workspace(ctypes.byref(pages()), 1, 1, 8, 0, 0, None) == lf.LF_ERR_ARG
     assert lib.lf_paged_decode_workspace(ctypes.byref(pages()), 1, 1, 24, 0, 0, ctypes.byref(n)) == \
         lf.LF_ERR_UNSUPPORTED
-    # short sequences need no workspace, by the table's width or by the window
-    assert lf.lf_paged_decode_workspace(pages(), 64, 4, 32) == 0
-    assert lf.lf_paged_decode_workspace(pages(), 64, 1000, 32, window=60, sinks=4) == 0
 
 
 def test_cache_refuses_what_is_no_pool():
