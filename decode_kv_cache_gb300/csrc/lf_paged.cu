@@ -156,6 +156,8 @@ int take_pool(const lf_pages* p, int batch, const int32_t* table, int max_pages,
       return fail(LF_ERR_ARG, "page, head and token strides must be >= 0, at most 2^40 elements "
                   "and whole multiples of 16 bytes");
   if (batch < 1 || batch > 65535) return fail(LF_ERR_ARG, "batch must be in [1, 65535]");
+  if ((int64_t)batch * p->kv_heads > INT_MAX)
+    return fail(LF_ERR_ARG, "batch * kv_heads must be below 2^31");
   if (max_pages < 1 || (int64_t)max_pages * p->page_size > INT_MAX - 256)
     return fail(LF_ERR_ARG, "max_pages must be >= 1 and max_pages * page_size below 2^31 - 256");
   if (!table || !lens) return fail(LF_ERR_ARG, "null page_table or lens");
@@ -200,13 +202,14 @@ int take_window(const lf::PagedPool& p, int window, int sinks, int* w, int* s) {
   return LF_OK;
 }
 
-// The rows of a prompt call fit a grid (every kernel takes at least 32 rows per block).
+// The rows of a prompt call fit a grid: 65535 tiles of 256 rows along one dimension, all
+// pieces of 32 rows or more along another.
 int take_rows(const lf::PagedPool& p, int group, int max_q) {
   if (max_q < 0) return fail(LF_ERR_ARG, "max_q < 0");
-  const int64_t tiles = ((int64_t)max_q * group + 31) / 32;
-  if ((int64_t)max_q * group > INT_MAX - 256 || tiles * 32 / 256 > 65535 ||
-      (int64_t)p.batch * p.kv_heads > INT_MAX || tiles > INT_MAX / ((int64_t)p.batch * p.kv_heads))
-    return fail(LF_ERR_ARG, "max_q * group must be at most 2^24 - 256, and times batch * kv_heads / 32 below 2^31");
+  const int64_t rows = (int64_t)max_q * group;
+  if ((rows + 255) / 256 > 65535 || (rows + 31) / 32 > INT_MAX / ((int64_t)p.batch * p.kv_heads))
+    return fail(LF_ERR_ARG, "max_q * group must be at most 65535 * 256, and times batch * kv_heads / 32 "
+                "below 2^31");
   return LF_OK;
 }
 

@@ -338,12 +338,14 @@ struct SimtTile {
 // position i below `sinks`, else i + gap.
 struct Seen {
   int len, seen, gap, tiles;
+  bool right;   // the length fits the sequence's row of the page table
 };
 
 template <int TT>
 __device__ __forceinline__ Seen seen_of(const PagedDecodeArgs& a, int b) {
   Seen s;
   s.len = paged_len(a.pool, b);
+  s.right = s.len == a.pool.lens[b];
   s.seen = s.len;
   if (a.window > 0) {
     const int64_t w = (int64_t)a.window + a.sinks;
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) paged_decode_kernel(const _
   auto issue = [&](int stage) {
     const uint32_t kd = ring + stage * 2 * kTile, vd = kd + kTile;
     // The new token's row comes from the call; the warp that meets it stores it.
-    const int fresh = a.k_new ? ld.s.seen - 1 - ld.t * TT : -1;
+    const int fresh = a.k_new && ld.s.right ? ld.s.seen - 1 - ld.t * TT : -1;
     const int64_t head = ld.g * a.pool.head_stride;
     const int64_t new_row = ((int64_t)ld.b * H + ld.g) * (NC * 16);
     constexpr int RPI = 32 / NC;   // rows that one instruction covers
@@ -635,7 +637,7 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) paged_decode_kernel(const _
       if (a.lse)
         for (int i = tid; i < heads; i += W * 32) a.lse[row + i] = kNegInf;
     }
-    if (tid == 0 && first_head == 0 && a.pool.err && a.pool.lens[b] != s.len) atomicOr(a.pool.err, LF_DEVERR_STATE);
+    if (tid == 0 && first_head == 0 && a.pool.err && !s.right) atomicOr(a.pool.err, LF_DEVERR_STATE);
   };
   if (a.whole_units) {
     const int b = blockIdx.x / H;

@@ -177,6 +177,14 @@ def test_decode_bad_pages_and_lengths_set_the_error_word():
     out = p.cache.decode(0, q, p.table, p.t_lens)
     assert p.cache.check() & lf.LF_DEVERR_STATE
     p.check(0, q[:1], 99, out[:1], None, weight_step=2.0 ** -17)
+    # a token past its row of the table is stored nowhere
+    was, kn = p.k.clone(), p.randn(3, 2, 128)
+    p.cache.decode(0, q, p.table, p.t_lens, kn, kn)
+    assert p.cache.check() & lf.LF_DEVERR_STATE
+    changed = (torch.nan_to_num(p.k, 77.0) != torch.nan_to_num(was, 77.0)).any(-1).any(1).nonzero().tolist()
+    x = int(p.np_table[0, 99 // 16])
+    y = int(p.np_table[1, 49 // 16])
+    assert sorted(changed) == sorted([[x, 99 % 16], [y, 49 % 16]])
     p.t_lens[2] = -3
     out = p.cache.decode(0, q, p.table, p.t_lens)
     assert p.cache.check() & lf.LF_DEVERR_STATE

@@ -116,6 +116,8 @@ def test_bad_sequences_are_refused(lib, call):
                     (dict(lens=None), "null page_table or lens")]:
         assert call(lib, pages(), **kw) == lf.LF_ERR_ARG, kw
         assert msg in lf.lf_last_error(), kw
+    assert call(lib, pages(kv_heads=65535), batch=65535) == lf.LF_ERR_ARG
+    assert "batch * kv_heads" in lf.lf_last_error()
 
 
 @pytest.mark.parametrize("call", [decode, prompt], ids=lambda f: f.__name__)
