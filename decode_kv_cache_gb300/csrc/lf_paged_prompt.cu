@@ -231,13 +231,19 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
 // ---- fp32: CUDA cores -----------------------------------------------------------------
 //
 // Two floats per multiply-add instruction.  A thread holds an M x 4 piece of S (sums over
-// even and over odd columns of d) and M rows x d/16 columns of O.  V is on its way while S is computed; P,
-// transposed, goes where K was.
+// even and over odd columns of d) and M rows x d/16 columns of O.  V is on its way while S is computed.
+
+// P has a place of its own where that leaves room for as many blocks, so that the next K
+// can come in as soon as S is done.
+template <int D, int R>
+constexpr bool own_p() {
+  return R == 32;
+}
 
 template <int D, int R>
 constexpr int fma_smem() {
   constexpr int LD = D + 4, LP = R + 4;   // eight rows' equal chunks fall into different banks
-  return (R * LD + kKeys * (LD > LP ? LD : LP) + kKeys * LD) * 4;
+  return (R * LD + kKeys * (own_p<D, R>() ? LD + LP : LD > LP ? LD : LP) + kKeys * LD) * 4;
 }
 
 template <int D, int R, int M>
@@ -251,8 +257,10 @@ __global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __gr
   constexpr int CP = (CW + 1) / 2;      // .. in pairs
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;                                  // [R][LD]
-  float* sk = sm + R * LD;                         // [kKeys][LD], then P^T [kKeys][LP]
-  float* sv = sk + kKeys * (LD > LP ? LD : LP);    // [kKeys][LD]
+  constexpr bool kOwnP = R == 32;   // own_p
+  float* sk = sm + R * LD;                         // [kKeys][LD]
+  float* sv = sk + kKeys * (kOwnP || LD > LP ? LD : LP);   // [kKeys][LD]
+  float* sp = kOwnP ? sv + kKeys * LD : sk;        // P^T [kKeys][LP]
   __shared__ int64_t s_off[kKeys];
   const int tid = threadIdx.x;
   Piece p;
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __gr
     for (int i = 0; i < M; ++i)
 #pragma unroll
       for (int n = 0; n < 4; ++n) s2[i][n] = 0ull;
-#pragma unroll 2
+#pragma unroll (M == 4 ? 4 : 2)
     for (int d = 0; d < D; d += 4) {
       ulonglong2 y[4];
 #pragma unroll
@@ -353,23 +361,29 @@ __global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __gr
       }
     }
     __syncthreads();   // K has been read
+    if (kOwnP && j + 1 < nt) {   // and the offsets, by the copies of V
+      look_up(j + 1);
+      __syncthreads();
+      issue(sk, a.pool.k);
+    }
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
       for (int i = 0; i < M; i += 4)
-        *reinterpret_cast<float4*>(sk + (cg + 16 * n) * LP + rg * M + i) =
+        *reinterpret_cast<float4*>(sp + (cg + 16 * n) * LP + rg * M + i) =
             make_float4(w[i][n], w[i + 1][n], w[i + 2][n], w[i + 3][n]);
-    if (j + 1 < nt) look_up(j + 1);
-    cp_async_wait<0>();
+    if (!kOwnP && j + 1 < nt) look_up(j + 1);
+    if (kOwnP && j + 1 < nt) cp_async_wait<1>();   // V; K goes on
+    else cp_async_wait<0>();
     __syncthreads();
     // Where some row does not see some key of the tile, a weight of zero takes
     // nothing of the value, which may hold anything there.
     auto accumulate = [&](auto part) {
-#pragma unroll 2
+#pragma unroll (M == 4 ? 8 : 2)
       for (int k = 0; k < kKeys; ++k) {
         float pi[M];
 #pragma unroll
-        for (int i = 0; i < M; i += 4) load16_f32(sk + k * LP + rg * M + i, pi + i);
+        for (int i = 0; i < M; i += 4) load16_f32(sp + k * LP + rg * M + i, pi + i);
         uint64_t v[CP];
 #pragma unroll
         for (int c = 0; c < CW; c += VW) {
@@ -396,7 +410,7 @@ __global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __gr
     if (hidden) accumulate(std::true_type{});
     else accumulate(std::false_type{});
     __syncthreads();   // P and V have been read
-    if (j + 1 < nt) issue(sk, a.pool.k);
+    if (!kOwnP && j + 1 < nt) issue(sk, a.pool.k);
   }
 
 #pragma unroll
