@@ -233,17 +233,12 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
 // Two floats per multiply-add instruction.  A thread holds an M x 4 piece of S (sums over
 // even and over odd columns of d) and M rows x d/16 columns of O.  V is on its way while S is computed.
 
-// P has a place of its own where that leaves room for as many blocks, so that the next K
-// can come in as soon as S is done.
-template <int D, int R>
-constexpr bool own_p() {
-  return R == 32;
-}
-
+// In blocks of 32 rows P has a place of its own, so that the next K can come in as soon
+// as S is done; in those of 64 it goes where K was, which leaves room for two blocks.
 template <int D, int R>
 constexpr int fma_smem() {
   constexpr int LD = D + 4, LP = R + 4;   // eight rows' equal chunks fall into different banks
-  return (R * LD + kKeys * (own_p<D, R>() ? LD + LP : LD > LP ? LD : LP) + kKeys * LD) * 4;
+  return (R * LD + kKeys * (R == 32 ? LD + LP : LD > LP ? LD : LP) + kKeys * LD) * 4;
 }
 
 template <int D, int R, int M>
@@ -257,7 +252,7 @@ __global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __gr
   constexpr int CP = (CW + 1) / 2;      // .. in pairs
   extern __shared__ __align__(16) float sm[];
   float* sq = sm;                                  // [R][LD]
-  constexpr bool kOwnP = R == 32;   // own_p
+  constexpr bool kOwnP = R == 32;
   float* sk = sm + R * LD;                         // [kKeys][LD]
   float* sv = sk + kKeys * (kOwnP || LD > LP ? LD : LP);   // [kKeys][LD]
   float* sp = kOwnP ? sv + kKeys * LD : sk;        // P^T [kKeys][LP]
@@ -567,12 +562,17 @@ PromptPlan paged_prompt_plan(const PagedPool& pool, int elem, int head_dim, int 
   }
   plan.pieces = pieces_of(pool, group, max_q, plan.rows);
   // Where the pieces leave half of the GPU idle and their keys may be many, several
-  // blocks share a piece's keys: at least four tiles for each of them.
+  // blocks share a piece's keys: at least four tiles for each of them.  (32 / 8 heads of
+  // 128, one to 64 tokens behind 8000: 93 us without, 26 us.)  fp32 pieces differ in
+  // length and take long, so that there halves of twice as many even out, up to the blocks
+  // that an SM holds at once.  (Eight heads of 64, one prompt of 2000 tokens: 180 us
+  // without, 135 us; three of 500 to 1000: 67 us, 57 us.)
+  if (plan.kernel == PromptPlan::kFma && plan.pieces >= sms) room = (head_dim == 128 ? 4 : 8) * sms;
   const int64_t all = (int64_t)pool.max_pages * pool.page_size;
   const int64_t most = window > 0 ? (int64_t)window + sinks + plan.rows + 2 * keys : all;
   const int64_t tiles = ((most < all ? most : all) + keys - 1) / keys;
   int64_t splits = 1;
-  if (plan.pieces <= room / 2 && tiles >= 16) {
+  if (plan.pieces <= room / 2 && tiles >= (plan.kernel == PromptPlan::kFma ? 8 : 16)) {
     splits = room / plan.pieces;
     if (splits > tiles / 4) splits = tiles / 4;
     if (splits > kMaxSplits) splits = kMaxSplits;
