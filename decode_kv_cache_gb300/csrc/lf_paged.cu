@@ -229,10 +229,17 @@ struct DecodeShape {
   size_t off_ml, off_unit, bytes;
 };
 
-// A CTA takes a whole unit (one sequence's KV head), and no second launch is needed,
-// where the units fit on the GPU at once and none can be long: some sweeps of a CTA's
-// warps, more of them where the units are about as many as the SMs.  Else every SM
-// takes an equal range of all units' tokens.
+// Either a CTA takes a whole unit (one sequence's KV head) and no second launch is needed,
+// or every SM takes an equal range of all units' tokens and the units that were cut are
+// joined.  A range costs its share of the work and the join, a whole unit all of its own
+// tokens: the SMs that units leave idle cost a whole unit's time times (sms - units) / sms,
+// and that may be four sweeps of a CTA's warps, about what the join costs.  Nearly as many
+// units as SMs could be as long as they like if they were equally long; twelve sweeps where
+// they are a quarter to all of it.  (bf16, 32 / 8 heads of 128, whole against cut, a sweep
+// being 128 tokens: 8 units of 4 sweeps 10.0 us, 10.6, of 8 sweeps 14.9, 11.3; 64 units of
+// 4 sweeps 11.2, 14.4, of 8 sweeps 15.7, 17.2, of 16 sweeps 25.3, 21.9; 136 units of 8
+// sweeps 18.5, 23.7, of 16 sweeps 30.1, 35.3, but ragged 27.7, 30.1, of 32 sweeps ragged
+// 44.8, 41.7.  Heads of 64 and fp32 cross over at the same numbers of sweeps.)
 int decode_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int window, int sinks,
                  DecodeShape* s) {
   const int64_t most = window > 0 ? (int64_t)window + sinks : (int64_t)pool.max_pages * pool.page_size;
@@ -240,8 +247,8 @@ int decode_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int wi
   int sms = 0;
   const int rc = sm_count(&sms);
   if (rc != LF_OK) return rc;
-  const int sweeps = 4 * units >= 3 * (int64_t)sms ? 10 : 4;
-  s->whole_units = units <= sms && most <= sweeps * (int64_t)lf::paged_decode_sweep(elem_bytes(p), p->head_dim);
+  const int64_t sweep = lf::paged_decode_sweep(elem_bytes(p), p->head_dim);
+  s->whole_units = units <= sms && most * (sms - units) <= 4 * sms * sweep && most <= 12 * sweep;
   s->grid = s->whole_units ? (int)units : sms;
   s->off_ml = s->off_unit = s->bytes = 0;
   if (s->whole_units) return LF_OK;
