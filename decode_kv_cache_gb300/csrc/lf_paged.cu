@@ -202,14 +202,12 @@ int take_window(const lf::PagedPool& p, int window, int sinks, int* w, int* s) {
   return LF_OK;
 }
 
-// The rows of a prompt call fit a grid: 65535 tiles of 256 rows along one dimension, all
-// pieces of 32 rows or more along another.
-int take_rows(const lf::PagedPool& p, int group, int max_q) {
-  if (max_q < 0) return fail(LF_ERR_ARG, "max_q < 0");
-  const int64_t rows = (int64_t)max_q * group;
-  if ((rows + 255) / 256 > 65535 || (rows + 31) / 32 > INT_MAX / ((int64_t)p.batch * p.kv_heads))
-    return fail(LF_ERR_ARG, "max_q * group must be at most 65535 * 256, and times batch * kv_heads / 32 "
-                "below 2^31");
+// The rows of a prompt call; their pieces, of 32 rows or more, fit a grid.
+int take_rows(const lf::PagedPool& p, int group, int total_q, int max_q) {
+  if (total_q < 0 || max_q < 0 || max_q > total_q) return fail(LF_ERR_ARG, "need 0 <= max_q <= total_q");
+  int tiles;
+  if (lf::paged_prompt_pieces(p, group, total_q, max_q, 32, false, &tiles) > INT_MAX)
+    return fail(LF_ERR_ARG, "max_q * group / 32 * batch * kv_heads must be below 2^31");
   return LF_OK;
 }
 
@@ -344,8 +342,8 @@ int lf_paged_decode(const lf_pages* pages, int batch, const int32_t* page_table,
   return e == cudaSuccess ? LF_OK : cuda_fail(e, "paged decode launch");
 }
 
-int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int max_q,
-                              int window, int sinks, size_t* bytes) {
+int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int total_q,
+                              int max_q, int window, int sinks, size_t* bytes) {
   lf::clear_last_error();
   if (!pages || !bytes) return fail(LF_ERR_ARG, "null pages or bytes");
   lf::PagedPool pool;
@@ -354,12 +352,14 @@ int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, i
   int rc = take_pool(pages, batch, &any, max_pages, &any, &pool);
   if (rc != LF_OK || (rc = take_heads(pages, q_heads, &group)) != LF_OK ||
       (rc = take_window(pool, window, sinks, &window, &sinks)) != LF_OK ||
-      (rc = take_rows(pool, group, max_q)) != LF_OK)
+      (rc = take_rows(pool, group, total_q, max_q)) != LF_OK)
     return rc;
   *bytes = 0;
   if (max_q == 0) return LF_OK;
   if ((rc = sm_count(&sms)) != LF_OK) return rc;
-  *bytes = lf::paged_prompt_plan(pool, elem_bytes(pages), pages->head_dim, group, max_q, window, sinks, sms).bytes;
+  *bytes = lf::paged_prompt_plan(pool, elem_bytes(pages), pages->head_dim, group, total_q, max_q, window, sinks,
+                                 sms)
+               .bytes;
   return LF_OK;
 }
 
@@ -373,11 +373,9 @@ int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table,
   if (rc != LF_OK || (rc = take_heads(pages, q_heads, &a.group)) != LF_OK ||
       (rc = take_window(a.pool, window, sinks, &a.window, &a.sinks)) != LF_OK)
     return rc;
-  if (total_q < 0 || max_q < 0 || max_q > total_q)
-    return fail(LF_ERR_ARG, "need 0 <= max_q <= total_q");
+  if ((rc = take_rows(a.pool, a.group, total_q, max_q)) != LF_OK) return rc;
   if (!q_start) return fail(LF_ERR_ARG, "null q_start");
   if (total_q == 0 || max_q == 0) return LF_OK;
-  if ((rc = take_rows(a.pool, a.group, max_q)) != LF_OK) return rc;
   if (!q || !out || !aligned16(q) || !aligned16(out))
     return fail(LF_ERR_ARG, "q and out must be non-null and 16-byte aligned");
   a.q = q;
@@ -391,7 +389,11 @@ int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table,
   int sms = 0;
   if ((rc = sm_count(&sms)) != LF_OK) return rc;
   const lf::PromptPlan plan =
-      lf::paged_prompt_plan(a.pool, elem_bytes(pages), pages->head_dim, a.group, max_q, a.window, a.sinks, sms);
+      lf::paged_prompt_plan(a.pool, elem_bytes(pages), pages->head_dim, a.group, total_q, max_q, a.window,
+                            a.sinks, sms);
+  a.tiles_per_seq = plan.tiles_per_seq;
+  a.piece_shift = 0;
+  while (a.group << a.piece_shift < plan.rows) ++a.piece_shift;
   a.splits = plan.splits;
   a.part_o = a.part_ml = nullptr;
   if (plan.bytes > 0) {

@@ -92,23 +92,39 @@ struct Piece {
   int64_t r0, rows, id;
 };
 
-// Piece `tile` of sequence and KV head number `head`; false: it has no rows.  `tell`: this
-// thread reports what is wrong with the sequence.
-__device__ __forceinline__ bool take_piece(const PagedPromptArgs& a, int head, int tile, int per_piece, bool tell,
-                                           Piece* p) {
-  p->id = (int64_t)tile * a.pool.batch * a.pool.kv_heads + head;
-  p->b = head / a.pool.kv_heads;
-  p->g = head - p->b * a.pool.kv_heads;
-  p->q0 = a.q_start[p->b];
-  const int n = a.q_start[p->b + 1] - p->q0;
-  const bool first = tell && tile == 0 && p->g == 0;
-  if (p->q0 < 0 || n < 0 || n > a.total_q - p->q0) {   // not rows of q
-    if (first && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
-    return false;
-  }
+// The sequence that piece number `id` belongs to, for the whole warp together: with numbers
+// that follow the rows (tiles_per_seq = 0) its lanes look at 32 sequences at a time for the
+// last one that starts at or before the number.
+__device__ __forceinline__ unsigned first_number(const PagedPromptArgs& a, int b, int start) {
+  // Starts outside the rows count as their ends, so that other sequences keep their numbers.
+  return ((unsigned)min(max(start, 0), a.total_q) >> a.piece_shift) + (unsigned)b;
+}
+__device__ __forceinline__ int locate(const PagedPromptArgs& a, unsigned id) {
+  const unsigned j = id / (unsigned)a.pool.kv_heads;
+  if (a.tiles_per_seq > 0) return (int)(j % (unsigned)a.pool.batch);
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = a.pool.batch;
+  do {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const bool in = lane * step < n;
+    // (starts that decrease may give any lane, but one that is `in`)
+    const int k =
+        __popc(__ballot_sync(0xffffffffu, in && (lane == 0 || first_number(a, i, a.q_start[i]) <= j))) - 1;
+    lo += k * step;
+    n = min(step, n - k * step);
+  } while (n > 1);
+  return __shfl_sync(0xffffffffu, lo, 0);   // uniform for the compiler too
+}
+
+// Is something wrong with a sequence's rows or its length?
+__device__ __forceinline__ bool wrong_sequence(const PagedPromptArgs& a, int b, int q0, int n) {
+  const int len = paged_len(a.pool, b);
+  return q0 < 0 || n < 0 || n > a.total_q - q0 || n > a.max_q || len != a.pool.lens[b] || n > len;
+}
+
+// Rows from piece `tile` of a sequence on, and what they see; false: it has none.
+__device__ __forceinline__ bool take_rows(const PagedPromptArgs& a, int tile, int per_piece, int n, Piece* p) {
   const int len = paged_len(a.pool, p->b);
-  if (first && a.pool.err && (n > a.max_q || len != a.pool.lens[p->b] || n > len))
-    atomicOr(a.pool.err, LF_DEVERR_STATE);
   p->r0 = (int64_t)tile * per_piece;
   p->rows = (int64_t)n * a.group;
   if (p->r0 >= p->rows) return false;
@@ -116,6 +132,47 @@ __device__ __forceinline__ bool take_piece(const PagedPromptArgs& a, int head, i
   p->p_lo = p->first_pos + (int)(p->r0 / a.group);
   p->p_hi = p->first_pos + (int)((min(p->r0 + per_piece, p->rows) - 1) / a.group);
   return true;
+}
+
+// Piece number `id`, which is one of sequence b's (locate); false: it has no rows.  The last
+// rows, which see the most keys, come first.  `tell`: this thread reports what is wrong with
+// sequence `id`, of the first `batch` blocks.
+__device__ __forceinline__ bool take_piece(const PagedPromptArgs& a, unsigned id, int b, int per_piece, bool tell,
+                                           Piece* p) {
+  if (tell && (int)id < a.pool.batch && a.pool.err) {
+    const int q0 = a.q_start[id];
+    if (wrong_sequence(a, (int)id, q0, a.q_start[id + 1] - q0)) atomicOr(a.pool.err, LF_DEVERR_STATE);
+  }
+  p->id = id;
+  p->b = b;
+  p->g = (int)(id % (unsigned)a.pool.kv_heads);
+  p->q0 = a.q_start[b];
+  const int n = a.q_start[b + 1] - p->q0;
+  if (p->q0 < 0 || n < 0 || n > a.total_q - p->q0) return false;   // not rows of q
+  const unsigned j = id / (unsigned)a.pool.kv_heads;
+  int tile;
+  if (a.tiles_per_seq > 0) {
+    tile = a.tiles_per_seq - 1 - (int)(j / (unsigned)a.pool.batch);
+  } else {
+    tile = (int)(((int64_t)n * a.group + per_piece - 1) / per_piece) - 1 - (int)(j - first_number(a, b, p->q0));
+    if (tile < 0 || (int64_t)tile * per_piece >= (int64_t)a.max_q * a.group) return false;
+  }
+  return take_rows(a, tile, per_piece, n, p);
+}
+
+// The same where every sequence has as many numbers (tiles_per_seq > 0), for kernels that
+// a few more instructions before their loops make slower.
+__device__ __forceinline__ bool take_piece_level(const PagedPromptArgs& a, int head, int tile, int per_piece, bool tell,
+                                                 Piece* p) {
+  p->id = (int64_t)(a.tiles_per_seq - 1 - tile) * a.pool.batch * a.pool.kv_heads + head;
+  p->b = head / a.pool.kv_heads;
+  p->g = head - p->b * a.pool.kv_heads;
+  p->q0 = a.q_start[p->b];
+  const int n = a.q_start[p->b + 1] - p->q0;
+  if (tell && tile == 0 && p->g == 0 && a.pool.err && wrong_sequence(a, p->b, p->q0, n))
+    atomicOr(a.pool.err, LF_DEVERR_STATE);
+  if (p->q0 < 0 || n < 0 || n > a.total_q - p->q0) return false;   // not rows of q
+  return take_rows(a, tile, per_piece, n, p);
 }
 
 // Row r (of the sequence's token and head pairs) as a row of q and out.
@@ -241,13 +298,14 @@ __device__ __forceinline__ void row_by_hand(const PagedPromptArgs& a, const Piec
   if (lane == 0) write_row_stats(a, row, m, l);
 }
 
-// Rows rr .. rr + n - 1 of a piece.  What describes it is worked out again, so that the
-// usual path keeps none of it in registers for this one.
+// Rows rr .. rr + n - 1 of a piece, for the whole warp together.  What describes it is
+// worked out again, so that the usual path keeps none of it in registers for this one.  (A call here
+// instead of its code slows the tensor-core kernel: 8192 tokens, 32 / 8 heads, 354 -> 414 us.)
 template <typename T, int D>
-__device__ __noinline__ void rows_by_hand(const PagedPromptArgs& a, int head, int tile, int share, int size,
-                                          int per_piece, int rr, int n, int lane) {
+__device__ __forceinline__ void rows_by_hand(const PagedPromptArgs& a, unsigned id, int share, int size, int per_piece,
+                                          int rr, int n, int lane) {
   Piece p;
-  if (!take_piece(a, head, tile, per_piece, false, &p)) return;
+  if (!take_piece(a, id, locate(a, id), per_piece, false, &p)) return;
   const Tiles tiles(a, p.p_lo, p.p_hi, size, share);
   for (int i = rr; i < rr + n && p.r0 + i < p.rows; ++i)
     row_by_hand<T, D>(a, p, tiles, share, size, per_piece, i, lane);

@@ -52,20 +52,26 @@ struct PagedPromptArgs {
   float* lse;                 // may be null
   int q_heads, group, window, sinks, total_q, max_q;
   float scale_log2;
+  int tiles_per_seq;          // pieces that each sequence has numbers for, or 0 (PromptPlan)
+  int piece_shift;            // log2 of a piece's tokens
   int splits;                 // blocks that share a piece's keys; 1: no join
   float* part_o;              // [pieces][splits][rows][head_dim] partial outputs
   float* part_ml;             // [pieces][splits][rows][2] their max and sum
 };
 
 // How a prompt call is spread over the GPU.  A piece of work is `rows` rows (token and
-// head of the group) of one KV head's queries of one sequence.
+// head of the group) of one KV head's queries of one sequence.  The host knows neither
+// the sequences' rows nor their sum, only bounds, so that some numbers name no piece and
+// their blocks end at once: either every sequence has as many as max_q rows need
+// (tiles_per_seq), or sequence b's start at b + (rows before it) / (a piece's rows), which
+// leaves at most one number of a sequence without a piece.
 struct PromptPlan {
   enum { kTensor, kMatrix, kFma } kernel;
-  int rows, splits;
-  int64_t pieces;
+  int rows, splits, tiles_per_seq;
+  int64_t pieces;             // numbers of pieces, of all KV heads
   size_t off_ml, bytes;       // workspace: part_o, part_ml
 };
-PromptPlan paged_prompt_plan(const PagedPool& pool, int elem, int head_dim, int group, int max_q,
+PromptPlan paged_prompt_plan(const PagedPool& pool, int elem, int head_dim, int group, int total_q, int max_q,
                              int window, int sinks, int sms);
 
 // Occupied tokens of sequence b, kept inside its row of the page table.
@@ -97,6 +103,21 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+
+// Numbers of the pieces of `rows` rows, of all KV heads; *tiles_per_seq as in PromptPlan.
+// Numbers that follow the rows need a search of the row starts, and a sequence's pieces come
+// together instead of all sequences' longest ones first, so they have to be a third fewer.
+// (32 / 8 heads of 128, bf16, each against following: one chunk of 512 among 255 single
+// tokens behind 1000, 412 us, 285; one prompt of 8192 among 31, 795, 517; chunks of 1 to 512
+// behind up to 2048, 153, 147; three fp32 prompts of 500 to 1000, 61, 67.)
+inline int64_t paged_prompt_pieces(const PagedPool& pool, int group, int total_q, int max_q, int rows,
+                                   bool may_follow, int* tiles_per_seq) {
+  auto pieces = [&](int64_t tokens) { return (tokens * group + rows - 1) / rows; };
+  const int64_t each = pieces(max_q) * pool.batch, all = pieces(total_q) + pool.batch - 1;
+  const bool level = !may_follow || 2 * each <= 3 * all;
+  *tiles_per_seq = level ? (int)pieces(max_q) : 0;
+  return (level ? each : all) * pool.kv_heads;
 }
 
 // Launches (one translation unit each).  They return the launch's error.

@@ -14,8 +14,8 @@
 // A CTA takes some rows of one KV head's queries, (token, head of the group) pairs
 // with the head inner: every key and value it loads serves all heads of the group.
 // Keys and values pass through shared memory in tiles of 64 tokens, 16-byte chunks
-// gathered by page; key tiles that no row sees are not visited.  Blocks with the most
-// keys start first.
+// gathered by page; key tiles that no row sees are not visited.  A sequence's
+// last rows, which see the most keys, start first.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,10 +44,9 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t s_off[2][kKeys];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int share = blockIdx.y;
   Piece p;
-  const int share = blockIdx.y, heads = a.pool.batch * a.pool.kv_heads;
-  const int id = gridDim.x - 1 - blockIdx.x, tile = id / heads;   // the last rows first
-  if (!take_piece(a, id - tile * heads, tile, kMmaRows, tid == 0 && share == 0, &p)) return;
+  if (!take_piece(a, blockIdx.x, locate(a, blockIdx.x), kMmaRows, tid == 0 && share == 0, &p)) return;
   const Tiles tiles(a, p.p_lo, p.p_hi, kKeys, share);
   const int nt = tiles.count();
   const uint32_t ring = smem_u32(smem);
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
 
   const float2 f = __bfloat1622float2(bad);
   if (__syncthreads_or(!(f.x == 0.f) || !(f.y == 0.f))) {
-    rows_by_hand<__nv_bfloat16, D>(a, id - tile * heads, tile, share, kKeys, kMmaRows, warp * 16, 16, lane);
+    rows_by_hand<__nv_bfloat16, D>(a, blockIdx.x, share, kKeys, kMmaRows, warp * 16, 16, lane);
     return;
   }
 #pragma unroll
@@ -261,7 +260,7 @@ __global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __gr
   Piece p;
   const int share = blockIdx.y, heads = a.pool.batch * a.pool.kv_heads;
   const int id = gridDim.x - 1 - blockIdx.x, tile = id / heads;   // the last rows first
-  if (!take_piece(a, id - tile * heads, tile, R, tid == 0 && share == 0, &p)) return;
+  if (!take_piece_level(a, id - tile * heads, tile, R, tid == 0 && share == 0, &p)) return;
   const Tiles tiles(a, p.p_lo, p.p_hi, kKeys, share);
   const int nt = tiles.count();
 
@@ -445,8 +444,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_prompt_join_kernel(cons
   const int64_t i = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
   const int rr = (int)(i % per_piece);
   Piece p;
-  const int id = (int)(i / per_piece), heads = a.pool.batch * a.pool.kv_heads;
-  if (!take_piece(a, id % heads, id / heads, per_piece, false, &p) || p.r0 + rr >= p.rows) return;
+  const unsigned id = (unsigned)(i / per_piece);
+  if (!take_piece(a, id, locate(a, id), per_piece, false, &p) || p.r0 + rr >= p.rows) return;
   const int64_t part = p.id * a.splits * per_piece + rr;   // share s: + s * per_piece
   float m = kNegInf, l = 0.f;
   if (lane < a.splits) {
@@ -494,10 +493,6 @@ cudaError_t launch_join_dim(const PagedPromptArgs& a, const PromptPlan& plan, in
   }
 }
 
-int64_t pieces_of(const PagedPool& pool, int group, int max_q, int rows) {
-  return ((int64_t)max_q * group + rows - 1) / rows * pool.batch * pool.kv_heads;
-}
-
 template <int D>
 cudaError_t launch_mma(const PagedPromptArgs& a, const PromptPlan& plan, cudaStream_t stream) {
   constexpr int kSmem = 4 * kKeys * D * 2;
@@ -538,7 +533,7 @@ cudaError_t launch_kernel(const PagedPromptArgs& a, const PromptPlan& plan, int 
 
 }  // namespace
 
-PromptPlan paged_prompt_plan(const PagedPool& pool, int elem, int head_dim, int group, int max_q,
+PromptPlan paged_prompt_plan(const PagedPool& pool, int elem, int head_dim, int group, int total_q, int max_q,
                              int window, int sinks, int sms) {
   PromptPlan plan;
   int keys = kKeys, room = 3 * sms;   // keys of a tile, blocks that run at once
@@ -558,9 +553,10 @@ PromptPlan paged_prompt_plan(const PagedPool& pool, int elem, int head_dim, int 
     // Shorter heads gain nothing from it: heads of 64, three of 2000 tokens, 362 against
     // 425.)
     plan.kernel = PromptPlan::kFma;
-    plan.rows = head_dim == 128 && pieces_of(pool, group, max_q, 64) >= 4 * (int64_t)sms ? 64 : 32;
+    const int64_t of64 = paged_prompt_pieces(pool, group, total_q, max_q, 64, false, &plan.tiles_per_seq);
+    plan.rows = head_dim == 128 && of64 >= 4 * (int64_t)sms ? 64 : 32;
   }
-  plan.pieces = pieces_of(pool, group, max_q, plan.rows);
+  plan.pieces = paged_prompt_pieces(pool, group, total_q, max_q, plan.rows, elem == 2, &plan.tiles_per_seq);
   // Where the pieces leave half of the GPU idle and their keys may be many, several
   // blocks share a piece's keys: at least four tiles for each of them.  (32 / 8 heads of
   // 128, one to 64 tokens behind 8000: 93 us without, 26 us.)  fp32 pieces differ in

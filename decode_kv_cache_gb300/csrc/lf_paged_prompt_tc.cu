@@ -5,9 +5,9 @@
 // Work.  A CTA takes 256 rows of one KV head's queries, (token, head of the group)
 // pairs with the head inner, as two tiles of 128: every key and value it loads
 // serves both tiles and all heads of the group.  Key tiles of 128 tokens that no
-// row sees are not visited.  CTAs with the most keys start first.
+// row sees are not visited.  A sequence's last rows, which see the most keys, start first.
 //
-// Roles (11 warps):
+// Roles (12 warps, of which one rests: the softmax groups start at a multiple of four):
 //   loader   gathers K and V tiles by page with TMA (one box per page and 64
 //            columns, one lane each; a page past the end is a box outside the
 //            tensor, which the hardware fills with zeros) into a ring;
@@ -42,7 +42,7 @@ namespace {
 
 constexpr int kTile = 128;                 // rows of a query tile, tokens of a key tile
 constexpr int kBlk = kTile * 128;          // a tile's 64 columns in shared memory (128-byte swizzle)
-constexpr int kMmaWarp = 0, kLoadWarp = 1, kScrubWarp = 2, kSoftWarp = 4;  // softmax: 4 .. 11 (3 rests)
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kScrubWarp = 2, kRestWarp = 3, kSoftWarp = 4;  // softmax: 4 .. 11
 constexpr int kThreadsTc = 384;
 constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
 constexpr float kGrow = 8.f;               // log2 growth of a maximum that is let pass
@@ -52,6 +52,11 @@ struct PromptTcArgs {
   PagedPromptArgs a;
   int box_rows;      // tokens of one TMA box: min(page_size, 128)
   int group_shift;
+};
+
+struct Work {
+  int p_lo, p_hi, sink, gap, first, last, q0, g;
+  int64_t r0, rows;
 };
 
 template <int D>
@@ -152,7 +157,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform for the compiler too
   const int G = a.group, gs = ta.group_shift;
-  const int b = blockIdx.x / a.pool.kv_heads;
+  const int b = locate(a, blockIdx.x);
 
   // The loader's lookups for the first key tile, before it is known whether that is
   // tile 0 (it is unless a window without sinks starts behind it).
@@ -165,11 +170,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     if (pi < a.pool.max_pages) guess = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
   }
   Piece piece;
-  // The last rows see the most keys: they start first.
-  if (!take_piece(a, blockIdx.x, gridDim.y - 1 - blockIdx.y, 2 * kTile, tid == 0 && blockIdx.z == 0, &piece)) return;
+  if (!take_piece(a, blockIdx.x, b, 2 * kTile, tid == kRestWarp * 32 && blockIdx.y == 0, &piece)) return;
   const int g = piece.g, q0 = piece.q0, first_pos = piece.first_pos, p_lo = piece.p_lo, p_hi = piece.p_hi;
   const int64_t r0 = piece.r0, rows = piece.rows;
-  const Tiles tiles(a, p_lo, p_hi, kTile, blockIdx.z);
+  const Tiles tiles(a, p_lo, p_hi, kTile, blockIdx.y);
   const int nt = tiles.count();
   // Does some row of the CTA not see some key of the tile at k0?
   auto masked = [&](int k0) { return some_hidden(a, p_lo, p_hi, k0, kTile); };
@@ -185,6 +189,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   uint64_t* ofull = pfull + 4;                          // [2] O_t final
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
   volatile int* misc = reinterpret_cast<volatile int*>(smem + 528);   // [0] a wait expired, [1] by hand
+  // The piece as the softmax threads read it, which have no registers to spare.
+  volatile Work* work = reinterpret_cast<volatile Work*>(smem + 768);
+  if (tid == kRestWarp * 32) {
+    work->p_lo = p_lo;
+    work->p_hi = p_hi;
+    work->sink = tiles.sink;
+    work->gap = tiles.gap;
+    work->first = tiles.first;
+    work->last = tiles.last;
+    work->q0 = q0;
+    work->g = g;
+    work->r0 = r0;
+    work->rows = rows;
+  }
   unsigned char* qs = smem + P::kOffQ;
   unsigned char* ring = smem + P::kOffRing;
 
@@ -397,15 +415,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   } else if (warp >= kSoftWarp) {
     // ---- softmax ----------------------------------------------------------------------
     const int t = (warp - kSoftWarp) >> 2;
-    const int64_t r = r0 + t * kTile + (warp & 3) * 32 + lane;
-    const bool live = r < rows;
-    const int pos = live ? first_pos + (int)(r >> gs) : -1;
+    const int rr0 = t * kTile + (warp & 3) * 32;   // the warp's first row in the piece
+    const bool live = work->r0 + rr0 + lane < work->rows;
+    const int pos = live ? work->p_lo + ((rr0 + lane) >> gs) : -1;
     const uint32_t ts = tm + t * 128 + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t to = tm + 256 + t * D + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = a.scale_log2;
     bool ok = true;
-    for (int j = 0; j < nt; ++j) {
-      const int k0 = tiles.at(j) * kTile;
+    const int n = work->last - work->first;
+    for (int j = 0; j < n; ++j) {
+      const int at = work->first + j;
+      const int k0 = (at < work->sink ? at : at + work->gap) * kTile;
+      const bool hidden = some_hidden(a, work->p_lo, work->p_hi, k0, kTile);
       ok = __all_sync(0xffffffffu, wait(&sfull[4 * t + (j & 3)], (uint32_t)((j >> 2) & 1)));
       if (!ok) break;
       tc_fence_after();
@@ -413,7 +434,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
 #pragma unroll
       for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
       tmem_wait_ld();
-      if (masked(k0)) {
+      if (hidden) {
         const int hi = pos - k0, sk = a.sinks - k0;
         const int lo = a.window > 0 && pos >= 0 ? pos - a.window + 1 - k0 : -1;
 #pragma unroll
@@ -477,16 +498,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     }
 
     // ---- rows out --------------------------------------------------------------------
-    ok = ok && (nt == 0 || __all_sync(0xffffffffu, wait(&ofull[t], 0)));
+    ok = ok && (n == 0 || __all_sync(0xffffffffu, wait(&ofull[t], 0)));
     tc_fence_after();
-    if (!ok) {
-      // nothing is right: leave the rows
-    } else if (misc[1]) {
-      rows_by_hand<__nv_bfloat16, D>(a, blockIdx.x, gridDim.y - 1 - blockIdx.y, blockIdx.z, kTile, 2 * kTile,
-                                     t * kTile + (warp & 3) * 32, 32, lane);
+    if (!ok || misc[1]) {
+      // nothing is right, or the rows are computed again below: leave them
     } else if (a.splits > 1) {   // a share of the row: few rows, stored as they lie
-      const int64_t id = (int64_t)(gridDim.y - 1 - blockIdx.y) * gridDim.x + blockIdx.x;
-      float* part = part_row<D>(a, id, blockIdx.z, 2 * kTile, t * kTile + (warp & 3) * 32 + lane, m, l, live);
+      float* part = part_row<D>(a, blockIdx.x, blockIdx.y, 2 * kTile, rr0 + lane, m, l, live);
 #pragma unroll 1
       for (int i = 0; i < D / 32; ++i) {
         float o[32];
@@ -496,15 +513,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(part + 32 * i + e) =
-                nt > 0 ? make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+                n > 0 ? make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
     } else {
       const float inv = l == 0.f ? 0.f : 1.f / l;
       unsigned char* stage = smem + P::kOffOut + (warp - kSoftWarp) * 4096;   // 32 rows x 64 columns
       // Row rr of the warp's 32 is head rr % G of token rr / G from its first.
-      const int64_t first = r - lane;
-      const int left = (int)min((int64_t)32, rows - first);
+      const int64_t first = work->r0 + rr0;
+      const int left = (int)min((int64_t)32, work->rows - first);
+      const int q0 = work->q0, g = work->g;
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) +
                            ((int64_t)(q0 + (first >> gs)) * a.q_heads + g * G) * D + (lane & 7) * 8;
       const int64_t token = (int64_t)a.q_heads * D;
@@ -536,7 +554,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
         }
       }
       if (live) {
-        write_row_stats(a, (int64_t)(q0 + (r >> gs)) * a.q_heads + g * G + (r & (G - 1)), m, l);
+        write_row_stats(a, (int64_t)(q0 + ((first + lane) >> gs)) * a.q_heads + g * G + (lane & (G - 1)), m, l);
       }
     }
   }
@@ -546,6 +564,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     tc_fence_after();
     tmem_dealloc(tm, 512);
     if (lane == 0 && misc[0] && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
+  }
+  if (misc[1] && !misc[0]) {
+    constexpr int kEach = (2 * kTile + kThreadsTc / 32 - 1) / (kThreadsTc / 32);   // rows of a warp
+    rows_by_hand<__nv_bfloat16, D>(a, blockIdx.x, blockIdx.y, kTile, 2 * kTile, warp * kEach,
+                                   min(kEach, 2 * kTile - warp * kEach), lane);
   }
 }
 
@@ -623,8 +646,7 @@ cudaError_t paged_prompt_tc_launch(const PagedPromptArgs& a, const PromptPlan& p
   if (!encode(fn, &ta.q, a.q, 3, qd, qst, qb) || !encode(fn, &ta.k, a.pool.k, 4, kd, kst, kb) ||
       !encode(fn, &ta.v, a.pool.v, 4, kd, kst, kb))
     return cudaErrorInvalidValue;
-  const unsigned heads = (unsigned)a.pool.batch * a.pool.kv_heads;
-  const dim3 grid(heads, (unsigned)(plan.pieces / heads), plan.splits);
+  const dim3 grid((unsigned)plan.pieces, plan.splits);
   return head_dim == 64 ? launch<64>(ta, grid, stream) : launch<128>(ta, grid, stream);
 }
 

@@ -148,7 +148,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.lf_paged_prompt.argtypes = [PG, I, VP, I, VP, I, VP, VP, I, I, VP, VP, I, I, VP,
                                     ctypes.c_size_t, VP]
     lib.lf_paged_prompt_workspace.restype = I
-    lib.lf_paged_prompt_workspace.argtypes = [PG, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
+    lib.lf_paged_prompt_workspace.argtypes = [PG, I, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
     _lib = lib
     return lib
 
@@ -334,11 +334,12 @@ def lf_paged_prompt(pages: LFPages, batch, page_table, max_pages, lens, q_heads,
         workspace_bytes, _stream(stream)))
 
 
-def lf_paged_prompt_workspace(pages: LFPages, batch, max_pages, q_heads, max_q, window=0, sinks=0) -> int:
+def lf_paged_prompt_workspace(pages: LFPages, batch, max_pages, q_heads, total_q, max_q, window=0,
+                              sinks=0) -> int:
     """Bytes of the workspace that such lf_paged_prompt calls need (0: none)."""
     n = ctypes.c_size_t(0)
-    _check(load_library().lf_paged_prompt_workspace(ctypes.byref(pages), batch, max_pages, q_heads, max_q,
-                                                    window, sinks, ctypes.byref(n)))
+    _check(load_library().lf_paged_prompt_workspace(ctypes.byref(pages), batch, max_pages, q_heads,
+                                                    total_q, max_q, window, sinks, ctypes.byref(n)))
     return int(n.value)
 
 
@@ -557,6 +558,13 @@ class LFPagedCache:
         with torch.cuda.device(self._index), torch.cuda.stream(stream):
             return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
 
+    def _ask(self, call, pages, key):
+        """The workspace that calls of this shape need, remembered (of the last few thousand shapes)."""
+        if len(self._need) >= 4096:
+            self._need.clear()
+        need = self._need[key] = call(pages, *key)
+        return need
+
     def append(self, layer, k_new, v_new, page_table, lens, new_start=None, stream=None):
         """lf_paged_append: k_new, v_new [tokens][kv_heads][head_dim] go to their pages;
         new_start int32 [batch + 1], or None: one token per sequence."""
@@ -594,7 +602,7 @@ class LFPagedCache:
         key = (batch, width, q_heads, window, sinks)
         need = self._need.get(key)
         if need is None:
-            need = self._need[key] = lf_paged_decode_workspace(pages, *key)
+            need = self._ask(lf_paged_decode_workspace, pages, key)
         if out is None:
             out = torch.empty_like(q)
         # a workspace of this call's own: calls on other streams and graphs cannot meet in it
@@ -619,10 +627,10 @@ class LFPagedCache:
 
     def _prompt(self, st, pages, batch, width, q_heads, page_table, lens, q, q_start, rows, max_q, out, lse,
                 window, sinks):
-        key = (batch, width, q_heads, max_q, window, sinks)
+        key = (batch, width, q_heads, rows, max_q, window, sinks)
         need = self._need.get(key)
         if need is None:
-            need = self._need[key] = lf_paged_prompt_workspace(pages, *key)
+            need = self._ask(lf_paged_prompt_workspace, pages, key)
         if out is None:
             out = torch.empty_like(q)
         ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None

@@ -386,9 +386,10 @@ int lf_prefill_fill_noalloc(const lf_layout* dst, int layer, const void* k, cons
  * LF_DEVERR_STATE for a page index outside [0, num_pages), a length outside [0,
  * max_pages * page_size] or row starts outside the rows (such tokens are not
  * stored or read as zeros; outputs of that sequence are unspecified, no other is
- * touched), LF_DEVERR_NONFINITE for a softmax sum that is not finite,
- * LF_DEVERR_TIMEOUT for an expired on-chip wait (that call's outputs are
- * unspecified).  The caller reads and clears the word.
+ * touched) or that decrease (outputs of the call are unspecified),
+ * LF_DEVERR_NONFINITE for a softmax sum that is not finite, LF_DEVERR_TIMEOUT for
+ * an expired on-chip wait (that call's outputs are unspecified).  The caller reads
+ * and clears the word.
  *
  * Query head h reads KV head floor(h / G), G = q_heads / kv_heads in {1, 2, 4, 8};
  * head_dim in {16, 32, 64, 128}; logits are scaled by 1 / sqrt(head_dim).  With
@@ -468,8 +469,8 @@ int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table,
 
 /* Bytes of the workspace of lf_paged_prompt calls with these arguments on the current
  * device; 0 when they need none. */
-int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int max_q,
-                              int window, int sinks, size_t* bytes);
+int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int total_q,
+                              int max_q, int window, int sinks, size_t* bytes);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* lf_last_error(void);

@@ -278,11 +278,57 @@ def test_prompt_longer(kind, d):
                                          ("f32", 64, 16), ("f32", 128, 64)])
 def test_prompt_few_rows_over_a_long_axis(kind, d, page):
     """Several blocks share the keys of few rows, and their parts are joined."""
-    assert lf.lf_paged_prompt_workspace(Paged(kind, 2, d, page, [1]).cache._pages[0], 3, 6000 // page, 8, 5) > 0
+    assert lf.lf_paged_prompt_workspace(Paged(kind, 2, d, page, [1]).cache._pages[0], 3, 6000 // page, 8, 9, 5) > 0
     run_prompt(kind, 2, 4, d, page, [5000, 0, 77], [3, 1, 5], seed=d)
     run_prompt(kind, 1, 8, d, page, [6000], [1], seed=d + 1)
     run_prompt(kind, 2, 1, d, page, [5000, 300], [40, 0], 3000, 200, seed=d + 2)
     run_prompt(kind, 1, 2, d, page, [0, 4000], [140, 130], seed=d + 3)
+
+
+@pytest.mark.parametrize("kind,d,group", [("bf16", 128, 4), ("bf16", 64, 1), ("bf16", 32, 8), ("f32", 64, 2)])
+def test_prompt_mixed_batches(kind, d, group):
+    """One long chunk among sequences of a token or none: pieces are numbered by the rows before them."""
+    new = [1, 0, 1, 130, 1, 0, 64, 1, 256, 0] + [1] * 30
+    old = [i * 7 % 90 for i in range(len(new))]
+    run_prompt(kind, 2, group, d, 16, old, new, seed=d + group)
+    run_prompt(kind, 1, group, d, 16, old, new[::-1], 20, 2, seed=d + group + 1)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("batch", [32, 33, 1024, 1025])
+def test_prompt_many_sequences(kind, batch):
+    """The sequence of a piece is found 32 at a time: one, two and three rounds of it."""
+    new = [3 if i % 97 == 5 else i % 2 for i in range(batch)]
+    new[batch // 2], new[-1] = 90, 70
+    run_prompt(kind, 1, 4, 64, 8, [i % 5 for i in range(batch)], new, seed=batch)
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 32), ("f32", 64)])
+def test_prompt_row_starts(kind, d):
+    """Rows in front of the first sequence are left; starts outside the rows spoil no other sequence."""
+    p = Paged(kind, 2, d, 16, [200, 90, 150], seed=d)
+    q = p.randn(700, 8, d)
+    step = 2.0 ** -8 if kind == "bf16" else 0.0
+
+    def run(st, most):
+        out = torch.full_like(q, 3.0)
+        p.cache.prompt(0, q, p.table, p.t_lens, torch.tensor(st, dtype=torch.int32, device="cuda"), most, out=out)
+        return out
+
+    out = run([300, 500, 560, 700], 200)
+    for b, (lo, hi) in enumerate([(300, 500), (500, 560), (560, 700)]):
+        p.check(b, q[lo:hi], p.lens[b] - (hi - lo), out[lo:hi], None, weight_step=step)
+    assert (out[:300] == 3).all() and p.cache.check() == 0
+    out = run([-1000, 100, 160, 300], 140)       # the first sequence starts in front of the rows
+    p.check(1, q[100:160], 30, out[100:160], None, weight_step=step)
+    p.check(2, q[160:300], 10, out[160:300], None, weight_step=step)
+    assert (out[300:] == 3).all() and p.cache.check() == lf.LF_DEVERR_STATE
+    out = run([0, 200, 260, 2**31 - 1], 200)     # the last one ends behind them
+    p.check(0, q[:200], 0, out[:200], None, weight_step=step)
+    p.check(1, q[200:260], 30, out[200:260], None, weight_step=step)
+    assert (out[260:] == 3).all() and p.cache.check() == lf.LF_DEVERR_STATE
+    run([0, 400, 100, 300], 200)                 # they decrease: reported, nothing more is said
+    assert p.cache.check() & lf.LF_DEVERR_STATE
 
 
 @pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 32), ("f32", 64)])
@@ -462,7 +508,7 @@ def test_workspaces_are_asked_for():
     pages, q = p.cache._pages[0], p.randn(2, 8, 128)
     out, st = torch.empty_like(q), torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
     n = lf.lf_paged_decode_workspace(pages, 2, p.width, 8)
-    m = lf.lf_paged_prompt_workspace(pages, 2, p.width, 8, 1)
+    m = lf.lf_paged_prompt_workspace(pages, 2, p.width, 8, 2, 1)
     assert n > 0 and m > 0
     # few short sequences need none, by the table's width or by the window
     assert lf.lf_paged_decode_workspace(pages, 2, 4, 8) == 0

@@ -146,18 +146,19 @@ def test_bad_append_calls_are_refused(lib):
 
 def test_bad_prompt_calls_are_refused(lib):
     for kw, msg in [(dict(total=-1), "total_q"), (dict(most=8), "max_q <= total_q"), (dict(most=-1), "max_q"),
-                    (dict(start=None), "q_start"), (dict(total=1 << 30, most=1 << 30), "max_q * group")]:
+                    (dict(start=None), "q_start"), (dict(total=2**31 - 1, most=2**31 - 1), "must be below 2^31")]:
         assert prompt(lib, pages(), **kw) == lf.LF_ERR_ARG, kw
         assert msg in lf.lf_last_error(), kw
     assert prompt(lib, pages(), total=0, most=0) == lf.LF_OK
     assert prompt(lib, pages(), most=0) == lf.LF_OK
     n = ctypes.c_size_t(7)
     call = lib.lf_paged_prompt_workspace
-    assert call(None, 1, 1, 8, 1, 0, 0, ctypes.byref(n)) == lf.LF_ERR_ARG
-    assert call(ctypes.byref(pages()), 1, 1, 8, 1, 0, 0, None) == lf.LF_ERR_ARG
-    assert call(ctypes.byref(pages()), 1, 1, 8, -1, 0, 0, ctypes.byref(n)) == lf.LF_ERR_ARG
-    assert call(ctypes.byref(pages()), 1, 1, 24, 1, 0, 0, ctypes.byref(n)) == lf.LF_ERR_UNSUPPORTED
-    assert call(ctypes.byref(pages()), 1, 1, 8, 0, 0, 0, ctypes.byref(n)) == lf.LF_OK and n.value == 0
+    assert call(None, 1, 1, 8, 1, 1, 0, 0, ctypes.byref(n)) == lf.LF_ERR_ARG
+    assert call(ctypes.byref(pages()), 1, 1, 8, 1, 1, 0, 0, None) == lf.LF_ERR_ARG
+    assert call(ctypes.byref(pages()), 1, 1, 8, 1, -1, 0, 0, ctypes.byref(n)) == lf.LF_ERR_ARG
+    assert call(ctypes.byref(pages()), 1, 1, 8, 1, 2, 0, 0, ctypes.byref(n)) == lf.LF_ERR_ARG
+    assert call(ctypes.byref(pages()), 1, 1, 24, 1, 1, 0, 0, ctypes.byref(n)) == lf.LF_ERR_UNSUPPORTED
+    assert call(ctypes.byref(pages()), 1, 1, 8, 1, 0, 0, 0, ctypes.byref(n)) == lf.LF_OK and n.value == 0
 
 
 def test_bad_decode_calls_are_refused(lib):
