@@ -24,6 +24,13 @@
 //     depend on which finished first.
 // Where a unit is too short for a cut to pay, a CTA takes a whole unit and there
 // is no second launch.
+//
+// Measured, bf16, 32 / 8 heads of 128, and share of a plain copy's 6.69 TB/s: 64 sequences of
+// 3276 tokens 138 us, 93 %; 256 of 64 to 3276 281 us, 93 %; two of 100 to 130 thousand 157 us,
+// 95 %; a window of 1000 and 4 sinks of 64 sequences 53 us, 74 %: about 9 us of a launch are
+// the first copies' latency and the last tiles, and the join, 5 us, waits for them.
+// One sequence of 300 tokens takes 9 us on the device, most of it three round trips to
+// memory: lengths, page indexes, keys.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -701,7 +708,8 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) paged_decode_kernel(const _
 // Block (w, h) joins head h of the unit that CTA w + 1's range starts inside, if
 // that is the first range that does: the last part of CTA w, then the first ones
 // of CTAs w + 1, w + 2, .. while they start inside the same unit.  Its warps take
-// the parts in turn and join through shared memory.
+// the parts in turn and join through shared memory.  Bound by latency: 5 us, part of
+// which passes while the first kernel drains.
 constexpr int kJoinWarps = 8;
 
 template <typename T, int D, int G>

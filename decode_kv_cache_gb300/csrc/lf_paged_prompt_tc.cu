@@ -27,6 +27,16 @@
 //
 // Rounding P to bf16 (half a step is 2^-8 of a weight) is what the tensor cores
 // take; a second product for the remainder would double the P V work.
+//
+// Bound by the MMAs and by what keeps them waiting.  Both query tiles'
+// products with a key tile are 2048 clocks of the tensor cores; a CTA takes 2700, 2590 with the
+// softmax left out.
+// Around its key tiles a CTA spends about 10 thousand clocks: barriers, lookups and
+// the first tiles' way in, the rows' way out, the next launch on the SM, and with one CTA per SM (all
+// of the tensor memory, 200 KB) nothing runs meanwhile.  Measured, bf16, heads of 128: one prompt of
+// 8192 tokens, 32 / 8 heads, 354 us, 1.55 PFLOP/s, 81 % of the library's dense product; 12000
+// with a window of 1000, 16 / 8 heads, 120 us; chunks of 1 to 512 of 24 sequences behind up
+// to 2048, 32 / 8 heads, 139 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
