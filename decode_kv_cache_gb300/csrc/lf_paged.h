@@ -63,8 +63,8 @@ struct PagedPromptArgs {
 // head of the group) of one KV head's queries of one sequence.  The host knows neither
 // the sequences' rows nor their sum, only bounds, so that some numbers name no piece and
 // their blocks end at once: either every sequence has as many as max_q rows need
-// (tiles_per_seq), or sequence b's start at b + (rows before it) / (a piece's rows), which
-// leaves at most one number of a sequence without a piece.
+// (tiles_per_seq), or the numbers follow the rows (locate), with at most one more than pieces
+// for each sequence.
 struct PromptPlan {
   enum { kTensor, kMatrix, kFma } kernel;
   int rows, splits, tiles_per_seq;
@@ -107,10 +107,10 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
 
 // Numbers of the pieces of `rows` rows, of all KV heads; *tiles_per_seq as in PromptPlan.
 // Numbers that follow the rows need a search of the row starts, and a sequence's pieces come
-// together instead of all sequences' longest ones first, so they have to be a third fewer.
+// together instead of all sequences' last ones first, so they have to be a third fewer.
 // (32 / 8 heads of 128, bf16, each against following: one chunk of 512 among 255 single
 // tokens behind 1000, 412 us, 285; one prompt of 8192 among 31, 795, 517; chunks of 1 to 512
-// behind up to 2048, 153, 147; three fp32 prompts of 500 to 1000, 61, 67.)
+// behind up to 2048, 153, 139; three fp32 prompts of 500 to 1000, 61, 67.)
 inline int64_t paged_prompt_pieces(const PagedPool& pool, int group, int total_q, int max_q, int rows,
                                    bool may_follow, int* tiles_per_seq) {
   auto pieces = [&](int64_t tokens) { return (tokens * group + rows - 1) / rows; };

@@ -48,7 +48,9 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = blockIdx.y;
   Piece p;
-  if (!take_piece(a, blockIdx.x, locate(a, blockIdx.x), kMmaRows, tid == 0 && share == 0, &p)) return;
+  int number;
+  const int b = locate(a, blockIdx.x, &number);
+  if (!take_piece(a, blockIdx.x, b, number, kMmaRows, tid == 0 && share == 0, &p)) return;
   const Tiles tiles(a, p.p_lo, p.p_hi, kKeys, share);
   const int nt = tiles.count();
   const uint32_t ring = smem_u32(smem);
@@ -450,7 +452,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_prompt_join_kernel(cons
   const int rr = (int)(i % per_piece);
   Piece p;
   const unsigned id = (unsigned)(i / per_piece);
-  if (!take_piece(a, id, locate(a, id), per_piece, false, &p) || p.r0 + rr >= p.rows) return;
+  int number;
+  const int b = locate(a, id, &number);
+  if (!take_piece(a, id, b, number, per_piece, false, &p) || p.r0 + rr >= p.rows) return;
   const int64_t part = p.id * a.splits * per_piece + rr;   // share s: + s * per_piece
   float m = kNegInf, l = 0.f;
   if (lane < a.splits) {

@@ -36,7 +36,7 @@
 // of the tensor memory, 200 KB) nothing runs meanwhile.  Measured, bf16, heads of 128: one prompt of
 // 8192 tokens, 32 / 8 heads, 354 us, 1.55 PFLOP/s, 81 % of the library's dense product; 12000
 // with a window of 1000, 16 / 8 heads, 120 us; chunks of 1 to 512 of 24 sequences behind up
-// to 2048, 32 / 8 heads, 139 us.
+// to 2048, 32 / 8 heads, 132 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform for the compiler too
   const int G = a.group, gs = ta.group_shift;
-  const int b = locate(a, blockIdx.x);
+  int number;
+  const int b = locate(a, blockIdx.x, &number);
 
   // The loader's lookups for the first key tile, before it is known whether that is
   // tile 0 (it is unless a window without sinks starts behind it).
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_prompt_tc_kernel(const __
     if (pi < a.pool.max_pages) guess = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
   }
   Piece piece;
-  if (!take_piece(a, blockIdx.x, b, 2 * kTile, tid == kRestWarp * 32 && blockIdx.y == 0, &piece)) return;
+  if (!take_piece(a, blockIdx.x, b, number, 2 * kTile, tid == kRestWarp * 32 && blockIdx.y == 0, &piece)) return;
   const int g = piece.g, q0 = piece.q0, first_pos = piece.first_pos, p_lo = piece.p_lo, p_hi = piece.p_hi;
   const int64_t r0 = piece.r0, rows = piece.rows;
   const Tiles tiles(a, p_lo, p_hi, kTile, blockIdx.y);
