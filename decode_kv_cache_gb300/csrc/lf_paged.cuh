@@ -193,7 +193,7 @@ __device__ __forceinline__ bool take_piece(const PagedPromptArgs& a, unsigned id
 
 // The same where every sequence has as many numbers (tiles_per_seq > 0), for the fp32 kernel,
 // which the search before its loop makes slower (8 heads of 64, one prompt of 2000 tokens: 135 us,
-// with it 143; 24 of 1 to 200 behind up to 2048: 29, 35).
+// with it 143; 24 prompts of 1 to 200: 29, 35).
 __device__ __forceinline__ bool take_piece_level(const PagedPromptArgs& a, int head, int tile, int per_piece, bool tell,
                                                  Piece* p) {
   p->id = (int64_t)(a.tiles_per_seq - 1 - tile) * a.pool.batch * a.pool.kv_heads + head;
