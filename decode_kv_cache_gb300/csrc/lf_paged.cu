@@ -23,11 +23,19 @@ namespace {
 // block takes `tokens_per_block` consecutive tokens: one warp's lanes look up
 // where each goes (sequence by a search of new_start, page, slot), then all
 // threads copy 16-byte chunks, K and V of the same chunk together, four chunks
-// of each in flight per thread.  (8 x 128 bf16: 32 prompts, 324 MB moved, 53.5 us, 6.05 TB/s,
+// of each in flight per thread (also of tokens that are not stored: the loads do not
+// wait for the lookup).  Tokens find their sequence by starts in order, and one whose
+// starts are wrong may have no token that finds it, so that the first threads of the
+// grid look at the sequences themselves.  (8 x 128 bf16: 32 prompts, 324 MB moved, 53.5 us, 6.05 TB/s,
 // 90 % of a plain copy's rate; one token of 64 sequences 5 us on the device.)
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendMaxTokens = 32;
+
+// Are a sequence's rows not rows of the call?
+__device__ __forceinline__ bool wrong_starts(const PagedAppendArgs& a, int first, int end) {
+  return first < 0 || end < first || end > a.total_new;
+}
 
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
   __shared__ int64_t dst[kAppendMaxTokens];  // byte offset of the token's rows, -1: not stored
@@ -48,8 +56,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
       b = lo;
       first = a.new_start[b];
       const int end = a.new_start[b + 1];
-      n = end - first;
-      mine = t >= first && t < end;   // rows behind the last sequence belong to none
+      // rows behind the last sequence belong to none, and those of wrong starts are left out
+      mine = !wrong_starts(a, first, end) && t >= first && t < end;
+      n = mine ? end - first : 0;
     }
     int64_t off = -1;
     if (mine) {
@@ -69,6 +78,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     }
     dst[tid] = off;
   }
+  if (a.new_start && a.pool.err)
+    for (int64_t b = (int64_t)blockIdx.x * kAppendThreads + tid; b < a.pool.batch; b += (int64_t)gridDim.x * kAppendThreads)
+      if (wrong_starts(a, a.new_start[b], a.new_start[b + 1])) atomicOr(a.pool.err, LF_DEVERR_STATE);
   __syncthreads();
   const unsigned per_head = (unsigned)a.row_bytes >> 4;
   const unsigned per_token = per_head * a.pool.kv_heads;

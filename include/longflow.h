@@ -386,7 +386,8 @@ int lf_prefill_fill_noalloc(const lf_layout* dst, int layer, const void* k, cons
  * LF_DEVERR_STATE for a page index outside [0, num_pages), a length outside [0,
  * max_pages * page_size] or row starts outside the rows (such tokens are not
  * stored or read as zeros; outputs of that sequence are unspecified, no other is
- * touched) or that decrease (outputs of the call are unspecified),
+ * touched) or that decrease (outputs of the call, and what it stores of sequences
+ * whose rows overlap, are unspecified),
  * LF_DEVERR_NONFINITE for a softmax sum that is not finite, LF_DEVERR_TIMEOUT for
  * an expired on-chip wait (that call's outputs are unspecified).  The caller reads
  * and clears the word.
@@ -418,8 +419,9 @@ typedef struct lf_pages {
  * Write a call's new tokens to their pages.  Sequence b's tokens are rows
  * new_start[b] .. new_start[b + 1] - 1 of k_new and v_new
  * [total_new][kv_heads][head_dim] (contiguous, 16-byte aligned), its last ones:
- * the first of n goes to position lens[b] - n.  Rows from new_start[batch] on
- * belong to no sequence and are not read.  new_start [batch + 1] may be NULL: one
+ * the first of n goes to position lens[b] - n, and those that a length has no place
+ * for are left out one by one.  Rows in front of new_start[0] and from
+ * new_start[batch] on belong to no sequence and are not stored.  new_start [batch + 1] may be NULL: one
  * token for each sequence, total_new = batch.  A page that is written belongs to
  * one sequence of the call.
  */
