@@ -212,15 +212,25 @@ __device__ __forceinline__ int64_t row_of(const PagedPromptArgs& a, const Piece&
   return (p.q0 + r / a.group) * a.q_heads + p.g * a.group + r % a.group;
 }
 
-// Byte offset in the pools of the piece's position `pos`, -1: nothing to read.
-__device__ __forceinline__ int64_t offset_of(const PagedPromptArgs& a, const Piece& p, int pos) {
+// Positions `sinks` .. this - 1 lie behind the window of every query from p_lo on: nothing there
+// reaches an output, and the caller may have given the pages back.
+__device__ __forceinline__ int behind_window(const PagedPromptArgs& a, int p_lo) {
+  return a.window > 0 ? max(p_lo, 0) - a.window + 1 : 0;
+}
+
+// Byte offset in the pools of the piece's position `pos`, -1: nothing to read.  kSkip: nor where no
+// row of the piece sees it (from `sinks` to behind() - 1), for the kernel that would find what is not
+// finite there; others ask only before they report an entry that is no page.
+template <bool kSkip, class Behind>
+__device__ __forceinline__ int64_t offset_of(const PagedPromptArgs& a, const Piece& p, int pos, Behind behind) {
   if (pos > p.p_hi) return -1;
   int pi, slot;
   paged_split(a.pool, pos, &pi, &slot);
   const int page = a.pool.table[(int64_t)p.b * a.pool.max_pages + pi];
-  if (page >= 0 && page < a.pool.num_pages)
+  auto unseen = [&] { return pos >= a.sinks && pos < behind(); };
+  if (page >= 0 && page < a.pool.num_pages && !(kSkip && unseen()))
     return page * a.pool.page_stride + slot * a.pool.token_stride + p.g * a.pool.head_stride;
-  if (a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+  if (a.pool.err && !unseen()) atomicOr(a.pool.err, LF_DEVERR_STATE);
   return -1;
 }
 
@@ -297,7 +307,7 @@ __device__ __forceinline__ void row_by_hand(const PagedPromptArgs& a, const Piec
     const int k0 = tiles.at(j) * size;
     for (int key = k0; key < k0 + size; ++key) {
       if (!sees(a, pos, key)) continue;
-      const int64_t off = offset_of(a, p, key);
+      const int64_t off = offset_of<false>(a, p, key, [] { return 0; });
       if (off < 0) continue;
       const T* k = reinterpret_cast<const T*>(a.pool.k + off) + lane * E;
       const T* v = reinterpret_cast<const T*>(a.pool.v + off) + lane * E;

@@ -35,7 +35,7 @@ constexpr int kKeys = 64;
 // A operands, S comes out as the C operand whose layout is the A operand of P.V, so P
 // (rounded to bf16: half a step is 2^-8 of a weight) never leaves the registers either.
 // Bound by these instructions' rate, 600 TFLOP/s here, and the softmax between them: 8192
-// tokens in pages of 24, 32 / 8 heads of 128, 2.0 ms, 275 TFLOP/s; 2000 tokens, heads of 32, 45 us.
+// tokens in pages of 24, 32 / 8 heads of 128, 1.65 ms, 334 TFLOP/s; 2000 tokens, heads of 32, 43 us.
 
 constexpr int kMmaThreads = 128, kMmaRows = 64;
 
@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __g
   const uint32_t ring = smem_u32(smem);
 
   auto look_up = [&](int j) {
-    if (tid < kKeys) s_off[j & 1][tid] = offset_of(a, p, tiles.at(j) * kKeys + tid);
+    if (tid < kKeys)
+      s_off[j & 1][tid] = offset_of<true>(a, p, tiles.at(j) * kKeys + tid, [&] { return behind_window(a, p.p_lo); });
   };
   auto issue = [&](int j) {
     const uint32_t kd = ring + (j & 1) * 2 * kTileBytes, vd = kd + kTileBytes;
@@ -271,8 +272,14 @@ __global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __gr
   const Tiles tiles(a, p.p_lo, p.p_hi, kKeys, share);
   const int nt = tiles.count();
 
+  // (From shared memory for an entry that is no page: worked out there from the piece it costs
+  // the loop 2 to 5 % by its registers.  Every thread that looks up has written it.)
+  __shared__ int s_behind;
+  if (tid < kKeys) s_behind = behind_window(a, p.p_lo);
   auto look_up = [&](int j) {
-    if (tid < kKeys) s_off[tid] = offset_of(a, p, tiles.at(j) * kKeys + tid);
+    if (tid < kKeys)
+      s_off[tid] = offset_of<false>(a, p, tiles.at(j) * kKeys + tid,
+                                    [&] { return *const_cast<const volatile int*>(&s_behind); });
   };
   auto issue = [&](float* dst, const char* pool) {
 #pragma unroll 4

@@ -399,7 +399,9 @@ int lf_prefill_fill_noalloc(const lf_layout* dst, int layer, const void* k, cons
  * query that sees nothing gives zeros and a log-sum-exp of -inf.  lse may be
  * NULL.  Softmax statistics and sums are fp32, outputs are rounded once (RNE).
  * Values of tokens behind a sequence's end or outside the window never reach an
- * output, whatever they hold (NaN included).
+ * output, whatever they hold (NaN included).  Pages all of whose positions lie behind
+ * the window of every query of the call, and not below `sinks`, are not looked up: the
+ * caller may have given them away, and their entries need not be pages.
  *
  * Calls are stream-ordered, run on the current device, allocate nothing, do not
  * synchronise the host and can be captured in a CUDA graph.

@@ -64,3 +64,57 @@ def test_append_row_starts_of_more_sequences_than_threads():
     p = Paged("bf16", 1, 16, 4, [9] * 1000, seed=4)
     assert append_and_compare(p, [0] * 1000 + [5], 4, []) == lf.LF_DEVERR_STATE
     assert append_and_compare(p, [0] * 1000 + [4], 4, [999]) == 0
+
+
+# ---- prompt: pages behind the window --------------------------------------------------------------
+
+@pytest.mark.parametrize("window,sinks", [(100, 4), (1, 0), (64, 0), (130, 140), (700, 1)])
+@pytest.mark.parametrize("kind,d,page", [("bf16", 128, 16), ("bf16", 64, 64), ("bf16", 128, 256), ("bf16", 128, 8),
+                                         ("bf16", 32, 16), ("bf16", 128, 24), ("f32", 64, 16), ("f32", 128, 16)])
+def test_prompt_positions_that_no_query_sees(kind, d, page, window, sinks):
+    """A caller gives the pages behind the window back: their entries are no pages any more, and the
+    places that are left behind in pages that it keeps hold NaN.  The results do not change by a bit (so
+    nothing was computed again because of a NaN), and there is no error."""
+    old, new = [900, 0, 1000, 300, 1500], [60, 20, 1, 150, 300]
+    lens = [a + b for a, b in zip(old, new)]
+    p = Paged(kind, 2, d, page, lens, seed=page + window)
+    st = starts(new)
+    q = p.randn(st[-1], 4, d)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device="cuda")
+    args = (p.table, p.t_lens, ints(st), max(new), window, sinks)
+    before = p.cache.prompt(0, q, *args, lse=lse)
+    before_lse = lse.clone()
+    gone = 0
+    for b in range(len(lens)):
+        lo, hi = sinks, old[b] - window + 1          # positions lo .. hi - 1: seen by none
+        if lo < hi:
+            p.hide(b, lo, hi)
+        for i in range(p.width):
+            if lo <= i * page and (i + 1) * page <= hi:
+                p.table[b, i] = -1
+                gone += 1
+    assert gone > 0
+    out = p.cache.prompt(0, q, *args, lse=lse)
+    assert p.cache.check() == 0
+    assert torch.equal(out, before) and torch.equal(lse, before_lse)
+    for b in range(len(lens)):
+        rows = slice(st[b], st[b + 1])
+        p.check(b, q[rows], old[b], out[rows], lse[rows], window, sinks, weight_step(kind))
+
+
+@pytest.mark.parametrize("kind,d,page", [("bf16", 128, 16), ("bf16", 32, 16), ("f32", 64, 16)])
+def test_prompt_positions_that_no_query_sees_with_shared_keys(kind, d, page):
+    """The same where several blocks share the keys of few rows."""
+    n, rows, window, sinks = 6000, 5, 3000, 20
+    p = Paged(kind, 1, d, page, [n], seed=d)
+    assert lf.lf_paged_prompt_workspace(p.cache._pages[0], 1, p.width, 2, rows, rows, window, sinks) > 0
+    q, st = p.randn(rows, 2, d), ints([0, rows])
+    before = p.cache.prompt(0, q, p.table, p.t_lens, st, rows, window, sinks)
+    hi = n - rows - window + 1
+    p.hide(0, sinks, hi)
+    for i in range(p.width):
+        if sinks <= i * page and (i + 1) * page <= hi:
+            p.table[0, i] = -1
+    out = p.cache.prompt(0, q, p.table, p.t_lens, st, rows, window, sinks)
+    assert p.cache.check() == 0 and torch.equal(out, before)
+    p.check(0, q, n - rows, out, None, window, sinks, weight_step(kind))
