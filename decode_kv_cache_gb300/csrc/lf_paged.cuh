@@ -158,6 +158,7 @@ __device__ __forceinline__ bool take_rows(const PagedPromptArgs& a, int tile, in
   const int len = paged_len(a.pool, p->b);
   p->r0 = (int64_t)tile * per_piece;
   p->rows = (int64_t)n * a.group;
+  if (n > a.max_q) p->rows = (int64_t)a.max_q * a.group;   // the rest is left
   if (p->r0 >= p->rows) return false;
   p->first_pos = len - n;      // may be negative: those rows see nothing
   p->p_lo = p->first_pos + (int)(p->r0 / a.group);

@@ -35,12 +35,14 @@ constexpr int kKeys = 64;
 // A operands, S comes out as the C operand whose layout is the A operand of P.V, so P
 // (rounded to bf16: half a step is 2^-8 of a weight) never leaves the registers either.
 // Bound by these instructions' rate, 600 TFLOP/s here, and the softmax between them: 8192
-// tokens in pages of 24, 32 / 8 heads of 128, 1.65 ms, 334 TFLOP/s; 2000 tokens, heads of 32, 43 us.
+// tokens in pages of 24, 32 / 8 heads of 128, 1.61 ms, 341 TFLOP/s; 2000 tokens, heads of 32, 43 us.
 
 constexpr int kMmaThreads = 128, kMmaRows = 64;
 
+// Three blocks of heads of 128 on an SM: a few registers more than that leaves make it two (pages of
+// 24: 1.61 ms against 1.97 to 2.15).
 template <int D>
-__global__ void __launch_bounds__(kMmaThreads) paged_prompt_mma_kernel(const __grid_constant__ PagedPromptArgs a) {
+__global__ void __launch_bounds__(kMmaThreads, D == 128 ? 3 : D >= 32 ? 4 : 5) paged_prompt_mma_kernel(const __grid_constant__ PagedPromptArgs a) {
   constexpr int NC = D / 8;                // 16-byte chunks of a row
   constexpr int kTileBytes = kKeys * NC * 16;
   extern __shared__ __align__(128) unsigned char smem[];

@@ -461,7 +461,8 @@ int lf_paged_decode_workspace(const lf_pages* pages, int batch, int max_pages, i
  * the first of n is at position lens[b] - n.  Rows from q_start[batch] on are left as
  * they are.
  *   q_start   device [batch + 1]
- *   max_q     no sequence has more rows (more: LF_DEVERR_STATE, the rest is left)
+ *   max_q     no sequence has more rows, 0 <= max_q <= total_q (of a sequence with more
+ *             rows the first max_q are computed and the rest is left: LF_DEVERR_STATE)
  *   lse       fp32 [total_q][q_heads], or NULL
  *   workspace lf_paged_prompt_workspace bytes, as lf_paged_decode's
  * Up to two launches: the keys of few rows are shared by several blocks and joined.

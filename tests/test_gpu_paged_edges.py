@@ -118,3 +118,40 @@ def test_prompt_positions_that_no_query_sees_with_shared_keys(kind, d, page):
     out = p.cache.prompt(0, q, p.table, p.t_lens, st, rows, window, sinks)
     assert p.cache.check() == 0 and torch.equal(out, before)
     p.check(0, q, n - rows, out, None, window, sinks, weight_step(kind))
+
+
+# ---- prompt: the bound on a sequence's rows ------------------------------------------------------
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 64), ("bf16", 32), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("others", [2, 20, 50])
+def test_prompt_rows_behind_the_bound_are_left(kind, d, others):
+    """A sequence with more rows than max_q: the rows up to max_q are computed, the rest is left and
+    reported.  (2, 20 and 50 other sequences: the three ways in which pieces are numbered.)"""
+    most = 201
+    new = [300] + [1] * others + [201]
+    old = [0] + [i % 30 for i in range(others)] + [5]
+    lens = [a + b for a, b in zip(old, new)]
+    p = Paged(kind, 2, d, 16, lens, seed=d + others)
+    st = starts(new)
+    q = p.randn(st[-1], 8, d)
+    out = torch.full_like(q, 3.0)
+    lse = torch.full(q.shape[:2], 3.0, dtype=torch.float32, device="cuda")
+    p.cache.prompt(0, q, p.table, p.t_lens, ints(st), most, out=out, lse=lse)
+    assert p.cache.check() == lf.LF_DEVERR_STATE
+    assert (out[most:300] == 3).all() and (lse[most:300] == 3).all()
+    for b in range(len(lens)):
+        rows = slice(st[b], min(st[b] + most, st[b + 1]))
+        p.check(b, q[rows], old[b], out[rows], lse[rows], weight_step=weight_step(kind))
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 32), ("f32", 64)])
+def test_prompt_rows_behind_the_bound_with_shared_keys(kind, d):
+    p = Paged(kind, 2, d, 16, [5000, 4000], seed=d)
+    assert lf.lf_paged_prompt_workspace(p.cache._pages[0], 2, p.width, 8, 8, 3) > 0
+    q, st = p.randn(8, 8, d), ints([0, 5, 8])
+    out = torch.full_like(q, 3.0)
+    p.cache.prompt(0, q, p.table, p.t_lens, st, 3, out=out)
+    assert p.cache.check() == lf.LF_DEVERR_STATE
+    assert (out[3:5] == 3).all()
+    p.check(0, q[:3], 4995, out[:3], None, weight_step=weight_step(kind))
+    p.check(1, q[5:], 3997, out[5:], None, weight_step=weight_step(kind))
