@@ -615,7 +615,8 @@ class LFPagedCache:
     def prompt(self, layer, q, page_table, lens, q_start, max_q, window=0, sinks=0, out=None, lse=None,
                stream=None):
         """lf_paged_prompt: q [rows][q_heads][head_dim] -> out of that shape; q_start int32
-        [batch + 1], max_q at least every sequence's number of rows."""
+        [batch + 1], max_q at least every sequence's number of rows (a chunk limit, say: what is
+        larger than the call's rows counts as these)."""
         pages = self._layer(layer)
         batch, width = self._sequences(page_table, lens)
         rows, q_heads, _ = self._sizes(q, "q", 3)
@@ -623,7 +624,7 @@ class LFPagedCache:
         self._expect(q_start, "q_start", torch.int32, (batch + 1,))
         self._outputs(q, out, lse)
         return self._run(stream, self._prompt, pages, batch, width, q_heads, page_table, lens, q, q_start,
-                         rows, max_q, out, lse, window, sinks)
+                         rows, min(max_q, rows), out, lse, window, sinks)
 
     def _prompt(self, st, pages, batch, width, q_heads, page_table, lens, q, q_start, rows, max_q, out, lse,
                 window, sinks):

@@ -155,3 +155,18 @@ def test_prompt_rows_behind_the_bound_with_shared_keys(kind, d):
     assert (out[3:5] == 3).all()
     p.check(0, q[:3], 4995, out[:3], None, weight_step=weight_step(kind))
     p.check(1, q[5:], 3997, out[5:], None, weight_step=weight_step(kind))
+
+
+def test_prompt_takes_a_bound_that_is_wider_than_the_call():
+    """max_q is a bound: one that is larger than the call's rows, as a chunk limit is, changes nothing."""
+    p = Paged("bf16", 2, 128, 16, [90, 40], seed=8)
+    q, st = p.randn(50, 8, 128), ints([0, 30, 50])
+    a = p.cache.prompt(0, q, p.table, p.t_lens, st, 30)
+    for most in (50, 51, 512, 2**31 - 1, 2**40):
+        b = p.cache.prompt(0, q, p.table, p.t_lens, st, most)
+        p.check(0, q[:30], 60, b[:30], None, weight_step=2.0 ** -8)
+        p.check(1, q[30:], 20, b[30:], None, weight_step=2.0 ** -8)
+        assert torch.equal(a, b)
+    assert p.cache.check() == 0
+    none = p.cache.prompt(0, q[:0], p.table, p.t_lens, ints([0, 0, 0]), 512)
+    assert none.shape == (0, 8, 128)
