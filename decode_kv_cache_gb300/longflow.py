@@ -473,6 +473,10 @@ class LFPagedCache:
     tensors that the caller owns, of that shape in any stride order with contiguous rows.  The
     caller hands out pages: ``page_table`` int32 ``[batch][max_pages]`` and ``lens`` int32
     ``[batch]`` (lengths including the call's own tokens) are contiguous tensors on the device.
+
+    Calls run on the current stream, or on ``stream`` (a torch stream or a raw handle), which the
+    caller orders behind the stream that made the inputs.  What a call returns belongs to the stream
+    that it ran on.
     """
 
     def __init__(self, layers, num_pages, page_size, kv_heads, head_dim, dtype="bf16", device=None):
@@ -550,12 +554,17 @@ class LFPagedCache:
 
     def _run(self, stream, call, *args):
         """call(stream handle, *args) with this cache's device and `stream` current, so that
-        what it allocates belongs to that stream."""
+        what it allocates belongs to that stream.  The allocator is told that a stream which the caller
+        names reads the tensors: they may be let go as soon as the call returns."""
         if stream is None and torch.cuda.current_device() == self._index:
             return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
         with torch.cuda.device(self._index), torch.cuda.stream(stream):
+            if stream is not None:
+                for t in (self.k, self.v, self.err, *args):
+                    if isinstance(t, torch.Tensor):
+                        t.record_stream(stream)
             return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
 
     def _ask(self, call, pages, key):

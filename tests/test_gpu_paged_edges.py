@@ -170,3 +170,107 @@ def test_prompt_takes_a_bound_that_is_wider_than_the_call():
     assert p.cache.check() == 0
     none = p.cache.prompt(0, q[:0], p.table, p.t_lens, ints([0, 0, 0]), 512)
     assert none.shape == (0, 8, 128)
+
+
+# ---- streams ------------------------------------------------------------------------------------
+
+def busy(stream=None, clocks=100_000_000):
+    """About 50 ms of work in front of what follows on the stream."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(clocks)
+
+
+def test_a_stream_handle_of_zero_is_the_default_stream():
+    """torch.cuda.default_stream().cuda_stream is 0: a call with it comes behind the default stream's work."""
+    p = Paged("bf16", 8, 128, 16, [3000, 50], seed=60)
+    real, st = p.randn(2, 32, 128), ints([0, 1, 2])
+    want = p.cache.decode(0, real, p.table, p.t_lens)
+    want_prompt = p.cache.prompt(0, real, p.table, p.t_lens, st, 1)
+    q = torch.zeros_like(real)
+    torch.cuda.synchronize()
+    assert torch.cuda.default_stream().cuda_stream == 0
+    busy()
+    q.copy_(real)
+    got = p.cache.decode(0, q, p.table, p.t_lens, stream=torch.cuda.default_stream().cuda_stream)
+    got_prompt = p.cache.prompt(0, q, p.table, p.t_lens, st, 1, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_prompt, want_prompt)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):      # and not the current one
+        busy()
+        q.zero_()
+        got = p.cache.decode(0, real, p.table, p.t_lens, stream=0)
+    torch.cuda.default_stream().synchronize()
+    assert torch.equal(got.clone(), want)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_tensors_that_are_let_go_while_another_stream_reads_them(handle):
+    """A call on a stream of the caller's, with tensors that the caller drops as soon as it returns: memory
+    that the stream still has to read is not handed out again."""
+    p = Paged("bf16", 8, 128, 16, [3000, 50], seed=61)
+    real, st = p.randn(2, 32, 128), ints([0, 1, 2])
+    kn, vn = p.randn(2, 8, 128), p.randn(2, 8, 128)
+    want_d = p.cache.decode(0, real, p.table, p.t_lens, kn, vn)
+    want_p = p.cache.prompt(0, real, p.table, p.t_lens, st, 1)
+    want_k = p.k.clone()
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if handle else side
+
+    def dropped(call):
+        """call's inputs as copies that nobody holds afterwards; their places are overwritten."""
+        torch.cuda.synchronize()
+        busy(side)
+        mine = [x.clone() for x in (real, kn, vn, p.table, p.t_lens, st)]
+        torch.cuda.current_stream().synchronize()     # the copies are made; the side stream has not begun
+        shapes = [(x.shape, x.dtype) for x in mine]
+        got = call(*mine)
+        del mine
+        junk = [torch.full(shape, 1, dtype=t, device="cuda") for shape, t in shapes for _ in range(3)]
+        torch.cuda.synchronize()
+        del junk
+        return got
+
+    got = dropped(lambda q, k, v, t, n, i: p.cache.decode(0, q, t, n, k, v, stream=s))
+    assert torch.equal(got, want_d)
+    got = dropped(lambda q, k, v, t, n, i: p.cache.prompt(0, q, t, n, i, 1, stream=s))
+    assert torch.equal(got, want_p)
+    dropped(lambda q, k, v, t, n, i: p.cache.append(0, k, v, t, n, i, stream=s))
+    assert torch.equal(torch.nan_to_num(p.k, 77.0), torch.nan_to_num(want_k, 77.0))
+    assert p.cache.check() == 0
+
+
+def test_a_cache_that_is_let_go_while_another_stream_uses_it():
+    p = Paged("bf16", 8, 128, 16, [3000, 50], seed=65)
+    q = p.randn(2, 32, 128)
+    want = p.cache.decode(0, q, p.table, p.t_lens)
+    side = torch.cuda.Stream()
+    k, v = p.k.clone(), p.v.clone()
+    cache = lf.LFPagedCache.over(k[None], v[None])
+    torch.cuda.synchronize()
+    busy(side)
+    got = cache.decode(0, q, p.table, p.t_lens, stream=side)
+    shape = k.shape
+    del k, v, cache
+    junk = [torch.full(shape, 1, dtype=torch.bfloat16, device="cuda") for _ in range(6)]
+    torch.cuda.synchronize()
+    del junk
+    assert torch.equal(got, want)
+
+
+def test_a_named_stream_under_capture():
+    """A call that names the stream on which a graph is captured, replayed after its inputs' makers are gone."""
+    p = Paged("bf16", 2, 128, 16, [3000, 50], seed=66)
+    q, st = p.randn(2, 8, 128), ints([0, 1, 2])
+    want = p.cache.decode(0, q, p.table, p.t_lens), p.cache.prompt(0, q, p.table, p.t_lens, st, 1)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        a = p.cache.decode(0, q, p.table, p.t_lens, stream=side)
+        b = p.cache.prompt(0, q, p.table, p.t_lens, st, 1, stream=side)
+    for _ in range(3):
+        a.zero_(), b.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
