@@ -560,6 +560,8 @@ class LFPagedCache:
             return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
+        if stream is not None and getattr(stream, "device", None) != self.device:
+            raise LFError(LF_ERR_ARG, f"stream: expected a stream of {self.device}, got {stream}")
         with torch.cuda.device(self._index), torch.cuda.stream(stream):
             if stream is not None:
                 for t in (self.k, self.v, self.err, *args):

@@ -1,0 +1,26 @@
+"""Paged key-value cache on the CPU, at the edges of what its Python calls allow."""
+import types
+
+import pytest
+import torch
+
+from decode_kv_cache_gb300 import longflow as lf
+
+
+def cache_on(index):
+    """A cache's Python side without its pools."""
+    c = lf.LFPagedCache.__new__(lf.LFPagedCache)
+    c.device, c._index = torch.device("cuda", index), index
+    return c
+
+
+@pytest.mark.parametrize("stream", [types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=77),
+                                    types.SimpleNamespace(device=torch.device("cpu")), "side", 1.5],
+                         ids=["another device", "cpu", "text", "number"])
+def test_streams_that_are_not_of_the_device_are_refused(monkeypatch, stream):
+    """A call on a stream of another device would run on the cache's device, on a stream that nobody named."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    called = []
+    with pytest.raises(lf.LFError, match="stream: expected a stream of cuda:0"):
+        cache_on(0)._run(stream, called.append)
+    assert not called
