@@ -512,8 +512,9 @@ class LFPagedCache:
         self.layers, self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self._index = k.get_device()
         self._row = (self.kv_heads, self.head_dim)
-        # the device error word, as a tensor of one int32
-        self.err = torch.zeros(1, dtype=torch.int32, device=k.device)
+        # the device error word, as a tensor of one int32; copied from the host, which waits, so that
+        # no stream that uses the cache can come before it
+        self.err = torch.zeros(1, dtype=torch.int32).to(k.device)
         step, pk, pv = strides[0] * k.element_size(), k.data_ptr(), v.data_ptr()
         self._pages = [LFPages(types[k.dtype], self.kv_heads, self.head_dim, self.page_size, self.num_pages,
                                strides[1], strides[2], strides[3], pk + i * step, pv + i * step,

@@ -274,3 +274,25 @@ def test_a_named_stream_under_capture():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+# ---- the error word ---------------------------------------------------------------------------------
+
+def test_the_error_word_is_clear_before_any_stream_reads_it():
+    """A cache made on a busy stream and used on another one starts without errors and keeps its own."""
+    k = torch.zeros(1, 4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    v, table, lens = torch.zeros_like(k), ints([[-5]]), ints([3])
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    junk = [torch.full((1,), 0x7fff, dtype=torch.int32, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    del junk                               # the allocator hands their places out again
+    side = torch.cuda.Stream()
+    busy()
+    cache = lf.LFPagedCache.over(k, v)
+    assert cache.check(side) == 0
+    busy()
+    cache = lf.LFPagedCache.over(k, v)
+    cache.decode(0, q, table, lens, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert cache.check() == lf.LF_DEVERR_STATE
