@@ -115,7 +115,18 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
   }
 }
 
+// ---- the error word ------------------------------------------------------------
+//
+// Read and cleared in one step: bits that another stream sets meanwhile stay or are taken,
+// but are not lost.  One thread; bound by its launch.
+__global__ void paged_take_errors_kernel(int32_t* err, int32_t* taken) { *taken = atomicExch(err, 0); }
+
 }  // namespace
+
+cudaError_t paged_take_errors_launch(int32_t* err, int32_t* taken, cudaStream_t stream) {
+  paged_take_errors_kernel<<<1, 1, 0, stream>>>(err, taken);
+  return cudaGetLastError();
+}
 
 cudaError_t paged_append_launch(const PagedAppendArgs& a, cudaStream_t stream) {
   const int blocks = (int)(((int64_t)a.total_new + a.tokens_per_block - 1) / a.tokens_per_block);
@@ -419,6 +430,15 @@ int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table,
   const cudaError_t e = lf::paged_prompt_launch(a, plan, elem_bytes(pages), pages->head_dim,
                                                 static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LF_OK : cuda_fail(e, "paged prompt launch");
+}
+
+int lf_paged_take_errors(const lf_pages* pages, int32_t* taken, lf_stream_t stream) {
+  lf::clear_last_error();
+  if (!pages || !pages->err || !taken) return fail(LF_ERR_ARG, "null pages, error word or taken");
+  if ((reinterpret_cast<uintptr_t>(pages->err) | reinterpret_cast<uintptr_t>(taken)) & 3u)
+    return fail(LF_ERR_ARG, "the error word and taken must be 4-byte aligned");
+  const cudaError_t e = lf::paged_take_errors_launch(pages->err, taken, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LF_OK : cuda_fail(e, "paged take errors launch");
 }
 
 }  // extern "C"

@@ -121,6 +121,7 @@ inline int64_t paged_prompt_pieces(const PagedPool& pool, int group, int total_q
 }
 
 // Launches (one translation unit each).  They return the launch's error.
+cudaError_t paged_take_errors_launch(int32_t* err, int32_t* taken, cudaStream_t stream);
 cudaError_t paged_append_launch(const PagedAppendArgs& a, cudaStream_t stream);
 // elem: bytes of an element (2 bf16, 4 fp32).  `grid`: CTAs of the attention kernel.
 cudaError_t paged_decode_launch(const PagedDecodeArgs& a, int elem, int head_dim, int grid,

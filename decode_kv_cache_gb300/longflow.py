@@ -30,7 +30,7 @@ __all__ = [
     "lf_prefill_fill_noalloc", "lf_rkv_compress", "lf_launch_plan", "lf_launch_plan_for",
     "LFCache",
     "LFPages", "lf_paged_append", "lf_paged_decode", "lf_paged_decode_workspace", "lf_paged_prompt",
-    "lf_paged_prompt_workspace",
+    "lf_paged_prompt_workspace", "lf_paged_take_errors",
     "LFPagedCache",
 ]
 
@@ -149,6 +149,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                     ctypes.c_size_t, VP]
     lib.lf_paged_prompt_workspace.restype = I
     lib.lf_paged_prompt_workspace.argtypes = [PG, I, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
+    lib.lf_paged_take_errors.restype = I
+    lib.lf_paged_take_errors.argtypes = [PG, VP, VP]
     _lib = lib
     return lib
 
@@ -341,6 +343,10 @@ def lf_paged_prompt_workspace(pages: LFPages, batch, max_pages, q_heads, total_q
     _check(load_library().lf_paged_prompt_workspace(ctypes.byref(pages), batch, max_pages, q_heads,
                                                     total_q, max_q, window, sinks, ctypes.byref(n)))
     return int(n.value)
+
+
+def lf_paged_take_errors(pages: LFPages, taken, stream=None) -> int:
+    return _check(load_library().lf_paged_take_errors(ctypes.byref(pages), _ptr(taken), _stream(stream)))
 
 
 # ---- convenience owner ------------------------------------------------------
@@ -656,8 +662,7 @@ class LFPagedCache:
         """The device error bits since the last check (0 when clean); synchronises the stream."""
         return self._run(stream, self._take_bits)
 
-    def _take_bits(self, _):
-        bits = int(self.err.item())
-        if bits:
-            self.err.zero_()
-        return bits
+    def _take_bits(self, st):
+        taken = torch.empty_like(self.err)
+        _check(self._lib.lf_paged_take_errors(self._pages[0], taken.data_ptr(), st))
+        return int(taken.item())

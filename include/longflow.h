@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define LF_ABI_VERSION 7
+#define LF_ABI_VERSION 8
 
 typedef struct lf_cache lf_cache; /* opaque; owns the slab */
 
@@ -390,7 +390,7 @@ int lf_prefill_fill_noalloc(const lf_layout* dst, int layer, const void* k, cons
  * whose rows overlap, are unspecified),
  * LF_DEVERR_NONFINITE for a softmax sum that is not finite, LF_DEVERR_TIMEOUT for
  * an expired on-chip wait (that call's outputs are unspecified).  The caller reads
- * and clears the word.
+ * and clears the word (lf_paged_take_errors).
  *
  * Query head h reads KV head floor(h / G), G = q_heads / kv_heads in {1, 2, 4, 8};
  * head_dim in {16, 32, 64, 128}; logits are scaled by 1 / sqrt(head_dim).  With
@@ -476,6 +476,13 @@ int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table,
  * device; 0 when they need none. */
 int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int total_q,
                               int max_q, int window, int sinks, size_t* bytes);
+
+/*
+ * *taken = *pages->err and *pages->err = 0 in one step, so that what calls on other
+ * streams report at the same time is not lost: taken now, or by the next call.
+ * Stream-ordered; taken: device memory, read once the stream has come there.
+ */
+int lf_paged_take_errors(const lf_pages* pages, int32_t* taken, lf_stream_t stream);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* lf_last_error(void);

@@ -296,3 +296,25 @@ def test_the_error_word_is_clear_before_any_stream_reads_it():
     side.synchronize()
     torch.cuda.synchronize()
     assert cache.check() == lf.LF_DEVERR_STATE
+
+
+def test_errors_that_come_during_a_check_are_kept():
+    """While one stream's errors are read and cleared, another stream reports its own: each is seen once."""
+    p = Paged("bf16", 1, 64, 16, [40], seed=62)
+    q = p.randn(1, 4, 64)
+    bad_table, bad_q = p.table.clone(), q.clone()
+    bad_table[0, 1] = -1
+    bad_q[0, 0, 0] = math.nan
+    side, lost = torch.cuda.Stream(), 0
+    torch.cuda.synchronize()
+    for i in range(400):
+        p.cache.decode(0, q, bad_table, p.t_lens)                 # LF_DEVERR_STATE
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(500 * (i % 200))                    # up to some 50 us
+            p.cache.decode(0, bad_q, p.table, p.t_lens)           # LF_DEVERR_NONFINITE
+        bits = p.cache.check()
+        torch.cuda.synchronize()
+        bits |= p.cache.check()
+        lost += bits != lf.LF_DEVERR_STATE | lf.LF_DEVERR_NONFINITE
+    assert lost == 0 and p.cache.check() == 0

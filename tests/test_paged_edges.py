@@ -1,4 +1,5 @@
 """Paged key-value cache on the CPU, at the edges of what its Python calls allow."""
+import ctypes
 import types
 
 import pytest
@@ -24,3 +25,19 @@ def test_streams_that_are_not_of_the_device_are_refused(monkeypatch, stream):
     with pytest.raises(lf.LFError, match="stream: expected a stream of cuda:0"):
         cache_on(0)._run(stream, called.append)
     assert not called
+
+
+def test_taking_errors_from_nowhere_is_refused():
+    from decode_kv_cache_gb300 import build as b
+    b.build()
+    lib, p = lf.load_library(), lf.LFPages()
+    call = lambda: lib.lf_paged_take_errors(ctypes.byref(p), taken, None)  # noqa: E731
+    taken = 0x10000
+    assert lib.lf_paged_take_errors(None, taken, None) == lf.LF_ERR_ARG and "null" in lf.lf_last_error()
+    assert call() == lf.LF_ERR_ARG and "error word" in lf.lf_last_error()
+    p.err, taken = 0x20000, None
+    assert call() == lf.LF_ERR_ARG and "taken" in lf.lf_last_error()
+    taken = 0x10002
+    assert call() == lf.LF_ERR_ARG and "aligned" in lf.lf_last_error()
+    p.err, taken = 0x20001, 0x10000
+    assert call() == lf.LF_ERR_ARG and "aligned" in lf.lf_last_error()
