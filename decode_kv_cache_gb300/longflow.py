@@ -46,6 +46,8 @@ LF_SCOPE_KV_HEAD, LF_SCOPE_LAYER = 0, 1
 _SCOPE = {"kv_head": LF_SCOPE_KV_HEAD, "layer": LF_SCOPE_LAYER}
 LF_DEVERR_NONFINITE, LF_DEVERR_STATE, LF_DEVERR_TIMEOUT = 1, 2, 4
 
+_INT_MAX = 2**31 - 1   # of the C calls' numbers, of which ctypes would take the low bits of larger ones
+
 _DTYPE = {"bf16": LF_BF16, "f32": LF_F32}
 _TORCH_DTYPE = {LF_BF16: torch.bfloat16, LF_F32: torch.float32}
 
@@ -514,6 +516,8 @@ class LFPagedCache:
         strides = k.stride()
         if k.numel() == 0 or (k.shape[4] > 1 and strides[4] != 1):
             raise LFError(LF_ERR_ARG, "the pools must not be empty and their rows must be contiguous")
+        if max(k.shape) > _INT_MAX:
+            raise LFError(LF_ERR_ARG, f"pools {tuple(k.shape)}: no size may be above 2^31 - 1")
         self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
         self.layers, self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self._index = k.get_device()
@@ -552,6 +556,12 @@ class LFPagedCache:
         self._expect(page_table, "page_table", torch.int32, shape)
         self._expect(lens, "lens", torch.int32, shape[:1])
         return shape
+
+    def _numbers(self, rows, window=0, sinks=0, max_q=0):
+        if rows > _INT_MAX or max_q < 0:
+            raise LFError(LF_ERR_ARG, f"need at most 2^31 - 1 tokens and max_q >= 0, got {rows} and {max_q}")
+        if not 0 <= window <= _INT_MAX or not 0 <= sinks <= _INT_MAX:
+            raise LFError(LF_ERR_ARG, f"window and sinks must be in [0, 2^31 - 1], got {window} and {sinks}")
 
     def _outputs(self, q, out, lse):
         if out is not None:
@@ -593,6 +603,7 @@ class LFPagedCache:
         self._expect(v_new, "v_new", self.dtype, (n, *self._row))
         if new_start is not None:
             self._expect(new_start, "new_start", torch.int32, (batch + 1,))
+            self._numbers(n)
         self._run(stream, self._append, pages, batch, width, page_table, lens, k_new, v_new, new_start, n)
 
     def _append(self, st, pages, batch, width, page_table, lens, k_new, v_new, new_start, n):
@@ -611,6 +622,7 @@ class LFPagedCache:
         if k_new is not None or v_new is not None:
             self._expect(k_new, "k_new", self.dtype, (batch, *self._row))
             self._expect(v_new, "v_new", self.dtype, (batch, *self._row))
+        self._numbers(batch, window, sinks)
         self._outputs(q, out, lse)
         return self._run(stream, self._decode, pages, batch, width, q_heads, page_table, lens, q, k_new,
                          v_new, out, lse, window, sinks)
@@ -640,6 +652,7 @@ class LFPagedCache:
         rows, q_heads, _ = self._sizes(q, "q", 3)
         self._expect(q, "q", self.dtype, (rows, q_heads, self.head_dim))
         self._expect(q_start, "q_start", torch.int32, (batch + 1,))
+        self._numbers(rows, window, sinks, max_q)
         self._outputs(q, out, lse)
         return self._run(stream, self._prompt, pages, batch, width, q_heads, page_table, lens, q, q_start,
                          rows, min(max_q, rows), out, lse, window, sinks)

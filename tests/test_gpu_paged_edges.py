@@ -318,3 +318,35 @@ def test_errors_that_come_during_a_check_are_kept():
         bits |= p.cache.check()
         lost += bits != lf.LF_DEVERR_STATE | lf.LF_DEVERR_NONFINITE
     assert lost == 0 and p.cache.check() == 0
+
+
+# ---- numbers that the C calls cannot take ------------------------------------------------------------
+
+def test_numbers_that_do_not_fit_the_c_calls_are_refused():
+    """ctypes takes the low 32 bits of a number without a word: a window of 2^32 + 1 would be one of 1."""
+    p = Paged("bf16", 2, 128, 16, [100, 50], seed=63)
+    q, st = p.randn(2, 8, 128), ints([0, 1, 2])
+    c = p.cache
+    for bad in (2**31, 2**32, 2**32 + 1, -1, -2**32 + 1):
+        with pytest.raises(lf.LFError, match="window"):
+            c.decode(0, q, p.table, p.t_lens, window=bad)
+        with pytest.raises(lf.LFError, match="window"):
+            c.prompt(0, q, p.table, p.t_lens, st, 1, window=bad)
+        with pytest.raises(lf.LFError, match="sinks"):
+            c.decode(0, q, p.table, p.t_lens, window=4, sinks=bad)
+        with pytest.raises(lf.LFError, match="sinks"):
+            c.prompt(0, q, p.table, p.t_lens, st, 1, window=4, sinks=bad)
+    with pytest.raises(lf.LFError, match="max_q"):
+        c.prompt(0, q, p.table, p.t_lens, st, -2**32 + 1)
+    whole = c.decode(0, q, p.table, p.t_lens)
+    assert torch.equal(whole, c.decode(0, q, p.table, p.t_lens, window=2**31 - 1, sinks=2**31 - 1))
+
+
+def test_pools_with_more_pages_than_an_int_are_refused():
+    """2^32 + 1 pages (all the same one here) would be one page."""
+    k = torch.zeros(1, 1, 1, 1, 16, dtype=torch.bfloat16, device="cuda")
+    for n in (2**31, 2**32 + 1):
+        big = k.expand(1, n, 1, 1, 16)
+        with pytest.raises(lf.LFError, match="2\\^31 - 1"):
+            lf.LFPagedCache.over(big, big)
+    lf.LFPagedCache.over(k.expand(1, 2**31 - 1, 1, 1, 16), k.expand(1, 2**31 - 1, 1, 1, 16))
