@@ -376,7 +376,9 @@ int lf_prefill_fill_noalloc(const lf_layout* dst, int layer, const void* k, cons
  * long as every row starts on 16 bytes.  Row b of page_table [batch][max_pages]
  * lists the pages of sequence b in order of position: position p is slot
  * p % page_size of page page_table[b][p / page_size].  Sequences may share pages
- * that no call writes.  Entries past a sequence's last token are not read.
+ * that no call writes.  Entries past a sequence's last token may hold anything.  The
+ * host knows lengths by max_pages alone: a table much wider than its sequences gives
+ * the same results, but work is spread as if they were as long.
  *
  * lens[b] is sequence b's length INCLUDING the tokens of the call that gets it: all
  * layers of one step share one page table and one lens.  Lengths, tables and row
@@ -397,7 +399,10 @@ int lf_prefill_fill_noalloc(const lf_layout* dst, int layer, const void* k, cons
  * window = W > 0 the query at position p sees positions p - W + 1 .. p and the
  * positions below `sinks`; window = 0: all of 0 .. p (sinks must be 0 too).  A
  * query that sees nothing gives zeros and a log-sum-exp of -inf.  lse may be
- * NULL.  Softmax statistics and sums are fp32, outputs are rounded once (RNE).
+ * NULL.  Softmax statistics and sums are fp32, outputs are rounded once (RNE).  Of a
+ * bf16 cache lf_paged_prompt rounds each weight of a value to bf16 (half a step is 2^-8
+ * of it) before the product with the value, while their sum keeps it unrounded;
+ * lf_paged_decode keeps 16 bits of it, fp32 caches all.
  * Values of tokens behind a sequence's end or outside the window never reach an
  * output, whatever they hold (NaN included).  Pages all of whose positions lie behind
  * the window of every query of the call, and not below `sinks`, are not looked up: the
@@ -441,7 +446,10 @@ int lf_paged_append(const lf_pages* pages, int batch, const int32_t* page_table,
  *   workspace     lf_paged_decode_workspace bytes, 16-byte aligned, contents of no
  *                 meaning before and after the call; not shared by calls that may run
  *                 at the same time (two streams, two graphs)
- * Results do not depend on how the work is split.  Up to two launches.
+ * The same call (arguments, lengths, device) gives the same bits again.  A sequence
+ * alone, in another batch or under a wider table may differ in the last ones: where
+ * its keys are cut follows all lengths, max_pages and the device, and with it the order of
+ * its fp32 sums.  Up to two launches.
  */
 int lf_paged_decode(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
                     const int32_t* lens, int q_heads, const void* q, const void* k_new,

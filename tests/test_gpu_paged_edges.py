@@ -350,3 +350,73 @@ def test_pools_with_more_pages_than_an_int_are_refused():
         with pytest.raises(lf.LFError, match="2\\^31 - 1"):
             lf.LFPagedCache.over(big, big)
     lf.LFPagedCache.over(k.expand(1, 2**31 - 1, 1, 1, 16), k.expand(1, 2**31 - 1, 1, 1, 16))
+
+
+# ---- a table that is much wider than its sequences, and company ----------------------------------------
+
+@pytest.mark.parametrize("kind,d,page", [("bf16", 128, 16), ("bf16", 64, 128), ("bf16", 32, 16), ("bf16", 128, 24),
+                                         ("f32", 64, 16), ("f32", 128, 64)])
+def test_tables_that_are_much_wider_than_their_sequences(kind, d, page):
+    """A table row is as wide as the longest context that a server allows.  The host sees the width alone, so
+    that it cuts units and shares keys that are not there: blocks whose share is empty, and their joins."""
+    lens, new = [5, 300, 0, 129, 700], [5, 2, 0, 129, 40]
+    st = starts(new)
+    p = Paged(kind, 2, d, page, lens, seed=d, width=8192)
+    q = p.randn(5, 8, d)
+    lse = torch.empty(5, 8, dtype=torch.float32, device="cuda")
+    for window, sinks in ((0, 0), (50, 3), (20000, 4)):
+        out = p.cache.decode(0, q, p.table, p.t_lens, window=window, sinks=sinks, lse=lse)
+        for b, n in enumerate(lens):
+            p.check(b, q[b:b + 1], n - 1, out[b:b + 1], lse[b:b + 1], window, sinks, 2.0 ** -17 if kind == "bf16" else 0.0)
+    for some in ([0, 1, 2, 3, 4], [0, 2], [1]):      # fewer pieces, more shares of each
+        count = [new[b] for b in some]
+        at = starts(count)
+        qq = p.randn(at[-1], 8, d)
+        ls = torch.empty(at[-1], 8, dtype=torch.float32, device="cuda")
+        assert lf.lf_paged_prompt_workspace(p.cache._pages[0], len(some), 8192, 8, at[-1], max(count)) > 0
+        for window, sinks in ((0, 0), (50, 3), (20000, 4)):
+            out = p.cache.prompt(0, qq, p.table[some], p.t_lens[some], ints(at), max(count), window, sinks, lse=ls)
+            for i, b in enumerate(some):
+                rows = slice(at[i], at[i + 1])
+                p.check(b, qq[rows], lens[b] - new[b], out[rows], ls[rows], window, sinks, weight_step(kind))
+    kn = p.randn(st[-1], 2, d)
+    want = paged_oracle.append(p.k.double().cpu().numpy(), p.np_table, lens, kn.double().cpu().numpy(), st, page)
+    p.cache.append(0, kn, kn, p.table, p.t_lens, ints(st))
+    np.testing.assert_array_equal(p.k.double().cpu().numpy(), want)
+    assert p.cache.check() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_decode_alone_in_a_batch_and_under_a_wider_table(kind):
+    """Where a sequence's keys are cut follows its company and its table's width, and with it the last bits of its
+    sums: each result is within the bounds of rounding, and the same call gives the same bits again."""
+    p = Paged(kind, 8, 128, 16, [3000, 50, 1777, 2999], seed=9, width=1024)
+    q = p.randn(4, 32, 128)
+    step = 2.0 ** -17 if kind == "bf16" else 0.0
+    batch = p.cache.decode(0, q, p.table, p.t_lens)
+    assert torch.equal(batch, p.cache.decode(0, q, p.table, p.t_lens))
+    for b, n in enumerate(p.lens):
+        p.check(b, q[b:b + 1], n - 1, batch[b:b + 1], None, weight_step=step)
+        for width in (-(-n // 16), 200, 1024):
+            if width * 16 < n:
+                continue
+            one = [x[b:b + 1].contiguous() for x in (q, p.table[:, :width], p.t_lens)]
+            alone = p.cache.decode(0, *one)
+            assert torch.equal(alone, p.cache.decode(0, *one))
+            p.check(b, q[b:b + 1], n - 1, alone, None, weight_step=step)
+
+
+def test_the_c_named_calls_do_what_the_cache_does():
+    p = Paged("bf16", 2, 128, 16, [70, 33], seed=64)
+    pages, st, q = p.cache._pages[0], ints([0, 70, 103]), p.randn(103, 8, 128)
+    kn, vn = p.randn(103, 2, 128), p.randn(103, 2, 128)
+    lf.lf_paged_append(pages, 2, p.table, p.width, p.t_lens, kn, vn, st, 103)
+    got = [x.clone() for x in (p.k, p.v)]
+    p.cache.append(0, vn, kn, p.table, p.t_lens, st)
+    p.cache.append(0, kn, vn, p.table, p.t_lens, st)
+    assert all(torch.equal(torch.nan_to_num(a, 7.0), torch.nan_to_num(b, 7.0)) for a, b in zip(got, (p.k, p.v)))
+    out = torch.empty_like(q)
+    need = lf.lf_paged_prompt_workspace(pages, 2, p.width, 8, 103, 70)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    lf.lf_paged_prompt(pages, 2, p.table, p.width, p.t_lens, 8, q, st, 103, 70, out, None, 0, 0, ws, need)
+    assert torch.equal(out, p.cache.prompt(0, q, p.table, p.t_lens, st, 70))
