@@ -488,8 +488,11 @@ class LFPagedCache:
     """
 
     def __init__(self, layers, num_pages, page_size, kv_heads, head_dim, dtype="bf16", device=None):
-        device = torch.device("cuda", torch.cuda.current_device() if device is None
-                              else torch.device(device).index or 0)
+        device = torch.device("cuda" if device is None else device)
+        if device.type != "cuda":
+            raise LFError(LF_ERR_ARG, f"device: expected a CUDA device, got {device}")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
         if min(layers, num_pages, page_size, kv_heads, head_dim) < 1:
             raise LFError(LF_ERR_ARG, "layers, num_pages, page_size, kv_heads and head_dim must be >= 1")
         if dtype not in _DTYPE:

@@ -41,3 +41,18 @@ def test_taking_errors_from_nowhere_is_refused():
     assert call() == lf.LF_ERR_ARG and "aligned" in lf.lf_last_error()
     p.err, taken = 0x20001, 0x10000
     assert call() == lf.LF_ERR_ARG and "aligned" in lf.lf_last_error()
+
+
+def test_pools_are_made_on_the_device_that_is_named(monkeypatch):
+    """"cuda" is the current device, as torch has it, and no other kind of device turns into cuda:0."""
+    made = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: made.append(device))
+    monkeypatch.setattr(lf.LFPagedCache, "_take", lambda self, k, v: None)
+    for device, want in ((None, 3), ("cuda", 3), ("cuda:1", 1), (torch.device("cuda", 0), 0), (2, 2)):
+        lf.LFPagedCache(1, 4, 16, 8, 128, device=device)
+        assert made.pop() == made.pop() == torch.device("cuda", want)
+    for device in ("cpu", torch.device("meta")):
+        with pytest.raises(lf.LFError, match="expected a CUDA device"):
+            lf.LFPagedCache(1, 4, 16, 8, 128, device=device)
+    assert not made
