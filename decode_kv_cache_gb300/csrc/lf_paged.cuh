@@ -88,6 +88,14 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+
+// A finished row's log-sum-exp, and the error word if its sum is not finite (Args: of decode or prompt).
+template <class Args>
+__device__ __forceinline__ void write_row_stats(const Args& a, int64_t row, float m, float l) {
+  if (a.lse) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
+  if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
+}
+
 // A piece of work: rows r0 .. of `rows` of a sequence's queries, and what they see.
 struct Piece {
   int b, g, q0, first_pos, p_lo, p_hi;
@@ -237,11 +245,6 @@ __device__ __forceinline__ int64_t offset_of(const PagedPromptArgs& a, const Pie
 
 __device__ __forceinline__ bool sees(const PagedPromptArgs& a, int pos, int key) {
   return key <= pos && (a.window == 0 || key > pos - a.window || key < a.sinks);
-}
-
-__device__ __forceinline__ void write_row_stats(const PagedPromptArgs& a, int64_t row, float m, float l) {
-  if (a.lse) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
-  if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
 }
 
 // The key tiles of `size` tokens that queries at positions p_lo .. p_hi visit: [0, sink)

@@ -44,12 +44,6 @@ namespace {
 // 1 / l; 0 for a row that saw nothing (l = 0), so that its output is zeros.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
-// A finished row's log-sum-exp, and the error word if its sum is not finite.
-__device__ __forceinline__ void write_stats(const PagedDecodeArgs& a, int64_t row, float m, float l) {
-  if (a.lse) a.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
-  if (a.pool.err && !(l <= 3.0e38f)) atomicOr(a.pool.err, LF_DEVERR_NONFINITE);
-}
-
 // ---- what one warp does with a tile ------------------------------------------
 //
 // A consumer holds a warp's running maximum (in units of log2), sum and output
@@ -171,7 +165,7 @@ struct MmaTile {
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
       out[4 * n] = pack_bf16((o[n][0] + o[n][2]) * inv, (o[n][1] + o[n][3]) * inv);
-    if ((lane & 3) == 0) write_stats(a, row + r, m, ls);
+    if ((lane & 3) == 0) write_row_stats(a, row + r, m, ls);
   }
 
   // The unit's maximum, sum and output (not normalised) into po [G][D], pml [G][2].
@@ -319,7 +313,7 @@ struct SimtTile {
       if (lane < NC)
         reinterpret_cast<float4*>(a.out)[(row + h) * NC + lane] =
             make_float4(o[h][0] * inv, o[h][1] * inv, o[h][2] * inv, o[h][3] * inv);
-      if (lane == 0) write_stats(a, row + h, m[h], l[h]);
+      if (lane == 0) write_row_stats(a, row + h, m[h], l[h]);
     }
   }
 
@@ -418,7 +412,7 @@ __device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int64_t row,
 #pragma unroll
     for (int i = 0; i < E; ++i) from_f32(acc[i] * inv, out + lane * E + i);
   }
-  if (lane == 0) write_stats(a, row, m, l);
+  if (lane == 0) write_row_stats(a, row, m, l);
 }
 
 // A warp's part of a unit that it does not take whole.
