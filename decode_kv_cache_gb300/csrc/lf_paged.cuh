@@ -319,9 +319,9 @@ __device__ __forceinline__ void row_by_hand(const PagedPromptArgs& a, const Piec
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (mine) s = fmaf(qv[e], to_f32(k[e]), s);
-      s = warp_sum(s) * a.scale_log2;
-      const float mn = fmaxf(m, s), mu = mn == kNegInf ? 0.f : mn;
-      const float f = ex2(m - mu), w = ex2(s - mu);
+      s = warp_sum(s);
+      const float mn = fmaxf(m, s * a.scale_log2), mu = mn == kNegInf ? 0.f : mn;
+      const float f = ex2(m - mu), w = ex2(fmaf(s, a.scale_log2, -mu));
       m = mn;
       l = l * f + w;
 #pragma unroll

@@ -46,6 +46,10 @@ __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 
 
 // ---- what one warp does with a tile ------------------------------------------
 //
+// The exponent of a weight, s log2(e) / sqrt(d) - m, is one multiply-add: its only rounding is that
+// of the difference, and that m itself is rounded drops out.  (A scaled logit that is rounded before
+// m is taken from it is off by 2^-24 of its own size, however near m it is.)
+//
 // A consumer holds a warp's running maximum (in units of log2), sum and output
 // of one unit: begin(unit's queries), tile(...), and store(m, l, O) of G heads.
 
@@ -115,11 +119,11 @@ struct MmaTile {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int j = 8 * n + 2 * (lane & 3) + i;
-        s[n][i] = j < valid ? s[n][i] * a.scale_log2 : kNegInf;
+        if (j >= valid) s[n][i] = kNegInf;
         top = fmaxf(top, s[n][i]);
       }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * a.scale_log2;
     if (__any_sync(0xffffffffu, top > m)) {
       const float mn = fmaxf(m, top);
       const float f = mn == kNegInf ? 1.f : ex2(m - mn);
@@ -134,7 +138,7 @@ struct MmaTile {
     uint32_t hi[NT], lo[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float p0 = ex2(s[n][0] - mu), p1 = ex2(s[n][1] - mu);
+      const float p0 = ex2(fmaf(s[n][0], a.scale_log2, -mu)), p1 = ex2(fmaf(s[n][1], a.scale_log2, -mu));
       l += p0 + p1;
       hi[n] = pack_bf16(p0, p1);
       const float2 h = bf2_to_f2(hi[n]);
@@ -249,13 +253,13 @@ struct SimtTile {
     for (int h = 0; h < G; ++h) {
 #pragma unroll
       for (int x = kTokens; x < 32; x <<= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], x);
-      s[h] = tok < valid ? s[h] * a.scale_log2 : kNegInf;
-      up |= s[h] > m[h];
+      if (tok >= valid) s[h] = kNegInf;
+      up |= s[h] * a.scale_log2 > m[h];
     }
     if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float mn = fmaxf(m[h], warp_max(s[h]));
+        const float mn = fmaxf(m[h], warp_max(s[h]) * a.scale_log2);
         const float f = mn == kNegInf ? 1.f : ex2(m[h] - mn);
         m[h] = mn;
         l[h] *= f;
@@ -266,7 +270,7 @@ struct SimtTile {
     __syncwarp();  // the last tile's weights have been read
 #pragma unroll
     for (int h = 0; h < G; ++h) {
-      const float p = ex2(s[h] - (m[h] == kNegInf ? 0.f : m[h]));
+      const float p = ex2(fmaf(s[h], a.scale_log2, m[h] == kNegInf ? 0.f : -m[h]));
       if (part == 0) {
         l[h] += p;
         ps[tok * G + h] = p;

@@ -347,17 +347,18 @@ __global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __gr
     float w[M][4];
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-      float top = m[i];
+      float top = kNegInf;
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         float x, y;
         unpair(s2[i][n], &x, &y);
-        w[i][n] = (x + y) * a.scale_log2;
+        w[i][n] = x + y;
         if (hidden && !sees(a, pos[i], k0 + cg + 16 * n)) w[i][n] = kNegInf;
         top = fmaxf(top, w[i][n]);
       }
 #pragma unroll
       for (int x = 1; x < 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      top = fmaxf(m[i], top * a.scale_log2);
       const float mu = top == kNegInf ? 0.f : top;
       const float f = ex2(m[i] - mu);
       m[i] = top;
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(16 * R / M) paged_prompt_fma_kernel(const __gr
       for (int c = 0; c < CP; ++c) o[i][c] = fma_pair(o[i][c], pair(f, f), 0ull);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        w[i][n] = ex2(w[i][n] - mu);
+        w[i][n] = ex2(fmaf(w[i][n], a.scale_log2, -mu));   // rounded as a difference, not at the logit's size
         l[i] += w[i][n];
       }
     }

@@ -420,3 +420,85 @@ def test_the_c_named_calls_do_what_the_cache_does():
     ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
     lf.lf_paged_prompt(pages, 2, p.table, p.width, p.t_lens, 8, q, st, 103, 70, out, None, 0, 0, ws, need)
     assert torch.equal(out, p.cache.prompt(0, q, p.table, p.t_lens, st, 70))
+
+
+# ---- logits that are large and close to one another ----------------------------------------------------
+
+def large_logits(kind, heads, d, page, n, seed):
+    """A sequence and a maker of queries whose logits are about 2^19 / sqrt(d), differ by some tens, and are
+    exact in fp32 in any order of summation: whole numbers, their sums below 2^24."""
+    p = Paged(kind, heads, d, page, [n], seed=seed)
+    whole = lambda *s: torch.randint(-3, 4, s, generator=p.g, device="cuda")  # noqa: E731
+    k = torch.zeros(heads, n, d, device="cuda")
+    k[..., 0], k[..., 1:9] = 2048.0, whole(heads, n, 8).float()
+    p.rows_k[0] = k.to(p.k.dtype)
+    for i in range(-(-n // page)):
+        m = min(page, n - i * page)
+        p.k[int(p.np_table[0, i]), :, :m] = p.rows_k[0][:, i * page:i * page + m]
+
+    def queries(rows, q_heads):
+        q = torch.zeros(rows, q_heads, d, device="cuda")
+        q[..., 0], q[..., 1:9] = 256.0, whole(rows, q_heads, 8).float()
+        return q.to(p.k.dtype)
+
+    return p, queries
+
+
+def check_large_logits(p, q, first_pos, out, step):
+    """Against fp64, with bounds that know nothing of the logits' size: an exponent is a difference of at most 64
+    in log2 (8 products of at most 9, twice, times log2(e) / 4), rounded once, with a factor that is rounded
+    once; 2^x, thrice where parts are joined, is good to 2^-21; a sum over n keys and its rescalings adds
+    n + 64 roundings; numerator and denominator alike.  (A logit rounded before the maximum is taken from it
+    would be off by 2^-24 of its size: 2^-24 * 2^19 / 8 * log2(e) * ln 2, 0.4 %.)"""
+    n = p.lens[0]
+    f = lambda x: x.double().cpu().numpy()  # noqa: E731
+    see = paged_oracle.visible(first_pos + np.arange(q.shape[0]), n, 0, 0)
+    ref, _, size, _ = paged_oracle.attend(f(q), f(p.rows_k[0]), f(p.rows_v[0]), see)
+    rel = 2 * (3 * 2.0 ** -21 + 2 * 64 * 2.0 ** -24 + (n + 64) * 2.0 ** -24)
+    half = 2.0 ** -8 if p.kind == "bf16" else 2.0 ** -24
+    err = (rel + step) * size
+    assert (np.abs(f(out) - ref) <= err + half * (np.abs(ref) + err)).all()
+
+
+@pytest.mark.parametrize("kind,d,group", [("f32", 64, 1), ("f32", 128, 4), ("f32", 16, 8), ("bf16", 128, 4),
+                                          ("bf16", 64, 1), ("bf16", 16, 2)])
+@pytest.mark.parametrize("n", [12, 300, 3000])
+def test_decode_large_logits(kind, d, group, n):
+    p, queries = large_logits(kind, 2, d, 16, n, d + n)
+    q = queries(1, 2 * group)
+    check_large_logits(p, q, n - 1, p.cache.decode(0, q, p.table, p.t_lens), 2.0 ** -17 if kind == "bf16" else 0.0)
+
+
+@pytest.mark.parametrize("kind,d,page", [("f32", 16, 16), ("f32", 64, 16), ("f32", 128, 16), ("bf16", 128, 16),
+                                         ("bf16", 64, 64), ("bf16", 128, 24), ("bf16", 32, 16)])
+@pytest.mark.parametrize("n,rows", [(12, 12), (200, 150), (3000, 3)])
+def test_prompt_large_logits(kind, d, page, n, rows):
+    p, queries = large_logits(kind, 2, d, page, n, d + n)
+    q = queries(rows, 8)
+    out = p.cache.prompt(0, q, p.table, p.t_lens, ints([0, rows]), rows)
+    check_large_logits(p, q, n - rows, out, weight_step(kind))
+
+
+def test_prompt_large_logits_in_pieces_of_64_rows():
+    """fp32, heads of 128, enough rows for the kernel that takes 64 of them at a time; the last ones are compared."""
+    n = 1300
+    p, queries = large_logits("f32", 16, 128, 16, n, 7)
+    q = queries(n, 32)
+    out = p.cache.prompt(0, q, p.table, p.t_lens, ints([0, n]), n)
+    check_large_logits(p, q[-2:], n - 2, out[-2:], 0.0)
+
+
+@pytest.mark.parametrize("d,page", [(128, 16), (32, 16)])
+def test_prompt_large_logits_beside_values_that_are_not_finite(d, page):
+    """The rows that are computed again, one by one."""
+    n = 100
+    p, queries = large_logits("bf16", 2, d, page, n, d)
+    q = queries(n, 4)
+    p.v[int(p.np_table[0, 99 // page]), :, 99 % page] = math.inf     # seen by the last row only
+    out = p.cache.prompt(0, q, p.table, p.t_lens, ints([0, n]), n)
+    p.lens[0] = 99
+    p.rows_k[0], p.rows_v[0] = p.rows_k[0][:, :99], p.rows_v[0][:, :99]
+    # Blocks take 32 tokens or more here: 96 .. 98 are computed again with 99, their weights not rounded to bf16.
+    # Blocks that do not read position 99 keep the products of the others, with weights that are.
+    check_large_logits(p, q[96:99], 96, out[96:99], 0.0)
+    check_large_logits(p, q[:96], 0, out[:96], weight_step("bf16"))
