@@ -226,31 +226,35 @@ struct SimtTile {
   __device__ __forceinline__ void tile(const PagedDecodeArgs& a, uint32_t ks, uint32_t vs, int valid,
                                        float* extra) {
     const int lane = threadIdx.x & 31;
-    const float4* q4 = reinterpret_cast<const float4*>(extra);
+    const ulonglong2* q4 = reinterpret_cast<const ulonglong2*>(extra);
     float* ps = extra + G * D;
     const int tok = lane % kTokens, part = lane / kTokens;
+    // Four sums of a share's products, by column modulo 4 and in pairs: one alone would be a chain of 32
+    // roundings, these are of at most 8.
     float s[G];
+    uint64_t s2[G][2];
 #pragma unroll
-    for (int h = 0; h < G; ++h) s[h] = 0.f;
+    for (int h = 0; h < G; ++h) s2[h][0] = s2[h][1] = 0ull;
 #pragma unroll
     for (int i = 0; i < NC / kShare; ++i) {
       const int c = i * kShare + part;
-      float4 k;
-      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                   : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w)
+      ulonglong2 k;
+      asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];"
+                   : "=l"(k.x), "=l"(k.y)
                    : "r"(ks + 16 * tile_chunk<NC>(tok, c)));
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float4 q = q4[h * NC + c];
-        s[h] = fmaf(q.x, k.x, s[h]);
-        s[h] = fmaf(q.y, k.y, s[h]);
-        s[h] = fmaf(q.z, k.z, s[h]);
-        s[h] = fmaf(q.w, k.w, s[h]);
+        const ulonglong2 q = q4[h * NC + c];
+        s2[h][0] = fma_pair(q.x, k.x, s2[h][0]);
+        s2[h][1] = fma_pair(q.y, k.y, s2[h][1]);
       }
     }
     bool up = false;
 #pragma unroll
     for (int h = 0; h < G; ++h) {
+      float x0, x1;
+      unpair(add_pair(s2[h][0], s2[h][1]), &x0, &x1);
+      s[h] = x0 + x1;
 #pragma unroll
       for (int x = kTokens; x < 32; x <<= 1) s[h] += __shfl_xor_sync(0xffffffffu, s[h], x);
       if (tok >= valid) s[h] = kNegInf;

@@ -502,3 +502,24 @@ def test_prompt_large_logits_beside_values_that_are_not_finite(d, page):
     # Blocks that do not read position 99 keep the products of the others, with weights that are.
     check_large_logits(p, q[96:99], 96, out[96:99], 0.0)
     check_large_logits(p, q[:96], 0, out[:96], weight_step("bf16"))
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+def test_decode_products_of_a_logit_are_no_single_chain(d):
+    """fp32.  One product of 1 and d - 1 of less than half a step of it: a chain of sums loses each that comes
+    behind the 1 in it.  With chains of at most 8, and at most 2 + 2 additions that join them, the logit is off by
+    12 halves of a step; its scaling, m and the log-sum-exp's factor are a rounding each, and the factors are
+    rounded themselves: 5 more."""
+    n = 2
+    for at in range(0, d, 3):
+        p = Paged("f32", 1, d, 16, [n], seed=d)
+        k = torch.full((1, n, d), 0.98 * 2.0 ** -24, device="cuda")
+        k[..., at] = 1.0
+        k[:, 1] = -1000.0      # the other key weighs nothing
+        p.rows_k[0] = k
+        p.k[int(p.np_table[0, 0]), :, :n] = k
+        q = torch.ones(1, 1, d, device="cuda")
+        lse = torch.empty(1, 1, dtype=torch.float32, device="cuda")
+        p.cache.decode(0, q, p.table, p.t_lens, lse=lse)
+        want = float(k[0, 0].double().sum()) / math.sqrt(d)
+        assert abs(float(lse) - want) <= 17 * 2.0 ** -24 * want, at
