@@ -157,6 +157,7 @@ int cuda_fail(cudaError_t e, const char* what) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int elem_bytes(const lf_pages* p) { return p->dtype == LF_BF16 ? 2 : 4; }
 
@@ -185,6 +186,8 @@ int take_pool(const lf_pages* p, int batch, const int32_t* table, int max_pages,
   if (max_pages < 1 || (int64_t)max_pages * p->page_size > INT_MAX - 256)
     return fail(LF_ERR_ARG, "max_pages must be >= 1 and max_pages * page_size below 2^31 - 256");
   if (!table || !lens) return fail(LF_ERR_ARG, "null page_table or lens");
+  if (!aligned4(table) || !aligned4(lens) || !aligned4(p->err))
+    return fail(LF_ERR_ARG, "page_table, lens and the error word must be 4-byte aligned");
   out->k = static_cast<char*>(p->k);
   out->v = static_cast<char*>(p->v);
   out->page_stride = p->page_stride * e;
@@ -299,6 +302,7 @@ int lf_paged_append(const lf_pages* pages, int batch, const int32_t* page_table,
   if (total_new == 0) return LF_OK;
   if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))
     return fail(LF_ERR_ARG, "k_new and v_new must be non-null and 16-byte aligned");
+  if (!aligned4(new_start)) return fail(LF_ERR_ARG, "new_start must be 4-byte aligned");
   a.k_new = static_cast<const char*>(k_new);
   a.v_new = static_cast<const char*>(v_new);
   a.new_start = new_start;
@@ -340,6 +344,7 @@ int lf_paged_decode(const lf_pages* pages, int batch, const int32_t* page_table,
     return fail(LF_ERR_ARG, "q and out must be non-null and 16-byte aligned");
   if (!k_new != !v_new || !aligned16(k_new) || !aligned16(v_new))
     return fail(LF_ERR_ARG, "k_new and v_new come together, 16-byte aligned (or both null)");
+  if (!aligned4(lse)) return fail(LF_ERR_ARG, "lse must be 4-byte aligned");
   a.q = q;
   a.k_new = static_cast<const char*>(k_new);
   a.v_new = static_cast<const char*>(v_new);
@@ -402,6 +407,7 @@ int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table,
   if (total_q == 0 || max_q == 0) return LF_OK;
   if (!q || !out || !aligned16(q) || !aligned16(out))
     return fail(LF_ERR_ARG, "q and out must be non-null and 16-byte aligned");
+  if (!aligned4(q_start) || !aligned4(lse)) return fail(LF_ERR_ARG, "q_start and lse must be 4-byte aligned");
   a.q = q;
   a.q_start = q_start;
   a.out = out;
@@ -435,7 +441,7 @@ int lf_paged_prompt(const lf_pages* pages, int batch, const int32_t* page_table,
 int lf_paged_take_errors(const lf_pages* pages, int32_t* taken, lf_stream_t stream) {
   lf::clear_last_error();
   if (!pages || !pages->err || !taken) return fail(LF_ERR_ARG, "null pages, error word or taken");
-  if ((reinterpret_cast<uintptr_t>(pages->err) | reinterpret_cast<uintptr_t>(taken)) & 3u)
+  if (!aligned4(pages->err) || !aligned4(taken))
     return fail(LF_ERR_ARG, "the error word and taken must be 4-byte aligned");
   const cudaError_t e = lf::paged_take_errors_launch(pages->err, taken, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LF_OK : cuda_fail(e, "paged take errors launch");

@@ -382,7 +382,8 @@ int lf_prefill_fill_noalloc(const lf_layout* dst, int layer, const void* k, cons
  *
  * lens[b] is sequence b's length INCLUDING the tokens of the call that gets it: all
  * layers of one step share one page table and one lens.  Lengths, tables and row
- * starts are read on the device, so a captured graph follows their contents.
+ * starts are read on the device, so a captured graph follows their contents.  They, the
+ * error word and lse are 4-byte aligned.
  *
  * Errors found on the device are OR-ed into *err where err is not NULL:
  * LF_DEVERR_STATE for a page index outside [0, num_pages), a length outside [0,

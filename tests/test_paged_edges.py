@@ -56,3 +56,32 @@ def test_pools_are_made_on_the_device_that_is_named(monkeypatch):
         with pytest.raises(lf.LFError, match="expected a CUDA device"):
             lf.LFPagedCache(1, 4, 16, 8, 128, device=device)
     assert not made
+
+
+def test_addresses_that_are_not_aligned_are_refused():
+    """Before any launch: an int or a float read from such an address would end the caller's context."""
+    from decode_kv_cache_gb300 import build as b
+    b.build()
+    lib = lf.load_library()
+    at = lambda i, off=0: 0x10000 * i + off  # noqa: E731
+
+    def pages(err=None):
+        return ctypes.byref(lf.LFPages(lf.LF_BF16, 8, 128, 16, 100, 8 * 16 * 128, 16 * 128, 128, at(1), at(2), err))
+
+    for off in (1, 2, 3):
+        for err, table, lens in ((at(9, off), at(3), at(4)), (None, at(3, off), at(4)), (None, at(3), at(4, off))):
+            for code in (lib.lf_paged_append(pages(err), 4, table, 10, lens, at(5), at(5), at(6), 7, None),
+                         lib.lf_paged_decode(pages(err), 4, table, 1000, lens, 32, at(5), None, None, at(5), None, 0, 0,
+                                             at(7), 1 << 40, None),
+                         lib.lf_paged_prompt(pages(err), 4, table, 10, lens, 32, at(5), at(6), 7, 3, at(5), None, 0, 0,
+                                             at(7), 1 << 40, None)):
+                assert code == lf.LF_ERR_ARG and "4-byte aligned" in lf.lf_last_error()
+        for code, name in (
+                (lib.lf_paged_append(pages(), 4, at(3), 10, at(4), at(5), at(5), at(6, off), 7, None), "new_start"),
+                (lib.lf_paged_decode(pages(), 4, at(3), 1000, at(4), 32, at(5), None, None, at(5), at(8, off), 0, 0, at(7),
+                                     1 << 40, None), "lse"),
+                (lib.lf_paged_prompt(pages(), 4, at(3), 10, at(4), 32, at(5), at(6, off), 7, 3, at(5), None, 0, 0, at(7),
+                                     1 << 40, None), "q_start"),
+                (lib.lf_paged_prompt(pages(), 4, at(3), 10, at(4), 32, at(5), at(6), 7, 3, at(5), at(8, off), 0, 0, at(7),
+                                     1 << 40, None), "lse")):
+            assert code == lf.LF_ERR_ARG and "4-byte aligned" in lf.lf_last_error(), name
