@@ -579,7 +579,9 @@ class LFPagedCache:
         if stream is None and torch.cuda.current_device() == self._index:
             return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self.device)
+            # 0, the default stream's handle, would make torch take a stream of its pool
+            stream = (torch.cuda.ExternalStream(stream, device=self.device) if stream
+                      else torch.cuda.default_stream(self.device))
         if stream is not None and getattr(stream, "device", None) != self.device:
             raise LFError(LF_ERR_ARG, f"stream: expected a stream of {self.device}, got {stream}")
         with torch.cuda.device(self._index), torch.cuda.stream(stream):

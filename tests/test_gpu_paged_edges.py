@@ -182,6 +182,7 @@ def busy(stream=None, clocks=100_000_000):
 
 def test_a_stream_handle_of_zero_is_the_default_stream():
     """torch.cuda.default_stream().cuda_stream is 0: a call with it comes behind the default stream's work."""
+    side = torch.cuda.Stream()      # (the first one makes torch's pool of them, which waits for the device)
     p = Paged("bf16", 8, 128, 16, [3000, 50], seed=60)
     real, st = p.randn(2, 32, 128), ints([0, 1, 2])
     want = p.cache.decode(0, real, p.table, p.t_lens)
@@ -195,7 +196,6 @@ def test_a_stream_handle_of_zero_is_the_default_stream():
     got_prompt = p.cache.prompt(0, q, p.table, p.t_lens, st, 1, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(got_prompt, want_prompt)
-    side = torch.cuda.Stream()
     with torch.cuda.stream(side):      # and not the current one
         busy()
         q.zero_()
