@@ -523,3 +523,137 @@ def test_decode_products_of_a_logit_are_no_single_chain(d):
         p.cache.decode(0, q, p.table, p.t_lens, lse=lse)
         want = float(k[0, 0].double().sum()) / math.sqrt(d)
         assert abs(float(lse) - want) <= 17 * 2.0 ** -24 * want, at
+
+
+# ---- calls that the header allows -------------------------------------------------------------------------
+
+def attend(q, k, v, n):
+    """fp64 attention of one query per sequence on the GPU: q [b][H][d], k, v [b][H][most][d], n [b]."""
+    q, k, v = q.double(), k.double(), v.double()
+    z = torch.einsum("bhd,bhnd->bhn", q, k) / math.sqrt(q.shape[-1])
+    z = z.masked_fill(torch.arange(k.shape[2], device="cuda")[None, None] >= n[:, None, None], -math.inf)
+    w = torch.softmax(z, -1)
+    dots = (torch.einsum("bhd,bhnd->bhn", q.abs(), k.abs()) / math.sqrt(q.shape[-1])).amax(-1)
+    return torch.einsum("bhn,bhnd->bhd", w, v), torch.einsum("bhn,bhnd->bhd", w, v.abs()), dots
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_the_largest_batch(kind):
+    """65535 sequences of one to four tokens: append, decode and a prompt of one token each."""
+    from paged_harness import TYPES, bounds
+    b, d, page = 65535, 16, 4
+    g = torch.Generator(device="cuda").manual_seed(70)
+    t = TYPES[kind]
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(t)  # noqa: E731
+    k, v = rnd(b, 1, page, d), rnd(b, 1, page, d)
+    cache = lf.LFPagedCache.over(k[None], v[None])
+    table = torch.randperm(b, generator=g, device="cuda").to(torch.int32)[:, None].contiguous()
+    lens = (1 + torch.arange(b, device="cuda") % 4).to(torch.int32)
+    kn, vn, q = rnd(b, 1, d), rnd(b, 1, d), rnd(b, 1, d)
+    want = k.clone()
+    want[table[:, 0].long(), :, lens.long() - 1] = kn
+    start = torch.arange(b + 1, dtype=torch.int32, device="cuda")
+    cache.append(0, kn, vn, table, lens, start)
+    assert torch.equal(k, want)
+    ref, size, dots = attend(q, k[table[:, 0].long()], v[table[:, 0].long()], lens)
+    f = lambda x: x.double().cpu().numpy()  # noqa: E731
+    k.zero_()
+    cache.append(0, want[table[:, 0].long(), :, lens.long() - 1].contiguous(), vn, table, lens)
+    assert torch.equal(k.sum((1, 2)), want[table[:, 0].long(), 0, lens.long() - 1][torch.argsort(table[:, 0])])
+    k.copy_(want)
+    for out, step in ((cache.decode(0, q, table, lens, kn, vn), 2.0 ** -17), (cache.decode(0, q, table, lens), 2.0 ** -17),
+                      (cache.prompt(0, q, table, lens, start, 1), 2.0 ** -8)):
+        tol, _ = bounds(kind, d, 4, f(ref), f(size), f(dots), step if kind == "bf16" else 0.0)
+        assert (np.abs(f(out) - f(ref)) <= tol).all()
+    assert torch.equal(k, want) and cache.check() == 0
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 64), ("bf16", 16), ("f32", 32)])
+def test_many_heads(kind, d):
+    p = Paged(kind, 700, d, 16, [37, 0, 5], seed=71)
+    q = p.randn(3, 700, d)
+    out = p.cache.decode(0, q, p.table, p.t_lens)
+    for b in (0, 2):
+        p.check(b, q[b:b + 1], p.lens[b] - 1, out[b:b + 1], None, weight_step=2.0 ** -17 if kind == "bf16" else 0.0)
+    q, st = p.randn(5, 700, d), ints([0, 3, 3, 5])
+    out = p.cache.prompt(0, q, p.table, p.t_lens, st, 3)
+    p.check(0, q[:3], 34, out[:3], None, weight_step=weight_step(kind))
+    p.check(2, q[3:], 3, out[3:], None, weight_step=weight_step(kind))
+    assert p.cache.check() == 0
+
+
+@pytest.mark.parametrize("page", [1000, 1024, 300])
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_a_page_that_holds_a_whole_sequence(kind, d, page):
+    p = Paged(kind, 2, d, page, [300, 257, 1], seed=page + d, spare=0)
+    for window, sinks in ((0, 0), (100, 3)):
+        q, st = p.randn(300 + 57 + 1, 4, d), ints([0, 300, 357, 358])
+        out = p.cache.prompt(0, q, p.table, p.t_lens, st, 300, window, sinks)
+        for b, (lo, hi) in enumerate([(0, 300), (300, 357), (357, 358)]):
+            p.check(b, q[lo:hi], p.lens[b] - (hi - lo), out[lo:hi], None, window, sinks, weight_step(kind))
+        out = p.cache.decode(0, q[:3].contiguous(), p.table, p.t_lens, window=window, sinks=sinks)
+        for b in range(3):
+            p.check(b, q[b:b + 1], p.lens[b] - 1, out[b:b + 1], None, window, sinks, 2.0 ** -17 if kind == "bf16" else 0.0)
+    assert p.cache.check() == 0
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 32), ("f32", 64)])
+def test_pages_that_sequences_share(kind, d):
+    """A prefix that three sequences have in common, one of them twice in the batch."""
+    p = Paged(kind, 2, d, 16, [200, 150, 96], seed=72)
+    table, rows_k, rows_v = p.table.clone(), p.rows_k, p.rows_v
+    table[1, :6] = table[2, :6] = table[0, :6]      # 96 tokens
+    for r in (rows_k, rows_v):
+        r[1][:, :96], r[2][:, :96] = r[0][:, :96], r[0][:, :96]
+    twice = table[[0, 1, 2, 1]].contiguous()
+    p.lens = [200, 150, 96, 150]
+    p.rows_k, p.rows_v = rows_k + [rows_k[1]], rows_v + [rows_v[1]]
+    lens, q = ints(p.lens), p.randn(4 * 20, 4, d)
+    out = p.cache.prompt(0, q, twice, lens, ints([0, 20, 40, 60, 80]), 20)
+    one = p.cache.decode(0, q[:4].contiguous(), twice, lens)
+    for b in range(4):
+        p.check(b, q[20 * b:20 * b + 20], p.lens[b] - 20, out[20 * b:20 * b + 20], None, weight_step=weight_step(kind))
+        p.check(b, q[b:b + 1], p.lens[b] - 1, one[b:b + 1], None, weight_step=2.0 ** -17 if kind == "bf16" else 0.0)
+
+
+@pytest.mark.parametrize("kind,d,batch", [("bf16", 128, 5), ("bf16", 128, 40), ("bf16", 32, 40), ("f32", 64, 5)])
+def test_a_captured_prompt_follows_its_starts_lengths_and_table(kind, d, batch):
+    """One graph of append and prompt for up to 300 rows, replayed for other chunks of other sequences."""
+    rows, most = 300, 120
+    rng = np.random.default_rng(d + batch)
+    p = Paged(kind, 2, d, 16, [400] * batch, seed=73)
+    q, kn, vn = p.randn(rows, 4, d), p.randn(rows, 2, d), p.randn(rows, 2, d)
+    table, lens, st = p.table.clone(), p.t_lens.clone(), ints([0] * (batch + 1))
+    out = torch.full_like(q, 3.0)
+    p.cache.append(0, kn, vn, table, lens, st)
+    p.cache.prompt(0, q, table, lens, st, most, 90, 4, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.cache.append(0, kn, vn, table, lens, st)
+        p.cache.prompt(0, q, table, lens, st, most, 90, 4, out=out)
+    whole_k, whole_v = p.rows_k, p.rows_v
+    for _ in range(4):
+        new = np.minimum(rng.integers(0, most + 1, batch), 0 if batch > 5 else most)
+        new[rng.integers(batch)] = most
+        new[rng.integers(batch)] = rng.integers(1, most)
+        if new.sum() > rows:
+            new[2:] = 0
+        old = rng.integers(0, 400 - most, batch)
+        order = rng.permutation(batch)
+        at = starts(new.tolist())
+        p.lens = (old + new).tolist()
+        table.copy_(p.table[ints(order.tolist()).long()])
+        lens.copy_(ints(p.lens)), st.copy_(ints(at)), out.fill_(3.0)
+        p.rows_k, p.rows_v = [], []
+        graph.replay()
+        torch.cuda.synchronize()
+        assert p.cache.check() == 0
+        for b in range(batch):
+            for mine, whole, fresh in ((p.rows_k, whole_k, kn), (p.rows_v, whole_v, vn)):
+                whole[order[b]][:, old[b]:old[b] + new[b]] = fresh[at[b]:at[b + 1]].transpose(0, 1)
+                mine.append(whole[order[b]][:, :p.lens[b]])
+        for b in range(batch):
+            r = slice(at[b], at[b + 1])
+            p.check(b, q[r], int(old[b]), out[r], None, 90, 4, weight_step(kind))
+        assert (out[at[-1]:] == 3).all()
