@@ -264,7 +264,10 @@ struct DecodeShape {
 // being 128 tokens: 8 units of 4 sweeps 10.0 us, 10.6, of 8 sweeps 14.9, 11.3; 64 units of
 // 4 sweeps 11.2, 14.4, of 8 sweeps 15.7, 17.2, of 16 sweeps 25.3, 21.9; 136 units of 8
 // sweeps 18.5, 23.7, of 16 sweeps 30.1, 35.3, but ragged 27.7, 30.1, of 32 sweeps ragged
-// 44.8, 41.7.  Heads of 64 and fp32 cross over at the same numbers of sweeps.)
+// 44.8, 41.7.  Heads of 64 and fp32 cross over at the same numbers of sweeps.)  The bounds are on
+// the careful side: 64 units of 8 sweeps and 136 of 16 are cut, though whole ones were faster.
+// Lengths are known here by the table's width: short sequences under a wide table are cut too (one of
+// 300 tokens under 8192 pages 10.3 us, 8.3 under its own 19; 17 fp32 ones of 1000 16.5, 13.6).
 int decode_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int window, int sinks,
                  DecodeShape* s) {
   const int64_t most = window > 0 ? (int64_t)window + sinks : (int64_t)pool.max_pages * pool.page_size;

@@ -34,10 +34,12 @@
 // softmax left out.
 // Around its key tiles a CTA spends about 10 thousand clocks: barriers, lookups and
 // the first tiles' way in, the rows' way out, the next launch on the SM, and with one CTA per SM (all
-// of the tensor memory, 200 KB) nothing runs meanwhile.  Measured, bf16, heads of 128: one prompt of
-// 8192 tokens, 32 / 8 heads, 354 us, 1.55 PFLOP/s, 81 % of the library's dense product; 12000
-// with a window of 1000, 16 / 8 heads, 120 us; chunks of 1 to 512 of 24 sequences behind up
-// to 2048, 32 / 8 heads, 132 us.
+// of the tensor memory, 200 KB) nothing runs meanwhile.  Measured, bf16, heads of 128, the same inputs
+// again and again (other inputs every time): one prompt of 8192 tokens, 32 / 8 heads, 350 us, 1.57
+// PFLOP/s, 82 % of the library's dense product (375 us, 1.46, 76 %); 12000 with a window of 1000,
+// 16 / 8 heads, 117 us (120); chunks of 1 to 512 of 24 sequences behind up to 2048, 32 / 8 heads, 119 us
+// (131).  Heads of 64 have half the products under the same softmax: 8192 tokens 293 us, 0.94 PFLOP/s.
+// The scrubber's reads are 2 us of the window's 117 (measured without them).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
