@@ -526,7 +526,9 @@ class LFPagedCache:
         self._index = k.get_device()
         self._row = (self.kv_heads, self.head_dim)
         # the device error word, as a tensor of one int32; copied from the host, which waits, so that
-        # no stream that uses the cache can come before it
+        # no stream that uses the cache can come before it (and which no graph can hold)
+        if torch.cuda.is_current_stream_capturing():
+            raise LFError(LF_ERR_ARG, "make the cache before the capture of a graph")
         self.err = torch.zeros(1, dtype=torch.int32).to(k.device)
         step, pk, pv = strides[0] * k.element_size(), k.data_ptr(), v.data_ptr()
         self._pages = [LFPages(types[k.dtype], self.kv_heads, self.head_dim, self.page_size, self.num_pages,

@@ -406,7 +406,7 @@ int lf_prefill_fill_noalloc(const lf_layout* dst, int layer, const void* k, cons
  * lf_paged_decode keeps 16 bits of it, fp32 caches all.
  * Values of tokens behind a sequence's end or outside the window never reach an
  * output, whatever they hold (NaN included).  Pages all of whose positions lie behind
- * the window of every query of the call, and not below `sinks`, are not looked up: the
+ * the window of every query of the call, and not below `sinks`, do not count: the
  * caller may have given them away, and their entries need not be pages.
  *
  * Calls are stream-ordered, run on the current device, allocate nothing, do not

@@ -657,3 +657,19 @@ def test_a_captured_prompt_follows_its_starts_lengths_and_table(kind, d, batch):
             r = slice(at[b], at[b + 1])
             p.check(b, q[r], int(old[b]), out[r], None, 90, 4, weight_step(kind))
         assert (out[at[-1]:] == 3).all()
+
+
+def test_a_cache_made_during_a_capture_is_refused():
+    """Before anything that would end the capture: the graph that is captured around it works."""
+    p = Paged("bf16", 2, 128, 16, [100, 50], seed=74)
+    q = p.randn(2, 8, 128)
+    want = p.cache.decode(0, q, p.table, p.t_lens)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        with pytest.raises(lf.LFError, match="before the capture"):
+            lf.LFPagedCache.over(p.k[None], p.v[None])
+        out = p.cache.decode(0, q, p.table, p.t_lens)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
