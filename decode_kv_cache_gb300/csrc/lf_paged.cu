@@ -10,6 +10,7 @@
 #include "lf_device.cuh"
 #include "lf_kernels.h"
 #include "lf_paged.h"
+#include "lf_paged_host.h"
 #include "longflow.h"
 
 namespace lf {
@@ -136,9 +137,9 @@ cudaError_t paged_append_launch(const PagedAppendArgs& a, cudaStream_t stream) {
 
 }  // namespace lf
 
-// ---- C ABI --------------------------------------------------------------------
+// ---- checks that the paged entry points share (lf_paged_host.h) ----------------
 
-namespace {
+namespace lf {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -146,7 +147,7 @@ int fail(int code, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
-  lf::set_last_error(code, buf);
+  set_last_error(code, buf);
   return code;
 }
 
@@ -156,14 +157,9 @@ int cuda_fail(cudaError_t e, const char* what) {
               cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-int elem_bytes(const lf_pages* p) { return p->dtype == LF_BF16 ? 2 : 4; }
-
 // The pools, the page table and the lengths of a call, checked, as the kernels take them.
 int take_pool(const lf_pages* p, int batch, const int32_t* table, int max_pages,
-              const int32_t* lens, lf::PagedPool* out) {
+              const int32_t* lens, PagedPool* out) {
   if (!p) return fail(LF_ERR_ARG, "null pages");
   if (p->dtype != LF_BF16 && p->dtype != LF_F32)
     return fail(LF_ERR_ARG, "dtype must be LF_BF16 or LF_F32");
@@ -217,6 +213,29 @@ int take_heads(const lf_pages* p, int q_heads, int* group) {
   return LF_OK;
 }
 
+// Streaming multiprocessors of the current device.
+int sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? LF_OK : cuda_fail(e, "device attributes");
+}
+
+}  // namespace lf
+
+// ---- C ABI --------------------------------------------------------------------
+
+namespace {
+
+using lf::aligned16;
+using lf::aligned4;
+using lf::cuda_fail;
+using lf::elem_bytes;
+using lf::fail;
+using lf::sm_count;
+using lf::take_heads;
+using lf::take_pool;
+
 // The window as the kernels take it: one that covers every position a table can
 // hold is none.
 int take_window(const lf::PagedPool& p, int window, int sinks, int* w, int* s) {
@@ -236,14 +255,6 @@ int take_rows(const lf::PagedPool& p, int group, int total_q, int max_q) {
   if (lf::paged_prompt_pieces(p, group, total_q, max_q, 32, false, &tiles) > INT_MAX)
     return fail(LF_ERR_ARG, "max_q * group / 32 * batch * kv_heads must be below 2^31");
   return LF_OK;
-}
-
-// Streaming multiprocessors of the current device.
-int sm_count(int* sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  return e == cudaSuccess ? LF_OK : cuda_fail(e, "device attributes");
 }
 
 // How a decode call is spread over the GPU, and its workspace: the parts that

@@ -12,6 +12,7 @@ views (through ``__cuda_array_interface__``) for tests, snapshots and restores.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence
 
@@ -32,6 +33,8 @@ __all__ = [
     "LFPages", "lf_paged_append", "lf_paged_decode", "lf_paged_decode_workspace", "lf_paged_prompt",
     "lf_paged_prompt_workspace", "lf_paged_take_errors",
     "LFPagedCache",
+    "LFRotaryTable", "LFRows", "lf_rotary_turns", "lf_rotate", "lf_paged_append_rotated",
+    "LFRotary",
 ]
 
 LF_OK, LF_ERR_ARG, LF_ERR_OOM, LF_ERR_CUDA, LF_ERR_DEVICE, LF_ERR_UNSUPPORTED = 0, -1, -2, -3, -5, -7
@@ -46,6 +49,7 @@ LF_SCOPE_KV_HEAD, LF_SCOPE_LAYER = 0, 1
 _SCOPE = {"kv_head": LF_SCOPE_KV_HEAD, "layer": LF_SCOPE_LAYER}
 LF_DEVERR_NONFINITE, LF_DEVERR_STATE, LF_DEVERR_TIMEOUT = 1, 2, 4
 
+_MAX_AXES = 4           # LF_ROTARY_MAX_AXES
 _INT_MAX = 2**31 - 1   # of the C calls' numbers, of which ctypes would take the low bits of larger ones
 
 _DTYPE = {"bf16": LF_BF16, "f32": LF_F32}
@@ -87,6 +91,17 @@ class LFPages(ctypes.Structure):
         "dtype", "kv_heads", "head_dim", "page_size", "num_pages")] + [
         (n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")] + [
         (n, ctypes.c_void_p) for n in ("k", "v", "err")]
+
+
+class LFRotaryTable(ctypes.Structure):
+    """lf_rotary."""
+    _fields_ = [(n, ctypes.c_int) for n in ("rotary_dim", "axes", "adjacent")] + [
+        ("scale", ctypes.c_float), ("turns", ctypes.c_void_p), ("axis", ctypes.c_void_p)]
+
+
+class LFRows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int)] + [
+        (n, ctypes.c_int64) for n in ("x_seq", "x_token", "x_head", "y_seq", "y_token", "y_head")]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -153,6 +168,13 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.lf_paged_prompt_workspace.argtypes = [PG, I, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
     lib.lf_paged_take_errors.restype = I
     lib.lf_paged_take_errors.argtypes = [PG, VP, VP]
+    RT, RW, LL = ctypes.POINTER(LFRotaryTable), ctypes.POINTER(LFRows), ctypes.c_int64
+    lib.lf_rotary_turns.restype = I
+    lib.lf_rotary_turns.argtypes = [ctypes.POINTER(ctypes.c_double), I, ctypes.POINTER(ctypes.c_uint64)]
+    lib.lf_rotate.restype = I
+    lib.lf_rotate.argtypes = [RT, I, I, I, I, RW, RW, VP, LL, I, VP]
+    lib.lf_paged_append_rotated.restype = I
+    lib.lf_paged_append_rotated.argtypes = [PG, I, VP, I, VP, VP, VP, VP, I, RT, VP, LL, I, VP, VP, VP]
     _lib = lib
     return lib
 
@@ -351,6 +373,30 @@ def lf_paged_take_errors(pages: LFPages, taken, stream=None) -> int:
     return _check(load_library().lf_paged_take_errors(ctypes.byref(pages), _ptr(taken), _stream(stream)))
 
 
+def lf_rotary_turns(frequency: Sequence[float]) -> list:
+    """Turns per position, in 2^-64 of a turn, of frequencies in radians per position."""
+    n = len(frequency)
+    turns = (ctypes.c_uint64 * n)()
+    _check(load_library().lf_rotary_turns((ctypes.c_double * n)(*frequency), n, turns))
+    return list(turns)
+
+
+def lf_rotate(rotary: LFRotaryTable, dtype, row_dim, seqs, tokens, q: LFRows, k: Optional[LFRows], positions,
+              axis_stride, inverse=False, stream=None) -> int:
+    return _check(load_library().lf_rotate(
+        ctypes.byref(rotary), _DTYPE[dtype] if isinstance(dtype, str) else int(dtype), row_dim, seqs, tokens,
+        ctypes.byref(q), None if k is None else ctypes.byref(k), _ptr(positions), axis_stride, int(bool(inverse)),
+        _stream(stream)))
+
+
+def lf_paged_append_rotated(pages: LFPages, batch, page_table, max_pages, lens, k_new, v_new, new_start, total_new,
+                            rotary: LFRotaryTable, positions, axis_stride, q_heads, q, q_out, stream=None) -> int:
+    return _check(load_library().lf_paged_append_rotated(
+        ctypes.byref(pages), batch, _ptr(page_table), max_pages, _ptr(lens), _ptr(k_new), _ptr(v_new),
+        _ptr(new_start), total_new, ctypes.byref(rotary), _ptr(positions), axis_stride, q_heads, _ptr(q), _ptr(q_out),
+        _stream(stream)))
+
+
 # ---- convenience owner ------------------------------------------------------
 
 class _DevArray:
@@ -473,6 +519,154 @@ class LFCache:
         }
 
 
+def _run_on(device, index, stream, held, call, *args):
+    """call(stream handle, *args) with the device and `stream` (None: the current one) current; a stream that the
+    caller names is known to the allocator as one that reads `held` and the tensors among args."""
+    if stream is None and torch.cuda.current_device() == index:
+        return call(torch._C._cuda_getCurrentRawStream(index), *args)
+    if isinstance(stream, int):
+        # 0, the default stream's handle, would make torch take a stream of its pool
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
+    if stream is not None and getattr(stream, "device", None) != device:
+        raise LFError(LF_ERR_ARG, f"stream: expected a stream of {device}, got {stream}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        if stream is not None:
+            for t in (*held, *args):
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(stream)
+        return call(torch._C._cuda_getCurrentRawStream(index), *args)
+
+
+def _cuda_device(device) -> torch.device:
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise LFError(LF_ERR_ARG, f"device: expected a CUDA device, got {device}")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+class LFRotary:
+    """Rotary positions of a model's heads: its frequencies, kept on the device, and the calls that rotate by them.
+
+    The first ``rotary_dim`` columns of a row are ``rotary_dim / 2`` pairs, columns ``(i, i + rotary_dim / 2)``, or
+    ``(2 i, 2 i + 1)`` if ``adjacent``.  Pair i turns by ``inv_freq[i]`` radians per position; without ``inv_freq`` by
+    ``base ** (-2 i / rotary_dim)``.  ``scale`` multiplies the turned columns.
+
+    Where tokens have a position on each of several axes (time, height, width), ``sections`` gives the number of
+    consecutive pairs of every axis, or ``axis`` each pair's axis.
+    """
+
+    def __init__(self, rotary_dim, base=10000.0, inv_freq=None, sections=None, axis=None, adjacent=False, scale=1.0,
+                 device=None):
+        if not isinstance(rotary_dim, int) or rotary_dim < 16 or rotary_dim % 16 or rotary_dim > 512:
+            raise LFError(LF_ERR_ARG, f"rotary_dim must be a multiple of 16 in [16, 512], got {rotary_dim}")
+        pairs = rotary_dim // 2
+        if inv_freq is None:
+            if not base > 0:
+                raise LFError(LF_ERR_ARG, f"base must be above 0, got {base}")
+            inv_freq = [float(base) ** (-2.0 * i / rotary_dim) for i in range(pairs)]
+        inv_freq = [float(f) for f in inv_freq]
+        if sections is not None:
+            if axis is not None:
+                raise LFError(LF_ERR_ARG, "sections and axis: at most one of them")
+            sections = [int(n) for n in sections]
+            if not 1 <= len(sections) <= _MAX_AXES or min(sections) < 0 or sum(sections) != pairs:
+                raise LFError(LF_ERR_ARG, f"sections: expected up to {_MAX_AXES} numbers of pairs that sum to {pairs}, "
+                                          f"got {sections}")
+            axis, self.axes = [a for a, n in enumerate(sections) for _ in range(n)], len(sections)
+        elif axis is not None:
+            axis = [int(a) for a in axis]
+            if axis and not 0 <= min(axis) <= max(axis) < _MAX_AXES:
+                raise LFError(LF_ERR_ARG, f"axis: expected axes in [0, {_MAX_AXES}), got {axis}")
+            self.axes = max(axis, default=0) + 1
+        else:
+            axis, self.axes = [0] * pairs, 1
+        if len(inv_freq) != pairs or len(axis) != pairs:
+            raise LFError(LF_ERR_ARG, f"expected {pairs} frequencies and axes, got {len(inv_freq)} and {len(axis)}")
+        if not math.isfinite(scale):
+            raise LFError(LF_ERR_ARG, f"scale must be finite, got {scale}")
+        turns = [t - 2**64 if t >= 2**63 else t for t in lf_rotary_turns(inv_freq)]
+        self.rotary_dim, self.adjacent, self.scale = rotary_dim, bool(adjacent), float(scale)
+        self.device = _cuda_device(device)
+        self._index = self.device.index
+        # copied from the host, which waits, so that no stream that uses them can come before it
+        if torch.cuda.is_current_stream_capturing():
+            raise LFError(LF_ERR_ARG, "make the rotary before the capture of a graph")
+        self._turns = torch.tensor(turns, dtype=torch.int64).to(self.device)
+        self._axis = torch.tensor(axis, dtype=torch.int32).to(self.device)
+        self._held = (self._turns, self._axis)
+        self._table = LFRotaryTable(rotary_dim, self.axes, int(self.adjacent), self.scale, self._turns.data_ptr(),
+                                    self._axis.data_ptr())
+        self._lib = load_library()
+
+    def _positions(self, positions, lead):
+        """The axis stride of positions [*lead], or [axes, *lead]."""
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 \
+                or positions.get_device() != self._index or not positions.is_contiguous() \
+                or (positions.shape != lead and positions.shape != (self.axes, *lead)):
+            got = (tuple(positions.shape), positions.dtype, str(positions.device)) \
+                if isinstance(positions, torch.Tensor) else type(positions)
+            raise LFError(LF_ERR_ARG, f"positions: expected contiguous torch.int32 {tuple(lead)} or "
+                                      f"{(self.axes, *lead)} on {self.device}, got {got}")
+        return 0 if positions.shape == lead else positions.numel() // self.axes
+
+    def _rows(self, x, y, name, dtype, lead):
+        """x and y (or None: a new tensor) as the C call takes them."""
+        for n, t in ((name, x), (name + "_out", y)):
+            if t is None and t is y:
+                continue
+            if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4) or t.dtype not in (torch.bfloat16, torch.float32) \
+                    or t.get_device() != self._index or (dtype is not None and t.dtype != dtype) \
+                    or (lead is not None and t.shape[:-2] != lead) or t.shape != x.shape \
+                    or (t.shape[-1] > 1 and t.stride(-1) != 1):
+                got = (tuple(t.shape), t.dtype, str(t.device)) if isinstance(t, torch.Tensor) else type(t)
+                raise LFError(LF_ERR_ARG, f"{n}: expected bf16 or fp32 rows [tokens][heads][dim] or [sequences][tokens]"
+                                          f"[heads][dim], of the call's type and tokens, on {self.device}, got {got}")
+        return x.shape[-2]
+
+    def rotate(self, q, positions, k=None, q_out=None, k_out=None, inverse=False, stream=None):
+        """lf_rotate: rows q [tokens][heads][dim] or [sequences][tokens][heads][dim], in any order in memory with
+        contiguous rows, and of k where it is given, by positions int32 [tokens] ([sequences][tokens]), or
+        [axes][...].  Returns q_out (a new tensor if None; q rotates in place), or (q_out, k_out) with k.
+        ``inverse`` turns back: the transpose, which takes a gradient of the result to that of the rows."""
+        q_heads = self._rows(q, q_out, "q", None, None)
+        lead, dim = q.shape[:-2], q.shape[-1]
+        k_heads = 0
+        if k is not None:
+            k_heads = self._rows(k, k_out, "k", q.dtype, lead)
+            if k.shape[-1] != dim:
+                raise LFError(LF_ERR_ARG, f"k: expected rows of q's {dim} columns, got {k.shape[-1]}")
+        elif k_out is not None:
+            raise LFError(LF_ERR_ARG, "k_out without k")
+        step = self._positions(positions, lead)
+        return _run_on(self.device, self._index, stream, self._held, self._rotate, q, positions, k, q_out, k_out,
+                       q_heads, k_heads, step, int(bool(inverse)))
+
+    def _rotate(self, st, q, positions, k, q_out, k_out, q_heads, k_heads, step, inverse):
+        seqs, tokens = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
+        if max(seqs, tokens) > _INT_MAX:
+            raise LFError(LF_ERR_ARG, f"need at most 2^31 - 1 tokens, got {seqs} x {tokens}")
+
+        def rows(x, y, heads):
+            sx, sy = ([st if n > 1 else 0 for n, st in zip(t.shape, t.stride())] for t in (x, y))
+            return LFRows(x.data_ptr(), y.data_ptr(), heads, sx[0] if len(sx) == 4 else 0, sx[-3], sx[-2],
+                          sy[0] if len(sy) == 4 else 0, sy[-3], sy[-2])
+
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k)
+        if q_heads == 0 or (k is not None and k_heads == 0):
+            raise LFError(LF_ERR_ARG, "rows without heads")
+        dtype = LF_BF16 if q.dtype == torch.bfloat16 else LF_F32
+        _check(self._lib.lf_rotate(
+            self._table, dtype, q.shape[-1], seqs, tokens, rows(q, q_out, q_heads),
+            None if k is None else rows(k, k_out, k_heads), positions.data_ptr(), step, inverse, st))
+        return q_out if k is None else (q_out, k_out)
+
+
 class LFPagedCache:
     """Paged K and V pools of a model's layers, and the calls that use them.
 
@@ -488,11 +682,7 @@ class LFPagedCache:
     """
 
     def __init__(self, layers, num_pages, page_size, kv_heads, head_dim, dtype="bf16", device=None):
-        device = torch.device("cuda" if device is None else device)
-        if device.type != "cuda":
-            raise LFError(LF_ERR_ARG, f"device: expected a CUDA device, got {device}")
-        if device.index is None:
-            device = torch.device("cuda", torch.cuda.current_device())
+        device = _cuda_device(device)
         if min(layers, num_pages, page_size, kv_heads, head_dim) < 1:
             raise LFError(LF_ERR_ARG, "layers, num_pages, page_size, kv_heads and head_dim must be >= 1")
         if dtype not in _DTYPE:
@@ -578,20 +768,7 @@ class LFPagedCache:
         """call(stream handle, *args) with this cache's device and `stream` current, so that
         what it allocates belongs to that stream.  The allocator is told that a stream which the caller
         names reads the tensors: they may be let go as soon as the call returns."""
-        if stream is None and torch.cuda.current_device() == self._index:
-            return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
-        if isinstance(stream, int):
-            # 0, the default stream's handle, would make torch take a stream of its pool
-            stream = (torch.cuda.ExternalStream(stream, device=self.device) if stream
-                      else torch.cuda.default_stream(self.device))
-        if stream is not None and getattr(stream, "device", None) != self.device:
-            raise LFError(LF_ERR_ARG, f"stream: expected a stream of {self.device}, got {stream}")
-        with torch.cuda.device(self._index), torch.cuda.stream(stream):
-            if stream is not None:
-                for t in (self.k, self.v, self.err, *args):
-                    if isinstance(t, torch.Tensor):
-                        t.record_stream(stream)
-            return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
+        return _run_on(self.device, self._index, stream, (self.k, self.v, self.err), call, *args)
 
     def _ask(self, call, pages, key):
         """The workspace that calls of this shape need, remembered (of the last few thousand shapes)."""
@@ -617,6 +794,42 @@ class LFPagedCache:
         _check(self._lib.lf_paged_append(
             pages, batch, page_table.data_ptr(), width, lens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
             None if new_start is None else new_start.data_ptr(), n, st))
+
+    def append_rotated(self, layer, k_new, v_new, page_table, lens, rotary, new_start=None, positions=None, q=None,
+                       q_out=None, stream=None):
+        """lf_paged_append_rotated: ``append`` with the rows of k_new rotated by ``rotary`` (an LFRotary) on the way,
+        and q [tokens][q_heads][head_dim] into q_out (a new tensor if None; q rotates in place), which is returned.
+        positions int32 [tokens] or [axes][tokens], or None: each token's position in the cache."""
+        pages = self._layer(layer)
+        batch, width = self._sequences(page_table, lens)
+        if not isinstance(rotary, LFRotary) or rotary.device != self.device:
+            raise LFError(LF_ERR_ARG, f"rotary: expected an LFRotary on {self.device}, got {rotary}")
+        n = batch if new_start is None else self._sizes(k_new, "k_new", 3)[0]
+        self._expect(k_new, "k_new", self.dtype, (n, *self._row))
+        self._expect(v_new, "v_new", self.dtype, (n, *self._row))
+        if new_start is not None:
+            self._expect(new_start, "new_start", torch.int32, (batch + 1,))
+        self._numbers(n)
+        step = 0 if positions is None else rotary._positions(positions, (n,))
+        q_heads = 0
+        if q is not None:
+            q_heads = self._sizes(q, "q", 3)[1]
+            self._expect(q, "q", self.dtype, (n, q_heads, self.head_dim))
+            if q_out is not None:
+                self._expect(q_out, "q_out", self.dtype, q.shape)
+        elif q_out is not None:
+            raise LFError(LF_ERR_ARG, "q_out without q")
+        return self._run(stream, self._append_rotated, pages, batch, width, page_table, lens, k_new, v_new, new_start,
+                         n, rotary, *rotary._held, positions, step, q_heads, q, q_out)
+
+    def _append_rotated(self, st, pages, batch, width, page_table, lens, k_new, v_new, new_start, n, rotary, _turns,
+                        _axis, positions, step, q_heads, q, q_out):
+        if q is not None and q_out is None:
+            q_out = torch.empty_like(q)
+        _check(self._lib.lf_paged_append_rotated(
+            pages, batch, page_table.data_ptr(), width, lens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+            _ptr(new_start), n, rotary._table, _ptr(positions), step, q_heads, _ptr(q), _ptr(q_out), st))
+        return q_out
 
     def decode(self, layer, q, page_table, lens, k_new=None, v_new=None, window=0, sinks=0, out=None,
                lse=None, stream=None):

@@ -72,7 +72,7 @@
 extern "C" {
 #endif
 
-#define LF_ABI_VERSION 8
+#define LF_ABI_VERSION 9
 
 typedef struct lf_cache lf_cache; /* opaque; owns the slab */
 
@@ -493,6 +493,65 @@ int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, i
  */
 int lf_paged_take_errors(const lf_pages* pages, int32_t* taken, lf_stream_t stream);
 
+/*
+ * Rotary positions (no counterpart on the pages).  Of a row's first rotary_dim columns the two of pair i
+ * turn by frequency_i * position: (x_a, x_b) becomes (x_a cos - x_b sin, x_b cos + x_a sin) * scale.  The
+ * other columns are copied.  Pair i is columns (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with adjacent = 1.
+ *
+ * With several axes (of images and video: time, height, width) a token has a position on each, and
+ * axis[i] says which one pair i turns by.  Positions are int32 and may be negative.
+ *
+ * Angles are exact modulo a turn: a frequency is held in 2^-64 of a turn per position, so that an angle is off
+ * by 2^-34 of a turn at the farthest position.  Cosines, sines and products are fp32, outputs are rounded once (RNE).
+ */
+#define LF_ROTARY_MAX_AXES 4
+typedef struct lf_rotary {
+  int rotary_dim;         /* a multiple of 16, at most the rows' columns */
+  int axes;               /* 1 .. LF_ROTARY_MAX_AXES */
+  int adjacent;           /* 0 or 1, above */
+  float scale;            /* of the columns that turn; 1: a rotation */
+  const uint64_t* turns;  /* device [rotary_dim / 2], from lf_rotary_turns; 8-byte aligned */
+  const int32_t* axis;    /* device [rotary_dim / 2], each in [0, axes) (others count as the nearest); not read
+                             with one axis; NULL: axis 0 */
+} lf_rotary;
+
+/* turns[i] = frequency[i] (radians per position) in 2^-64 of a turn, rounded to nearest.  Host memory; finite
+ * frequencies of up to 1024 in size. */
+int lf_rotary_turns(const double* frequency, int pairs, uint64_t* turns);
+
+/* Rows to rotate: row (s, t, h) of row_dim columns starts at element s * x_seq + t * x_token + h * x_head of x and goes
+ * to the same of y.  16-byte aligned, strides multiples of 16 bytes.  y may be x, with its strides; otherwise what is
+ * written overlaps nothing that is read. */
+typedef struct lf_rows {
+  const void* x;
+  void* y;
+  int heads;
+  int64_t x_seq, x_token, x_head, y_seq, y_token, y_head;   /* elements, >= 0 */
+} lf_rows;
+
+/*
+ * Rotate the rows of q, and of k where that is not NULL, of seqs x tokens tokens.
+ *   row_dim      columns of a row: a multiple of 16 up to 512
+ *   positions    device [axes][seqs * tokens], axis_stride elements from axis to axis (0: one set for every axis)
+ *   inverse      1: by the negative angle (the transpose: takes a gradient with respect to y to that of x)
+ * One launch, bound by HBM.
+ */
+int lf_rotate(const lf_rotary* rotary, int dtype, int row_dim, int seqs, int tokens, const lf_rows* q, const lf_rows* k,
+              const int32_t* positions, int64_t axis_stride, int inverse, lf_stream_t stream);
+
+/*
+ * lf_paged_append with the rotation on the way: k_new's rows are rotated, v_new's are copied.  Queries of the
+ * same tokens, q [total_new][q_heads][head_dim], are rotated into q_out (which may be q); both NULL: none.  Rows that belong
+ * to no sequence are neither stored nor written to q_out.
+ *   positions    device [axes][total_new], axis_stride elements from axis to axis (0: one set); NULL: each token's
+ *                position in the cache, on every axis
+ * One launch.
+ */
+int lf_paged_append_rotated(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
+                            const int32_t* lens, const void* k_new, const void* v_new, const int32_t* new_start,
+                            int total_new, const lf_rotary* rotary, const int32_t* positions, int64_t axis_stride,
+                            int q_heads, const void* q, void* q_out, lf_stream_t stream);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* lf_last_error(void);
 
@@ -501,7 +560,7 @@ const char* lf_last_error(void);
  * LF_ERR_UNSUPPORTED, LF_ERR_OOM (the slab does not fit in device memory) or
  * LF_ERR_CUDA.  It keeps its value until the next failure, or until one of
  * lf_cache_create*, lf_cache_destroy, lf_prefill_fill, lf_prefill_fill_noalloc,
- * lf_cache_check, lf_cache_layout and lf_paged_* resets it (with the message) on entry. */
+ * lf_cache_check, lf_cache_layout, lf_paged_*, lf_rotary_turns and lf_rotate resets it (with the message) on entry. */
 int lf_last_status(void);
 
 /* LF_ABI_VERSION of the loaded library. */
