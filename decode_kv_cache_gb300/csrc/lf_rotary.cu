@@ -11,21 +11,27 @@
 // of a turn for each position.  Its nearest quarter is taken off as an integer too, and sincospif gets the rest,
 // at most an eighth of a turn, rounded to 2^-25 of itself.
 //
-// Work.  A row's eight columns and the eight that they turn with make an item, which one thread reads, turns
-// and writes (so that a tensor may be rotated in place); its pairs' cosines and sines are the same for every head of the
-// token and stay in its registers.  A warp takes a token, or a slice of the token's heads where there are
-// few tokens: its lanes first ask for their first items, then look up where the token goes and what
-// its position is, share the token's sines through shared memory, and go on.  Bound by HBM: every
-// row is read and written once.
+// Work.  Two 16-byte chunks of a row make an item, which one thread reads, turns and writes: those that turn with
+// each other where pairs are half a row apart, so that a tensor may be rotated in place.  Neighbouring lanes take neighbouring
+// chunks (with 32 bytes a lane fp32 read half sectors: 17 slab prompts 20 us instead of 12).  An item's cosines and sines are the
+// same for every head of the token and stay in registers.  A warp takes a token, a slice of its heads where
+// there are few tokens, or a few tokens where they are short.  Its lanes first ask for their first items (a ring of
+// cp.async copies), then look up where the tokens go and what their positions are, share the sines through shared
+// memory, and go on.  Warps that walked the whole call with such a ring were slower (32 prompts 129 us against 110):
+// their lookups come one after another, those of fresh warps side by side.
+//
+// Bound by HBM: every row is read and written once.  Measured, other inputs every time, of a plain copy's 6.77 TB/s:
+// 32 prompts, 34 thousand tokens of 48 rows of 128 bf16 columns, 110 us, 97 %; 16000 video tokens of 40 rows 52.8 us, 92 %; 17
+// slab prompts of 1000 fp32 tokens 12.1 us, 85 %; two prompts of 6000 video tokens 37.5 us, 78 % (start and end of two waves of warps);
+// a step of 64 sequences 3.1 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <climits>
 #include <cmath>
 
-#include "lf_device.cuh"
 #include "lf_kernels.h"
-#include "lf_paged.h"
+#include "lf_paged.cuh"
 #include "lf_paged_host.h"
 #include "longflow.h"
 
@@ -34,8 +40,16 @@ namespace lf {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kMaxRow = 512;         // columns of a row: an item for each lane at most
-constexpr int kMaxPairs = kMaxRow / 2;
+constexpr int kMaxRowBytes = 1024;   // an item of 32 bytes for each lane at most
+constexpr int kMaxPairs = kMaxRowBytes / 4;
+constexpr int kMaxTokens = 4;        // of a warp: a lane for each position of each axis
+constexpr int kDepth = 4;            // steps of a thread's ring; 6 and 8 were 0 to 6 % slower
+constexpr int kFill = 16;            // warps of an SM that there should be
+
+// Blocks on an SM: three leave bf16 85 registers a thread (32 prompts 110 us, four 113), fp32, which holds fewer
+// cosines, does with 64 (17 slab prompts 12.1 us, three blocks 13.8).
+template <typename T>
+constexpr int blocks_of() { return sizeof(T) == 2 ? 3 : 4; }
 
 struct RotaryRows {                  // strides in bytes
   const char* x;
@@ -57,43 +71,22 @@ struct RotaryArgs {
   int items, heads_at_once;          // items of a row, heads that a warp's lanes cover
   int64_t tokens;
   int tokens_per_seq;                // not paged
-  int slices, steps;                 // warps of a token, steps of heads_at_once heads in all
+  int slices, steps, per_warp;       // warps of a token, steps of heads_at_once heads in all; tokens of a warp
   PagedPool pool;                    // paged
   const int32_t* new_start;          // paged: [batch + 1], or null: one token per sequence
 };
 
-// The sequence that token t of a paged call belongs to and its place in the pools, for the whole warp together.
-// *row: the token is one of a sequence's, *offset: where its rows go, -1: nowhere.
-__device__ __forceinline__ void find_token(const RotaryArgs& a, int t, int lane, bool* row, int64_t* pos,
-                                           int64_t* offset) {
-  int b = t, first = t, end = t + 1;
-  if (a.new_start) {
-    int lo = 0, n = a.pool.batch;    // the last sequence of [lo, lo + n) that starts at or before t
-    do {
-      const int step = (n + 31) / 32, i = lane * step;
-      const bool in = i < n;
-      const int k = __popc(__ballot_sync(0xffffffffu, in && (lane == 0 || a.new_start[lo + i] <= t))) - 1;
-      lo += k * step;
-      n = min(step, n - k * step);
-    } while (n > 1);
-    b = lo;
-    first = a.new_start[b];
-    end = a.new_start[b + 1];
-  }
-  *offset = -1;
-  *pos = 0;
-  *row = first >= 0 && end >= first && end <= a.tokens && t >= first && t < end;
-  if (!*row) return;
-  *pos = (int64_t)a.pool.lens[b] - end + t;
-  bool ok = *pos >= 0 && *pos < (int64_t)a.pool.max_pages * a.pool.page_size;
-  if (ok) {
-    int pi, slot;
-    paged_split(a.pool, (int)*pos, &pi, &slot);
-    const int page = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
-    ok = page >= 0 && page < a.pool.num_pages;
-    if (ok) *offset = page * a.pool.page_stride + slot * a.pool.token_stride;
-  }
-  if (!ok && lane == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+// The sequence whose rows token t of a paged call lies behind the start of, for the whole warp together.
+__device__ __forceinline__ int find_sequence(const RotaryArgs& a, int t, int lane) {
+  int lo = 0, n = a.pool.batch;    // the last sequence of [lo, lo + n) that starts at or before t
+  do {
+    const int step = (n + 31) / 32, i = lane * step;
+    const bool in = i < n;
+    const int k = __popc(__ballot_sync(0xffffffffu, in && (lane == 0 || a.new_start[lo + i] <= t))) - 1;
+    lo += k * step;
+    n = min(step, n - k * step);
+  } while (n > 1);
+  return lo;
 }
 
 // Cosine and sine of a position's angle, given as turns per position (2^-64 of a turn).
@@ -110,8 +103,9 @@ __device__ __forceinline__ float2 turn_of(uint64_t per_position, int64_t positio
   return quarter & 2 ? make_float2(-c, -s) : make_float2(c, s);
 }
 
-__device__ __forceinline__ void unpack(const uint4 (&x)[1], float (&f)[8]) {
-  const uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+// A 16-byte chunk as floats, and back.
+__device__ __forceinline__ void unpack(const uint4& x, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 y = bf2_to_f2(w[i]);
@@ -119,161 +113,226 @@ __device__ __forceinline__ void unpack(const uint4 (&x)[1], float (&f)[8]) {
     f[2 * i + 1] = y.y;
   }
 }
-__device__ __forceinline__ void unpack(const uint4 (&x)[2], float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    f[4 * i] = __uint_as_float(x[i].x);
-    f[4 * i + 1] = __uint_as_float(x[i].y);
-    f[4 * i + 2] = __uint_as_float(x[i].z);
-    f[4 * i + 3] = __uint_as_float(x[i].w);
-  }
+__device__ __forceinline__ void unpack(const uint4& x, float (&f)[4]) {
+  f[0] = __uint_as_float(x.x);
+  f[1] = __uint_as_float(x.y);
+  f[2] = __uint_as_float(x.z);
+  f[3] = __uint_as_float(x.w);
 }
-__device__ __forceinline__ uint32_t two_bf16(float x, float y) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
-  return r;
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
 }
-__device__ __forceinline__ void pack(const float (&f)[8], uint4 (&x)[1]) {
-  x[0] = make_uint4(two_bf16(f[0], f[1]), two_bf16(f[2], f[3]), two_bf16(f[4], f[5]), two_bf16(f[6], f[7]));
-}
-__device__ __forceinline__ void pack(const float (&f)[8], uint4 (&x)[2]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    x[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
-                      __float_as_uint(f[4 * i + 3]));
+__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
 template <typename T, bool kPaged, bool kAdjacent>
-__global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-  constexpr int W = sizeof(T) / 2;         // 16-byte words of eight columns
-  constexpr int U = 4 / W;                 // items under way per thread
+__global__ void __launch_bounds__(kWarps * 32, blocks_of<T>()) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+  constexpr int E = 16 / sizeof(T);        // columns of a chunk
   __shared__ float2 s_turn[kWarps][kMaxPairs];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
+  const unsigned id = blockIdx.x * kWarps + warp;
   if constexpr (kPaged) {
     if (a.new_start && a.pool.err)   // a sequence whose starts are wrong may have no token that finds it
-      for (int64_t b = id * 32 + lane; b < a.pool.batch; b += (int64_t)gridDim.x * kWarps * 32) {
+      for (int64_t b = (int64_t)id * 32 + lane; b < a.pool.batch; b += (int64_t)gridDim.x * kWarps * 32) {
         const int first = a.new_start[b], end = a.new_start[b + 1];
         if (first < 0 || end < first || end > a.tokens) atomicOr(a.pool.err, LF_DEVERR_STATE);
       }
   }
-  const int64_t t = id / a.slices;
-  const int slice = (int)(id - t * a.slices);
-  if (t >= a.tokens) return;
-  const int from = (int)((int64_t)a.steps * slice / a.slices), to = (int)((int64_t)a.steps * (slice + 1) / a.slices);
+  // Tokens t0 .. t0 + nt - 1, of each a slice of the heads.
+  const unsigned group = id / (unsigned)a.slices;
+  const int slice = (int)(id - group * a.slices);
+  const int64_t t0 = (int64_t)group * a.per_warp;
+  if (t0 >= a.tokens) return;
+  const int nt = (int)min((int64_t)a.per_warp, a.tokens - t0);
+  const int from = a.steps * slice / a.slices, to = a.steps * (slice + 1) / a.slices;
 
-  // This thread's item: eight columns at lo and eight at hi, in bytes.
+  // This thread's item: the chunks at bytes `one` and `two` of a row.  Lanes take chunks in a row, so that what
+  // an instruction reads or writes is whole sectors.
   const int item = lane % a.items, first_head = lane / a.items;
-  const int turning = a.half / 8;          // items that turn
+  const int turning = a.half / E;          // items that turn
   const bool turns = item < turning;
-  int lo = 16 * item, hi = lo + 8;
-  if (!kAdjacent && turns) {
-    lo = 8 * item;
-    hi = a.half + lo;
-  }
-  const int64_t seq = kPaged ? 0 : t / a.tokens_per_seq, ti = kPaged ? t : t - seq * a.tokens_per_seq;
-  const char* qx = a.q.x + seq * a.q.xs + ti * a.q.xt;
-  const char* kx = a.k.x + seq * a.k.xs + ti * a.k.xt;
-  const char* vx = a.v + ti * a.k.xt;
+  const int at_one = turns ? item : turning + item, at_two = at_one + (turns ? turning : a.items - turning);
+  const int one = 16 * at_one, two = 16 * at_two;
   const int all = a.q.heads + a.k.heads * (kPaged ? 2 : 1);
   auto head_of = [&](int step) {           // of q, k and v in this order; -1: none
     const int h = step * a.heads_at_once + first_head;
     return first_head < a.heads_at_once && h < all ? h : -1;
   };
-  uint4 xl[U][W], xh[U][W];
-  auto load = [&](int step) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = step + u < to ? head_of(step + u) : -1, g = h - a.q.heads;
-      if (h < 0) continue;
-      const char* row = h < a.q.heads ? qx + h * a.q.xh : g < a.k.heads ? kx + g * a.k.xh : vx + (g - a.k.heads) * a.k.xh;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        xl[u][w] = __ldcs(reinterpret_cast<const uint4*>(row + lo * (int)sizeof(T)) + w);
-        xh[u][w] = __ldcs(reinterpret_cast<const uint4*>(row + hi * (int)sizeof(T)) + w);
-      }
+
+  // A ring of kDepth steps, of which each thread reads only what it has copied itself.  It is filled before
+  // the lookups and runs on from token to token.
+  extern __shared__ uint4 s_ring[];
+  uint4* ring = s_ring + warp * (kDepth * 2 * 32) + lane;
+  int64_t seq = 0, ti = t0;
+  if (!kPaged) {
+    seq = (unsigned)t0 / (unsigned)a.tokens_per_seq;
+    ti = t0 - seq * a.tokens_per_seq;
+  }
+  struct Cursor { int64_t seq, ti; };
+  auto advance = [&](Cursor& c) {
+    if (++c.ti == a.tokens_per_seq) {
+      c.ti = 0;
+      ++c.seq;
     }
   };
-  load(from);
-
-  bool row = true;
-  int64_t cache_pos = 0, offset = -1;
-  if constexpr (kPaged) find_token(a, (int)t, lane, &row, &cache_pos, &offset);
-  if (!row) return;                        // of no sequence: left as it is
-  for (int i = lane; i < a.half; i += 32) {
-    int64_t p = cache_pos;
-    if (a.positions) {
-      const int ax = a.axis ? min(max(a.axis[i], 0), a.axes - 1) : 0;
-      p = a.positions[ax * a.axis_stride + t];
+  Cursor in{seq, ti};
+  int next = from, next_token = 0;
+  const char *qx, *kx, *vx;
+  auto open = [&]() {
+    qx = a.q.x + in.seq * a.q.xs + in.ti * a.q.xt;
+    kx = a.k.x + in.seq * a.k.xs + in.ti * a.k.xt;
+    vx = a.v + in.ti * a.k.xt;
+  };
+  open();
+  auto issue = [&](int stage) {
+    if (next_token < nt) {
+      const int h = head_of(next), g = h - a.q.heads;
+      if (h >= 0) {
+        const char* row = h < a.q.heads ? qx + h * a.q.xh : g < a.k.heads ? kx + g * a.k.xh : vx + (g - a.k.heads) * a.k.xh;
+        cp_async16(smem_u32(ring + 64 * stage), row + one, 1);
+        cp_async16(smem_u32(ring + 64 * stage + 32), row + two, 1);
+      }
+      if (++next == to) {
+        next = from;
+        ++next_token;
+        advance(in);
+        open();
+      }
     }
-    float2 y = turn_of(a.turns[i], a.inverse ? -p : p);
-    y.x *= a.scale;
-    y.y *= a.scale;
-    s_turn[warp][i] = y;
+    cp_async_commit();   // a group per step, empty ones at the end
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) issue(i);
+
+  // Lane j looks up where token j goes, and lane axis * nt + j what its position on an axis is.
+  bool mine = true;                        // of some sequence: others are left as they are
+  int64_t offset = -1;                     // of its rows in the pools, -1: not stored
+  int pos = 0;
+  if constexpr (kPaged) {
+    int b = (int)t0 + lane, first = b, end = b + 1;
+    if (a.new_start) {
+      int f = 0, e = 0, bs = 0;
+      for (int j = 0; j < nt; ++j) {       // tokens in a row are most often of one sequence
+        const int t = (int)t0 + j;
+        if (j == 0 || t < f || t >= e) {
+          bs = find_sequence(a, t, lane);
+          f = a.new_start[bs];
+          e = a.new_start[bs + 1];
+        }
+        if (lane == j) {
+          b = bs;
+          first = f;
+          end = e;
+        }
+      }
+    }
+    const int t = (int)t0 + lane;
+    mine = lane < nt && first >= 0 && end >= first && end <= a.tokens && t >= first && t < end;
+    if (mine) {
+      const int64_t at = (int64_t)a.pool.lens[b] - end + t;
+      pos = (int)at;
+      bool ok = at >= 0 && at < (int64_t)a.pool.max_pages * a.pool.page_size;
+      if (ok) {
+        int pi, slot;
+        paged_split(a.pool, pos, &pi, &slot);
+        const int page = a.pool.table[(int64_t)b * a.pool.max_pages + pi];
+        ok = page >= 0 && page < a.pool.num_pages;
+        if (ok) offset = page * a.pool.page_stride + slot * a.pool.token_stride;
+      }
+      if (!ok && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+    }
+  }
+  if (a.positions && lane < a.axes * nt) pos = a.positions[lane / nt * a.axis_stride + t0 + lane % nt];
+  for (int i0 = 0; i0 < a.half; i0 += 32) {
+    const int i = i0 + lane;
+    const uint64_t per_position = i < a.half ? a.turns[i] : 0;
+    int ax = 0;
+    if (a.positions && a.axis && i < a.half) ax = min(max(a.axis[i], 0), a.axes - 1);
+    for (int j = 0; j < nt; ++j) {
+      const int64_t p = __shfl_sync(0xffffffffu, pos, ax * nt + j);
+      if (i < a.half) {
+        float2 y = turn_of(per_position, a.inverse ? -p : p);
+        y.x *= a.scale;
+        y.y *= a.scale;
+        s_turn[warp][j * a.half + i] = y;
+      }
+    }
   }
   __syncwarp();
-  float c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float2 y = turns ? s_turn[warp][8 * item + e] : make_float2(1.f, 0.f);
-    c[e] = y.x;
-    s[e] = y.y;
-  }
 
-  char* qy = a.q.y + seq * a.q.ys + ti * a.q.yt;
-  char* ky = kPaged ? a.pool.k + offset : a.k.y + seq * a.k.ys + ti * a.k.yt;
-  char* vy = kPaged ? a.pool.v + offset : nullptr;
-  const int64_t kyh = kPaged ? a.pool.head_stride : a.k.yh;
-  for (int step = from;;) {
+  Cursor at{seq, ti};
+  int stage = 0;
+#pragma unroll 1
+  for (int j = 0; j < nt; ++j) {
+    float c[E], s[E];                      // of the pairs of both chunks
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = step + u < to ? head_of(step + u) : -1, g = h - a.q.heads;
-      if (h < 0 || (kPaged && g >= 0 && offset < 0)) continue;
+    for (int e = 0; e < E; ++e) {
+      const int i = !kAdjacent ? E * item + e : e < E / 2 ? E / 2 * at_one + e : E / 2 * at_two + e - E / 2;
+      const float2 y = turns ? s_turn[warp][j * a.half + i] : make_float2(1.f, 0.f);
+      c[e] = y.x;
+      s[e] = y.y;
+    }
+    const int64_t off = kPaged ? __shfl_sync(0xffffffffu, offset, j) : 0;
+    const bool row = kPaged ? __shfl_sync(0xffffffffu, (int)mine, j) != 0 : true;
+    char* qy = a.q.y + at.seq * a.q.ys + at.ti * a.q.yt;
+    char* ky = kPaged ? a.pool.k + off : a.k.y + at.seq * a.k.ys + at.ti * a.k.yt;
+    char* vy = kPaged ? a.pool.v + off : nullptr;
+    const int64_t kyh = kPaged ? a.pool.head_stride : a.k.yh;
+#pragma unroll 1
+    for (int step = from; step < to; ++step) {
+      const int h = head_of(step), g = h - a.q.heads;
+      cp_async_wait<kDepth - 1>();
+      uint4 x = ring[64 * stage], y = ring[64 * stage + 32];
       if (turns && g < a.k.heads) {
-        float l[8], r[8], yl[8], yr[8];
-        unpack(xl[u], l);
-        unpack(xh[u], r);
+        float p[E], q[E], u[E], v[E];
+        unpack(x, p);
+        unpack(y, q);
         if constexpr (kAdjacent) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            yl[2 * e] = l[2 * e] * c[e] - l[2 * e + 1] * s[e];
-            yl[2 * e + 1] = l[2 * e + 1] * c[e] + l[2 * e] * s[e];
-            yr[2 * e] = r[2 * e] * c[4 + e] - r[2 * e + 1] * s[4 + e];
-            yr[2 * e + 1] = r[2 * e + 1] * c[4 + e] + r[2 * e] * s[4 + e];
+          for (int e = 0; e < E / 2; ++e) {
+            u[2 * e] = p[2 * e] * c[e] - p[2 * e + 1] * s[e];
+            u[2 * e + 1] = p[2 * e + 1] * c[e] + p[2 * e] * s[e];
+            v[2 * e] = q[2 * e] * c[E / 2 + e] - q[2 * e + 1] * s[E / 2 + e];
+            v[2 * e + 1] = q[2 * e + 1] * c[E / 2 + e] + q[2 * e] * s[E / 2 + e];
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            yl[e] = l[e] * c[e] - r[e] * s[e];
-            yr[e] = r[e] * c[e] + l[e] * s[e];
+          for (int e = 0; e < E; ++e) {
+            u[e] = p[e] * c[e] - q[e] * s[e];
+            v[e] = q[e] * c[e] + p[e] * s[e];
           }
         }
-        pack(yl, xl[u]);
-        pack(yr, xh[u]);
+        x = pack(u);
+        y = pack(v);
       }
-      char* out = h < a.q.heads ? qy + h * a.q.yh : g < a.k.heads ? ky + g * kyh : vy + (g - a.k.heads) * kyh;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        *(reinterpret_cast<uint4*>(out + lo * (int)sizeof(T)) + w) = xl[u][w];
-        *(reinterpret_cast<uint4*>(out + hi * (int)sizeof(T)) + w) = xh[u][w];
+      if (h >= 0 && row && !(kPaged && g >= 0 && off < 0)) {
+        char* out = h < a.q.heads ? qy + h * a.q.yh : g < a.k.heads ? ky + g * kyh : vy + (g - a.k.heads) * kyh;
+        *reinterpret_cast<uint4*>(out + one) = x;
+        *reinterpret_cast<uint4*>(out + two) = y;
       }
+      issue(stage);
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
     }
-    step += U;
-    if (step >= to) break;
-    load(step);
+    advance(at);
   }
 }
 
 template <typename T, bool kPaged>
 cudaError_t launch(const RotaryArgs& a, int adjacent, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((a.tokens * a.slices + kWarps - 1) / kWarps);
-  if (adjacent) rotary_kernel<T, kPaged, true><<<grid, kWarps * 32, 0, stream>>>(a);
-  else rotary_kernel<T, kPaged, false><<<grid, kWarps * 32, 0, stream>>>(a);
+  constexpr int kSmem = kWarps * kDepth * 2 * 32 * 16;
+  const int64_t warps = (a.tokens + a.per_warp - 1) / a.per_warp * a.slices;
+  const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
+  auto* kernel = adjacent ? &rotary_kernel<T, kPaged, true> : &rotary_kernel<T, kPaged, false>;
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kSmem, done[adjacent]);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kWarps * 32, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
 // Everything that does not depend on where the rows lie.
-int take_rotary(const lf_rotary* r, int row_dim, const int32_t* positions, int64_t axis_stride, RotaryArgs* a) {
+int take_rotary(const lf_rotary* r, int row_dim, int elem, const int32_t* positions, int64_t axis_stride, RotaryArgs* a) {
   if (!r) return fail(LF_ERR_ARG, "null rotary");
   if (r->rotary_dim < 16 || r->rotary_dim % 16 != 0 || r->rotary_dim > row_dim)
     return fail(LF_ERR_ARG, "rotary_dim (%d) must be a multiple of 16 and at most the rows' %d columns", r->rotary_dim,
@@ -296,7 +355,7 @@ int take_rotary(const lf_rotary* r, int row_dim, const int32_t* positions, int64
   a->inverse = 0;
   a->q = a->k = RotaryRows{};
   a->v = nullptr;
-  a->items = row_dim / 16;
+  a->items = row_dim * elem / 32;
   a->heads_at_once = 32 / a->items;
   a->pool = PagedPool{};
   a->new_start = nullptr;
@@ -304,7 +363,7 @@ int take_rotary(const lf_rotary* r, int row_dim, const int32_t* positions, int64
 }
 
 // Rows of lf_rotate; `rows` may be null for none.
-int take_rows(const lf_rows* rows, const char* name, int elem, RotaryRows* out) {
+int rows_to_turn(const lf_rows* rows, const char* name, int elem, RotaryRows* out) {
   if (!rows) return LF_OK;
   if (rows->heads < 1 || rows->heads > 65535) return fail(LF_ERR_ARG, "%s: heads must be in [1, 65535]", name);
   if (!rows->x || !rows->y || !aligned16(rows->x) || !aligned16(rows->y))
@@ -318,14 +377,21 @@ int take_rows(const lf_rows* rows, const char* name, int elem, RotaryRows* out) 
   return LF_OK;
 }
 
-// How many warps a token gets: as many as it takes to fill the GPU with warps.
+// How many warps a token gets, or how many tokens a warp: enough warps to fill the GPU, and then, where a token has
+// few steps, several tokens that look things up together (17 slab prompts of 1000 fp32 tokens, two steps each: four
+// tokens 12.1 us, one 14.2; two video prompts of 6000, eight steps: two tokens 37.5, one 37.9).
 int take_slices(RotaryArgs* a, int heads) {
   int sms = 0;
   const int rc = sm_count(&sms);
   if (rc != LF_OK) return rc;
+  const int64_t warps = (int64_t)sms * kFill;
   a->steps = (heads + a->heads_at_once - 1) / a->heads_at_once;
-  const int64_t want = ((int64_t)sms * 32 + a->tokens - 1) / a->tokens;
+  const int64_t want = (warps + a->tokens - 1) / a->tokens;
   a->slices = (int)(want < a->steps ? want : a->steps);
+  a->per_warp = 1;
+  while (a->slices == 1 && 2 * a->per_warp <= kMaxTokens && 2 * a->per_warp * a->steps <= 16 &&
+         2 * a->per_warp * a->half <= kMaxPairs && a->tokens >= warps * 2 * a->per_warp)
+    a->per_warp *= 2;
   return LF_OK;
 }
 
@@ -378,18 +444,18 @@ int lf_rotate(const lf_rotary* rotary, int dtype, int row_dim, int seqs, int tok
               const int32_t* positions, int64_t axis_stride, int inverse, lf_stream_t stream) {
   lf::clear_last_error();
   if (dtype != LF_BF16 && dtype != LF_F32) return fail(LF_ERR_ARG, "dtype must be LF_BF16 or LF_F32");
-  if (row_dim < 16 || row_dim % 16 != 0 || row_dim > lf::kMaxRow)
-    return fail(LF_ERR_ARG, "row_dim (%d) must be a multiple of 16 in [16, %d]", row_dim, lf::kMaxRow);
+  const int elem = dtype == LF_BF16 ? 2 : 4;
+  if (row_dim < 16 || row_dim % 16 != 0 || row_dim * (int64_t)elem > lf::kMaxRowBytes)
+    return fail(LF_ERR_ARG, "row_dim (%d) must be a multiple of 16 in [16, %d]", row_dim, lf::kMaxRowBytes / elem);
   lf::RotaryArgs a;
-  int rc = lf::take_rotary(rotary, row_dim, positions, axis_stride, &a);
+  int rc = lf::take_rotary(rotary, row_dim, elem, positions, axis_stride, &a);
   if (rc != LF_OK) return rc;
   if (seqs < 0 || tokens < 0 || (int64_t)seqs * tokens > INT_MAX)
     return fail(LF_ERR_ARG, "need seqs, tokens >= 0 and seqs * tokens below 2^31");
   if (inverse != 0 && inverse != 1) return fail(LF_ERR_ARG, "inverse must be 0 or 1");
   if (!q) return fail(LF_ERR_ARG, "null q");
-  const int elem = dtype == LF_BF16 ? 2 : 4;
   if (seqs == 0 || tokens == 0) return LF_OK;
-  if ((rc = lf::take_rows(q, "q", elem, &a.q)) != LF_OK || (rc = lf::take_rows(k, "k", elem, &a.k)) != LF_OK) return rc;
+  if ((rc = lf::rows_to_turn(q, "q", elem, &a.q)) != LF_OK || (rc = lf::rows_to_turn(k, "k", elem, &a.k)) != LF_OK) return rc;
   if (!positions) return fail(LF_ERR_ARG, "null positions");
   a.inverse = inverse;
   a.tokens = (int64_t)seqs * tokens;
@@ -409,7 +475,7 @@ int lf_paged_append_rotated(const lf_pages* pages, int batch, const int32_t* pag
   lf::PagedPool pool;
   lf::RotaryArgs a;
   int rc = lf::take_pool(pages, batch, page_table, max_pages, lens, &pool);
-  if (rc != LF_OK || (rc = lf::take_rotary(rotary, pages->head_dim, positions, axis_stride, &a)) != LF_OK) return rc;
+  if (rc != LF_OK || (rc = lf::take_rotary(rotary, pages->head_dim, lf::elem_bytes(pages), positions, axis_stride, &a)) != LF_OK) return rc;
   if (total_new < 0) return fail(LF_ERR_ARG, "total_new < 0");
   if (!new_start && total_new != batch)
     return fail(LF_ERR_ARG, "without new_start every sequence takes one token: total_new (%d) must "

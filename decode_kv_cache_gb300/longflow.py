@@ -547,6 +547,19 @@ def _cuda_device(device) -> torch.device:
     return device
 
 
+_ROW_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _rows(x, y) -> LFRows:
+    """Rows of x, to be written to y of the same shape.  A size of one has no use for its stride."""
+    shape, sx, sy = x.shape, x.stride(), y.stride()
+    if 1 in shape:
+        sx, sy = ([s if n > 1 else 0 for n, s in zip(shape, st)] for st in (sx, sy))
+    if len(shape) == 3:
+        return LFRows(x.data_ptr(), y.data_ptr(), shape[1], 0, sx[0], sx[1], 0, sy[0], sy[1])
+    return LFRows(x.data_ptr(), y.data_ptr(), shape[2], *sx[:3], *sy[:3])
+
+
 class LFRotary:
     """Rotary positions of a model's heads: its frequencies, kept on the device, and the calls that rotate by them.
 
@@ -603,67 +616,65 @@ class LFRotary:
 
     def _positions(self, positions, lead):
         """The axis stride of positions [*lead], or [axes, *lead]."""
-        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 \
-                or positions.get_device() != self._index or not positions.is_contiguous() \
-                or (positions.shape != lead and positions.shape != (self.axes, *lead)):
-            got = (tuple(positions.shape), positions.dtype, str(positions.device)) \
-                if isinstance(positions, torch.Tensor) else type(positions)
-            raise LFError(LF_ERR_ARG, f"positions: expected contiguous torch.int32 {tuple(lead)} or "
-                                      f"{(self.axes, *lead)} on {self.device}, got {got}")
-        return 0 if positions.shape == lead else positions.numel() // self.axes
+        if isinstance(positions, torch.Tensor) and positions.dtype == torch.int32 \
+                and positions.get_device() == self._index and positions.is_contiguous():
+            shape = positions.shape
+            if shape == lead:
+                return 0
+            if shape[0] == self.axes and shape[1:] == lead:
+                return positions.numel() // self.axes
+        got = (tuple(positions.shape), positions.dtype, str(positions.device)) \
+            if isinstance(positions, torch.Tensor) else type(positions)
+        raise LFError(LF_ERR_ARG, f"positions: expected contiguous torch.int32 {tuple(lead)} or "
+                                  f"{(self.axes, *lead)} on {self.device}, got {got}")
 
-    def _rows(self, x, y, name, dtype, lead):
-        """x and y (or None: a new tensor) as the C call takes them."""
-        for n, t in ((name, x), (name + "_out", y)):
-            if t is None and t is y:
-                continue
-            if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4) or t.dtype not in (torch.bfloat16, torch.float32) \
-                    or t.get_device() != self._index or (dtype is not None and t.dtype != dtype) \
-                    or (lead is not None and t.shape[:-2] != lead) or t.shape != x.shape \
-                    or (t.shape[-1] > 1 and t.stride(-1) != 1):
-                got = (tuple(t.shape), t.dtype, str(t.device)) if isinstance(t, torch.Tensor) else type(t)
-                raise LFError(LF_ERR_ARG, f"{n}: expected bf16 or fp32 rows [tokens][heads][dim] or [sequences][tokens]"
-                                          f"[heads][dim], of the call's type and tokens, on {self.device}, got {got}")
-        return x.shape[-2]
+    def _expect(self, t, name, dtype=None, shape=None):
+        """Rows of a call: with `dtype` and `shape`, of these; -> their shape."""
+        if isinstance(t, torch.Tensor) and t.get_device() == self._index:
+            mine = t.shape
+            if (t.dtype == dtype if dtype else t.dtype in _ROW_TYPES) and (mine == shape if shape else 3 <= len(mine) <= 4) \
+                    and (t.stride(-1) == 1 or mine[-1] <= 1):
+                return mine
+        got = (tuple(t.shape), t.dtype, str(t.device)) if isinstance(t, torch.Tensor) else type(t)
+        raise LFError(LF_ERR_ARG, f"{name}: expected bf16 or fp32 rows [tokens][heads][dim] or [sequences][tokens][heads]"
+                                  f"[dim], of the call's type and tokens, on {self.device}, got {got}")
 
     def rotate(self, q, positions, k=None, q_out=None, k_out=None, inverse=False, stream=None):
         """lf_rotate: rows q [tokens][heads][dim] or [sequences][tokens][heads][dim], in any order in memory with
         contiguous rows, and of k where it is given, by positions int32 [tokens] ([sequences][tokens]), or
         [axes][...].  Returns q_out (a new tensor if None; q rotates in place), or (q_out, k_out) with k.
         ``inverse`` turns back: the transpose, which takes a gradient of the result to that of the rows."""
-        q_heads = self._rows(q, q_out, "q", None, None)
-        lead, dim = q.shape[:-2], q.shape[-1]
-        k_heads = 0
+        shape = self._expect(q, "q")
+        if q_out is not None:
+            self._expect(q_out, "q_out", q.dtype, shape)
         if k is not None:
-            k_heads = self._rows(k, k_out, "k", q.dtype, lead)
-            if k.shape[-1] != dim:
-                raise LFError(LF_ERR_ARG, f"k: expected rows of q's {dim} columns, got {k.shape[-1]}")
+            k_shape = self._expect(k, "k", q.dtype)
+            if k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
+                raise LFError(LF_ERR_ARG, f"k: expected q's {tuple(shape[:-2])} tokens and {shape[-1]} columns, got "
+                                          f"{tuple(k_shape)}")
+            if k_out is not None:
+                self._expect(k_out, "k_out", q.dtype, k_shape)
         elif k_out is not None:
             raise LFError(LF_ERR_ARG, "k_out without k")
-        step = self._positions(positions, lead)
-        return _run_on(self.device, self._index, stream, self._held, self._rotate, q, positions, k, q_out, k_out,
-                       q_heads, k_heads, step, int(bool(inverse)))
+        step = self._positions(positions, shape[:-2])
+        return _run_on(self.device, self._index, stream, self._held, self._rotate, q, positions, k, q_out, k_out, step,
+                       1 if inverse else 0)
 
-    def _rotate(self, st, q, positions, k, q_out, k_out, q_heads, k_heads, step, inverse):
-        seqs, tokens = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
-        if max(seqs, tokens) > _INT_MAX:
-            raise LFError(LF_ERR_ARG, f"need at most 2^31 - 1 tokens, got {seqs} x {tokens}")
-
-        def rows(x, y, heads):
-            sx, sy = ([st if n > 1 else 0 for n, st in zip(t.shape, t.stride())] for t in (x, y))
-            return LFRows(x.data_ptr(), y.data_ptr(), heads, sx[0] if len(sx) == 4 else 0, sx[-3], sx[-2],
-                          sy[0] if len(sy) == 4 else 0, sy[-3], sy[-2])
-
+    def _rotate(self, st, q, positions, k, q_out, k_out, step, inverse):
+        shape = q.shape
+        seqs, tokens = (1, shape[0]) if len(shape) == 3 else shape[:2]
+        if max(shape) > _INT_MAX or (k is not None and k.shape[-2] > _INT_MAX):
+            raise LFError(LF_ERR_ARG, f"no size may be above 2^31 - 1, got {tuple(shape)}")
         if q_out is None:
             q_out = torch.empty_like(q)
-        if k is not None and k_out is None:
-            k_out = torch.empty_like(k)
-        if q_heads == 0 or (k is not None and k_heads == 0):
-            raise LFError(LF_ERR_ARG, "rows without heads")
-        dtype = LF_BF16 if q.dtype == torch.bfloat16 else LF_F32
+        k_rows = None
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty_like(k)
+            k_rows = _rows(k, k_out)
         _check(self._lib.lf_rotate(
-            self._table, dtype, q.shape[-1], seqs, tokens, rows(q, q_out, q_heads),
-            None if k is None else rows(k, k_out, k_heads), positions.data_ptr(), step, inverse, st))
+            self._table, LF_BF16 if q.dtype == torch.bfloat16 else LF_F32, shape[-1], seqs, tokens, _rows(q, q_out),
+            k_rows, positions.data_ptr(), step, inverse, st))
         return q_out if k is None else (q_out, k_out)
 
 
@@ -768,6 +779,8 @@ class LFPagedCache:
         """call(stream handle, *args) with this cache's device and `stream` current, so that
         what it allocates belongs to that stream.  The allocator is told that a stream which the caller
         names reads the tensors: they may be let go as soon as the call returns."""
+        if stream is None and torch.cuda.current_device() == self._index:
+            return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
         return _run_on(self.device, self._index, stream, (self.k, self.v, self.err), call, *args)
 
     def _ask(self, call, pages, key):
@@ -802,7 +815,7 @@ class LFPagedCache:
         positions int32 [tokens] or [axes][tokens], or None: each token's position in the cache."""
         pages = self._layer(layer)
         batch, width = self._sequences(page_table, lens)
-        if not isinstance(rotary, LFRotary) or rotary.device != self.device:
+        if not isinstance(rotary, LFRotary) or rotary._index != self._index:
             raise LFError(LF_ERR_ARG, f"rotary: expected an LFRotary on {self.device}, got {rotary}")
         n = batch if new_start is None else self._sizes(k_new, "k_new", 3)[0]
         self._expect(k_new, "k_new", self.dtype, (n, *self._row))

@@ -531,7 +531,7 @@ typedef struct lf_rows {
 
 /*
  * Rotate the rows of q, and of k where that is not NULL, of seqs x tokens tokens.
- *   row_dim      columns of a row: a multiple of 16 up to 512
+ *   row_dim      columns of a row: a multiple of 16 up to 512 (fp32: 256)
  *   positions    device [axes][seqs * tokens], axis_stride elements from axis to axis (0: one set for every axis)
  *   inverse      1: by the negative angle (the transpose: takes a gradient with respect to y to that of x)
  * One launch, bound by HBM.

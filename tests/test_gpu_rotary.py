@@ -106,11 +106,12 @@ def test_far_positions_keep_their_angles():
     pos = np.array([[2**31 - 1, -2**31, 10**9 + 7, 123456789, 1]])
     x = values("f32", 5, 1, 16)
     want, size = rotary_oracle.rotate(f64(x), pos, [1.0, -1.0, 0.1, 3e-9, 0.0, 1024.0, 1e-4, 6.25])
-    # (an angle of 2^41 radians has 2^-12 of one left in 64 bits: that pair's expectation is too rough)
+    # The expectation's own angles are products in 64 bits, off by 2^-53 of up to 2^41 radians at frequency 1024: 2^-12,
+    # too rough, and that pair is left out; at 6.25, 2^34 radians, by 2^-19, which the rest is given for.
     got = f64(r.rotate(x, ints(pos[0])))
     keep = [i for i in range(16) if i % 8 != 5]
-    # frequency 1 times 2^31 rounds by 2^-23 of a radian in 64 bits at 6.25: 13.4e9 needs 34 bits of 53
-    close("f32", got[..., keep], want[..., keep], size[..., keep] + 2.0 ** -20)
+    err = 7 * 2.0 ** -24 * size + 2.0 ** -19 * size
+    assert (np.abs(got - want) <= err + 2.0 ** -24 * (np.abs(want) + err))[..., keep].all()
     near, size = rotary_oracle.rotate(f64(x), pos * 0 + 3, [1.0, -1.0, 0.1, 3e-9, 0.0, 1024.0, 1e-4, 6.25])
     close("f32", f64(r.rotate(x, ints(pos[0] * 0 + 3))), near, size)
 
@@ -190,7 +191,8 @@ def test_refusals():
                           ((x.transpose(1, 2), pos), {}, "q:"), ((x, pos), dict(q_out=x[:5]), "q_out"),
                           ((x, pos), dict(k=x.float()), "k:"), ((x, pos), dict(k=x[:5]), "k:"),
                           ((x, pos), dict(k=torch.zeros(6, 4, 128, dtype=x.dtype, device="cuda")), "columns"),
-                          ((x, pos), dict(k_out=x), "k_out without k"), ((x[:, :0], pos), {}, "without heads"),
+                          ((values("f32", 6, 4, 272), pos), {}, "row_dim"),
+                          ((x, pos), dict(k_out=x), "k_out without k"), ((x[:, :0], pos), {}, "heads"),
                           ((x[..., :48], pos), {}, "rotary_dim"), ((values("bf16", 6, 4, 72), pos), {}, "row_dim"),
                           ((values("bf16", 6, 4, 72)[..., 4:68], pos), {}, "aligned")]:
         with pytest.raises(lf.LFError, match=msg):
