@@ -279,15 +279,16 @@ struct DecodeShape {
 // the careful side: 64 units of 8 sweeps and 136 of 16 are cut, though whole ones were faster.
 // Lengths are known here by the table's width: short sequences under a wide table are cut too (one of
 // 300 tokens under 8192 pages 10.3 us, 8.3 under its own 19; 17 fp32 ones of 1000 16.5, 13.6).
+// Behind a prefix the table's width says nothing of what is left: ranges, and the join takes them as they are.
 int decode_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int window, int sinks,
-                 DecodeShape* s) {
+                 DecodeShape* s, bool behind = false) {
   const int64_t most = window > 0 ? (int64_t)window + sinks : (int64_t)pool.max_pages * pool.page_size;
   const int64_t units = (int64_t)pool.batch * pool.kv_heads;
   int sms = 0;
   const int rc = sm_count(&sms);
   if (rc != LF_OK) return rc;
   const int64_t sweep = lf::paged_decode_sweep(elem_bytes(p), p->head_dim);
-  s->whole_units = units <= sms && most * (sms - units) <= 4 * sms * sweep && most <= 12 * sweep;
+  s->whole_units = !behind && units <= sms && most * (sms - units) <= 4 * sms * sweep && most <= 12 * sweep;
   s->grid = s->whole_units ? (int)units : sms;
   s->off_ml = s->off_unit = s->bytes = 0;
   if (s->whole_units) return LF_OK;
@@ -295,6 +296,32 @@ int decode_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int wi
   s->off_ml = up((size_t)s->grid * 2 * group * p->head_dim * 4);
   s->off_unit = s->off_ml + up((size_t)s->grid * 2 * group * 2 * 4);
   s->bytes = s->off_unit + up((size_t)s->grid * 4);
+  return LF_OK;
+}
+
+// A call behind shared prefixes: the rest's shape, the prefixes' plan, and the workspace, each piece 256-byte aligned.
+struct SharedShape {
+  DecodeShape rest;
+  lf::SharedPlan plan;
+  size_t off_rest_o, off_rest_ml, off_part_o, off_part_ml, off_segments, off_first, bytes;
+};
+
+int shared_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int groups, SharedShape* s) {
+  if (groups < 1 || groups > pool.batch) return fail(LF_ERR_ARG, "groups must be in [1, batch]");
+  int sms = 0;
+  int rc = sm_count(&sms);
+  if (rc != LF_OK || (rc = decode_shape(p, pool, group, 0, 0, &s->rest, true)) != LF_OK) return rc;
+  s->plan = lf::paged_shared_plan(pool, elem_bytes(p), p->head_dim, group, groups, sms);
+  if (s->plan.grid > INT_MAX) return fail(LF_ERR_ARG, "batch * kv_heads is too large for one call");
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = (size_t)pool.batch * pool.kv_heads * group, d = p->head_dim;
+  s->off_rest_o = up(s->rest.bytes);
+  s->off_rest_ml = s->off_rest_o + up(rows * d * 4);
+  s->off_part_o = s->off_rest_ml + up(rows * 2 * 4);
+  s->off_part_ml = s->off_part_o + up((size_t)s->plan.part_rows * d * 4);
+  s->off_segments = s->off_part_ml + up((size_t)s->plan.part_rows * 2 * 4);
+  s->off_first = s->off_segments + up((size_t)groups * 4);
+  s->bytes = s->off_first + up((size_t)groups * 8);
   return LF_OK;
 }
 
@@ -369,6 +396,8 @@ int lf_paged_decode(const lf_pages* pages, int batch, const int32_t* page_table,
   DecodeShape shape;
   if ((rc = decode_shape(pages, a.pool, a.group, a.window, a.sinks, &shape)) != LF_OK) return rc;
   a.whole_units = shape.whole_units;
+  a.prefix_lens = nullptr;
+  a.rest_o = a.rest_ml = nullptr;
   a.part_o = a.part_ml = nullptr;
   a.part_unit = nullptr;
   if (shape.bytes > 0) {
@@ -383,6 +412,84 @@ int lf_paged_decode(const lf_pages* pages, int batch, const int32_t* page_table,
   const cudaError_t e = lf::paged_decode_launch(a, elem_bytes(pages), pages->head_dim, shape.grid,
                                                 static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LF_OK : cuda_fail(e, "paged decode launch");
+}
+
+int lf_paged_decode_shared_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int groups,
+                                     size_t* bytes) {
+  lf::clear_last_error();
+  if (!pages || !bytes) return fail(LF_ERR_ARG, "null pages or bytes");
+  lf::PagedPool pool;
+  static const int32_t any = 0;  // only the shape counts here
+  int group = 0;
+  SharedShape shape;
+  int rc = take_pool(pages, batch, &any, max_pages, &any, &pool);
+  if (rc != LF_OK || (rc = take_heads(pages, q_heads, &group)) != LF_OK ||
+      (rc = shared_shape(pages, pool, group, groups, &shape)) != LF_OK)
+    return rc;
+  *bytes = shape.bytes;
+  return LF_OK;
+}
+
+int lf_paged_decode_shared(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
+                           const int32_t* lens, int q_heads, const void* q, const int32_t* group_start, int groups,
+                           const int32_t* prefix_lens, const void* k_new, const void* v_new, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, lf_stream_t stream) {
+  lf::clear_last_error();
+  lf::PagedDecodeArgs d = {};
+  int rc = take_pool(pages, batch, page_table, max_pages, lens, &d.pool);
+  if (rc != LF_OK || (rc = take_heads(pages, q_heads, &d.group)) != LF_OK) return rc;
+  if (!q || !out || !aligned16(q) || !aligned16(out))
+    return fail(LF_ERR_ARG, "q and out must be non-null and 16-byte aligned");
+  if (!group_start || !prefix_lens || !aligned4(group_start) || !aligned4(prefix_lens))
+    return fail(LF_ERR_ARG, "group_start and prefix_lens must be non-null and 4-byte aligned");
+  if (!k_new != !v_new || !aligned16(k_new) || !aligned16(v_new))
+    return fail(LF_ERR_ARG, "k_new and v_new come together, 16-byte aligned (or both null)");
+  if (!aligned4(lse)) return fail(LF_ERR_ARG, "lse must be 4-byte aligned");
+  if (groups < 1 || groups > batch) return fail(LF_ERR_ARG, "groups must be in [1, batch]");
+  SharedShape shape;
+  if ((rc = shared_shape(pages, d.pool, d.group, groups, &shape)) != LF_OK) return rc;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0 || workspace_bytes < shape.bytes)
+    return fail(LF_ERR_ARG, "workspace: need %zu bytes, 16-byte aligned "
+                "(lf_paged_decode_shared_workspace), got %zu", shape.bytes, workspace_bytes);
+  char* w = static_cast<char*>(workspace);
+  auto floats = [&](size_t off) { return reinterpret_cast<float*>(w + off); };
+  d.q = q;
+  d.k_new = static_cast<const char*>(k_new);
+  d.v_new = static_cast<const char*>(v_new);
+  d.out = out;
+  d.lse = lse;
+  d.q_heads = q_heads;
+  d.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)pages->head_dim));
+  d.part_o = floats(0);
+  d.part_ml = floats(shape.rest.off_ml);
+  d.part_unit = reinterpret_cast<int32_t*>(w + shape.rest.off_unit);
+  d.prefix_lens = prefix_lens;
+  d.rest_o = floats(shape.off_rest_o);
+  d.rest_ml = floats(shape.off_rest_ml);
+  lf::PagedSharedArgs a = {};
+  a.pool = d.pool;
+  a.q = q;
+  a.group_start = group_start;
+  a.prefix_lens = prefix_lens;
+  a.groups = groups;
+  a.q_heads = q_heads;
+  a.group = d.group;
+  a.fresh = k_new != nullptr;
+  a.rows = shape.plan.rows;
+  a.slots = shape.plan.slots;
+  a.rounds = shape.plan.rounds;
+  a.scale_log2 = d.scale_log2;
+  a.part_rows = shape.plan.part_rows;
+  a.part_o = floats(shape.off_part_o);
+  a.part_ml = floats(shape.off_part_ml);
+  a.segments = reinterpret_cast<int32_t*>(w + shape.off_segments);
+  a.first_row = reinterpret_cast<int64_t*>(w + shape.off_first);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int e = elem_bytes(pages);
+  cudaError_t err = lf::paged_decode_launch(d, e, pages->head_dim, shape.rest.grid, st);
+  if (err == cudaSuccess) err = lf::paged_shared_launch(a, shape.plan, pages->head_dim, st);
+  if (err == cudaSuccess) err = lf::paged_shared_join_launch(a, d, e, pages->head_dim, shape.rest.grid, st);
+  return err == cudaSuccess ? LF_OK : cuda_fail(err, "paged shared decode launch");
 }
 
 int lf_paged_prompt_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int total_q,

@@ -89,6 +89,40 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   return r;
 }
 
+// 1 / l; 0 for a row that saw nothing (l = 0), so that its output is zeros.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+// One head's row of parts i = 0 .. n - 1 (maximum and sum at ml(i), output at o(i)[D]),
+// joined in their order: lane j holds columns E j .. E j + E - 1.
+template <int D, class Ml, class O>
+__device__ __forceinline__ void join_parts(int n, Ml ml, O o, int lane, float* m_out, float* l_out,
+                                           float* acc) {
+  constexpr int E = D >= 32 ? D / 32 : 1;
+  const int col = (lane * E) % D;
+  float m = kNegInf;
+  for (int i = 0; i < n; ++i) m = fmaxf(m, ml(i)[0]);
+  const float mu = m == kNegInf ? 0.f : m;
+  float l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* s = ml(i);
+    const float f = ex2(s[0] - mu);
+    l = fmaf(s[1], f, l);
+    const float* p = o(i) + col;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(p[e], f, acc[e]);
+  }
+  *m_out = m;
+  *l_out = l;
+}
+
+// The positions of a sequence of `len` tokens that its group's prefix holds; a new token (`fresh`) is its own.
+__device__ __forceinline__ int shared_len(int prefix, int len, bool fresh) {
+  return max(0, min(prefix, fresh ? len - 1 : len));
+}
+
 // A finished row's log-sum-exp, and the error word if its sum is not finite (Args: of decode or prompt).
 template <class Args>
 __device__ __forceinline__ void write_row_stats(const Args& a, int64_t row, float m, float l) {
@@ -251,6 +285,7 @@ __device__ __forceinline__ bool sees(const PagedPromptArgs& a, int pos, int key)
 // and [from, to); with splits, a block takes its share of them.
 struct Tiles {
   int sink, gap, first, last;   // tile j of them is number j below `sink`, else j + gap
+  Tiles() = default;
   __device__ Tiles(const PagedPromptArgs& a, int p_lo, int p_hi, int size, int share)
       : sink(0), gap(0), first(0), last(0) {
     if (p_hi < 0) return;

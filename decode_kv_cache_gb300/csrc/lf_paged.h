@@ -42,6 +42,11 @@ struct PagedDecodeArgs {
   float* part_o;              // level ranges: [2 grid][group][head_dim] partial outputs
   float* part_ml;             // [2 grid][group][2] their max and sum
   int32_t* part_unit;         // [grid] the unit a CTA's range starts inside, or -1
+  // Behind a shared prefix (else null): the positions below it are left to PagedSharedArgs' kernel, and whole
+  // units go to rest_o, rest_ml as parts do.
+  const int32_t* prefix_lens; // [batch]
+  float* rest_o;              // [batch][q_heads][head_dim]
+  float* rest_ml;             // [batch][q_heads][2]
 };
 
 struct PagedPromptArgs {
@@ -66,13 +71,41 @@ struct PagedPromptArgs {
 // (tiles_per_seq), or the numbers follow the rows (locate), with at most one more than pieces
 // for each sequence.
 struct PromptPlan {
-  enum { kTensor, kMatrix, kFma } kernel;
+  enum Kernel { kTensor, kMatrix, kFma } kernel;
   int rows, splits, tiles_per_seq;
   int64_t pieces;             // numbers of pieces, of all KV heads
   size_t off_ml, bytes;       // workspace: part_o, part_ml
 };
 PromptPlan paged_prompt_plan(const PagedPool& pool, int elem, int head_dim, int group, int total_q, int max_q,
                              int window, int sinks, int sms);
+
+// The last tokens of groups of sequences before the prefix that each group shares.  A piece is
+// up to `rows` rows (sequence and head of the group) of one KV head, a unit a piece of one KV head; a unit's
+// key tiles are cut into segments of `chunk`, one block each.
+struct PagedSharedArgs {
+  PagedPool pool;
+  const void* q;
+  const int32_t* group_start; // [groups + 1]
+  const int32_t* prefix_lens; // [batch]
+  int groups, q_heads, group;
+  int fresh;                  // 1: the last token comes with the call, and is no part of a prefix
+  int rows;
+  int slots, rounds;          // blocks that run at once; rounds of them that the grid has room for
+  float scale_log2;
+  int64_t part_rows;          // rows that part_o and part_ml have
+  float* part_o;              // [part_rows][head_dim] partial outputs
+  float* part_ml;             // [part_rows][2] their max and sum
+  int32_t* segments;          // [groups] segments of a unit, for the join
+  int64_t* first_row;         // [groups] the first of the group's rows in part_o
+};
+
+// Its kernel by type, heads and pages, and the rows of a piece.
+struct SharedPlan {
+  PromptPlan::Kernel kernel;
+  int rows, keys, slots, rounds;
+  int64_t grid, part_rows;
+};
+SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int group, int groups, int sms);
 
 // Occupied tokens of sequence b, kept inside its row of the page table.
 __device__ __forceinline__ int paged_len(const PagedPool& p, int b) {
@@ -132,6 +165,12 @@ cudaError_t paged_prompt_launch(const PagedPromptArgs& a, const PromptPlan& plan
 bool paged_prompt_tc_takes(const PagedPool& pool, int head_dim);
 cudaError_t paged_prompt_tc_launch(const PagedPromptArgs& a, const PromptPlan& plan, int head_dim,
                                    cudaStream_t stream);
+
+// The prefixes of a decode call behind them, placed while the kernel before it drains (which has to have waited for
+// what came before itself), and the join of its parts with the rest of every sequence.
+cudaError_t paged_shared_launch(const PagedSharedArgs& a, const SharedPlan& plan, int head_dim, cudaStream_t stream);
+cudaError_t paged_shared_join_launch(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int elem, int head_dim,
+                                     int grid, cudaStream_t stream);
 
 // Tokens that one CTA of the decode kernel takes in one sweep of its warps.
 int paged_decode_sweep(int elem, int head_dim);

@@ -41,9 +41,6 @@ namespace lf {
 
 namespace {
 
-// 1 / l; 0 for a row that saw nothing (l = 0), so that its output is zeros.
-__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
-
 // ---- what one warp does with a tile ------------------------------------------
 //
 // The exponent of a weight, s log2(e) / sqrt(d) - m, is one multiply-add: its only rounding is that
@@ -160,6 +157,7 @@ struct MmaTile {
 
   // The whole unit's output rows, first row `row`.
   __device__ __forceinline__ void write(const PagedDecodeArgs& a, int64_t row) {
+    if (a.rest_o) return store(a.rest_o + row * D, a.rest_ml + row * 2);
     const int lane = threadIdx.x & 31, r = lane >> 2;
     float ls = l + __shfl_xor_sync(0xffffffffu, l, 1);
     ls += __shfl_xor_sync(0xffffffffu, ls, 2);
@@ -313,6 +311,7 @@ struct SimtTile {
   }
 
   __device__ __forceinline__ void write(const PagedDecodeArgs& a, int64_t row) {
+    if (a.rest_o) return store(a.rest_o + row * D, a.rest_ml + row * 2);
     const int lane = threadIdx.x & 31;
     join_lanes();
 #pragma unroll
@@ -360,6 +359,8 @@ __device__ __forceinline__ Seen seen_of(const PagedDecodeArgs& a, int b) {
     const int64_t w = (int64_t)a.window + a.sinks;
     if (w < s.len) s.seen = (int)w;
   }
+  // The positions below the prefix are not seen here (there is no window then).
+  if (a.prefix_lens) s.seen = s.len - shared_len(a.prefix_lens[b], s.len, a.k_new != nullptr);
   s.gap = s.len - s.seen;
   s.tiles = (int)(((unsigned)s.seen + TT - 1) / TT);
   return s;
@@ -384,36 +385,21 @@ __device__ __forceinline__ void step(const PagedDecodeArgs& a, Place& p) {
   } while (p.s.tiles == 0);
 }
 
-// One head's row of parts i = 0 .. n - 1 (maximum and sum at ml(i), output at o(i)[D]),
-// joined in their order: lane j holds columns E j .. E j + E - 1.
-template <int D, class Ml, class O>
-__device__ __forceinline__ void join_parts(int n, Ml ml, O o, int lane, float* m_out, float* l_out,
-                                           float* acc) {
-  constexpr int E = D >= 32 ? D / 32 : 1;
-  const int col = (lane * E) % D;
-  float m = kNegInf;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, ml(i)[0]);
-  const float mu = m == kNegInf ? 0.f : m;
-  float l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* s = ml(i);
-    const float f = ex2(s[0] - mu);
-    l = fmaf(s[1], f, l);
-    const float* p = o(i) + col;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(p[e], f, acc[e]);
-  }
-  *m_out = m;
-  *l_out = l;
-}
-
 template <typename T, int D>
 __device__ __forceinline__ void write_row(const PagedDecodeArgs& a, int64_t row, int lane, float m,
                                           float l, const float* acc) {
   constexpr int E = D >= 32 ? D / 32 : 1;
+  if (a.rest_o) {
+    if (lane * E < D) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) a.rest_o[row * D + lane * E + i] = acc[i];
+    }
+    if (lane == 0) {
+      a.rest_ml[row * 2] = m;
+      a.rest_ml[row * 2 + 1] = l;
+    }
+    return;
+  }
   const float inv = inverse_sum(l);
   T* out = reinterpret_cast<T*>(a.out) + row * D;
   if (lane * E < D) {
@@ -640,7 +626,13 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) paged_decode_kernel(const _
   auto nothing_seen = [&](int b, int first_head, int heads) {
     const Seen s = seen_of<TT>(a, b);
     const int64_t row = (int64_t)b * a.q_heads + first_head;
-    if (s.tiles == 0) {
+    if (s.tiles == 0 && a.rest_o) {
+      for (int i = tid; i < heads * D; i += W * 32) a.rest_o[row * D + i] = 0.f;
+      for (int i = tid; i < heads; i += W * 32) {
+        a.rest_ml[(row + i) * 2] = kNegInf;
+        a.rest_ml[(row + i) * 2 + 1] = 0.f;
+      }
+    } else if (s.tiles == 0) {
       T* out = reinterpret_cast<T*>(a.out) + row * D;
       for (int i = tid; i < heads * D; i += W * 32) from_f32(0.f, out + i);
       if (a.lse)
@@ -774,7 +766,7 @@ cudaError_t launch(const PagedDecodeArgs& a, int grid, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<C, D, G>, a);
-  if (e != cudaSuccess || a.whole_units || grid < 2) return e;
+  if (e != cudaSuccess || a.whole_units || grid < 2 || a.rest_o) return e;   // (a prefix's join takes the parts too)
   cfg.gridDim = dim3(grid - 1, G, 1);
   cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = 0;

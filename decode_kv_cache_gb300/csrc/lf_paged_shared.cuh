@@ -1,0 +1,265 @@
+// Before a shared prefix: which rows and keys a block takes.
+#pragma once
+
+#include "lf_paged.cuh"
+
+namespace lf {
+
+constexpr int kMaxMembers = 256;   // sequences of a piece
+
+// A segment's rows and keys: the group's sequences b0 .. b0 + members - 1, KV head g, key tiles first .. last - 1
+// of the pages that sequence `leader` lists.
+struct Segment {
+  int b0, members, g, leader, first, last;
+  int p_lo, p_hi;            // least and largest last position that a row sees
+  int64_t row;               // of part_o
+};
+
+// What a group asks for: `pieces` pieces of `tiles` key tiles, of each KV head.
+struct Family {
+  int start, members, prefix, tiles, pieces;
+  bool right;
+};
+
+__device__ __forceinline__ Family family_of(const PagedSharedArgs& a, int i, int keys) {
+  Family f;
+  f.start = a.group_start[i];
+  const int end = a.group_start[i + 1];
+  f.right = f.start >= 0 && end >= f.start && end <= a.pool.batch;
+  f.members = f.right ? end - f.start : 0;
+  f.prefix = f.tiles = f.pieces = 0;
+  if (f.members > 0) {
+    const int64_t most = (int64_t)a.pool.max_pages * a.pool.page_size;
+    f.prefix = (int)min((int64_t)max(a.prefix_lens[f.start], 0), most);
+    f.tiles = (f.prefix + keys - 1) / keys;
+    const int each = a.rows / a.group;
+    f.pieces = (f.members + each - 1) / each;
+  }
+  return f;
+}
+
+// Tiles of a segment.  A block costs its tiles and, for its start and its rows' way out, about as much as
+// four; U units of T tiles in all, the longest of `longest`, are cut so that r rounds of all blocks that run at once take
+// them, with the r that costs least.
+__device__ __forceinline__ int segment_tiles(const PagedSharedArgs& a, int64_t units, int64_t tiles, int longest) {
+  constexpr int kStart = 4;
+  int best = longest;
+  int64_t cost = INT64_MAX;
+  const int64_t r0 = units / a.slots + 1;
+  for (int64_t r = r0; r < r0 + 2 && r <= a.rounds; ++r) {
+    const int64_t room = r * a.slots - units;
+    const int64_t c = min((int64_t)longest, max((int64_t)1, (tiles + room - 1) / room));
+    const int64_t used = c == longest ? (units + a.slots - 1) / a.slots : r;
+    if (used * (c + kStart) < cost) {
+      cost = used * (c + kStart);
+      best = (int)c;
+    }
+  }
+  return best;
+}
+
+// Segment number blockIdx.x, for the whole block together; false: there is none.  Every block goes through
+// the groups itself (two scans of them): a launch that did so for all would be one more to wait for.
+template <int kThreads>
+__device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys, Segment* out, const int** limits) {
+  constexpr int kW = kThreads / 32;
+  __shared__ int64_t s_sum[2][kW + 1];
+  __shared__ int s_max[2][kW];
+  __shared__ Segment s_seg;
+  __shared__ int s_limit[kMaxMembers];   // the last position that a member sees of the prefix
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.groups + kThreads - 1) / kThreads;
+  const int from = min(tid * per, a.groups), to = min(from + per, a.groups);
+  const int H = a.pool.kv_heads;
+
+  int64_t units = 0, tiles = 0;
+  int longest = 0;
+  for (int i = from; i < to; ++i) {
+    const Family f = family_of(a, i, keys);
+    if (f.tiles > 0) {
+      units += (int64_t)f.pieces * H;
+      tiles += (int64_t)f.pieces * H * f.tiles;
+      longest = max(longest, f.tiles);
+    }
+    if (!f.right && blockIdx.x == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  }
+  if (lane == 0) {
+    s_sum[0][warp] = units;
+    s_sum[1][warp] = tiles;
+    s_max[0][warp] = longest;
+  }
+  if (tid == 0) s_seg.members = 0;
+  __syncthreads();
+  units = tiles = 0;
+  longest = 0;
+  for (int w = 0; w < kW; ++w) {
+    units += s_sum[0][w];
+    tiles += s_sum[1][w];
+    longest = max(longest, s_max[0][w]);
+  }
+  __syncthreads();
+  if (units == 0) {
+    if (blockIdx.x == 0)
+      for (int i = from; i < to; ++i) a.segments[i] = 0;
+    return false;
+  }
+  const int chunk = segment_tiles(a, units, tiles, longest);
+
+  // Segments and rows before this thread's groups.
+  int64_t seg = 0, row = 0;
+  auto cut = [&](const Family& f) { return (f.tiles + chunk - 1) / chunk; };
+  for (int i = from; i < to; ++i) {
+    const Family f = family_of(a, i, keys);
+    seg += (int64_t)f.pieces * H * cut(f);
+    row += (int64_t)f.members * a.q_heads * cut(f);
+  }
+  int64_t seg_to = seg, row_to = row;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, seg_to, o), y = __shfl_up_sync(0xffffffffu, row_to, o);
+    if (lane >= o) {
+      seg_to += x;
+      row_to += y;
+    }
+  }
+  if (lane == 31) {
+    s_sum[0][warp] = seg_to;
+    s_sum[1][warp] = row_to;
+  }
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) {
+    seg_to += s_sum[0][w];
+    row_to += s_sum[1][w];
+  }
+  seg = seg_to - seg;
+  row = row_to - row;
+  const int64_t id = blockIdx.x;
+  if (blockIdx.x == 0 || (id >= seg && id < seg_to)) {
+    for (int i = from; i < to; ++i) {
+      const Family f = family_of(a, i, keys);
+      const int n = cut(f);
+      if (blockIdx.x == 0) {
+        a.segments[i] = n;
+        a.first_row[i] = row;
+      }
+      const int64_t mine = (int64_t)f.pieces * H * n;
+      if (id >= seg && id < seg + mine) {
+        const int64_t unit = (id - seg) / n;
+        const int j = (int)(id - seg - unit * n), piece = (int)(unit / H), each = a.rows / a.group;
+        Segment s;
+        s.g = (int)(unit - (int64_t)piece * H);
+        s.b0 = f.start + piece * each;
+        s.members = min(each, f.members - piece * each);
+        s.leader = f.start;
+        s.first = (int)((int64_t)f.tiles * j / n);
+        s.last = (int)((int64_t)f.tiles * (j + 1) / n);
+        s.p_lo = s.p_hi = f.prefix;
+        s.row = row + (int64_t)piece * each * a.q_heads * n + ((int64_t)s.g * n + j) * s.members * a.group;
+        s_seg = s;
+      }
+      seg += mine;
+      row += (int64_t)f.members * a.q_heads * n;
+    }
+  }
+  __syncthreads();
+  Segment s = s_seg;
+  // (Starts that decrease may ask for more than there is room for.)
+  if (s.members == 0 || s.row + (int64_t)s.members * a.group > a.part_rows) return false;
+
+  // What its sequences see of the prefix.
+  int lo = INT_MAX, hi = -1;
+  for (int i = tid; i < s.members; i += kThreads) {
+    const int b = s.b0 + i, own = a.prefix_lens[b];
+    const int p = min(shared_len(own, paged_len(a.pool, b), a.fresh != 0), s.p_hi) - 1;
+    if (own > s.p_hi && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);   // more than the group's first
+    s_limit[i] = p;
+    lo = min(lo, p);
+    hi = max(hi, p);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    s_max[0][warp] = lo;
+    s_max[1][warp] = hi;
+  }
+  __syncthreads();
+  s.p_lo = s_max[0][0];
+  s.p_hi = s_max[1][0];
+  for (int w = 1; w < kW; ++w) {
+    s.p_lo = min(s.p_lo, s_max[0][w]);
+    s.p_hi = max(s.p_hi, s_max[1][w]);
+  }
+  s.last = max(s.first, min(s.last, s.p_hi < 0 ? 0 : s.p_hi / keys + 1));
+  *out = s;
+  *limits = s_limit;
+  return true;
+}
+
+// Byte offset in the pools of the prefix's position `pos`, -1: nothing to read.
+__device__ __forceinline__ int64_t shared_offset(const PagedSharedArgs& a, const Segment& s, int pos) {
+  if (pos > s.p_hi) return -1;
+  int pi, slot;
+  paged_split(a.pool, pos, &pi, &slot);
+  const int page = a.pool.table[(int64_t)s.leader * a.pool.max_pages + pi];
+  if (page >= 0 && page < a.pool.num_pages)
+    return page * a.pool.page_stride + slot * a.pool.token_stride + s.g * a.pool.head_stride;
+  if (a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+  return -1;
+}
+
+// Row r of a segment as a row of q.
+__device__ __forceinline__ int64_t shared_row(const PagedSharedArgs& a, const Segment& s, int r) {
+  return (int64_t)(s.b0 + r / a.group) * a.q_heads + s.g * a.group + r % a.group;
+}
+
+// Row r's share by the definition, a warp at a time, where values that are not finite lie where some row
+// does not look (0 * NaN is NaN).
+template <typename T, int D>
+__device__ __forceinline__ void shared_row_by_hand(const PagedSharedArgs& a, const Segment& s, int keys, int r, int limit,
+                                                   int lane) {
+  constexpr int E = D >= 32 ? D / 32 : 1;
+  const bool mine = lane * E < D;   // lanes past a short row take nothing
+  const T* q = reinterpret_cast<const T*>(a.q) + shared_row(a, s, r) * D + lane * E;
+  float qv[E], acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    qv[e] = mine ? to_f32(q[e]) : 0.f;
+    acc[e] = 0.f;
+  }
+  float m = kNegInf, l = 0.f;
+  const int64_t end = min((int64_t)s.last * keys, (int64_t)limit + 1);
+  for (int64_t key = (int64_t)s.first * keys; key < end; ++key) {
+    const int64_t off = shared_offset(a, s, (int)key);
+    if (off < 0) continue;
+    const T* k = reinterpret_cast<const T*>(a.pool.k + off) + lane * E;
+    const T* v = reinterpret_cast<const T*>(a.pool.v + off) + lane * E;
+    float x = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (mine) x = fmaf(qv[e], to_f32(k[e]), x);
+    x = warp_sum(x);
+    const float mn = fmaxf(m, x * a.scale_log2), mu = mn == kNegInf ? 0.f : mn;
+    const float f = ex2(m - mu), w = ex2(fmaf(x, a.scale_log2, -mu));
+    m = mn;
+    l = l * f + w;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (mine) acc[e] = acc[e] * f + w * to_f32(v[e]);
+  }
+  float* o = a.part_o + (s.row + r) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (mine) o[e] = acc[e];
+  if (lane == 0) {
+    a.part_ml[2 * (s.row + r)] = m;
+    a.part_ml[2 * (s.row + r) + 1] = l;
+  }
+}
+
+}  // namespace lf

@@ -35,6 +35,7 @@ __all__ = [
     "LFPagedCache",
     "LFRotaryTable", "LFRows", "lf_rotary_turns", "lf_rotate", "lf_paged_append_rotated",
     "LFRotary",
+    "lf_paged_decode_shared", "lf_paged_decode_shared_workspace",
 ]
 
 LF_OK, LF_ERR_ARG, LF_ERR_OOM, LF_ERR_CUDA, LF_ERR_DEVICE, LF_ERR_UNSUPPORTED = 0, -1, -2, -3, -5, -7
@@ -168,6 +169,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.lf_paged_prompt_workspace.argtypes = [PG, I, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
     lib.lf_paged_take_errors.restype = I
     lib.lf_paged_take_errors.argtypes = [PG, VP, VP]
+    lib.lf_paged_decode_shared.restype = I
+    lib.lf_paged_decode_shared.argtypes = [PG, I, VP, I, VP, I, VP, VP, I, VP, VP, VP, VP, VP, VP, ctypes.c_size_t, VP]
+    lib.lf_paged_decode_shared_workspace.restype = I
+    lib.lf_paged_decode_shared_workspace.argtypes = [PG, I, I, I, I, ctypes.POINTER(ctypes.c_size_t)]
     RT, RW, LL = ctypes.POINTER(LFRotaryTable), ctypes.POINTER(LFRows), ctypes.c_int64
     lib.lf_rotary_turns.restype = I
     lib.lf_rotary_turns.argtypes = [ctypes.POINTER(ctypes.c_double), I, ctypes.POINTER(ctypes.c_uint64)]
@@ -349,6 +354,22 @@ def lf_paged_decode_workspace(pages: LFPages, batch, max_pages, q_heads, window=
     n = ctypes.c_size_t(0)
     _check(load_library().lf_paged_decode_workspace(ctypes.byref(pages), batch, max_pages, q_heads,
                                                     window, sinks, ctypes.byref(n)))
+    return int(n.value)
+
+
+def lf_paged_decode_shared(pages: LFPages, batch, page_table, max_pages, lens, q_heads, q, group_start, groups,
+                           prefix_lens, k_new, v_new, out, lse, workspace, workspace_bytes, stream=None) -> int:
+    return _check(load_library().lf_paged_decode_shared(
+        ctypes.byref(pages), batch, _ptr(page_table), max_pages, _ptr(lens), q_heads, _ptr(q), _ptr(group_start), groups,
+        _ptr(prefix_lens), _ptr(k_new), _ptr(v_new), _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def lf_paged_decode_shared_workspace(pages: LFPages, batch, max_pages, q_heads, groups) -> int:
+    """Bytes of the workspace that such lf_paged_decode_shared calls need."""
+    n = ctypes.c_size_t(0)
+    _check(load_library().lf_paged_decode_shared_workspace(ctypes.byref(pages), batch, max_pages, q_heads, groups,
+                                                           ctypes.byref(n)))
     return int(n.value)
 
 
@@ -873,6 +894,43 @@ class LFPagedCache:
         _check(self._lib.lf_paged_decode(
             pages, batch, page_table.data_ptr(), width, lens.data_ptr(), q_heads, q.data_ptr(), _ptr(k_new),
             _ptr(v_new), out.data_ptr(), _ptr(lse), window, sinks, _ptr(ws), need, st))
+        return out
+
+    def decode_shared(self, layer, q, page_table, lens, group_start, prefix_lens, k_new=None, v_new=None, out=None,
+                      lse=None, stream=None):
+        """lf_paged_decode_shared: ``decode`` for sequences in groups that share prefixes, each read once.  group_start
+        int32 [groups + 1]: sequences group_start[i] .. group_start[i + 1] - 1 are group i; prefix_lens int32 [batch]:
+        sequence b's first prefix_lens[b] positions are those of its group's first sequence, in the pages that
+        one's row of the page table lists, and no member's is longer than that one's."""
+        pages = self._layer(layer)
+        batch, width = self._sequences(page_table, lens)
+        q_heads = self._sizes(q, "q", 3)[1]
+        self._expect(q, "q", self.dtype, (batch, q_heads, self.head_dim))
+        groups = self._sizes(group_start, "group_start", 1)[0] - 1
+        self._expect(group_start, "group_start", torch.int32, (groups + 1,))
+        self._expect(prefix_lens, "prefix_lens", torch.int32, (batch,))
+        if not 1 <= groups <= batch:
+            raise LFError(LF_ERR_ARG, f"group_start: expected 1 to {batch} groups, got {groups}")
+        if k_new is not None or v_new is not None:
+            self._expect(k_new, "k_new", self.dtype, (batch, *self._row))
+            self._expect(v_new, "v_new", self.dtype, (batch, *self._row))
+        self._numbers(batch)
+        self._outputs(q, out, lse)
+        return self._run(stream, self._decode_shared, pages, batch, width, q_heads, page_table, lens, q, group_start,
+                         groups, prefix_lens, k_new, v_new, out, lse)
+
+    def _decode_shared(self, st, pages, batch, width, q_heads, page_table, lens, q, group_start, groups, prefix_lens,
+                       k_new, v_new, out, lse):
+        key = (batch, width, q_heads, groups)
+        need = self._need.get(key)
+        if need is None:
+            need = self._ask(lf_paged_decode_shared_workspace, pages, key)
+        if out is None:
+            out = torch.empty_like(q)
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)   # of this call's own
+        _check(self._lib.lf_paged_decode_shared(
+            pages, batch, page_table.data_ptr(), width, lens.data_ptr(), q_heads, q.data_ptr(), group_start.data_ptr(),
+            groups, prefix_lens.data_ptr(), _ptr(k_new), _ptr(v_new), out.data_ptr(), _ptr(lse), ws.data_ptr(), need, st))
         return out
 
     def prompt(self, layer, q, page_table, lens, q_start, max_q, window=0, sinks=0, out=None, lse=None,

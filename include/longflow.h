@@ -463,6 +463,33 @@ int lf_paged_decode_workspace(const lf_pages* pages, int batch, int max_pages, i
                               int window, int sinks, size_t* bytes);
 
 /*
+ * lf_paged_decode (without a window) for sequences that share prefixes, whose keys and values are read once for a
+ * whole group.  Sequences group_start[i] .. group_start[i + 1] - 1 are group i.  Of sequence b the first
+ * prefix_lens[b] positions are those of its group's first sequence: they are looked up in that one's row
+ * of page_table (of b's row the entries that lie wholly below prefix_lens[b] are not read), whatever that
+ * sequence's own length.  The others are b's own.
+ *   group_start  device [groups + 1], 1 <= groups <= batch; every sequence is in a group
+ *   prefix_lens  device [batch]: no sequence's is above its group's first one's.  It counts as 0 below 0 and as the
+ *                sequence's length above that; the token that comes with the call (k_new) is the sequence's own in any
+ *                case.  0 for a sequence that shares nothing: it is decoded as lf_paged_decode does
+ *   k_new, v_new and the rest as lf_paged_decode's; the pages that they are written to hold no shared position that another
+ *                sequence of the call reads, but for the places behind the prefix in its last page
+ *   workspace    lf_paged_decode_shared_workspace bytes, as lf_paged_decode's
+ * A sequence of no group, or with a longer prefix than its group's first, is reported (LF_DEVERR_STATE) and its rows of
+ * out and lse are left as they are; group starts that decrease are reported too, and the outputs of the sequences they
+ * overlap in are unspecified.  A bf16 cache's weights of values in the prefix are rounded as lf_paged_prompt's.  Three
+ * launches.
+ */
+int lf_paged_decode_shared(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
+                           const int32_t* lens, int q_heads, const void* q, const int32_t* group_start, int groups,
+                           const int32_t* prefix_lens, const void* k_new, const void* v_new, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, lf_stream_t stream);
+
+/* Bytes of the workspace of lf_paged_decode_shared calls with these arguments on the current device. */
+int lf_paged_decode_shared_workspace(const lf_pages* pages, int batch, int max_pages, int q_heads, int groups,
+                                     size_t* bytes);
+
+/*
  * Causal attention of the last tokens of every sequence over its pages, which hold
  * their keys and values already (lf_paged_append): whole prompts, or chunks behind
  * tokens that are cached.  Sequence b's queries are rows q_start[b] .. q_start[b +
