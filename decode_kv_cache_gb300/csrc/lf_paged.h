@@ -169,6 +169,8 @@ cudaError_t paged_prompt_tc_launch(const PagedPromptArgs& a, const PromptPlan& p
 // The prefixes of a decode call behind them, placed while the kernel before it drains (which has to have waited for
 // what came before itself), and the join of its parts with the rest of every sequence.
 cudaError_t paged_shared_launch(const PagedSharedArgs& a, const SharedPlan& plan, int head_dim, cudaStream_t stream);
+// Its tensor-core kernel, for what paged_prompt_tc_takes.
+cudaError_t paged_shared_tc_launch(const PagedSharedArgs& a, const SharedPlan& plan, int head_dim, cudaStream_t stream);
 cudaError_t paged_shared_join_launch(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int elem, int head_dim,
                                      int grid, cudaStream_t stream);
 

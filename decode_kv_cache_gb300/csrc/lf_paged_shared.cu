@@ -27,10 +27,9 @@ template <int kThreads>
 struct SharedTask {
   using Args = PagedSharedArgs;
   Segment s;
-  const int* limits;
 
   __device__ __forceinline__ bool take(const Args& a, int, int keys) {
-    const bool ok = take_segment<kThreads>(a, keys, &s, &limits);
+    const bool ok = take_segment<kThreads>(a, keys, &s);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!ok) finish();
     return ok;
@@ -39,7 +38,7 @@ struct SharedTask {
   __device__ __forceinline__ int count() const { return s.last - s.first; }
   __device__ __forceinline__ int at(int j) const { return s.first + j; }
   __device__ __forceinline__ bool live(const Args& a, int r) const { return r < s.members * a.group; }
-  __device__ __forceinline__ int pos(const Args& a, int r) const { return live(a, r) ? limits[r / a.group] : -1; }
+  __device__ __forceinline__ int pos(const Args& a, int r) const { return live(a, r) ? last_seen(a, s.prefix, s.b0 + r / a.group) : -1; }
   __device__ __forceinline__ int64_t q_row(const Args& a, int r) const { return shared_row(a, s, r); }
   __device__ __forceinline__ int behind(const Args&) const { return 0; }
   template <bool kSkip, class Behind>
@@ -241,7 +240,12 @@ cudaError_t join_dim(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int 
 SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int group, int groups, int sms) {
   SharedPlan p;
   p.keys = kKeys;
-  if (elem == 2) {
+  if (elem == 2 && paged_prompt_tc_takes(pool, head_dim)) {
+    p.kernel = PromptPlan::kTensor;
+    p.rows = 256;
+    p.keys = 128;
+    p.slots = sms;
+  } else if (elem == 2) {
     p.kernel = PromptPlan::kMatrix;
     p.rows = kMmaRows;
     p.slots = sms * (head_dim == 128 ? 3 : head_dim >= 32 ? 4 : 5);
@@ -263,6 +267,7 @@ SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int 
 }
 
 cudaError_t paged_shared_launch(const PagedSharedArgs& a, const SharedPlan& plan, int head_dim, cudaStream_t stream) {
+  if (plan.kernel == PromptPlan::kTensor) return paged_shared_tc_launch(a, plan, head_dim, stream);
   if (plan.kernel == PromptPlan::kMatrix) {
     switch (head_dim) {
       case 16: return launch_mma<16>(a, plan.grid, stream);

@@ -5,13 +5,12 @@
 
 namespace lf {
 
-constexpr int kMaxMembers = 256;   // sequences of a piece
-
 // A segment's rows and keys: the group's sequences b0 .. b0 + members - 1, KV head g, key tiles first .. last - 1
 // of the pages that sequence `leader` lists.
 struct Segment {
   int b0, members, g, leader, first, last;
-  int p_lo, p_hi;            // least and largest last position that a row sees
+  int prefix;                // the group's
+  int p_lo, p_hi;            // least and largest last position that a row sees of it
   int64_t row;               // of part_o
 };
 
@@ -38,6 +37,11 @@ __device__ __forceinline__ Family family_of(const PagedSharedArgs& a, int i, int
   return f;
 }
 
+// The last position that sequence b of a segment sees of its group's prefix, -1: none.
+__device__ __forceinline__ int last_seen(const PagedSharedArgs& a, int prefix, int b) {
+  return min(shared_len(a.prefix_lens[b], paged_len(a.pool, b), a.fresh != 0), prefix) - 1;
+}
+
 // Tiles of a segment.  A block costs its tiles and, for its start and its rows' way out, about as much as
 // four; U units of T tiles in all, the longest of `longest`, are cut so that r rounds of all blocks that run at once take
 // them, with the r that costs least.
@@ -61,12 +65,11 @@ __device__ __forceinline__ int segment_tiles(const PagedSharedArgs& a, int64_t u
 // Segment number blockIdx.x, for the whole block together; false: there is none.  Every block goes through
 // the groups itself (two scans of them): a launch that did so for all would be one more to wait for.
 template <int kThreads>
-__device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys, Segment* out, const int** limits) {
+__device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys, Segment* out) {
   constexpr int kW = kThreads / 32;
   __shared__ int64_t s_sum[2][kW + 1];
   __shared__ int s_max[2][kW];
   __shared__ Segment s_seg;
-  __shared__ int s_limit[kMaxMembers];   // the last position that a member sees of the prefix
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.groups + kThreads - 1) / kThreads;
   const int from = min(tid * per, a.groups), to = min(from + per, a.groups);
@@ -159,7 +162,8 @@ __device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys,
         s.leader = f.start;
         s.first = (int)((int64_t)f.tiles * j / n);
         s.last = (int)((int64_t)f.tiles * (j + 1) / n);
-        s.p_lo = s.p_hi = f.prefix;
+        s.prefix = f.prefix;
+        s.p_lo = s.p_hi = -1;
         s.row = row + (int64_t)piece * each * a.q_heads * n + ((int64_t)s.g * n + j) * s.members * a.group;
         s_seg = s;
       }
@@ -175,10 +179,7 @@ __device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys,
   // What its sequences see of the prefix.
   int lo = INT_MAX, hi = -1;
   for (int i = tid; i < s.members; i += kThreads) {
-    const int b = s.b0 + i, own = a.prefix_lens[b];
-    const int p = min(shared_len(own, paged_len(a.pool, b), a.fresh != 0), s.p_hi) - 1;
-    if (own > s.p_hi && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);   // more than the group's first
-    s_limit[i] = p;
+    const int p = last_seen(a, s.prefix, s.b0 + i);
     lo = min(lo, p);
     hi = max(hi, p);
   }
@@ -197,7 +198,6 @@ __device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys,
   }
   s.last = max(s.first, min(s.last, s.p_hi < 0 ? 0 : s.p_hi / keys + 1));
   *out = s;
-  *limits = s_limit;
   return true;
 }
 

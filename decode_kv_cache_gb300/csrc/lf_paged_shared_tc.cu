@@ -1,0 +1,420 @@
+// The prefixes of groups of sequences on the tensor cores (tcgen05): bf16 caches, head_dim 64 and 128, as
+// lf_paged_prompt_tc.cu does a prompt's rows; the formula is lf_paged_shared.cu's.
+//
+// Work.  A CTA takes up to 256 rows of one KV head, (sequence, head of the group) pairs with the head inner, as one or
+// two tiles of 128, and a segment of the key tiles of their prefix: every key and value that it loads serves all of
+// its group's sequences.  Its rows' shares (fp32, with their maximum and sum) go to the workspace.
+//
+// The roles are the prompt kernel's: a loader that gathers K and V by page with TMA, a warp that issues S = Q K^T and
+// O += P V for the query tiles in turn, two groups of softmax warps with a thread per row, and a scrubber for the tiles
+// that some row does not see all of (prefixes of other lengths, or the last tile).
+#include "lf_paged_shared.cuh"
+#include "lf_paged_tc.cuh"
+#include "longflow.h"
+
+namespace lf {
+
+namespace {
+
+struct SharedTcArgs {
+  CUtensorMap q, k, v;
+  PagedSharedArgs a;
+  int box_rows;      // tokens of one TMA box: min(page_size, 128)
+  int group_shift;
+};
+
+// The kernel before this one ends before this one does, and with it before the join.
+__device__ __forceinline__ void end_behind() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __grid_constant__ SharedTcArgs ta) {
+  using P = TcPlan<D>;
+  constexpr int S = P::kStages;
+  const PagedSharedArgs& a = ta.a;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform for the compiler too
+  const int gs = ta.group_shift;
+  if (warp == kLoadWarp && lane < 3) tma_prefetch_desc(lane == 0 ? &ta.q : lane == 1 ? &ta.k : &ta.v);
+
+  Segment seg;
+  const bool any = take_segment<kThreadsTc>(a, kTile, &seg);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!any) {
+    if (tid == 0) end_behind();
+    return;
+  }
+  const int rows = seg.members << gs, nt = seg.last - seg.first;
+  const int nq = rows > kTile ? 2 : 1;   // query tiles
+  // Does some row not see some key of the tile at k0?
+  auto masked = [&](int k0) { return k0 + kTile - 1 > seg.p_lo; };
+
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);   // [S] a tile is ready for the MMAs
+  uint64_t* raw = full + S;                             // [S] V landed, to be scrubbed
+  uint64_t* qfull = raw + S;
+  uint64_t* sfull = qfull + 1;                          // [t][j & 3] S_t of key tile j ready, and
+                                                        // every MMA before it done
+  uint64_t* pfull = sfull + 8;                          // [2][2] half of P_t written (O_t scaled)
+  uint64_t* ofull = pfull + 4;                          // [2] O_t final
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + 528);   // [0] a wait expired, [1] by hand
+  unsigned char* qs = smem + P::kOffQ;
+  unsigned char* ring = smem + P::kOffRing;
+
+  // The loader sets up the barriers and starts on the queries and the first key tile
+  // at once; the others meet it behind.
+  const int boxes = kTile / ta.box_rows, box = lane % boxes, blk = lane / boxes;
+  auto page_of = [&](int j, int* slot) {   // of this lane's box of key tile j; num_pages: zeros
+    const int p = (seg.first + j) * kTile + box * ta.box_rows;
+    *slot = 0;
+    if (lane >= boxes * (D / 64) || p > seg.p_hi) return a.pool.num_pages;
+    int pi;
+    paged_split(a.pool, p, &pi, slot);
+    const int page = a.pool.table[(int64_t)seg.leader * a.pool.max_pages + pi];
+    if (page >= 0 && page < a.pool.num_pages) return page;
+    if (a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+    return a.pool.num_pages;
+  };
+  auto load = [&](int i, bool scrub, int page, int slot) {   // K (i even) or V of key tile i / 2
+    const int st = i % S;
+    uint64_t* bar = (i & 1) && scrub ? &raw[st] : &full[st];
+    if (lane == 0) mbar_arrive_expect_tx(bar, P::kTileBytes);
+    __syncwarp();
+    if (lane < boxes * (D / 64))
+      tma_load_4d(ring + st * P::kTileBytes + blk * kBlk + box * ta.box_rows * 128, (i & 1) ? &ta.v : &ta.k,
+                  blk * 64, slot, seg.g, page, bar);
+  };
+  int page = 0, slot = 0;
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < S; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&raw[i], 1);
+      }
+      mbar_init(qfull, 1);
+      for (int t = 0; t < 2; ++t) {
+        for (int i = 0; i < 4; ++i) mbar_init(&sfull[4 * t + i], 1);
+        mbar_init(&pfull[2 * t], 4);
+        mbar_init(&pfull[2 * t + 1], 4);
+        mbar_init(&ofull[t], 1);
+      }
+      fence_mbar_init();
+      misc[0] = misc[1] = 0;
+    }
+    __syncwarp();
+    if (nt > 0) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(qfull, nq * P::kTileBytes);
+        for (int t = 0; t < nq; ++t)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(qs + t * P::kTileBytes + c * kBlk, &ta.q, c * 64, seg.g << gs, seg.b0 + t * (kTile >> gs), qfull);
+      }
+      page = page_of(0, &slot);
+      load(0, masked(seg.first * kTile), page, slot);
+      load(1, masked(seg.first * kTile), page, slot);
+    }
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_longer(bar, parity, misc);
+  };
+
+  if (warp == kLoadWarp) {
+    // ---- loader ---------------------------------------------------------------------
+    bool ok = true;
+    uint64_t* done = sfull + 4 * (nq - 1);   // S of the last query tile: the others' are done too
+    if (nt > 1) page = page_of(1, &slot);
+    for (int j = 1; j < nt && ok; ++j) {
+      const int cur_page = page, cur_slot = slot;
+      if (j + 1 < nt) page = page_of(j + 1, &slot);   // a tile ahead
+      const bool scrub = masked((seg.first + j) * kTile);
+      for (int i = 2 * j; i < 2 * j + 2; ++i) {
+        // The stage held load i - S, K or V of key tile u: K_u has been read once the last S
+        // of tile u is there, V_u once that of tile u + 1 is.  (u >= j - 4, and S of
+        // tile j waits for this load: of four barriers in turn none is a lap ahead.)
+        const int u = (i - S + 1) >> 1;
+        static_assert(S <= 8, "sfull barriers");
+        if (i >= S) ok = wait(&done[u & 3], (uint32_t)((u >> 2) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        load(i, scrub, cur_page, cur_slot);
+      }
+    }
+    // The MMAs wait for every copy, so none is in flight when the CTA exits, unless a
+    // wait ran out: then give the copies a second.
+    if (!ok) {
+      const unsigned long long t0 = global_ns();
+      while (global_ns() - t0 < kWaitLimitNs) {}
+    }
+    __syncwarp();
+  } else if (warp == kScrubWarp) {
+    // ---- scrubber -------------------------------------------------------------------
+    uint32_t phase = 0;   // a bit per stage: its raw barrier's next parity
+    for (int j = 0; j < nt; ++j) {
+      const int k0 = (seg.first + j) * kTile;
+      if (!masked(k0)) continue;
+      const int st = (2 * j + 1) % S;
+      const bool ok = wait(&raw[st], (phase >> st) & 1u);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      phase ^= 1u << st;
+      unsigned char* v = ring + st * P::kTileBytes;
+      const int valid = min(kTile, seg.p_hi + 1 - k0);
+      __nv_bfloat162 bad = __float2bfloat162_rn(0.f);
+      auto look = [&](const uint4& x) {   // 0 * x is 0, or NaN where x is not finite
+        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, bad);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, bad);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, bad);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, bad);
+      };
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint4* rows4 = reinterpret_cast<uint4*>(v + c * kBlk);   // eight chunks per row
+#pragma unroll 8
+        for (int i = lane; i < valid * 8; i += 32) look(rows4[i]);
+        for (int i = valid * 8 + lane; i < kTile * 8; i += 32) rows4[i] = make_uint4(0, 0, 0, 0);
+      }
+      const float2 f = __bfloat1622float2(bad);
+      if (__any_sync(0xffffffffu, !(f.x == 0.f) || !(f.y == 0.f)) && lane == 0) misc[1] = 1;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- MMA ------------------------------------------------------------------------
+    if (nt > 0) {
+      constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
+      const uint32_t lead = lane == 0;
+      // Descriptors of an operand differ in their start address alone (16-byte units).
+      const uint32_t dq = (uint32_t)sw128_desc(smem_u32(qs), 16, 1024);
+      const uint32_t dk = (uint32_t)sw128_desc(smem_u32(ring), 16, 1024);
+      const uint32_t dv = (uint32_t)sw128_desc(smem_u32(ring), kBlk, 1024);
+      auto all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+      auto mma_s = [&](int t, int j, int st) {
+        const uint32_t qd = dq + (uint32_t)(t * (P::kTileBytes >> 4));
+        const uint32_t kd = dk + (uint32_t)(st * (P::kTileBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (uint32_t)(((kk >> 2) * kBlk + (kk & 3) * 32) >> 4);
+          mma_ss(lead, tm + t * 128, qd + o, kd + o, kIdS, kk > 0 ? 1u : 0u);
+        }
+        if (lead) tc_commit(&sfull[4 * t + (j & 3)]);
+      };
+      auto mma_o = [&](int t, int st, int half, uint32_t acc) {
+        const uint32_t vd = dv + (uint32_t)(st * (P::kTileBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts(lead, tm + 256 + t * D, tm + t * 128 + half * 32 + kk * 8,
+                 vd + (uint32_t)((half * 4 + kk) * 128), kIdO, kk > 0 ? 1u : acc);
+      };
+      bool ok = all(qfull, 0) && all(&full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        mma_s(0, 0, 0);
+        if (nq == 2) mma_s(1, 0, 0);
+      }
+      int sv = 1 % S, sk = 2 % S;           // stages of V_j and K_(j+1)
+      uint32_t pv = 0, pk = 2 / S;          // and their parities
+      for (int j = 0; j < nt && ok; ++j) {
+        const bool last = j + 1 == nt;
+        const uint32_t pj = (uint32_t)(j & 1);
+        ok = all(&full[sv], pv);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t == nq) break;
+          ok = ok && all(&pfull[2 * t], pj);
+          if (!ok) break;
+          tc_fence_after();
+          mma_o(t, sv, 0, j > 0 ? 1u : 0u);
+          if (t == 0 && !last) ok = all(&full[sk], pk);
+          ok = ok && all(&pfull[2 * t + 1], pj);
+          if (!ok) break;
+          tc_fence_after();
+          mma_o(t, sv, 1, 1u);
+          if (!last) mma_s(t, j + 1, sk);
+          else if (lead) tc_commit(&ofull[t]);
+        }
+        sv += 2;
+        if (sv >= S) {
+          sv -= S;
+          pv ^= 1u;
+        }
+        sk += 2;
+        if (sk >= S) {
+          sk -= S;
+          pk ^= 1u;
+        }
+      }
+      if (!ok && lead) {   // MMAs in flight end before the tensor memory is given back
+        tc_commit(qfull);
+        (void)mbar_wait_bounded(qfull, 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kSoftWarp && (warp - kSoftWarp) >> 2 < nq) {
+    // ---- softmax ----------------------------------------------------------------------
+    const int t = (warp - kSoftWarp) >> 2;
+    const int rr0 = t * kTile + (warp & 3) * 32;   // the warp's first row in the segment
+    const bool live = rr0 + lane < rows;
+    const int pos = live ? last_seen(a, seg.prefix, seg.b0 + ((rr0 + lane) >> gs)) : -1;
+    const uint32_t ts = tm + t * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t to = tm + 256 + t * D + ((uint32_t)((warp & 3) * 32) << 16);
+    const float c = a.scale_log2;
+    float m = kNegInf, l = 0.f;   // the row's maximum (log2) and sum
+    bool ok = true;
+    for (int j = 0; j < nt; ++j) {
+      const int k0 = (seg.first + j) * kTile;
+      ok = __all_sync(0xffffffffu, wait(&sfull[4 * t + (j & 3)], (uint32_t)((j >> 2) & 1)));
+      if (!ok) break;
+      tc_fence_after();
+      float x[kTile];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
+      tmem_wait_ld();
+      if (masked(k0)) {
+        const int hi = pos - k0;
+#pragma unroll
+        for (int c0 = 0; c0 < kTile; c0 += 32)   // 32 keys that all rows of the warp see stay as they are
+          if (__any_sync(0xffffffffu, c0 + 31 > hi)) {
+#pragma unroll
+            for (int i = c0; i < c0 + 32; ++i)
+              if (i > hi) x[i] = kNegInf;
+          }
+      }
+      float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int i = 4; i < kTile; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e + 4 < kTile) top[e] = max3(top[e], x[i + e], x[i + e + 4]);
+          else top[e] = fmaxf(top[e], x[i + e]);
+      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+      // O_t holds no product yet at j = 0; later, every product before S_t is done.
+      if (__any_sync(0xffffffffu, mx > m + kGrow)) {
+        const float mn = fmaxf(m, mx);
+        const float f = mn == kNegInf ? 1.f : ex2(m - mn);
+        m = mn;
+        l *= f;
+        if (j > 0) {
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i) {
+            float o[16];
+            tmem_ld16(to + 16 * i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= f;
+            tmem_st16(to + 16 * i, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+      }
+      const float mu = m == kNegInf ? 0.f : m;
+      const uint64_t cc = pair(c, c), mm = pair(-mu, -mu);
+      uint64_t sum[2] = {0ull, 0ull};   // two pairs of zeros
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float u, w;
+          unpair(fma_pair(pair(x[64 * h + 2 * i], x[64 * h + 2 * i + 1]), cc, mm), &u, &w);
+          u = ex2(u);
+          w = ex2(w);
+          sum[i & 1] = add_pair(sum[i & 1], pair(u, w));
+          p[i] = pack_bf16(u, w);
+        }
+        tmem_st32(ts + 32 * h, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[2 * t + h]);
+      }
+      float u, w;
+      unpair(add_pair(sum[0], sum[1]), &u, &w);
+      l += u + w;
+    }
+
+    // ---- shares out --------------------------------------------------------------------
+    ok = ok && (nt == 0 || __all_sync(0xffffffffu, wait(&ofull[t], 0)));
+    tc_fence_after();
+    if (ok && !misc[1]) {   // (otherwise nothing is right, or the rows are computed again below)
+      unsigned char* stage = smem + P::kOffOut + (warp - kSoftWarp) * 4096;   // 32 rows x 32 columns
+      float* out = a.part_o + (seg.row + rr0) * D + (lane & 7) * 4;
+      const int left = rows - rr0;
+#pragma unroll 1
+      for (int h = 0; h < D / 32; ++h) {   // through shared memory: whole lines of global memory
+        float o[32];
+        tmem_ld32(to + 32 * h, o);
+        tmem_wait_ld();
+        __syncwarp();   // the columns before have been read
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+              nt > 0 ? make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3);
+          if (rr < left)
+            *reinterpret_cast<float4*>(out + (int64_t)rr * D + 32 * h) =
+                *reinterpret_cast<const float4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+        }
+      }
+      if (live) *reinterpret_cast<float2*>(a.part_ml + 2 * (seg.row + rr0 + lane)) = make_float2(m, l);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+    if (lane == 0 && misc[0] && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
+  }
+  if (misc[1] && !misc[0])
+    for (int r = warp; r < rows; r += kThreadsTc / 32)
+      shared_row_by_hand<__nv_bfloat16, D>(a, seg, kTile, r, last_seen(a, seg.prefix, seg.b0 + (r >> gs)), lane);
+  if (tid == 0) end_behind();
+}
+
+template <int D>
+cudaError_t launch(const SharedTcArgs& ta, int64_t grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  static_assert(TcPlan<D>::kSmem + 512 <= 232448, "with take_segment's own");
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_shared_tc_kernel<D>), TcPlan<D>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(kThreadsTc, 1, 1);
+  cfg.dynamicSmemBytes = TcPlan<D>::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_shared_tc_kernel<D>, ta);
+}
+
+}  // namespace
+
+cudaError_t paged_shared_tc_launch(const PagedSharedArgs& a, const SharedPlan& plan, int head_dim, cudaStream_t stream) {
+  const int ps = a.pool.page_size;
+  if (!encoder()) return cudaErrorNotSupported;
+  SharedTcArgs ta;
+  ta.a = a;
+  ta.box_rows = ps < kTile ? ps : kTile;
+  ta.group_shift = a.group == 1 ? 0 : a.group == 2 ? 1 : a.group == 4 ? 2 : 3;
+  if (!encode_maps(a.pool, a.q, a.q_heads, a.group, a.pool.batch, head_dim, ta.box_rows, &ta.q, &ta.k, &ta.v))
+    return cudaErrorInvalidValue;
+  return head_dim == 64 ? launch<64>(ta, plan.grid, stream) : launch<128>(ta, plan.grid, stream);
+}
+
+}  // namespace lf
