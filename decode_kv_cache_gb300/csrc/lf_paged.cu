@@ -486,9 +486,15 @@ int lf_paged_decode_shared(const lf_pages* pages, int batch, const int32_t* page
   a.first_row = reinterpret_cast<int64_t*>(w + shape.off_first);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int e = elem_bytes(pages);
-  cudaError_t err = lf::paged_decode_launch(d, e, pages->head_dim, shape.rest.grid, st);
-  if (err == cudaSuccess) err = lf::paged_shared_launch(a, shape.plan, pages->head_dim, st);
-  if (err == cudaSuccess) err = lf::paged_shared_join_launch(a, d, e, pages->head_dim, shape.rest.grid, st);
+  const int ctas = shape.rest.grid;
+  cudaError_t err;
+  if (shape.plan.kernel == lf::PromptPlan::kTensor) {
+    err = lf::paged_shared_tc_launch(a, d, pages->head_dim, ctas, st);
+  } else {
+    err = lf::paged_decode_launch(d, e, pages->head_dim, ctas, st);
+    if (err == cudaSuccess) err = lf::paged_shared_launch(a, shape.plan, pages->head_dim, st);
+  }
+  if (err == cudaSuccess) err = lf::paged_shared_join_launch(a, d, e, pages->head_dim, ctas, st);
   return err == cudaSuccess ? LF_OK : cuda_fail(err, "paged shared decode launch");
 }
 

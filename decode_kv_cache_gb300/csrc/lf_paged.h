@@ -166,13 +166,14 @@ bool paged_prompt_tc_takes(const PagedPool& pool, int head_dim);
 cudaError_t paged_prompt_tc_launch(const PagedPromptArgs& a, const PromptPlan& plan, int head_dim,
                                    cudaStream_t stream);
 
-// The prefixes of a decode call behind them, placed while the kernel before it drains (which has to have waited for
-// what came before itself), and the join of its parts with the rest of every sequence.
+// A decode call behind prefixes, and the join of its shares; `ctas`: those that the rest's walk may have had.  On the
+// tensor cores prefixes and rest are one launch of `ctas` CTAs.  Otherwise the prefixes follow the rest's launch, placed while
+// that drains (it has waited for what came before it).
+cudaError_t paged_shared_tc_launch(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int head_dim, int ctas,
+                                   cudaStream_t stream);
 cudaError_t paged_shared_launch(const PagedSharedArgs& a, const SharedPlan& plan, int head_dim, cudaStream_t stream);
-// Its tensor-core kernel, for what paged_prompt_tc_takes.
-cudaError_t paged_shared_tc_launch(const PagedSharedArgs& a, const SharedPlan& plan, int head_dim, cudaStream_t stream);
 cudaError_t paged_shared_join_launch(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int elem, int head_dim,
-                                     int grid, cudaStream_t stream);
+                                     int ctas, cudaStream_t stream);
 
 // Tokens that one CTA of the decode kernel takes in one sweep of its warps.
 int paged_decode_sweep(int elem, int head_dim);

@@ -267,7 +267,6 @@ SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int 
 }
 
 cudaError_t paged_shared_launch(const PagedSharedArgs& a, const SharedPlan& plan, int head_dim, cudaStream_t stream) {
-  if (plan.kernel == PromptPlan::kTensor) return paged_shared_tc_launch(a, plan, head_dim, stream);
   if (plan.kernel == PromptPlan::kMatrix) {
     switch (head_dim) {
       case 16: return launch_mma<16>(a, plan.grid, stream);

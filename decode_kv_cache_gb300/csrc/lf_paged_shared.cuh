@@ -43,162 +43,201 @@ __device__ __forceinline__ int last_seen(const PagedSharedArgs& a, int prefix, i
 }
 
 // Tiles of a segment.  A block costs its tiles and, for its start and its rows' way out, about as much as
-// four; U units of T tiles in all, the longest of `longest`, are cut so that r rounds of all blocks that run at once take
-// them, with the r that costs least.
-__device__ __forceinline__ int segment_tiles(const PagedSharedArgs& a, int64_t units, int64_t tiles, int longest) {
-  constexpr int kStart = 4;
+// kSegmentStart of them; `units` units of `tiles` tiles in all, the longest of `longest`, are cut so that r rounds of `slots` blocks
+// take them, with the r, up to `rounds`, that costs least.
+constexpr int kSegmentStart = 4;
+
+__device__ __forceinline__ int segment_tiles(int slots, int rounds, int64_t units, int64_t tiles, int longest) {
   int best = longest;
   int64_t cost = INT64_MAX;
-  const int64_t r0 = units / a.slots + 1;
-  for (int64_t r = r0; r < r0 + 2 && r <= a.rounds; ++r) {
-    const int64_t room = r * a.slots - units;
+  const int64_t r0 = units / slots + 1;
+  for (int64_t r = r0; r < r0 + 2 && r <= rounds; ++r) {
+    const int64_t room = r * slots - units;
     const int64_t c = min((int64_t)longest, max((int64_t)1, (tiles + room - 1) / room));
-    const int64_t used = c == longest ? (units + a.slots - 1) / a.slots : r;
-    if (used * (c + kStart) < cost) {
-      cost = used * (c + kStart);
+    const int64_t used = c == longest ? (units + slots - 1) / slots : r;
+    if (used * (c + kSegmentStart) < cost) {
+      cost = used * (c + kSegmentStart);
       best = (int)c;
     }
   }
   return best;
 }
 
-// Segment number blockIdx.x, for the whole block together; false: there is none.  Every block goes through
-// the groups itself (two scans of them): a launch that did so for all would be one more to wait for.
+// The segments of all groups, numbered group by group, piece by piece, head by head.  Every block goes through
+// the groups itself: a launch that did so for all would be one more to wait for.  Calls are for the whole block
+// together; a thread has a run of the groups.
 template <int kThreads>
-__device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys, Segment* out) {
-  constexpr int kW = kThreads / 32;
-  __shared__ int64_t s_sum[2][kW + 1];
-  __shared__ int s_max[2][kW];
-  __shared__ Segment s_seg;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.groups + kThreads - 1) / kThreads;
-  const int from = min(tid * per, a.groups), to = min(from + per, a.groups);
-  const int H = a.pool.kv_heads;
+struct SegmentList {
+  static constexpr int kW = kThreads / 32;
+  int from, to, chunk;
+  int64_t seg, seg_to, row;   // segments before this thread's groups and with them, rows of part_o before them
+  int64_t segments;
 
-  int64_t units = 0, tiles = 0;
-  int longest = 0;
-  for (int i = from; i < to; ++i) {
-    const Family f = family_of(a, i, keys);
-    if (f.tiles > 0) {
-      units += (int64_t)f.pieces * H;
-      tiles += (int64_t)f.pieces * H * f.tiles;
-      longest = max(longest, f.tiles);
-    }
-    if (!f.right && blockIdx.x == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    units += __shfl_xor_sync(0xffffffffu, units, o);
-    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-  }
-  if (lane == 0) {
-    s_sum[0][warp] = units;
-    s_sum[1][warp] = tiles;
-    s_max[0][warp] = longest;
-  }
-  if (tid == 0) s_seg.members = 0;
-  __syncthreads();
-  units = tiles = 0;
-  longest = 0;
-  for (int w = 0; w < kW; ++w) {
-    units += s_sum[0][w];
-    tiles += s_sum[1][w];
-    longest = max(longest, s_max[0][w]);
-  }
-  __syncthreads();
-  if (units == 0) {
-    if (blockIdx.x == 0)
-      for (int i = from; i < to; ++i) a.segments[i] = 0;
-    return false;
-  }
-  const int chunk = segment_tiles(a, units, tiles, longest);
-
-  // Segments and rows before this thread's groups.
-  int64_t seg = 0, row = 0;
-  auto cut = [&](const Family& f) { return (f.tiles + chunk - 1) / chunk; };
-  for (int i = from; i < to; ++i) {
-    const Family f = family_of(a, i, keys);
-    seg += (int64_t)f.pieces * H * cut(f);
-    row += (int64_t)f.members * a.q_heads * cut(f);
-  }
-  int64_t seg_to = seg, row_to = row;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, seg_to, o), y = __shfl_up_sync(0xffffffffu, row_to, o);
-    if (lane >= o) {
-      seg_to += x;
-      row_to += y;
-    }
-  }
-  if (lane == 31) {
-    s_sum[0][warp] = seg_to;
-    s_sum[1][warp] = row_to;
-  }
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) {
-    seg_to += s_sum[0][w];
-    row_to += s_sum[1][w];
-  }
-  seg = seg_to - seg;
-  row = row_to - row;
-  const int64_t id = blockIdx.x;
-  if (blockIdx.x == 0 || (id >= seg && id < seg_to)) {
+  // Units, tiles and the longest unit's tiles of all groups, and the sum of every thread's `more`.
+  __device__ __forceinline__ void sum(const PagedSharedArgs& a, int keys, int64_t* units, int64_t* tiles, int* longest,
+                                      int64_t* more) {
+    __shared__ int64_t s_sum[3][kW];
+    __shared__ int s_max[kW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.groups + kThreads - 1) / kThreads;
+    from = min(tid * per, a.groups);
+    to = min(from + per, a.groups);
+    int64_t u = 0, t = 0, x = *more;
+    int most = 0;
     for (int i = from; i < to; ++i) {
       const Family f = family_of(a, i, keys);
-      const int n = cut(f);
-      if (blockIdx.x == 0) {
-        a.segments[i] = n;
-        a.first_row[i] = row;
+      if (f.tiles > 0) {
+        u += (int64_t)f.pieces * a.pool.kv_heads;
+        t += (int64_t)f.pieces * a.pool.kv_heads * f.tiles;
+        most = max(most, f.tiles);
       }
-      const int64_t mine = (int64_t)f.pieces * H * n;
-      if (id >= seg && id < seg + mine) {
-        const int64_t unit = (id - seg) / n;
-        const int j = (int)(id - seg - unit * n), piece = (int)(unit / H), each = a.rows / a.group;
-        Segment s;
-        s.g = (int)(unit - (int64_t)piece * H);
-        s.b0 = f.start + piece * each;
-        s.members = min(each, f.members - piece * each);
-        s.leader = f.start;
-        s.first = (int)((int64_t)f.tiles * j / n);
-        s.last = (int)((int64_t)f.tiles * (j + 1) / n);
-        s.prefix = f.prefix;
-        s.p_lo = s.p_hi = -1;
-        s.row = row + (int64_t)piece * each * a.q_heads * n + ((int64_t)s.g * n + j) * s.members * a.group;
-        s_seg = s;
-      }
-      seg += mine;
-      row += (int64_t)f.members * a.q_heads * n;
+      if (!f.right && blockIdx.x == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      u += __shfl_xor_sync(0xffffffffu, u, o);
+      t += __shfl_xor_sync(0xffffffffu, t, o);
+      x += __shfl_xor_sync(0xffffffffu, x, o);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      s_sum[0][warp] = u;
+      s_sum[1][warp] = t;
+      s_sum[2][warp] = x;
+      s_max[warp] = most;
+    }
+    __syncthreads();
+    *units = *tiles = *more = 0;
+    *longest = 0;
+    for (int w = 0; w < kW; ++w) {
+      *units += s_sum[0][w];
+      *tiles += s_sum[1][w];
+      *more += s_sum[2][w];
+      *longest = max(*longest, s_max[w]);
     }
   }
-  __syncthreads();
-  Segment s = s_seg;
-  // (Starts that decrease may ask for more than there is room for.)
-  if (s.members == 0 || s.row + (int64_t)s.members * a.group > a.part_rows) return false;
 
-  // What its sequences see of the prefix.
-  int lo = INT_MAX, hi = -1;
-  for (int i = tid; i < s.members; i += kThreads) {
-    const int p = last_seen(a, s.prefix, s.b0 + i);
-    lo = min(lo, p);
-    hi = max(hi, p);
+  __device__ __forceinline__ int cuts(const Family& f) const { return (f.tiles + chunk - 1) / chunk; }
+
+  // Cut into segments of up to `tiles` tiles; block 0 tells the join.
+  __device__ __forceinline__ void cut(const PagedSharedArgs& a, int keys, int tiles) {
+    __shared__ int64_t s_sum[2][kW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    chunk = tiles;
+    int64_t n = 0, r = 0;
+    for (int i = from; i < to; ++i) {
+      const Family f = family_of(a, i, keys);
+      n += (int64_t)f.pieces * a.pool.kv_heads * cuts(f);
+      r += (int64_t)f.members * a.q_heads * cuts(f);
+    }
+    seg_to = n;
+    row = r;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, seg_to, o), y = __shfl_up_sync(0xffffffffu, row, o);
+      if (lane >= o) {
+        seg_to += x;
+        row += y;
+      }
+    }
+    if (lane == 31) {
+      s_sum[0][warp] = seg_to;
+      s_sum[1][warp] = row;
+    }
+    __syncthreads();
+    segments = 0;
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) {
+        seg_to += s_sum[0][w];
+        row += s_sum[1][w];
+      }
+      segments += s_sum[0][w];
+    }
+    seg = seg_to - n;
+    row -= r;
+    if (blockIdx.x == 0) {
+      int64_t at = row;
+      for (int i = from; i < to; ++i) {
+        const Family f = family_of(a, i, keys);
+        a.segments[i] = cuts(f);
+        a.first_row[i] = at;
+        at += (int64_t)f.members * a.q_heads * cuts(f);
+      }
+    }
   }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lane == 0) {
-    s_max[0][warp] = lo;
-    s_max[1][warp] = hi;
+
+  // Segment number `id`; false: there is none.
+  __device__ __forceinline__ bool find(const PagedSharedArgs& a, int keys, int64_t id, Segment* out) const {
+    __shared__ Segment s_seg;
+    __shared__ int s_lo[kW], s_hi[kW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int H = a.pool.kv_heads;
+    if (tid == 0) s_seg.members = 0;
+    __syncthreads();
+    if (id >= seg && id < seg_to) {
+      int64_t before = seg, r = row;
+      for (int i = from; i < to; ++i) {
+        const Family f = family_of(a, i, keys);
+        const int n = cuts(f);
+        const int64_t mine = (int64_t)f.pieces * H * n;
+        if (id >= before && id < before + mine) {
+          const int64_t unit = (id - before) / n;
+          const int j = (int)(id - before - unit * n), piece = (int)(unit / H), each = a.rows / a.group;
+          Segment s;
+          s.g = (int)(unit - (int64_t)piece * H);
+          s.b0 = f.start + piece * each;
+          s.members = min(each, f.members - piece * each);
+          s.leader = f.start;
+          s.first = (int)((int64_t)f.tiles * j / n);
+          s.last = (int)((int64_t)f.tiles * (j + 1) / n);
+          s.prefix = f.prefix;
+          s.p_lo = s.p_hi = -1;
+          s.row = r + (int64_t)piece * each * a.q_heads * n + ((int64_t)s.g * n + j) * s.members * a.group;
+          s_seg = s;
+        }
+        before += mine;
+        r += (int64_t)f.members * a.q_heads * n;
+      }
+    }
+    __syncthreads();
+    Segment s = s_seg;
+    // What its sequences see of the prefix.
+    int lo = INT_MAX, hi = -1;
+    for (int i = tid; i < s.members; i += kThreads) {
+      const int p = last_seen(a, s.prefix, s.b0 + i);
+      lo = min(lo, p);
+      hi = max(hi, p);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      s_lo[warp] = lo;
+      s_hi[warp] = hi;
+    }
+    __syncthreads();
+    // (Starts that decrease may ask for more than there is room for.)
+    if (s.members == 0 || s.row + (int64_t)s.members * a.group > a.part_rows) return false;
+    s.p_lo = s_lo[0];
+    s.p_hi = s_hi[0];
+    for (int w = 1; w < kW; ++w) {
+      s.p_lo = min(s.p_lo, s_lo[w]);
+      s.p_hi = max(s.p_hi, s_hi[w]);
+    }
+    s.last = max(s.first, min(s.last, s.p_hi < 0 ? 0 : s.p_hi / keys + 1));
+    *out = s;
+    return true;
   }
-  __syncthreads();
-  s.p_lo = s_max[0][0];
-  s.p_hi = s_max[1][0];
-  for (int w = 1; w < kW; ++w) {
-    s.p_lo = min(s.p_lo, s_max[0][w]);
-    s.p_hi = max(s.p_hi, s_max[1][w]);
-  }
-  s.last = max(s.first, min(s.last, s.p_hi < 0 ? 0 : s.p_hi / keys + 1));
-  *out = s;
-  return true;
+};
+
+// Segment number blockIdx.x, where each block takes one; false: there is none.
+template <int kThreads>
+__device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys, Segment* out) {
+  SegmentList<kThreads> list;
+  int64_t units, tiles, none = 0;
+  int longest;
+  list.sum(a, keys, &units, &tiles, &longest, &none);
+  list.cut(a, keys, units > 0 ? segment_tiles(a.slots, a.rounds, units, tiles, longest) : 1);
+  return blockIdx.x < list.segments && list.find(a, keys, blockIdx.x, out);
 }
 
 // Byte offset in the pools of the prefix's position `pos`, -1: nothing to read.

@@ -1,13 +1,17 @@
-// The prefixes of groups of sequences on the tensor cores (tcgen05): bf16 caches, head_dim 64 and 128, as
-// lf_paged_prompt_tc.cu does a prompt's rows; the formula is lf_paged_shared.cu's.
+// Attention of one new token per sequence behind shared prefixes, bf16 caches, head_dim 64 and 128: the prefixes on the
+// tensor cores (tcgen05), as lf_paged_prompt_tc.cu does a prompt's rows, and the rest by lf_paged_decode.cu's walk, side by
+// side in one launch; the formula and the join are lf_paged_shared.cu's.
 //
-// Work.  A CTA takes up to 256 rows of one KV head, (sequence, head of the group) pairs with the head inner, as one or
-// two tiles of 128, and a segment of the key tiles of their prefix: every key and value that it loads serves all of
-// its group's sequences.  Its rows' shares (fp32, with their maximum and sum) go to the workspace.
+// Work.  One CTA per SM.  Some take segments of the prefixes, the others ranges of the rest, as many of
+// each as there are key tiles (each CTA works that out from the lengths): one kind behind the other would wait for the first's last
+// tiles and the second's first ones.  A prefix CTA takes up to 256 rows of one KV head, (sequence, head of the group)
+// pairs with the head inner, as one or two tiles of 128, and a segment of the key tiles of their prefix: every key and value that it
+// loads serves all of its group's sequences.  Its rows' shares (fp32, with their maximum and sum) go to the workspace.
 //
-// The roles are the prompt kernel's: a loader that gathers K and V by page with TMA, a warp that issues S = Q K^T and
+// A prefix CTA's roles are the prompt kernel's: a loader that gathers K and V by page with TMA, a warp that issues S = Q K^T and
 // O += P V for the query tiles in turn, two groups of softmax warps with a thread per row, and a scrubber for the tiles
 // that some row does not see all of (prefixes of other lengths, or the last tile).
+#include "lf_paged_decode.cuh"
 #include "lf_paged_shared.cuh"
 #include "lf_paged_tc.cuh"
 #include "longflow.h"
@@ -19,37 +23,62 @@ namespace {
 struct SharedTcArgs {
   CUtensorMap q, k, v;
   PagedSharedArgs a;
+  PagedDecodeArgs rest;
   int box_rows;      // tokens of one TMA box: min(page_size, 128)
   int group_shift;
 };
 
-// The kernel before this one ends before this one does, and with it before the join.
-__device__ __forceinline__ void end_behind() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void mbar_inval(uint64_t* bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
-template <int D>
+template <int D, int G>
 __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __grid_constant__ SharedTcArgs ta) {
   using P = TcPlan<D>;
+  using C = MmaTile<D, G>;
   constexpr int S = P::kStages;
   const PagedSharedArgs& a = ta.a;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform for the compiler too
   const int gs = ta.group_shift;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   if (warp == kLoadWarp && lane < 3) tma_prefetch_desc(lane == 0 ? &ta.q : lane == 1 ? &ta.k : &ta.v);
-
-  Segment seg;
-  const bool any = take_segment<kThreadsTc>(a, kTile, &seg);
+  // Everything below reads what earlier launches of the stream wrote.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (!any) {
-    if (tid == 0) end_behind();
+
+  // ---- who does what ------------------------------------------------------------------
+  SegmentList<kThreadsTc> list;
+  int64_t units, tiles, rest = 0;
+  int longest;
+  for (int b = tid; b < a.pool.batch; b += kThreadsTc) rest += seen_of<C::kTokens>(ta.rest, b).tiles;
+  list.sum(a, kTile, &units, &tiles, &longest, &rest);
+  const int ctas = gridDim.x;
+  int prefix_ctas = 0;
+  if (units > 0) {
+    const float mine = (float)(tiles + kSegmentStart * units);
+    const float others = (float)rest * ((float)a.pool.kv_heads * C::kTokens / kTile);
+    prefix_ctas = max(1, min(ctas - 1, __float2int_rn(ctas * mine / (mine + others))));
+  }
+  list.cut(a, kTile, units > 0 ? segment_tiles(prefix_ctas, INT_MAX, units, tiles, longest) : 1);
+  if (list.segments < prefix_ctas) prefix_ctas = (int)list.segments;
+  if ((int)blockIdx.x >= prefix_ctas) {
+    if (warp < C::kWarps)
+      decode_walk<C, D, G>(ta.rest, smem, blockIdx.x - prefix_ctas, ctas - prefix_ctas,
+                           [] { named_bar_sync(1, C::kWarps * 32); });
     return;
   }
+  if (tid == 0) ta.rest.part_unit[ctas - 1 - blockIdx.x] = -1;   // the ranges that are not taken
+  bool again = false;
+  for (int64_t id = blockIdx.x; id < list.segments; id += prefix_ctas) {
+  Segment seg;
+  if (!list.find(a, kTile, id, &seg)) continue;
   const int rows = seg.members << gs, nt = seg.last - seg.first;
   const int nq = rows > kTile ? 2 : 1;   // query tiles
   // Does some row not see some key of the tile at k0?
   auto masked = [&](int k0) { return k0 + kTile - 1 > seg.p_lo; };
 
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);   // [S] a tile is ready for the MMAs
   uint64_t* raw = full + S;                             // [S] V landed, to be scrubbed
   uint64_t* qfull = raw + S;
@@ -88,6 +117,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   int page = 0, slot = 0;
   if (warp == kLoadWarp) {
     if (lane == 0) {
+      static_assert(2 * S + 1 + 8 + 4 + 2 <= 64, "barriers in front of tmem_slot");
+      if (again)   // every wait on them is over, and every copy and product that arrives at them
+        for (int i = 0; i < 2 * S + 15; ++i) mbar_inval(full + i);
       for (int i = 0; i < S; ++i) {
         mbar_init(&full[i], 1);
         mbar_init(&raw[i], 1);
@@ -115,10 +147,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
       load(1, masked(seg.first * kTile), page, slot);
     }
   }
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp && !again) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  again = true;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -373,22 +406,28 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
-    tc_fence_after();
-    tmem_dealloc(tm, 512);
-    if (lane == 0 && misc[0] && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
-  }
-  if (misc[1] && !misc[0])
+  tc_fence_after();
+  if (misc[0]) break;   // a wait ran out
+  if (misc[1])
     for (int r = warp; r < rows; r += kThreadsTc / 32)
       shared_row_by_hand<__nv_bfloat16, D>(a, seg, kTile, r, last_seen(a, seg.prefix, seg.b0 + (r >> gs)), lane);
-  if (tid == 0) end_behind();
+  __syncthreads();   // misc has been read
+  }
+  if (!again) return;
+  if (warp == kMmaWarp) {
+    tmem_dealloc(*reinterpret_cast<uint32_t*>(smem + 512), 512);
+    if (lane == 0 && *reinterpret_cast<volatile int*>(smem + 528) && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
+  }
 }
 
-template <int D>
+template <int D, int G>
 cudaError_t launch(const SharedTcArgs& ta, int64_t grid, cudaStream_t stream) {
+  using C = MmaTile<D, G>;
+  constexpr int kWalk = C::kWarps * warp_bytes<C, D, G>() + 1024;
+  constexpr int kSmem = TcPlan<D>::kSmem > kWalk ? TcPlan<D>::kSmem : kWalk;
+  static_assert(kSmem + 1024 <= 232448, "with the lists' own");
   static std::atomic<uint64_t> done{0};
-  static_assert(TcPlan<D>::kSmem + 512 <= 232448, "with take_segment's own");
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_shared_tc_kernel<D>), TcPlan<D>::kSmem, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_shared_tc_kernel<D, G>), kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -396,25 +435,37 @@ cudaError_t launch(const SharedTcArgs& ta, int64_t grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(kThreadsTc, 1, 1);
-  cfg.dynamicSmemBytes = TcPlan<D>::kSmem;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_shared_tc_kernel<D>, ta);
+  return cudaLaunchKernelEx(&cfg, paged_shared_tc_kernel<D, G>, ta);
+}
+
+template <int D>
+cudaError_t launch_group(const SharedTcArgs& ta, int64_t grid, cudaStream_t stream) {
+  switch (ta.a.group) {
+    case 1: return launch<D, 1>(ta, grid, stream);
+    case 2: return launch<D, 2>(ta, grid, stream);
+    case 4: return launch<D, 4>(ta, grid, stream);
+    default: return launch<D, 8>(ta, grid, stream);
+  }
 }
 
 }  // namespace
 
-cudaError_t paged_shared_tc_launch(const PagedSharedArgs& a, const SharedPlan& plan, int head_dim, cudaStream_t stream) {
+cudaError_t paged_shared_tc_launch(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int head_dim, int grid,
+                                   cudaStream_t stream) {
   const int ps = a.pool.page_size;
   if (!encoder()) return cudaErrorNotSupported;
   SharedTcArgs ta;
   ta.a = a;
+  ta.rest = rest;
   ta.box_rows = ps < kTile ? ps : kTile;
   ta.group_shift = a.group == 1 ? 0 : a.group == 2 ? 1 : a.group == 4 ? 2 : 3;
   if (!encode_maps(a.pool, a.q, a.q_heads, a.group, a.pool.batch, head_dim, ta.box_rows, &ta.q, &ta.k, &ta.v))
     return cudaErrorInvalidValue;
-  return head_dim == 64 ? launch<64>(ta, plan.grid, stream) : launch<128>(ta, plan.grid, stream);
+  return head_dim == 64 ? launch_group<64>(ta, grid, stream) : launch_group<128>(ta, grid, stream);
 }
 
 }  // namespace lf
