@@ -303,7 +303,7 @@ int decode_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int wi
 struct SharedShape {
   DecodeShape rest;
   lf::SharedPlan plan;
-  size_t off_rest_o, off_rest_ml, off_part_o, off_part_ml, off_segments, off_first, bytes;
+  size_t off_rest_o, off_rest_ml, off_part_o, off_part_ml, off_segments, off_first, off_ranges, bytes;
 };
 
 int shared_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int groups, SharedShape* s) {
@@ -312,7 +312,7 @@ int shared_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int gr
   int rc = sm_count(&sms);
   if (rc != LF_OK || (rc = decode_shape(p, pool, group, 0, 0, &s->rest, true)) != LF_OK) return rc;
   s->plan = lf::paged_shared_plan(pool, elem_bytes(p), p->head_dim, group, groups, sms);
-  if (s->plan.grid > INT_MAX) return fail(LF_ERR_ARG, "batch * kv_heads is too large for one call");
+  if (!s->plan.fits) return fail(LF_ERR_ARG, "batch * kv_heads * max_pages * page_size is too large for one call");
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = (size_t)pool.batch * pool.kv_heads * group, d = p->head_dim;
   s->off_rest_o = up(s->rest.bytes);
@@ -321,7 +321,8 @@ int shared_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int gr
   s->off_part_ml = s->off_part_o + up((size_t)s->plan.part_rows * d * 4);
   s->off_segments = s->off_part_ml + up((size_t)s->plan.part_rows * 2 * 4);
   s->off_first = s->off_segments + up((size_t)groups * 4);
-  s->bytes = s->off_first + up((size_t)groups * 8);
+  s->off_ranges = s->off_first + up((size_t)groups * 8);
+  s->bytes = s->off_ranges + up(3 * 4);
   return LF_OK;
 }
 
@@ -484,6 +485,8 @@ int lf_paged_decode_shared(const lf_pages* pages, int batch, const int32_t* page
   a.part_ml = floats(shape.off_part_ml);
   a.segments = reinterpret_cast<int32_t*>(w + shape.off_segments);
   a.first_row = reinterpret_cast<int64_t*>(w + shape.off_first);
+  a.ranges = reinterpret_cast<int32_t*>(w + shape.off_ranges);
+  a.slot_rows = shape.plan.slot_rows;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int e = elem_bytes(pages);
   const int ctas = shape.rest.grid;

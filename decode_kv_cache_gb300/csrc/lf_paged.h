@@ -95,15 +95,21 @@ struct PagedSharedArgs {
   int64_t part_rows;          // rows that part_o and part_ml have
   float* part_o;              // [part_rows][head_dim] partial outputs
   float* part_ml;             // [part_rows][2] their max and sum
-  int32_t* segments;          // [groups] segments of a unit, for the join
-  int64_t* first_row;         // [groups] the first of the group's rows in part_o
+  // For the join, of every group.  Blocks of a segment each: segments of a unit, first row of the group in part_o.
+  // Ranges (ranges[0] > 0 CTAs of ranges[1] places, ranges[2] in front of a unit; slot_rows rows of part_o per CTA):
+  // tiles of a unit, the group's first place.
+  int32_t* segments;          // [groups]
+  int64_t* first_row;         // [groups]
+  int32_t* ranges;            // [3]
+  int slot_rows;
 };
 
 // Its kernel by type, heads and pages, and the rows of a piece.
 struct SharedPlan {
   PromptPlan::Kernel kernel;
-  int rows, keys, slots, rounds;
+  int rows, keys, slots, rounds, slot_rows;
   int64_t grid, part_rows;
+  bool fits;                  // the kernels' numbers hold such a call
 };
 SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int group, int groups, int sms);
 

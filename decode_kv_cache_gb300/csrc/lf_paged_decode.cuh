@@ -26,11 +26,11 @@ namespace {
 // rows 0-7 take the group's queries, zero behind them.  For P.V rows 0-7 hold
 // bf16(p) and rows 8-15 bf16(p - bf16(p)), so p keeps 16 bits at no cost: O is
 // the sum of the two halves.
-template <int D, int G>
-struct MmaTile {
+template <int D, int G, int Warps, int Stages>
+struct MmaWalk {
   using T = __nv_bfloat16;
   static constexpr int kTokens = D == 128 ? 16 : D == 64 ? 32 : 64;
-  static constexpr int kWarps = 8, kStages = 3, kExtra = 0;
+  static constexpr int kWarps = Warps, kStages = Stages, kExtra = 0;
   static constexpr int NC = D / 8;  // 16-byte chunks of a row
   uint32_t qa[D / 16][2];
   float o[D / 8][4];
@@ -157,6 +157,9 @@ struct MmaTile {
     }
   }
 };
+
+template <int D, int G>
+struct MmaTile : MmaWalk<D, G, 8, 3> {};
 
 // fp32: multiply-adds on the CUDA cores (tf32 would drop 13 bits of every
 // factor).  For the logits a lane takes a token and a share of d; for P.V it
@@ -568,9 +571,10 @@ __device__ __forceinline__ void decode_walk(const PagedDecodeArgs& a, unsigned c
     cp_async_wait<S - 2>();
     __syncwarp();
     const uint32_t kd = ring + stage * 2 * kTile;
+    if constexpr (S == 2) load_next(stage ^ 1);   // on its way while this one is taken
     c.tile(a, kd, kd + kTile, min(TT, at.s.seen - at.t * TT), extra);
     __syncwarp();
-    load_next(stage == 0 ? S - 1 : stage - 1);
+    if constexpr (S > 2) load_next(stage == 0 ? S - 1 : stage - 1);
     stage = stage + 1 == S ? 0 : stage + 1;
     const bool unit_end = at.t + 1 == at.s.tiles;
     if (unit_end && from_start) {

@@ -147,25 +147,33 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_shared_join_kernel(cons
     }
   __syncthreads();
   const int w = s_first, rest = s_count > 0 ? s_count + 1 : 1;
-  const int each = a.rows / G, piece = (b - start) / each;
-  const int segs = a.segments[lo], members = min(each, end - start - piece * each);
-  int64_t row = 0;
+  // The prefix's shares: `segs` rows of part_o from `row`, `apart` rows apart.
+  const int each = a.rows / G, piece = (b - start) / each, members = min(each, end - start - piece * each);
+  int segs = a.segments[lo];
+  int64_t row = 0, apart = (int64_t)members * G;
   bool room = true;
-  if (segs > 0) {
-    row = a.first_row[lo] + (int64_t)piece * each * a.q_heads * segs + (int64_t)g * segs * members * G +
-          (b - start - piece * each) * G;
-    room = row + (int64_t)(segs - 1) * members * G + G <= a.part_rows;
+  if (segs > 0 && a.ranges[0] > 0) {
+    const Ranges ranges(a.ranges[1], a.ranges[0]);
+    const unsigned size = segs + a.ranges[2];
+    const unsigned first = (unsigned)a.first_row[lo] + (unsigned)(piece * a.pool.kv_heads + g) * size + a.ranges[2];
+    const unsigned cta = ranges.owner(first);
+    segs = ranges.owner(first + segs - 1) - cta + 1;
+    apart = a.slot_rows;
+    row = cta * apart + (int64_t)(start + piece * each) * a.q_heads + (int64_t)g * members * G + (b - start - piece * each) * G;
+  } else if (segs > 0) {
+    row = a.first_row[lo] + (int64_t)piece * each * a.q_heads * segs + g * segs * apart + (b - start - piece * each) * G;
   }
+  if (segs != 0) room = segs > 0 && row >= 0 && row + (segs - 1) * apart + G <= a.part_rows;
   const int parts = rest + (room ? segs : 0);
   const int h = warp % G, stripe = warp / G;
   const int64_t out_row = (int64_t)b * a.q_heads + g * G + h;
   auto ml = [&](int i) -> const float* {
-    if (i >= rest) return a.part_ml + 2 * (row + (int64_t)(i - rest) * members * G + h);
+    if (i >= rest) return a.part_ml + 2 * (row + (i - rest) * apart + h);
     if (rest == 1) return d.rest_ml + 2 * out_row;
     return d.part_ml + ((i == 0 ? 2 * (int64_t)(w - 1) + 1 : 2 * (int64_t)(w - 1 + i)) * G + h) * 2;
   };
   auto o = [&](int i) -> const float* {
-    if (i >= rest) return a.part_o + (row + (int64_t)(i - rest) * members * G + h) * D;
+    if (i >= rest) return a.part_o + (row + (i - rest) * apart + h) * D;
     if (rest == 1) return d.rest_o + out_row * D;
     return d.part_o + ((i == 0 ? 2 * (int64_t)(w - 1) + 1 : 2 * (int64_t)(w - 1 + i)) * G + h) * D;
   };
@@ -258,11 +266,20 @@ SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int 
   const int64_t each = p.rows / group;
   const int64_t pieces = ((int64_t)pool.batch + groups * (each - 1)) / each;
   const int64_t units = (pieces < pool.batch ? pieces : pool.batch) * pool.kv_heads;
+  p.slot_rows = (int)((int64_t)pool.batch * group < p.rows ? (int64_t)pool.batch * group : p.rows);
+  if (p.kernel == PromptPlan::kTensor) {   // ranges: a slot for each CTA, and a unit's own rows
+    const int64_t tiles = ((int64_t)pool.max_pages * pool.page_size + p.keys - 1) / p.keys;
+    p.grid = sms;
+    p.rounds = 1;
+    p.part_rows = (int64_t)sms * p.slot_rows + (int64_t)pool.batch * group * pool.kv_heads;
+    p.fits = units * (tiles + 8) <= INT_MAX;
+    return p;
+  }
   p.rounds = 2 * units <= p.slots ? 1 : (int)(units / p.slots) + 2;
   p.grid = (int64_t)p.rounds * p.slots;
   // A unit of c-tile segments has at most one more than its share of the room (segment_tiles).
-  const int64_t all = (int64_t)pool.batch * group, most = all < p.rows ? all : p.rows;
-  p.part_rows = most * 2 * p.slots + all * pool.kv_heads;
+  p.part_rows = (int64_t)p.slot_rows * 2 * p.slots + (int64_t)pool.batch * group * pool.kv_heads;
+  p.fits = p.grid <= INT_MAX;
   return p;
 }
 

@@ -163,6 +163,7 @@ struct SegmentList {
         a.first_row[i] = at;
         at += (int64_t)f.members * a.q_heads * cuts(f);
       }
+      if (threadIdx.x == 0) a.ranges[0] = 0;
     }
   }
 
@@ -238,6 +239,160 @@ __device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys,
   list.sum(a, keys, &units, &tiles, &longest, &none);
   list.cut(a, keys, units > 0 ? segment_tiles(a.slots, a.rounds, units, tiles, longest) : 1);
   return blockIdx.x < list.segments && list.find(a, keys, blockIdx.x, out);
+}
+
+// ---- ranges: prefixes and the rest in one launch ------------------------------------------
+//
+// The units of all groups (group by group, piece by piece, head by head) lie one behind another, each `start` places, for what
+// a CTA spends on a unit besides its tiles, and then a place for each of its tiles.  The first `ctas` CTAs take equal ranges of the
+// list, the others the rest of the sequences.  Numbers are below 2^31 (the entry point sees to it).  Every place belongs to one
+// thread's groups.
+
+// CTA i's range: q places, one more for the first r CTAs.
+struct Ranges {
+  unsigned q, r;
+  __device__ __forceinline__ Ranges(unsigned places, unsigned ctas) : q(places / ctas), r(places - places / ctas * ctas) {}
+  __device__ __forceinline__ unsigned first(unsigned i) const { return q * i + min(i, r); }
+  __device__ __forceinline__ unsigned owner(unsigned x) const {
+    const unsigned wide = r * (q + 1);
+    return x < wide ? x / (q + 1) : r + (x - wide) / q;
+  }
+};
+
+constexpr float kPrefixTile = 1.25f;   // a prefix's tile, in tiles' worth of the rest
+
+template <int kThreads>
+struct RangeList {
+  int from, to;                // this thread's groups
+  unsigned units, tiles;       // of all groups
+  unsigned before_units, before_tiles, own_units, own_tiles;
+  unsigned start;              // places in front of a unit's tiles
+  int ctas;                    // that take prefixes
+
+  // `rest`: this thread's share of the rest, in key tiles of a head.
+  __device__ __forceinline__ void plan(const PagedSharedArgs& a, int keys, float rest) {
+    constexpr int kW = kThreads / 32;
+    __shared__ unsigned s_units[kW], s_tiles[kW], s_members[kW];
+    __shared__ float s_rest[kW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.groups + kThreads - 1) / kThreads;
+    from = min(tid * per, a.groups);
+    to = min(from + per, a.groups);
+    own_units = own_tiles = 0;
+    unsigned members = 0;
+    for (int i = from; i < to; ++i) {
+      const Family f = family_of(a, i, keys);
+      members += f.members;
+      const unsigned u = f.tiles > 0 ? f.pieces * a.pool.kv_heads : 0;
+      own_units += u;
+      own_tiles += u * f.tiles;
+      if (!f.right && blockIdx.x == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+    }
+    unsigned u = own_units, t = own_tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned x = __shfl_up_sync(0xffffffffu, u, o), y = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) {
+        u += x;
+        t += y;
+      }
+      rest += __shfl_xor_sync(0xffffffffu, rest, o);
+    }
+    members = __reduce_add_sync(0xffffffffu, members);
+    if (lane == 31) {
+      s_units[warp] = u;
+      s_tiles[warp] = t;
+      s_members[warp] = members;
+      s_rest[warp] = rest;
+    }
+    __syncthreads();
+    before_units = u - own_units;
+    before_tiles = t - own_tiles;
+    units = tiles = members = 0;
+    rest = 0.f;
+#pragma unroll 1
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) {
+        before_units += s_units[w];
+        before_tiles += s_tiles[w];
+      }
+      units += s_units[w];
+      tiles += s_tiles[w];
+      members += s_members[w];
+      rest += s_rest[w];
+    }
+    // Starts that decrease: groups overlap, and their units may be more than there is room for.
+    const bool none = members > (unsigned)a.pool.batch;
+    if (none) units = 0;
+    // As many CTAs for the prefixes as they are of the work; whole numbers of CTAs for each unit, or of a few units for each CTA.
+    const float mine = kPrefixTile * (float)tiles + (float)(kSegmentStart * units);
+    const int n = gridDim.x;
+    ctas = 0;
+    if (units > 0) {
+      ctas = max(1, min(n - 1, __float2int_rn((float)n * mine / (mine + rest * (float)a.pool.kv_heads))));
+      ctas = min(ctas, (int)min(tiles, (unsigned)INT_MAX));
+      if (units <= (unsigned)ctas) ctas -= ctas % (int)units;
+    }
+    start = units > (unsigned)ctas ? kSegmentStart : 0;
+    if (blockIdx.x == 0) {   // for the join
+      unsigned at = before_tiles + start * before_units;
+      for (int i = from; i < to; ++i) {
+        const Family f = family_of(a, i, keys);
+        a.segments[i] = none ? 0 : f.tiles;
+        a.first_row[i] = at;
+        at += f.pieces * a.pool.kv_heads * (f.tiles > 0 ? f.tiles + start : 0);
+      }
+      if (tid == 0) {
+        a.ranges[0] = ctas;
+        a.ranges[1] = (int)(tiles + start * units);
+        a.ranges[2] = (int)start;
+      }
+    }
+  }
+  __device__ __forceinline__ unsigned places() const { return tiles + start * units; }
+
+  // The thread whose groups place x lies in writes what this CTA's range, up to `end`, has of the unit there: a segment,
+  // and in `next` where the unit ends.  members = 0: the range ends within the unit's start.
+  __device__ __forceinline__ void find(const PagedSharedArgs& a, int keys, unsigned x, unsigned end, Segment* s,
+                                       unsigned* next) const {
+    unsigned at = before_tiles + start * before_units;
+    if (x < at || x >= at + own_tiles + start * own_units) return;
+#pragma unroll 1
+    for (int i = from; i < to; ++i) {
+      const Family f = family_of(a, i, keys);
+      if (f.tiles == 0) continue;
+      const unsigned size = f.tiles + start, all = f.pieces * a.pool.kv_heads * size;
+      if (x < at + all) {
+        const unsigned unit = (x - at) / size, piece = unit / a.pool.kv_heads;
+        const int each = a.rows / a.group;
+        const unsigned t0 = at + unit * size + start, t1 = t0 + f.tiles;   // the unit's tiles
+        s->g = unit - piece * a.pool.kv_heads;
+        s->b0 = f.start + piece * each;
+        s->leader = f.start;
+        s->prefix = f.prefix;
+        s->first = max(x, t0) - t0;
+        s->last = min(end, t1) - t0;
+        s->members = end > t0 ? min(each, f.members - (int)piece * each) : 0;
+        s->row = (int64_t)blockIdx.x * a.slot_rows + (int64_t)s->b0 * a.q_heads + (int64_t)s->g * s->members * a.group;
+        *next = t1;
+        return;
+      }
+      at += all;
+    }
+  }
+};
+
+// What a segment's rows see, for each warp by itself.
+__device__ __forceinline__ void see_segment(const PagedSharedArgs& a, int keys, Segment& s, int lane) {
+  int lo = INT_MAX, hi = -1;
+  for (int i = lane; i < s.members; i += 32) {
+    const int p = last_seen(a, s.prefix, s.b0 + i);
+    lo = min(lo, p);
+    hi = max(hi, p);
+  }
+  s.p_lo = __reduce_min_sync(0xffffffffu, lo);
+  s.p_hi = __reduce_max_sync(0xffffffffu, hi);
+  s.last = max(s.first, min(s.last, s.p_hi < 0 ? 0 : s.p_hi / keys + 1));
 }
 
 // Byte offset in the pools of the prefix's position `pos`, -1: nothing to read.

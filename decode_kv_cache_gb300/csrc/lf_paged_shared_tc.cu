@@ -35,7 +35,7 @@ __device__ __forceinline__ void mbar_inval(uint64_t* bar) {
 template <int D, int G>
 __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __grid_constant__ SharedTcArgs ta) {
   using P = TcPlan<D>;
-  using C = MmaTile<D, G>;
+  using C = MmaWalk<D, G, G == 8 ? 10 : 12, 2>;
   constexpr int S = P::kStages;
   const PagedSharedArgs& a = ta.a;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -48,37 +48,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- who does what ------------------------------------------------------------------
-  SegmentList<kThreadsTc> list;
-  int64_t units, tiles, rest = 0;
-  int longest;
-  for (int b = tid; b < a.pool.batch; b += kThreadsTc) rest += seen_of<C::kTokens>(ta.rest, b).tiles;
-  list.sum(a, kTile, &units, &tiles, &longest, &rest);
-  const int ctas = gridDim.x;
-  int prefix_ctas = 0;
-  if (units > 0) {
-    const float mine = (float)(tiles + kSegmentStart * units);
-    const float others = (float)rest * ((float)a.pool.kv_heads * C::kTokens / kTile);
-    prefix_ctas = max(1, min(ctas - 1, __float2int_rn(ctas * mine / (mine + others))));
-  }
-  list.cut(a, kTile, units > 0 ? segment_tiles(prefix_ctas, INT_MAX, units, tiles, longest) : 1);
-  if (list.segments < prefix_ctas) prefix_ctas = (int)list.segments;
-  if ((int)blockIdx.x >= prefix_ctas) {
-    if (warp < C::kWarps)
-      decode_walk<C, D, G>(ta.rest, smem, blockIdx.x - prefix_ctas, ctas - prefix_ctas,
-                           [] { named_bar_sync(1, C::kWarps * 32); });
-    return;
-  }
-  if (tid == 0) ta.rest.part_unit[ctas - 1 - blockIdx.x] = -1;   // the ranges that are not taken
-  bool again = false;
-  for (int64_t id = blockIdx.x; id < list.segments; id += prefix_ctas) {
-  Segment seg;
-  if (!list.find(a, kTile, id, &seg)) continue;
-  const int rows = seg.members << gs, nt = seg.last - seg.first;
-  const int nq = rows > kTile ? 2 : 1;   // query tiles
-  // Does some row not see some key of the tile at k0?
-  auto masked = [&](int k0) { return k0 + kTile - 1 > seg.p_lo; };
-
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);   // [S] a tile is ready for the MMAs
   uint64_t* raw = full + S;                             // [S] V landed, to be scrubbed
   uint64_t* qfull = raw + S;
@@ -88,11 +57,67 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   uint64_t* ofull = pfull + 4;                          // [2] O_t final
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
   volatile int* misc = reinterpret_cast<volatile int*>(smem + 528);   // [0] a wait expired, [1] by hand
+  Segment* s_seg = reinterpret_cast<Segment*>(smem + 768);
+  unsigned* s_next = reinterpret_cast<unsigned*>(smem + 960);
+  static_assert(2 * S + 1 + 8 + 4 + 2 <= 64 && sizeof(Segment) <= 192, "in front of kOffQ");
   unsigned char* qs = smem + P::kOffQ;
   unsigned char* ring = smem + P::kOffRing;
 
-  // The loader sets up the barriers and starts on the queries and the first key tile
-  // at once; the others meet it behind.
+  // ---- who does what ------------------------------------------------------------------
+  RangeList<kThreadsTc> list;
+  const int ctas = gridDim.x;
+  float rest = 0.f;
+  for (int b = tid; b < a.pool.batch; b += kThreadsTc) rest += (float)seen_of<C::kTokens>(ta.rest, b).tiles;
+  list.plan(a, kTile, rest * ((float)C::kTokens / kTile));
+  if ((int)blockIdx.x >= list.ctas) {
+    if (warp < C::kWarps)
+      decode_walk<C, D, G>(ta.rest, smem, blockIdx.x - list.ctas, ctas - list.ctas,
+                           [] { named_bar_sync(1, C::kWarps * 32); });
+    return;
+  }
+  if (tid == 0) ta.rest.part_unit[ctas - 1 - blockIdx.x] = -1;   // the ranges that are not taken
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  const Ranges ranges(list.places(), list.ctas);
+  const unsigned x_end = ranges.first(blockIdx.x + 1);
+  bool again = false;
+#pragma unroll 1
+  for (unsigned x = ranges.first(blockIdx.x); x < x_end;) {
+  if (warp == kLoadWarp && lane == 0) {
+    if (again)   // every wait on them is over, and every copy and product that arrives at them
+      for (int i = 0; i < 2 * S + 15; ++i) mbar_inval(full + i);
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&raw[i], 1);
+    }
+    mbar_init(qfull, 1);
+    for (int t = 0; t < 2; ++t) {
+      for (int i = 0; i < 4; ++i) mbar_init(&sfull[4 * t + i], 1);
+      mbar_init(&pfull[2 * t], 4);
+      mbar_init(&pfull[2 * t + 1], 4);
+      mbar_init(&ofull[t], 1);
+    }
+    fence_mbar_init();
+    misc[0] = misc[1] = 0;
+  }
+  again = true;
+  list.find(a, kTile, x, x_end, s_seg, s_next);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  Segment seg = *s_seg;
+  x = *s_next;
+  if (seg.members == 0) break;   // (it was the range's last)
+  see_segment(a, kTile, seg, lane);
+  const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const int rows = seg.members << gs, nt = seg.last - seg.first;
+  const int nq = rows > kTile ? 2 : 1;   // query tiles
+  // Does some row not see some key of the tile at k0?
+  auto masked = [&](int k0) { return k0 + kTile - 1 > seg.p_lo; };
+
+  // The loader starts on the queries and the first key tile.
   const int boxes = kTile / ta.box_rows, box = lane % boxes, blk = lane / boxes;
   auto page_of = [&](int j, int* slot) {   // of this lane's box of key tile j; num_pages: zeros
     const int p = (seg.first + j) * kTile + box * ta.box_rows;
@@ -116,25 +141,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   };
   int page = 0, slot = 0;
   if (warp == kLoadWarp) {
-    if (lane == 0) {
-      static_assert(2 * S + 1 + 8 + 4 + 2 <= 64, "barriers in front of tmem_slot");
-      if (again)   // every wait on them is over, and every copy and product that arrives at them
-        for (int i = 0; i < 2 * S + 15; ++i) mbar_inval(full + i);
-      for (int i = 0; i < S; ++i) {
-        mbar_init(&full[i], 1);
-        mbar_init(&raw[i], 1);
-      }
-      mbar_init(qfull, 1);
-      for (int t = 0; t < 2; ++t) {
-        for (int i = 0; i < 4; ++i) mbar_init(&sfull[4 * t + i], 1);
-        mbar_init(&pfull[2 * t], 4);
-        mbar_init(&pfull[2 * t + 1], 4);
-        mbar_init(&ofull[t], 1);
-      }
-      fence_mbar_init();
-      misc[0] = misc[1] = 0;
-    }
-    __syncwarp();
     if (nt > 0) {
       if (lane == 0) {
         mbar_arrive_expect_tx(qfull, nq * P::kTileBytes);
@@ -147,15 +153,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
       load(1, masked(seg.first * kTile), page, slot);
     }
   }
-  if (warp == kMmaWarp && !again) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
-  }
-  again = true;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_longer(bar, parity, misc);
   };
@@ -413,16 +410,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
       shared_row_by_hand<__nv_bfloat16, D>(a, seg, kTile, r, last_seen(a, seg.prefix, seg.b0 + (r >> gs)), lane);
   __syncthreads();   // misc has been read
   }
-  if (!again) return;
   if (warp == kMmaWarp) {
-    tmem_dealloc(*reinterpret_cast<uint32_t*>(smem + 512), 512);
-    if (lane == 0 && *reinterpret_cast<volatile int*>(smem + 528) && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
+    tmem_dealloc(*tmem_slot, 512);
+    if (lane == 0 && misc[0] && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
   }
 }
 
 template <int D, int G>
 cudaError_t launch(const SharedTcArgs& ta, int64_t grid, cudaStream_t stream) {
-  using C = MmaTile<D, G>;
+  using C = MmaWalk<D, G, G == 8 ? 10 : 12, 2>;
   constexpr int kWalk = C::kWarps * warp_bytes<C, D, G>() + 1024;
   constexpr int kSmem = TcPlan<D>::kSmem > kWalk ? TcPlan<D>::kSmem : kWalk;
   static_assert(kSmem + 1024 <= 232448, "with the lists' own");
