@@ -102,9 +102,58 @@ cudaError_t launch_fma(const PagedSharedArgs& a, int64_t grid, cudaStream_t stre
 // ---- the join --------------------------------------------------------------------------
 //
 // A block per sequence and KV head.  The rest's share is in its place, or in the parts of the CTAs whose ranges
-// met it (lf_paged_decode.cu); the prefix's shares are `segments` blocks' rows.  Warps take a row of the group each, or
-// a part of its shares, and join through shared memory.  Bound by latency and by the shares' way through L2.
-constexpr int kJoinWarps = 8;
+// met it (lf_paged_decode.cu); the prefix's shares are rows that its blocks left.  Warps take a row of the group each, or
+// every so many of its shares, and join through shared memory, in order of position.  Bound by latency: what the call was given is
+// read while the kernel before drains, then come two reads that depend on each other, places and shares.
+constexpr int kJoinWarps = 8, kJoinBatch = 4;
+
+// Shares i = 0 .. n - 1 of a row (maximum and sum at ml(i), output at o(i)[D]) joined in their order, kJoinBatch of
+// them read at once: lane j holds columns E j .. E j + E - 1.
+template <int D, class Ml, class O>
+__device__ __forceinline__ void join_shares(int n, Ml ml, O o, int lane, float* m_out, float* l_out, float* acc) {
+  constexpr int E = D >= 32 ? D / 32 : 1;
+  const int col = (lane * E) % D;
+  float m = kNegInf, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kJoinBatch) {
+    float s[kJoinBatch], t[kJoinBatch], v[kJoinBatch][E];
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) {
+      s[u] = kNegInf;
+      if (i0 + u < n) {
+        const float* p = ml(i0 + u);
+        s[u] = p[0];
+        t[u] = p[1];
+        const float* x = o(i0 + u) + col;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[u][e] = x[e];
+      } else {
+        t[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) top = fmaxf(top, s[u]);
+    const float mu = top == kNegInf ? 0.f : top, f = ex2(m - mu);
+    m = top;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) {
+      const float w = ex2(s[u] - mu);
+      l = fmaf(t[u], w, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(v[u][e], w, acc[e]);
+    }
+  }
+  *m_out = m;
+  *l_out = l;
+}
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs a,
@@ -114,7 +163,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_shared_join_kernel(cons
   constexpr int kStripes = kJoinWarps / G;
   __shared__ float s_o[kJoinWarps][D];
   __shared__ float s_ml[kJoinWarps][2];
-  __shared__ int s_first, s_count;
+  __shared__ int s_first[kJoinWarps], s_count[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / a.pool.kv_heads, g = blockIdx.x - b * a.pool.kv_heads;
   // The sequence's group: the last one that starts at or before it.
@@ -126,60 +175,69 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_shared_join_kernel(cons
     n = min(step, n - k * step);
   } while (n > 1);
   const int start = a.group_start[lo], end = a.group_start[lo + 1];
-  const bool right = start >= 0 && b >= start && b < end && end <= a.pool.batch &&
-                     a.prefix_lens[b] <= max(a.prefix_lens[start], 0);
-  if (tid == 0) {
-    s_first = INT_MAX;
-    s_count = 0;
-  }
+  bool right = start >= 0 && b >= start && b < end && end <= a.pool.batch;
+  if (right) right = a.prefix_lens[b] <= max(a.prefix_lens[start], 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!right) {   // of no group, or a longer prefix than its group's: left as it is
     if (tid == 0 && g == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
     return;
   }
-  // The CTAs whose ranges start inside the rest of this unit.
+  // The CTAs whose ranges start inside the rest of this unit; what the prefix's blocks say of the group.
   const int unit = b * a.pool.kv_heads + g;
-  __syncthreads();
+  int segs = a.segments[lo];
+  const int64_t group_first = a.first_row[lo];
+  const unsigned range_ctas = a.ranges[0], places = a.ranges[1], in_front = a.ranges[2];
+  int w0 = INT_MAX, count = 0;
   for (int i = tid; i < ctas; i += kJoinWarps * 32)
     if (d.part_unit[i] == unit) {
-      atomicMin(&s_first, i);
-      atomicAdd(&s_count, 1);
+      w0 = min(w0, i);
+      ++count;
     }
-  __syncthreads();
-  const int w = s_first, rest = s_count > 0 ? s_count + 1 : 1;
+  w0 = __reduce_min_sync(0xffffffffu, w0);
+  count = __reduce_add_sync(0xffffffffu, count);
+  if (lane == 0) {
+    s_first[warp] = w0;
+    s_count[warp] = count;
+  }
   // The prefix's shares: `segs` rows of part_o from `row`, `apart` rows apart.
   const int each = a.rows / G, piece = (b - start) / each, members = min(each, end - start - piece * each);
-  int segs = a.segments[lo];
   int64_t row = 0, apart = (int64_t)members * G;
   bool room = true;
-  if (segs > 0 && a.ranges[0] > 0) {
-    const Ranges ranges(a.ranges[1], a.ranges[0]);
-    const unsigned size = segs + a.ranges[2];
-    const unsigned first = (unsigned)a.first_row[lo] + (unsigned)(piece * a.pool.kv_heads + g) * size + a.ranges[2];
+  if (segs > 0 && range_ctas > 0) {
+    const Ranges ranges(places, range_ctas);
+    const unsigned first = (unsigned)group_first + (unsigned)(piece * a.pool.kv_heads + g) * (segs + in_front) + in_front;
     const unsigned cta = ranges.owner(first);
     segs = ranges.owner(first + segs - 1) - cta + 1;
     apart = a.slot_rows;
     row = cta * apart + (int64_t)(start + piece * each) * a.q_heads + (int64_t)g * members * G + (b - start - piece * each) * G;
   } else if (segs > 0) {
-    row = a.first_row[lo] + (int64_t)piece * each * a.q_heads * segs + g * segs * apart + (b - start - piece * each) * G;
+    row = group_first + (int64_t)piece * each * a.q_heads * segs + g * segs * apart + (b - start - piece * each) * G;
   }
   if (segs != 0) room = segs > 0 && row >= 0 && row + (segs - 1) * apart + G <= a.part_rows;
+  __syncthreads();
+  w0 = INT_MAX;
+  count = 0;
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) {
+    w0 = min(w0, s_first[i]);
+    count += s_count[i];
+  }
+  const int w = w0, rest = count > 0 ? count + 1 : 1;
   const int parts = rest + (room ? segs : 0);
   const int h = warp % G, stripe = warp / G;
   const int64_t out_row = (int64_t)b * a.q_heads + g * G + h;
+  auto slot = [&](int i) { return (i == 0 ? 2 * (int64_t)(w - 1) + 1 : 2 * (int64_t)(w - 1 + i)) * G + h; };
   auto ml = [&](int i) -> const float* {
     if (i >= rest) return a.part_ml + 2 * (row + (i - rest) * apart + h);
-    if (rest == 1) return d.rest_ml + 2 * out_row;
-    return d.part_ml + ((i == 0 ? 2 * (int64_t)(w - 1) + 1 : 2 * (int64_t)(w - 1 + i)) * G + h) * 2;
+    return rest == 1 ? d.rest_ml + 2 * out_row : d.part_ml + 2 * slot(i);
   };
   auto o = [&](int i) -> const float* {
     if (i >= rest) return a.part_o + (row + (i - rest) * apart + h) * D;
-    if (rest == 1) return d.rest_o + out_row * D;
-    return d.part_o + ((i == 0 ? 2 * (int64_t)(w - 1) + 1 : 2 * (int64_t)(w - 1 + i)) * G + h) * D;
+    return rest == 1 ? d.rest_o + out_row * D : d.part_o + slot(i) * D;
   };
   const int mine = parts > stripe ? (parts - stripe + kStripes - 1) / kStripes : 0;
   float m, l, acc[E];
-  join_parts<D>(
+  join_shares<D>(
       mine, [&](int i) { return ml(stripe + i * kStripes); }, [&](int i) { return o(stripe + i * kStripes); }, lane, &m, &l,
       acc);
   if constexpr (kStripes > 1) {
@@ -193,7 +251,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_shared_join_kernel(cons
     }
     __syncthreads();
     if (stripe > 0) return;
-    join_parts<D>(
+    join_shares<D>(
         min(parts, kStripes), [&](int i) { return s_ml[h + i * G]; }, [&](int i) { return s_o[h + i * G]; }, lane, &m, &l,
         acc);
   }

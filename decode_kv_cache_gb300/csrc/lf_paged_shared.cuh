@@ -248,18 +248,20 @@ __device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys,
 // list, the others the rest of the sequences.  Numbers are below 2^31 (the entry point sees to it).  Every place belongs to one
 // thread's groups.
 
-// CTA i's range: q places, one more for the first r CTAs.
+// CTA i's range starts at place floor(places * i / ctas).  (Products that 32 bits do not hold are rare, and their divisions slow.)
 struct Ranges {
-  unsigned q, r;
-  __device__ __forceinline__ Ranges(unsigned places, unsigned ctas) : q(places / ctas), r(places - places / ctas * ctas) {}
-  __device__ __forceinline__ unsigned first(unsigned i) const { return q * i + min(i, r); }
-  __device__ __forceinline__ unsigned owner(unsigned x) const {
-    const unsigned wide = r * (q + 1);
-    return x < wide ? x / (q + 1) : r + (x - wide) / q;
+  unsigned places, ctas;
+  bool small;
+  __device__ __forceinline__ Ranges(unsigned p, unsigned c) : places(p), ctas(c), small(p < 0xffffffffu / (c + 1)) {}
+  __device__ __forceinline__ unsigned first(unsigned i) const {
+    return small ? places * i / ctas : (unsigned)((uint64_t)places * i / ctas);
+  }
+  __device__ __forceinline__ unsigned owner(unsigned x) const {   // the last i with first(i) <= x
+    return small ? ((x + 1) * ctas - 1) / places : (unsigned)((((uint64_t)x + 1) * ctas - 1) / places);
   }
 };
 
-constexpr float kPrefixTile = 1.25f;   // a prefix's tile, in tiles' worth of the rest
+constexpr float kPrefixTile = 1.5f;   // a prefix's tile, in tiles' worth of the rest
 
 template <int kThreads>
 struct RangeList {
@@ -330,10 +332,12 @@ struct RangeList {
     ctas = 0;
     if (units > 0) {
       ctas = max(1, min(n - 1, __float2int_rn((float)n * mine / (mine + rest * (float)a.pool.kv_heads))));
-      ctas = min(ctas, (int)min(tiles, (unsigned)INT_MAX));
-      if (units <= (unsigned)ctas) ctas -= ctas % (int)units;
+      // Where a whole number of CTAs for each unit is about as many, no CTA has the end of one and the start of the next.
+      const int u = min(units, (unsigned)n), near = (ctas + u / 2) / u * u;
+      if (near > 0 && near < n && 8 * abs(near - ctas) <= ctas) ctas = near;
+      ctas = min(ctas, (int)min(tiles, (unsigned)n));
     }
-    start = units > (unsigned)ctas ? kSegmentStart : 0;
+    start = ctas > 0 && (unsigned)ctas % max(units, 1u) != 0 ? kSegmentStart : 0;
     if (blockIdx.x == 0) {   // for the join
       unsigned at = before_tiles + start * before_units;
       for (int i = from; i < to; ++i) {

@@ -32,6 +32,16 @@ __device__ __forceinline__ void mbar_inval(uint64_t* bar) {
   asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// `bytes` bytes of shared memory to global memory, as a group of copies of this thread's; 16-byte aligned.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+// This thread's copies have been read, or are done.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 template <int D, int G>
 __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __grid_constant__ SharedTcArgs ta) {
   using P = TcPlan<D>;
@@ -373,32 +383,29 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
     }
 
     // ---- shares out --------------------------------------------------------------------
-    ok = ok && (nt == 0 || __all_sync(0xffffffffu, wait(&ofull[t], 0)));
+    // A thread puts its row into the ring, which is done with once the last products are, and copies it out from
+    // there: rows lie 16 bytes more than their length apart, so that eight lanes' chunks fall into eight bank groups.
+    for (int i = 0; i < nq; ++i) ok = ok && (nt == 0 || __all_sync(0xffffffffu, wait(&ofull[i], 0)));
     tc_fence_after();
     if (ok && !misc[1]) {   // (otherwise nothing is right, or the rows are computed again below)
-      unsigned char* stage = smem + P::kOffOut + (warp - kSoftWarp) * 4096;   // 32 rows x 32 columns
-      float* out = a.part_o + (seg.row + rr0) * D + (lane & 7) * 4;
-      const int left = rows - rr0;
-#pragma unroll 1
-      for (int h = 0; h < D / 32; ++h) {   // through shared memory: whole lines of global memory
+      static_assert(2 * kTile * (D * 4 + 16) <= P::kSmem - 1024 - P::kOffRing, "rows fit the ring and what is behind it");
+      unsigned char* mine = ring + (rr0 + lane) * (D * 4 + 16);
+#pragma unroll
+      for (int h = 0; h < D / 32; ++h) {
         float o[32];
         tmem_ld32(to + 32 * h, o);
         tmem_wait_ld();
-        __syncwarp();   // the columns before have been read
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+          *reinterpret_cast<float4*>(mine + 128 * h + 16 * e) =
               nt > 0 ? make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 4 * i + (lane >> 3);
-          if (rr < left)
-            *reinterpret_cast<float4*>(out + (int64_t)rr * D + 32 * h) =
-                *reinterpret_cast<const float4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-        }
       }
-      if (live) *reinterpret_cast<float2*>(a.part_ml + 2 * (seg.row + rr0 + lane)) = make_float2(m, l);
+      fence_proxy_async_smem();
+      if (live) {
+        bulk_s2g(a.part_o + (seg.row + rr0 + lane) * D, mine, D * 4);
+        *reinterpret_cast<float2*>(a.part_ml + 2 * (seg.row + rr0 + lane)) = make_float2(m, l);
+      }
+      bulk_wait_read();   // before the ring is filled again
     }
   }
   tc_fence_before();
@@ -410,6 +417,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
       shared_row_by_hand<__nv_bfloat16, D>(a, seg, kTile, r, last_seen(a, seg.prefix, seg.b0 + (r >> gs)), lane);
   __syncthreads();   // misc has been read
   }
+  if (warp >= kSoftWarp) bulk_wait();
   if (warp == kMmaWarp) {
     tmem_dealloc(*tmem_slot, 512);
     if (lane == 0 && misc[0] && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_TIMEOUT);
