@@ -308,21 +308,15 @@ struct RangeList {
       s_rest[warp] = rest;
     }
     __syncthreads();
-    before_units = u - own_units;
-    before_tiles = t - own_tiles;
-    units = tiles = members = 0;
-    rest = 0.f;
-#pragma unroll 1
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) {
-        before_units += s_units[w];
-        before_tiles += s_tiles[w];
-      }
-      units += s_units[w];
-      tiles += s_tiles[w];
-      members += s_members[w];
-      rest += s_rest[w];
-    }
+    // Lane w of every warp has warp w's sums.
+    const bool in = lane < kW;
+    const unsigned wu = in ? s_units[lane] : 0, wt = in ? s_tiles[lane] : 0;
+    units = __reduce_add_sync(0xffffffffu, wu);
+    tiles = __reduce_add_sync(0xffffffffu, wt);
+    before_units = u - own_units + __reduce_add_sync(0xffffffffu, lane < warp ? wu : 0);
+    before_tiles = t - own_tiles + __reduce_add_sync(0xffffffffu, lane < warp ? wt : 0);
+    members = __reduce_add_sync(0xffffffffu, in ? s_members[lane] : 0);
+    rest = warp_sum(in ? s_rest[lane] : 0.f);
     // Starts that decrease: groups overlap, and their units may be more than there is room for.
     const bool none = members > (unsigned)a.pool.batch;
     if (none) units = 0;
