@@ -245,8 +245,7 @@ __device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys,
 //
 // The units of all groups (group by group, piece by piece, head by head) lie one behind another, each `start` places, for what
 // a CTA spends on a unit besides its tiles, and then a place for each of its tiles.  The first `ctas` CTAs take equal ranges of the
-// list, the others the rest of the sequences.  Numbers are below 2^31 (the entry point sees to it).  Every place belongs to one
-// thread's groups.
+// list, the others the rest of the sequences.  Numbers are below 2^31 (the entry point sees to it).
 
 // CTA i's range starts at place floor(places * i / ctas).  (Products that 32 bits do not hold are rare, and their divisions slow.)
 struct Ranges {
@@ -265,23 +264,18 @@ constexpr float kPrefixTile = 1.5f;   // a prefix's tile, in tiles' worth of the
 
 template <int kThreads>
 struct RangeList {
-  int from, to;                // this thread's groups
-  unsigned units, tiles;       // of all groups
-  unsigned before_units, before_tiles, own_units, own_tiles;
-  unsigned start;              // places in front of a unit's tiles
+  unsigned places, start;      // in all, in front of a unit's tiles
   int ctas;                    // that take prefixes
 
-  // `rest`: this thread's share of the rest, in key tiles of a head.
+  // For the whole block together.  `rest`: this thread's share of the rest, in key tiles of a head.
   __device__ __forceinline__ void plan(const PagedSharedArgs& a, int keys, float rest) {
     constexpr int kW = kThreads / 32;
     __shared__ unsigned s_units[kW], s_tiles[kW], s_members[kW];
     __shared__ float s_rest[kW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.groups + kThreads - 1) / kThreads;
-    from = min(tid * per, a.groups);
-    to = min(from + per, a.groups);
-    own_units = own_tiles = 0;
-    unsigned members = 0;
+    const int from = min(tid * per, a.groups), to = min(from + per, a.groups);   // this thread's groups
+    unsigned own_units = 0, own_tiles = 0, members = 0;
     for (int i = from; i < to; ++i) {
       const Family f = family_of(a, i, keys);
       members += f.members;
@@ -311,10 +305,10 @@ struct RangeList {
     // Lane w of every warp has warp w's sums.
     const bool in = lane < kW;
     const unsigned wu = in ? s_units[lane] : 0, wt = in ? s_tiles[lane] : 0;
-    units = __reduce_add_sync(0xffffffffu, wu);
-    tiles = __reduce_add_sync(0xffffffffu, wt);
-    before_units = u - own_units + __reduce_add_sync(0xffffffffu, lane < warp ? wu : 0);
-    before_tiles = t - own_tiles + __reduce_add_sync(0xffffffffu, lane < warp ? wt : 0);
+    unsigned units = __reduce_add_sync(0xffffffffu, wu);
+    const unsigned tiles = __reduce_add_sync(0xffffffffu, wt);
+    const unsigned before_units = u - own_units + __reduce_add_sync(0xffffffffu, lane < warp ? wu : 0);
+    const unsigned before_tiles = t - own_tiles + __reduce_add_sync(0xffffffffu, lane < warp ? wt : 0);
     members = __reduce_add_sync(0xffffffffu, in ? s_members[lane] : 0);
     rest = warp_sum(in ? s_rest[lane] : 0.f);
     // Starts that decrease: groups overlap, and their units may be more than there is room for.
@@ -332,6 +326,7 @@ struct RangeList {
       ctas = min(ctas, (int)min(tiles, (unsigned)n));
     }
     start = ctas > 0 && (unsigned)ctas % max(units, 1u) != 0 ? kSegmentStart : 0;
+    places = tiles + start * units;
     if (blockIdx.x == 0) {   // for the join
       unsigned at = before_tiles + start * before_units;
       for (int i = from; i < to; ++i) {
@@ -342,45 +337,55 @@ struct RangeList {
       }
       if (tid == 0) {
         a.ranges[0] = ctas;
-        a.ranges[1] = (int)(tiles + start * units);
+        a.ranges[1] = (int)places;
         a.ranges[2] = (int)start;
       }
     }
   }
-  __device__ __forceinline__ unsigned places() const { return tiles + start * units; }
-
-  // The thread whose groups place x lies in writes what this CTA's range, up to `end`, has of the unit there: a segment,
-  // and in `next` where the unit ends.  members = 0: the range ends within the unit's start.
-  __device__ __forceinline__ void find(const PagedSharedArgs& a, int keys, unsigned x, unsigned end, Segment* s,
-                                       unsigned* next) const {
-    unsigned at = before_tiles + start * before_units;
-    if (x < at || x >= at + own_tiles + start * own_units) return;
-#pragma unroll 1
-    for (int i = from; i < to; ++i) {
-      const Family f = family_of(a, i, keys);
-      if (f.tiles == 0) continue;
-      const unsigned size = f.tiles + start, all = f.pieces * a.pool.kv_heads * size;
-      if (x < at + all) {
-        const unsigned unit = (x - at) / size, piece = unit / a.pool.kv_heads;
-        const int each = a.rows / a.group;
-        const unsigned t0 = at + unit * size + start, t1 = t0 + f.tiles;   // the unit's tiles
-        s->g = unit - piece * a.pool.kv_heads;
-        s->b0 = f.start + piece * each;
-        s->leader = f.start;
-        s->prefix = f.prefix;
-        s->first = max(x, t0) - t0;
-        s->last = min(end, t1) - t0;
-        s->members = end > t0 ? min(each, f.members - (int)piece * each) : 0;
-        s->row = (int64_t)blockIdx.x * a.slot_rows + (int64_t)s->b0 * a.q_heads + (int64_t)s->g * s->members * a.group;
-        *next = t1;
-        return;
-      }
-      at += all;
-    }
-  }
 };
 
-// What a segment's rows see, for each warp by itself.
+// What the range that starts at place x and ends at `end` has of the unit at x: a segment, and in `next` where the unit ends.
+// members = 0: the range ends within the unit's start.  For one warp together; it goes through the groups again, 32 at
+// a time, so that no thread holds what it knew of them.
+__device__ __forceinline__ void find_segment(const PagedSharedArgs& a, int keys, unsigned start, unsigned x, unsigned end, int lane,
+                                             Segment* s, unsigned* next) {
+  unsigned before = 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < a.groups; i0 += 32) {
+    Family f;
+    f.tiles = f.pieces = 0;
+    if (i0 + lane < a.groups) f = family_of(a, i0 + lane, keys);
+    const unsigned size = f.tiles + start, all = f.tiles > 0 ? f.pieces * a.pool.kv_heads * size : 0;
+    unsigned at = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
+    }
+    at += before;   // behind this lane's group
+    const bool mine = x < at && x >= at - all;
+    if (mine) {
+      at -= all;
+      const unsigned unit = (x - at) / size, piece = unit / a.pool.kv_heads;
+      const int each = a.rows / a.group;
+      const unsigned t0 = at + unit * size + start, t1 = t0 + f.tiles;   // the unit's tiles
+      s->g = unit - piece * a.pool.kv_heads;
+      s->b0 = f.start + piece * each;
+      s->leader = f.start;
+      s->prefix = f.prefix;
+      s->first = max(x, t0) - t0;
+      s->last = min(end, t1) - t0;
+      s->members = end > t0 ? min(each, f.members - (int)piece * each) : 0;
+      s->row = (int64_t)blockIdx.x * a.slot_rows + (int64_t)s->b0 * a.q_heads + (int64_t)s->g * s->members * a.group;
+      *next = t1;
+    }
+    if (__any_sync(0xffffffffu, mine)) break;
+    before = __shfl_sync(0xffffffffu, at, 31);
+  }
+  __syncwarp();
+}
+
+// What a segment's rows see, by one warp.
 __device__ __forceinline__ void see_segment(const PagedSharedArgs& a, int keys, Segment& s, int lane) {
   int lo = INT_MAX, hi = -1;
   for (int i = lane; i < s.members; i += 32) {

@@ -11,6 +11,8 @@
 // A prefix CTA's roles are the prompt kernel's: a loader that gathers K and V by page with TMA, a warp that issues S = Q K^T and
 // O += P V for the query tiles in turn, two groups of softmax warps with a thread per row, and a scrubber for the tiles
 // that some row does not see all of (prefixes of other lengths, or the last tile).
+#include <type_traits>
+
 #include "lf_paged_decode.cuh"
 #include "lf_paged_shared.cuh"
 #include "lf_paged_tc.cuh"
@@ -26,6 +28,16 @@ struct SharedTcArgs {
   PagedDecodeArgs rest;
   int box_rows;      // tokens of one TMA box: min(page_size, 128)
   int group_shift;
+};
+
+// Shared memory of a prefix CTA: the prompt kernel's, with the room of its output rows for a fifth stage of heads of 128.
+template <int D>
+struct SharedPlanTc {
+  static constexpr int kTileBytes = TcPlan<D>::kTileBytes;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffQ = 1024;
+  static constexpr int kOffRing = kOffQ + 2 * kTileBytes;
+  static constexpr int kSmem = kOffRing + kStages * kTileBytes + 1024;   // + alignment slack
 };
 
 __device__ __forceinline__ void mbar_inval(uint64_t* bar) {
@@ -44,7 +56,7 @@ __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_g
 
 template <int D, int G>
 __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __grid_constant__ SharedTcArgs ta) {
-  using P = TcPlan<D>;
+  using P = SharedPlanTc<D>;
   using C = MmaWalk<D, G, G == 8 ? 10 : 12, 2>;
   constexpr int S = P::kStages;
   const PagedSharedArgs& a = ta.a;
@@ -90,11 +102,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  const Ranges ranges(list.places(), list.ctas);
-  const unsigned x_end = ranges.first(blockIdx.x + 1);
+  const unsigned start = list.start;
+  unsigned x, x_end;
+  {
+    const Ranges ranges(list.places, list.ctas);
+    x = ranges.first(blockIdx.x);
+    x_end = ranges.first(blockIdx.x + 1);
+  }
   bool again = false;
 #pragma unroll 1
-  for (unsigned x = ranges.first(blockIdx.x); x < x_end;) {
+  while (x < x_end) {
   if (warp == kLoadWarp && lane == 0) {
     if (again)   // every wait on them is over, and every copy and product that arrives at them
       for (int i = 0; i < 2 * S + 15; ++i) mbar_inval(full + i);
@@ -113,14 +130,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
     misc[0] = misc[1] = 0;
   }
   again = true;
-  list.find(a, kTile, x, x_end, s_seg, s_next);
+  if (warp == kLoadWarp) {
+    find_segment(a, kTile, start, x, x_end, lane, s_seg, s_next);
+    Segment s = *s_seg;
+    see_segment(a, kTile, s, lane);
+    __syncwarp();
+    if (lane == 0) *s_seg = s;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  Segment seg = *s_seg;
-  x = *s_next;
+  // (Read where they are needed: the softmax threads have no registers to spare.)
+  volatile Segment& seg = *s_seg;
+  x = *reinterpret_cast<volatile unsigned*>(s_next);
   if (seg.members == 0) break;   // (it was the range's last)
-  see_segment(a, kTile, seg, lane);
   const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const int rows = seg.members << gs, nt = seg.last - seg.first;
   const int nq = rows > kTile ? 2 : 1;   // query tiles
@@ -256,44 +279,49 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
           mma_ts(lead, tm + 256 + t * D, tm + t * 128 + half * 32 + kk * 8,
                  vd + (uint32_t)((half * 4 + kk) * 128), kIdO, kk > 0 ? 1u : acc);
       };
-      bool ok = all(qfull, 0) && all(&full[0], 0);
-      if (ok) {
-        tc_fence_after();
-        mma_s(0, 0, 0);
-        if (nq == 2) mma_s(1, 0, 0);
-      }
-      int sv = 1 % S, sk = 2 % S;           // stages of V_j and K_(j+1)
-      uint32_t pv = 0, pk = 2 / S;          // and their parities
-      for (int j = 0; j < nt && ok; ++j) {
-        const bool last = j + 1 == nt;
-        const uint32_t pj = (uint32_t)(j & 1);
-        ok = all(&full[sv], pv);
+      // Straight code for one query tile and for two: a branch around an instruction costs more than it.
+      auto walk = [&](auto tiles) {
+        constexpr int N = decltype(tiles)::value;
+        bool ok = all(qfull, 0) && all(&full[0], 0);
+        if (ok) {
+          tc_fence_after();
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t == nq) break;
-          ok = ok && all(&pfull[2 * t], pj);
-          if (!ok) break;
-          tc_fence_after();
-          mma_o(t, sv, 0, j > 0 ? 1u : 0u);
-          if (t == 0 && !last) ok = all(&full[sk], pk);
-          ok = ok && all(&pfull[2 * t + 1], pj);
-          if (!ok) break;
-          tc_fence_after();
-          mma_o(t, sv, 1, 1u);
-          if (!last) mma_s(t, j + 1, sk);
-          else if (lead) tc_commit(&ofull[t]);
+          for (int t = 0; t < N; ++t) mma_s(t, 0, 0);
         }
-        sv += 2;
-        if (sv >= S) {
-          sv -= S;
-          pv ^= 1u;
+        int sv = 1 % S, sk = 2 % S;           // stages of V_j and K_(j+1)
+        uint32_t pv = 0, pk = 2 / S;          // and their parities
+        for (int j = 0; j < nt && ok; ++j) {
+          const bool last = j + 1 == nt;
+          const uint32_t pj = (uint32_t)(j & 1);
+          ok = all(&full[sv], pv);
+#pragma unroll
+          for (int t = 0; t < N; ++t) {
+            ok = ok && all(&pfull[2 * t], pj);
+            if (!ok) break;
+            tc_fence_after();
+            mma_o(t, sv, 0, j > 0 ? 1u : 0u);
+            if (t == 0 && !last) ok = all(&full[sk], pk);
+            ok = ok && all(&pfull[2 * t + 1], pj);
+            if (!ok) break;
+            tc_fence_after();
+            mma_o(t, sv, 1, 1u);
+            if (!last) mma_s(t, j + 1, sk);
+            else if (lead) tc_commit(&ofull[t]);
+          }
+          sv += 2;
+          if (sv >= S) {
+            sv -= S;
+            pv ^= 1u;
+          }
+          sk += 2;
+          if (sk >= S) {
+            sk -= S;
+            pk ^= 1u;
+          }
         }
-        sk += 2;
-        if (sk >= S) {
-          sk -= S;
-          pk ^= 1u;
-        }
-      }
+        return ok;
+      };
+      const bool ok = nq == 2 ? walk(std::integral_constant<int, 2>{}) : walk(std::integral_constant<int, 1>{});
       if (!ok && lead) {   // MMAs in flight end before the tensor memory is given back
         tc_commit(qfull);
         (void)mbar_wait_bounded(qfull, 1);
@@ -388,7 +416,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
     for (int i = 0; i < nq; ++i) ok = ok && (nt == 0 || __all_sync(0xffffffffu, wait(&ofull[i], 0)));
     tc_fence_after();
     if (ok && !misc[1]) {   // (otherwise nothing is right, or the rows are computed again below)
-      static_assert(2 * kTile * (D * 4 + 16) <= P::kSmem - 1024 - P::kOffRing, "rows fit the ring and what is behind it");
+      static_assert(2 * kTile * (D * 4 + 16) <= S * P::kTileBytes, "rows fit the ring");
       unsigned char* mine = ring + (rr0 + lane) * (D * 4 + 16);
 #pragma unroll
       for (int h = 0; h < D / 32; ++h) {
@@ -414,7 +442,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   if (misc[0]) break;   // a wait ran out
   if (misc[1])
     for (int r = warp; r < rows; r += kThreadsTc / 32)
-      shared_row_by_hand<__nv_bfloat16, D>(a, seg, kTile, r, last_seen(a, seg.prefix, seg.b0 + (r >> gs)), lane);
+      shared_row_by_hand<__nv_bfloat16, D>(a, *s_seg, kTile, r, last_seen(a, seg.prefix, seg.b0 + (r >> gs)), lane);
   __syncthreads();   // misc has been read
   }
   if (warp >= kSoftWarp) bulk_wait();
@@ -428,7 +456,7 @@ template <int D, int G>
 cudaError_t launch(const SharedTcArgs& ta, int64_t grid, cudaStream_t stream) {
   using C = MmaWalk<D, G, G == 8 ? 10 : 12, 2>;
   constexpr int kWalk = C::kWarps * warp_bytes<C, D, G>() + 1024;
-  constexpr int kSmem = TcPlan<D>::kSmem > kWalk ? TcPlan<D>::kSmem : kWalk;
+  constexpr int kSmem = SharedPlanTc<D>::kSmem > kWalk ? SharedPlanTc<D>::kSmem : kWalk;
   static_assert(kSmem + 1024 <= 232448, "with the lists' own");
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_shared_tc_kernel<D, G>), kSmem, done);
