@@ -260,7 +260,11 @@ struct Ranges {
   }
 };
 
-constexpr float kPrefixTile = 1.5f;   // a prefix's tile, in tiles' worth of the rest
+// What a prefix's tile costs, for one query tile and for two, and a unit's start, in tiles of the rest.  Beside
+// CTAs that take the rest, with memory as busy as it gets, a tile of theirs took 1.1 to 1.6 us, one of a prefix 1.5 to 1.9 and
+// 1.8 to 2.5, and a segment 8 to 10 us besides.
+constexpr float kOneTile = 1.35f, kTwoTiles = 1.8f;
+constexpr int kUnitStart = 6;
 
 template <int kThreads>
 struct RangeList {
@@ -271,17 +275,19 @@ struct RangeList {
   __device__ __forceinline__ void plan(const PagedSharedArgs& a, int keys, float rest) {
     constexpr int kW = kThreads / 32;
     __shared__ unsigned s_units[kW], s_tiles[kW], s_members[kW];
-    __shared__ float s_rest[kW];
+    __shared__ float s_rest[kW], s_mine[kW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.groups + kThreads - 1) / kThreads;
     const int from = min(tid * per, a.groups), to = min(from + per, a.groups);   // this thread's groups
     unsigned own_units = 0, own_tiles = 0, members = 0;
+    float mine = 0.f;
     for (int i = from; i < to; ++i) {
       const Family f = family_of(a, i, keys);
       members += f.members;
       const unsigned u = f.tiles > 0 ? f.pieces * a.pool.kv_heads : 0;
       own_units += u;
       own_tiles += u * f.tiles;
+      mine += (float)u * ((f.members * a.group > 128 ? kTwoTiles : kOneTile) * (float)f.tiles + (float)kUnitStart);
       if (!f.right && blockIdx.x == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
     }
     unsigned u = own_units, t = own_tiles;
@@ -295,11 +301,13 @@ struct RangeList {
       rest += __shfl_xor_sync(0xffffffffu, rest, o);
     }
     members = __reduce_add_sync(0xffffffffu, members);
+    mine = warp_sum(mine);
     if (lane == 31) {
       s_units[warp] = u;
       s_tiles[warp] = t;
       s_members[warp] = members;
       s_rest[warp] = rest;
+      s_mine[warp] = mine;
     }
     __syncthreads();
     // Lane w of every warp has warp w's sums.
@@ -311,11 +319,11 @@ struct RangeList {
     const unsigned before_tiles = t - own_tiles + __reduce_add_sync(0xffffffffu, lane < warp ? wt : 0);
     members = __reduce_add_sync(0xffffffffu, in ? s_members[lane] : 0);
     rest = warp_sum(in ? s_rest[lane] : 0.f);
+    mine = warp_sum(in ? s_mine[lane] : 0.f);
     // Starts that decrease: groups overlap, and their units may be more than there is room for.
     const bool none = members > (unsigned)a.pool.batch;
     if (none) units = 0;
     // As many CTAs for the prefixes as they are of the work; whole numbers of CTAs for each unit, or of a few units for each CTA.
-    const float mine = kPrefixTile * (float)tiles + (float)(kSegmentStart * units);
     const int n = gridDim.x;
     ctas = 0;
     if (units > 0) {
@@ -325,7 +333,7 @@ struct RangeList {
       if (near > 0 && near < n && 8 * abs(near - ctas) <= ctas) ctas = near;
       ctas = min(ctas, (int)min(tiles, (unsigned)n));
     }
-    start = ctas > 0 && (unsigned)ctas % max(units, 1u) != 0 ? kSegmentStart : 0;
+    start = ctas > 0 && (unsigned)ctas % max(units, 1u) != 0 ? kUnitStart : 0;
     places = tiles + start * units;
     if (blockIdx.x == 0) {   // for the join
       unsigned at = before_tiles + start * before_units;

@@ -89,7 +89,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   RangeList<kThreadsTc> list;
   const int ctas = gridDim.x;
   float rest = 0.f;
-  for (int b = tid; b < a.pool.batch; b += kThreadsTc) rest += (float)seen_of<C::kTokens>(ta.rest, b).tiles;
+  for (int b = tid; b < a.pool.batch; b += kThreadsTc) {   // a unit costs about a tile of the walk's besides its own
+    const int own = seen_of<C::kTokens>(ta.rest, b).tiles;
+    if (own > 0) rest += (float)(own + 1);
+  }
   list.plan(a, kTile, rest * ((float)C::kTokens / kTile));
   if ((int)blockIdx.x >= list.ctas) {
     if (warp < C::kWarps)
