@@ -327,10 +327,14 @@ struct RangeList {
     const int n = gridDim.x;
     ctas = 0;
     if (units > 0) {
-      ctas = max(1, min(n - 1, __float2int_rn((float)n * mine / (mine + rest * (float)a.pool.kv_heads))));
-      // Where a whole number of CTAs for each unit is about as many, no CTA has the end of one and the start of the next.
+      const float others = rest * (float)a.pool.kv_heads;
+      ctas = max(1, min(n - 1, __float2int_rn((float)n * mine / (mine + others))));
+      // With a whole number of CTAs for each unit none has the end of one and the start of the next.
       const int u = min(units, (unsigned)n), near = (ctas + u / 2) / u * u;
-      if (near > 0 && near < n && 8 * abs(near - ctas) <= ctas) ctas = near;
+      if (near > 0 && near < n &&
+          fmaxf(mine / (float)near, others / (float)(n - near)) <=
+              fmaxf(mine / (float)ctas + (float)kUnitStart, others / (float)(n - ctas)))
+        ctas = near;
       ctas = min(ctas, (int)min(tiles, (unsigned)n));
     }
     start = ctas > 0 && (unsigned)ctas % max(units, 1u) != 0 ? kUnitStart : 0;

@@ -150,8 +150,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const int rows = seg.members << gs, nt = seg.last - seg.first;
   const int nq = rows > kTile ? 2 : 1;   // query tiles
-  // Does some row not see some key of the tile at k0?
-  auto masked = [&](int k0) { return k0 + kTile - 1 > seg.p_lo; };
+  // From this key tile of the segment on some row does not see some key.
+  const int clear = ((seg.p_lo + 1) >> 7) - seg.first;
+  static_assert(kTile == 1 << 7, "");
 
   // The loader starts on the queries and the first key tile.
   const int boxes = kTile / ta.box_rows, box = lane % boxes, blk = lane / boxes;
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
             tma_load_3d(qs + t * P::kTileBytes + c * kBlk, &ta.q, c * 64, seg.g << gs, seg.b0 + t * (kTile >> gs), qfull);
       }
       page = page_of(0, &slot);
-      load(0, masked(seg.first * kTile), page, slot);
-      load(1, masked(seg.first * kTile), page, slot);
+      load(0, 0 >= clear, page, slot);
+      load(1, 0 >= clear, page, slot);
     }
   }
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
     for (int j = 1; j < nt && ok; ++j) {
       const int cur_page = page, cur_slot = slot;
       if (j + 1 < nt) page = page_of(j + 1, &slot);   // a tile ahead
-      const bool scrub = masked((seg.first + j) * kTile);
+      const bool scrub = j >= clear;
       for (int i = 2 * j; i < 2 * j + 2; ++i) {
         // The stage held load i - S, K or V of key tile u: K_u has been read once the last S
         // of tile u is there, V_u once that of tile u + 1 is.  (u >= j - 4, and S of
@@ -224,9 +225,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   } else if (warp == kScrubWarp) {
     // ---- scrubber -------------------------------------------------------------------
     uint32_t phase = 0;   // a bit per stage: its raw barrier's next parity
-    for (int j = 0; j < nt; ++j) {
+    for (int j = max(clear, 0); j < nt; ++j) {
       const int k0 = (seg.first + j) * kTile;
-      if (!masked(k0)) continue;
       const int st = (2 * j + 1) % S;
       const bool ok = wait(&raw[st], (phase >> st) & 1u);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -343,7 +343,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
     float m = kNegInf, l = 0.f;   // the row's maximum (log2) and sum
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
-      const int k0 = (seg.first + j) * kTile;
       ok = __all_sync(0xffffffffu, wait(&sfull[4 * t + (j & 3)], (uint32_t)((j >> 2) & 1)));
       if (!ok) break;
       tc_fence_after();
@@ -351,8 +350,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
 #pragma unroll
       for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
       tmem_wait_ld();
-      if (masked(k0)) {
-        const int hi = pos - k0;
+      if (j >= clear) {
+        const int hi = pos - (seg.first + j) * kTile;
 #pragma unroll
         for (int c0 = 0; c0 < kTile; c0 += 32)   // 32 keys that all rows of the warp see stay as they are
           if (__any_sync(0xffffffffu, c0 + 31 > hi)) {
