@@ -479,6 +479,7 @@ int lf_paged_decode_shared(const lf_pages* pages, int batch, const int32_t* page
   a.rows = shape.plan.rows;
   a.slots = shape.plan.slots;
   a.rounds = shape.plan.rounds;
+  a.least = shape.plan.least;
   a.scale_log2 = d.scale_log2;
   a.part_rows = shape.plan.part_rows;
   a.part_o = floats(shape.off_part_o);

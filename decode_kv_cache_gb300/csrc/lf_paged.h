@@ -90,7 +90,7 @@ struct PagedSharedArgs {
   int groups, q_heads, group;
   int fresh;                  // 1: the last token comes with the call, and is no part of a prefix
   int rows;
-  int slots, rounds;          // blocks that run at once; rounds of them that the grid has room for
+  int slots, rounds, least;   // blocks that run at once; rounds of them that the grid has room for; tiles of a segment at least
   float scale_log2;
   int64_t part_rows;          // rows that part_o and part_ml have
   float* part_o;              // [part_rows][head_dim] partial outputs
@@ -107,7 +107,7 @@ struct PagedSharedArgs {
 // Its kernel by type, heads and pages, and the rows of a piece.
 struct SharedPlan {
   PromptPlan::Kernel kernel;
-  int rows, keys, slots, rounds, slot_rows;
+  int rows, keys, slots, rounds, least, slot_rows;
   int64_t grid, part_rows;
   bool fits;                  // the kernels' numbers hold such a call
 };

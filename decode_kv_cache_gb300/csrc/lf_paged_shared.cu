@@ -306,13 +306,18 @@ cudaError_t join_dim(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int 
 SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int group, int groups, int sms) {
   SharedPlan p;
   p.keys = kKeys;
+  p.least = 1;
   if (elem == 2 && paged_prompt_tc_takes(pool, head_dim)) {
     p.kernel = PromptPlan::kTensor;
     p.rows = 256;
     p.keys = 128;
     p.slots = sms;
   } else if (elem == 2) {
+    // Shares of three tiles or more: of one they are as much as its keys (four groups of eight behind 1000 to 2000 tokens, heads
+    // of 32, 16.2 us, of one tile 21.0).  A tile of fp32 takes longer than a block's start (24 behind 3000, heads of
+    // 64, shares of one tile 30 us, of two 36).
     p.kernel = PromptPlan::kMatrix;
+    p.least = 3;
     p.rows = kMmaRows;
     p.slots = sms * (head_dim == 128 ? 3 : head_dim >= 32 ? 4 : 5);
   } else {

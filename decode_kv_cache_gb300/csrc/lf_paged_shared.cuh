@@ -44,16 +44,16 @@ __device__ __forceinline__ int last_seen(const PagedSharedArgs& a, int prefix, i
 
 // Tiles of a segment.  A block costs its tiles and, for its start and its rows' way out, about as much as
 // kSegmentStart of them; `units` units of `tiles` tiles in all, the longest of `longest`, are cut so that r rounds of `slots` blocks
-// take them, with the r, up to `rounds`, that costs least.
+// take them, with the r, up to `rounds`, that costs least; `least` tiles or more.
 constexpr int kSegmentStart = 4;
 
-__device__ __forceinline__ int segment_tiles(int slots, int rounds, int64_t units, int64_t tiles, int longest) {
+__device__ __forceinline__ int segment_tiles(int slots, int rounds, int least, int64_t units, int64_t tiles, int longest) {
   int best = longest;
   int64_t cost = INT64_MAX;
   const int64_t r0 = units / slots + 1;
   for (int64_t r = r0; r < r0 + 2 && r <= rounds; ++r) {
     const int64_t room = r * slots - units;
-    const int64_t c = min((int64_t)longest, max((int64_t)1, (tiles + room - 1) / room));
+    const int64_t c = min((int64_t)longest, max((int64_t)least, (tiles + room - 1) / room));
     const int64_t used = c == longest ? (units + slots - 1) / slots : r;
     if (used * (c + kSegmentStart) < cost) {
       cost = used * (c + kSegmentStart);
@@ -237,7 +237,7 @@ __device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys,
   int64_t units, tiles, none = 0;
   int longest;
   list.sum(a, keys, &units, &tiles, &longest, &none);
-  list.cut(a, keys, units > 0 ? segment_tiles(a.slots, a.rounds, units, tiles, longest) : 1);
+  list.cut(a, keys, units > 0 ? segment_tiles(a.slots, a.rounds, a.least, units, tiles, longest) : 1);
   return blockIdx.x < list.segments && list.find(a, keys, blockIdx.x, out);
 }
 
