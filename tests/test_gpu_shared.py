@@ -381,3 +381,72 @@ def test_rotated_steps_behind_a_shared_prompt():
             size = torch.einsum("ghn,ngd->ghd", torch.softmax(z, -1), vv.abs()).reshape(hq, d)
             assert ((out[b].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -13) * size + 2.0 ** -8 * want.abs()).all()
     assert cache.check() == 0
+
+
+# ---- found by looking for what the tests above do not reach ----------------------------------------
+
+@pytest.mark.parametrize("kind,d,page,group", [("bf16", 128, 16, 4), ("bf16", 64, 32, 8), ("bf16", 128, 24, 2), ("f32", 64, 16, 1)])
+def test_branches_in_all_rows_of_a_block(kind, d, page, group):
+    """Members that leave the prefix everywhere, in both query tiles and in several pieces, behind groups of other lengths, so
+    that ranges end inside units; with new tokens."""
+    rng = np.random.default_rng(page)
+    shape = [[(700, 720)] + [(int(p), int(p) + 1 + int(t)) for p, t in zip(rng.integers(0, 701, 99), rng.integers(0, 60, 99))],
+             [(2000, 2001)] + [(int(p), int(p) + 1 + int(t)) for p, t in zip(rng.integers(1900, 2001, 9), rng.integers(0, 300, 9))],
+             [(130, 150)] * 3, [(0, 1500)], [(5, 6), (5, 700)]]
+    f = Family(kind, 2, d, page, shape, seed=group)
+    batch = len(f.lens)
+    q, kn, vn = f.randn(batch, 2 * group, d), f.randn(batch, 2, d), f.randn(batch, 2, d)
+    lse = torch.empty(batch, 2 * group, dtype=torch.float32, device="cuda")
+    out = f.decode(q, kn, vn, lse=lse)
+    again = f.decode(q, kn, vn)
+    assert torch.equal(out, again) and f.cache.check() == 0
+    f.write_new(kn, vn)
+    f.check(q, out, lse, which=list(range(0, batch, 7)) + [99, 100, 109, 110, 113, batch - 2, batch - 1], fresh=True)
+
+
+@pytest.mark.parametrize("kind,d", [("bf16", 128), ("bf16", 32), ("f32", 64)])
+def test_prefixes_behind_every_length(kind, d):
+    """The largest number there is as a prefix: every sequence is all prefix, whatever the table holds behind it."""
+    f = Family(kind, 2, d, 16, [[(333, 333), (333, 200), (333, 0), (333, 1)], [(64, 64)]], seed=17)
+    q = f.randn(5, 8, d)
+    want = f.decode(q)
+    f.check(q, want)
+    top = ints([2**31 - 1] * 5)
+    out = f.cache.decode_shared(0, q, f.table, f.t_lens, f.t_start, top)
+    assert f.cache.check() == 0
+    f.check(q, out)
+
+
+@pytest.mark.parametrize("kind,d,batch", [("bf16", 64, 3000), ("f32", 16, 2000)])
+def test_large_batches(kind, d, batch):
+    """More sequences and groups than a block has threads, one KV head, a page for each."""
+    rng = np.random.default_rng(batch)
+    shape = [[(int(p), int(p) + int(t)) for t in rng.integers(0, 9, int(rng.integers(1, 4)))]
+             for p in rng.integers(0, 20, batch // 2)]
+    f = Family(kind, 1, d, 16, shape, seed=batch)
+    q = f.randn(len(f.lens), 2, d)
+    out = f.decode(q)
+    assert f.cache.check() == 0
+    f.check(q, out, which=range(0, len(f.lens), 61))
+
+
+def test_layers_and_strides():
+    """Another layer's pools, K and V of a token side by side."""
+    f = Family("bf16", 2, 128, 16, [[(100, 130), (100, 120)]], seed=18)
+    pages = f.k.shape[0]
+    both = torch.full((2, pages, 2, 16, 2, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    both[1, :, :, :, 0], both[1, :, :, :, 1] = f.k, f.v
+    cache = lf.LFPagedCache.over(both[:, :, :, :, 0], both[:, :, :, :, 1])
+    q = f.randn(2, 8, 128)
+    assert torch.equal(cache.decode_shared(1, q, f.table, f.t_lens, f.t_start, f.t_prefix), f.decode(q))
+    assert cache.check() == 0
+
+
+def test_neighbours_of_the_call_keep_their_bits():
+    """What lies around out and lse is not written."""
+    f = Family("bf16", 2, 128, 16, [[(100, 130), (100, 120), (40, 0)]], seed=19)
+    q = f.randn(3, 8, 128)
+    wide, flat = torch.full((5, 8, 128), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((5, 8), 3.0, device="cuda")
+    f.decode(q, out=wide[1:4], lse=flat[1:4])
+    assert (wide[[0, 4]] == 3).all() and (flat[[0, 4]] == 3).all()
+    f.check(q, wide[1:4], flat[1:4])
