@@ -542,7 +542,7 @@ class LFCache:
 
 def _run_on(device, index, stream, held, call, *args):
     """call(stream handle, *args) with the device and `stream` (None: the current one) current; a stream that the
-    caller names is known to the allocator as one that reads `held` and the tensors among args."""
+    caller names is known to the allocator as one that reads held() and the tensors among args."""
     if stream is None and torch.cuda.current_device() == index:
         return call(torch._C._cuda_getCurrentRawStream(index), *args)
     if isinstance(stream, int):
@@ -553,7 +553,7 @@ def _run_on(device, index, stream, held, call, *args):
         raise LFError(LF_ERR_ARG, f"stream: expected a stream of {device}, got {stream}")
     with torch.cuda.device(index), torch.cuda.stream(stream):
         if stream is not None:
-            for t in (*held, *args):
+            for t in (*held(), *args):
                 if isinstance(t, torch.Tensor):
                     t.record_stream(stream)
         return call(torch._C._cuda_getCurrentRawStream(index), *args)
@@ -678,7 +678,7 @@ class LFRotary:
         elif k_out is not None:
             raise LFError(LF_ERR_ARG, "k_out without k")
         step = self._positions(positions, shape[:-2])
-        return _run_on(self.device, self._index, stream, self._held, self._rotate, q, positions, k, q_out, k_out, step,
+        return _run_on(self.device, self._index, stream, lambda: self._held, self._rotate, q, positions, k, q_out, k_out, step,
                        1 if inverse else 0)
 
     def _rotate(self, st, q, positions, k, q_out, k_out, step, inverse):
@@ -802,7 +802,7 @@ class LFPagedCache:
         names reads the tensors: they may be let go as soon as the call returns."""
         if stream is None and torch.cuda.current_device() == self._index:
             return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
-        return _run_on(self.device, self._index, stream, (self.k, self.v, self.err), call, *args)
+        return _run_on(self.device, self._index, stream, lambda: (self.k, self.v, self.err), call, *args)
 
     def _ask(self, call, pages, key):
         """The workspace that calls of this shape need, remembered (of the last few thousand shapes)."""
