@@ -285,7 +285,6 @@ __device__ __forceinline__ bool sees(const PagedPromptArgs& a, int pos, int key)
 // and [from, to); with splits, a block takes its share of them.
 struct Tiles {
   int sink, gap, first, last;   // tile j of them is number j below `sink`, else j + gap
-  Tiles() = default;
   __device__ Tiles(const PagedPromptArgs& a, int p_lo, int p_hi, int size, int share)
       : sink(0), gap(0), first(0), last(0) {
     if (p_hi < 0) return;

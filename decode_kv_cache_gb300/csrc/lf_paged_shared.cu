@@ -4,67 +4,455 @@
 //   out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s,  m = max_s m_s
 //
 // over shares s of a row's keys, each with its maximum m_s (log2), sum l_s and output O_s (not normalised): shares of
-// the prefix, and what lies behind it.  Three launches:
+// the prefix, and what lies behind it.  bf16 with heads of 64 and 128 has a kernel for both (lf_paged_shared_tc.cu).  Others take
+// two launches:
 //   - lf_paged_decode.cu's kernel walks every sequence from its prefix's end on;
-//   - the prefix's kernel (here or lf_paged_shared_tc.cu) takes up to 256 rows, (sequence, head of the group) pairs, of
-//     a KV head against a segment of the prefix's keys, so that with G rows from each of n sequences a key is used n G
-//     times.  It depends on nothing that the first one writes and is placed while that drains (programmatic
-//     dependent launch); it ends behind it;
-//   - the join below adds the shares up, in order of position.
-// Bound by HBM while a KV head has fewer than about 500 rows, and by the matrix instructions above.
+//   - a kernel here takes up to 64 rows, (sequence, head of the group) pairs, of a KV head against a segment of the
+//     prefix's keys.  It depends on nothing that the first one writes and is placed while that drains (programmatic
+//     dependent launch); it ends behind it.
+// The join, the last launch of either way, adds the shares up, in order of position.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "lf_paged_generic.cuh"
+#include <type_traits>
+
 #include "lf_paged_shared.cuh"
 
 namespace lf {
 
 namespace {
 
-// A segment as the kernels of lf_paged_generic.cuh take it.
-template <int kThreads>
-struct SharedTask {
-  using Args = PagedSharedArgs;
+// A segment as its block's threads see it.
+struct Block {
   Segment s;
 
-  __device__ __forceinline__ bool take(const Args& a, int, int keys) {
-    const bool ok = take_segment<kThreads>(a, keys, &s);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!ok) finish();
-    return ok;
-  }
-  __device__ __forceinline__ bool take_level(const Args& a, int per_piece, int keys) { return take(a, per_piece, keys); }
+  template <int kThreads>
+  __device__ __forceinline__ bool take(const PagedSharedArgs& a);
   __device__ __forceinline__ int count() const { return s.last - s.first; }
   __device__ __forceinline__ int at(int j) const { return s.first + j; }
-  __device__ __forceinline__ bool live(const Args& a, int r) const { return r < s.members * a.group; }
-  __device__ __forceinline__ int pos(const Args& a, int r) const { return live(a, r) ? last_seen(a, s.prefix, s.b0 + r / a.group) : -1; }
-  __device__ __forceinline__ int64_t q_row(const Args& a, int r) const { return shared_row(a, s, r); }
-  __device__ __forceinline__ int behind(const Args&) const { return 0; }
-  template <bool kSkip, class Behind>
-  __device__ __forceinline__ int64_t offset(const Args& a, int pos, Behind) const { return shared_offset(a, s, pos); }
-  __device__ __forceinline__ bool hidden(const Args&, int k0, int keys) const { return k0 + keys - 1 > s.p_lo; }
-  __device__ __forceinline__ bool sees(const Args&, int pos, int key) const { return key <= pos; }
-  __device__ __forceinline__ bool parts(const Args&) const { return true; }
+  __device__ __forceinline__ bool live(const PagedSharedArgs& a, int r) const { return r < s.members * a.group; }
+  // The last position that row r sees, -1: none, or no row.
+  __device__ __forceinline__ int pos(const PagedSharedArgs& a, int r) const {
+    return live(a, r) ? last_seen(a, s.prefix, s.b0 + r / a.group) : -1;
+  }
+  // Where row r's share goes.
   template <int D>
-  __device__ __forceinline__ float* part(const Args& a, int, int r, float m, float l, bool first) const {
+  __device__ __forceinline__ float* part(const PagedSharedArgs& a, int r, float m, float l, bool first) const {
     if (first) {
       a.part_ml[2 * (s.row + r)] = m;
       a.part_ml[2 * (s.row + r) + 1] = l;
     }
     return a.part_o + (s.row + r) * D;
   }
-  __device__ __forceinline__ void* out(const Args&) const { return nullptr; }
-  __device__ __forceinline__ void stats(const Args&, int64_t, float, float) const {}
-  template <typename T, int D>
-  __device__ __forceinline__ void by_hand(const Args& a, int keys, int, int r, int n, int lane) const {
-    for (int i = r; i < r + n && live(a, i); ++i) shared_row_by_hand<T, D>(a, s, keys, i, pos(a, i), lane);
-  }
   // The kernel before this one ends before this one does, and with it before the join.
   __device__ __forceinline__ void finish() const {
     if (threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   }
 };
+
+constexpr int kKeys = 64;
+
+template <int kThreads>
+__device__ __forceinline__ bool Block::take(const PagedSharedArgs& a) {
+  const bool ok = take_segment<kThreads>(a, kKeys, &s);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!ok) finish();
+  return ok;
+}
+
+// ---- bf16: m16n8k16 ------------------------------------------------------------------
+//
+// For short heads and for pages that a tensor map's boxes do not divide into.  Four warps of 16 rows, two stages of K and V
+// tiles of 64 tokens, 16-byte chunks gathered by page.  The queries stay in registers as A operands, S comes out as the C operand
+// whose layout is the A operand of P.V, so P (rounded to bf16: half a step is 2^-8 of a weight) never leaves the registers either.
+// Bound by these instructions' rate and the softmax between them, and with few tiles by the launches' starts: 32 sequences
+// behind 8192 in pages of 24, 32 / 8 heads of 128, 46 us with the rest and the join; four groups of eight behind 1000 to 2000, heads of
+// 32, 16 us.
+
+constexpr int kMmaThreads = 128, kMmaRows = 64;
+
+// Three blocks of heads of 128 on an SM.
+template <int D>
+__global__ void __launch_bounds__(kMmaThreads, D == 128 ? 3 : D >= 32 ? 4 : 5) paged_shared_mma_kernel(const __grid_constant__ PagedSharedArgs a) {
+  constexpr int NC = D / 8;                // 16-byte chunks of a row
+  constexpr int kTileBytes = kKeys * NC * 16;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t s_off[2][kKeys];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Block block;
+  if (!block.take<kMmaThreads>(a)) return;
+  const int nt = block.count();
+  const uint32_t ring = smem_u32(smem);
+
+  auto look_up = [&](int j) {
+    if (tid < kKeys)
+      s_off[j & 1][tid] = shared_offset(a, block.s, block.at(j) * kKeys + tid);
+  };
+  auto issue = [&](int j) {
+    const uint32_t kd = ring + (j & 1) * 2 * kTileBytes, vd = kd + kTileBytes;
+    constexpr int kStep = kMmaThreads / NC;   // rows that the block covers at once
+    const int c = tid % NC;
+#pragma unroll
+    for (int i = 0; i < (kKeys + kStep - 1) / kStep; ++i) {
+      const int r = i * kStep + tid / NC;
+      if (kKeys % kStep == 0 || r < kKeys) {
+        const int64_t off = s_off[j & 1][r];
+        const uint32_t d = 16 * tile_chunk<NC>(r, c);
+        cp_async16(kd + d, a.pool.k + (off >= 0 ? off + c * 16 : 0), off >= 0);
+        cp_async16(vd + d, a.pool.v + (off >= 0 ? off + c * 16 : 0), off >= 0);
+      }
+    }
+  };
+
+  const int ra = warp * 16 + (lane >> 2);   // and ra + 8
+  uint32_t qa[D / 16][4];
+  int pos[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = ra + 8 * i;
+    const bool live = block.live(a, r);
+    pos[i] = block.pos(a, r);
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + (live ? shared_row(a, block.s, r) * (D / 2) : 0) + (lane & 3);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      qa[kk][i] = live ? q[8 * kk] : 0u;
+      qa[kk][2 + i] = live ? q[8 * kk + 4] : 0u;
+    }
+  }
+  float o[D / 8][4], m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+  __nv_bfloat162 bad = __float2bfloat162_rn(0.f);
+
+  if (nt > 0) {
+    look_up(0);
+    __syncthreads();
+    issue(0);
+    cp_async_commit();
+    if (nt > 1) look_up(1);
+  }
+#pragma unroll 1
+  for (int j = 0; j < nt; ++j) {
+    __syncthreads();   // the other stage has been read, its new offsets are there
+    if (j + 1 < nt) issue(j + 1);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncthreads();
+    if (j + 2 < nt) look_up(j + 2);
+    const uint32_t ks = ring + (j & 1) * 2 * kTileBytes, vs = ks + kTileBytes;
+    const int k0 = block.at(j) * kKeys;
+    const bool hidden = k0 + kKeys - 1 > block.s.p_lo;
+    if (hidden) {   // a weight of 0 must take nothing: are there values that are not finite?
+      const uint4* v = reinterpret_cast<const uint4*>(smem + (j & 1) * 2 * kTileBytes + kTileBytes);
+      const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+      for (int i = tid; i < kKeys * NC; i += kMmaThreads) {
+        const uint4 x = v[i];
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, bad);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, bad);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, bad);
+        bad = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, bad);
+      }
+    }
+    float s[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      if constexpr (D >= 32) {
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) {
+          uint32_t kb[4];
+          ldmatrix4(ks + 16 * tile_chunk<NC>(8 * n + (lane & 7), c + (lane >> 3)), kb);
+          mma16816(s[n], qa[c / 2][0], qa[c / 2][1], qa[c / 2][2], qa[c / 2][3], kb[0], kb[1]);
+          mma16816(s[n], qa[c / 2 + 1][0], qa[c / 2 + 1][1], qa[c / 2 + 1][2], qa[c / 2 + 1][3], kb[2], kb[3]);
+        }
+      } else if ((n & 1) == 0) {
+        uint32_t kb[4];
+        ldmatrix4(ks + 16 * tile_chunk<NC>(8 * n + (lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1), kb);
+        mma16816(s[n], qa[0][0], qa[0][1], qa[0][2], qa[0][3], kb[0], kb[1]);
+        mma16816(s[n + 1], qa[0][0], qa[0][1], qa[0][2], qa[0][3], kb[2], kb[3]);
+      }
+    }
+    if (hidden) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (k0 + 8 * n + 2 * (lane & 3) + (i & 1) > pos[i >> 1]) s[n][i] = kNegInf;
+    }
+    float top[2] = {kNegInf, kNegInf};
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
+    bool up = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2)) * a.scale_log2;
+      up |= top[i] > m[i];
+    }
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mn = fmaxf(m[i], top[i]);
+        const float f = mn == kNegInf ? 1.f : ex2(m[i] - mn);
+        m[i] = mn;
+        l[i] *= f;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][2 * i] *= f;
+          o[n][2 * i + 1] *= f;
+        }
+      }
+    }
+    const float mu[2] = {m[0] == kNegInf ? 0.f : m[0], m[1] == kNegInf ? 0.f : m[1]};
+    uint32_t pa[8][2];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float x = ex2(fmaf(s[n][2 * i], a.scale_log2, -mu[i]));
+        const float y = ex2(fmaf(s[n][2 * i + 1], a.scale_log2, -mu[i]));
+        l[i] += x + y;
+        pa[n][i] = pack_bf16(x, y);
+      }
+#pragma unroll
+    for (int kk = 0; kk < kKeys / 16; ++kk) {
+      const int row = 16 * kk + (lane & 7) + 8 * ((lane >> 3) & 1);
+#pragma unroll
+      for (int c = 0; c < NC; c += 2) {
+        uint32_t vb[4];
+        ldmatrix4_trans(vs + 16 * tile_chunk<NC>(row, c + (lane >> 4)), vb);
+        mma16816(o[c], pa[2 * kk][0], pa[2 * kk][1], pa[2 * kk + 1][0], pa[2 * kk + 1][1], vb[0], vb[1]);
+        mma16816(o[c + 1], pa[2 * kk][0], pa[2 * kk][1], pa[2 * kk + 1][0], pa[2 * kk + 1][1], vb[2], vb[3]);
+      }
+    }
+  }
+
+  const float2 f = __bfloat1622float2(bad);
+  if (__syncthreads_or(!(f.x == 0.f) || !(f.y == 0.f))) {
+    for (int r = warp * 16; r < warp * 16 + 16 && block.live(a, r); ++r)
+      shared_row_by_hand<__nv_bfloat16, D>(a, block.s, kKeys, r, block.pos(a, r), lane);
+    block.finish();
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float ls = l[i] + __shfl_xor_sync(0xffffffffu, l[i], 1);
+    ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+    const int r = ra + 8 * i;
+    if (!block.live(a, r)) continue;
+    float* part = block.part<D>(a, r, m[i], ls, (lane & 3) == 0) + 2 * (lane & 3);
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+      *reinterpret_cast<float2*>(part + 8 * n) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+  }
+  block.finish();
+}
+
+// ---- fp32: CUDA cores -----------------------------------------------------------------
+//
+// (A tf32 product drops 13 bits of each factor.)  Two floats per multiply-add instruction.  A thread holds an M x 4 piece of S
+// (sums over even and over odd columns of d) and M rows x d/16 columns of O.  V is on its way while S is computed.  Bound by
+// the chain of a tile's steps: a tile of 64 keys takes about 6 us.  24 sequences behind 3000, 8 heads of 64, 30 us with
+// the rest and the join; 16 behind 4000, 32 / 8 heads of 128, 64 us; 64 behind 8192, 8 heads of 64, 57 us.
+
+// In blocks of 32 rows P has a place of its own, so that the next K can come in as soon
+// as S is done; in those of 64 it goes where K was, which leaves room for two blocks.
+template <int D, int R>
+constexpr int fma_smem() {
+  constexpr int LD = D + 4, LP = R + 4;   // eight rows' equal chunks fall into different banks
+  return (R * LD + kKeys * (R == 32 ? LD + LP : LD > LP ? LD : LP) + kKeys * LD) * 4;
+}
+
+template <int D, int R, int M>
+__global__ void __launch_bounds__(16 * R / M, D <= 64 ? 4 : 1) paged_shared_fma_kernel(const __grid_constant__ PagedSharedArgs a) {
+  constexpr int kThreads = 16 * R / M;
+  static_assert(kThreads >= kKeys && M % 4 == 0, "one thread looks up a key");
+  constexpr int LD = D + 4, LP = R + 4;
+  constexpr int NC = D / 4;
+  constexpr int CW = D / 16;            // columns of O per thread
+  constexpr int VW = CW < 4 ? CW : 4;   // .. in runs of
+  constexpr int CP = (CW + 1) / 2;      // .. in pairs
+  extern __shared__ __align__(16) float sm[];
+  float* sq = sm;                                  // [R][LD]
+  constexpr bool kOwnP = R == 32;
+  float* sk = sm + R * LD;                         // [kKeys][LD]
+  float* sv = sk + kKeys * (kOwnP || LD > LP ? LD : LP);   // [kKeys][LD]
+  float* sp = kOwnP ? sv + kKeys * LD : sk;        // P^T [kKeys][LP]
+  __shared__ int64_t s_off[kKeys];
+  const int tid = threadIdx.x;
+  Block block;
+  if (!block.take<kThreads>(a)) return;
+  const int nt = block.count();
+
+  auto look_up = [&](int j) {
+    if (tid < kKeys) s_off[tid] = shared_offset(a, block.s, block.at(j) * kKeys + tid);
+  };
+  auto issue = [&](float* dst, const char* pool) {
+#pragma unroll 4
+    for (int i = tid; i < kKeys * NC; i += kThreads) {
+      const int r = i / NC, c = i - r * NC;
+      const int64_t off = s_off[r];
+      cp_async16(smem_u32(dst + r * LD + c * 4), pool + (off >= 0 ? off + c * 16 : 0), off >= 0);
+    }
+    cp_async_commit();
+  };
+  if (nt > 0) look_up(0);
+  for (int i = tid; i < R * NC; i += kThreads) {
+    const int r = i / NC, c = i - r * NC;
+    const bool live = block.live(a, r);
+    const float* q = reinterpret_cast<const float*>(a.q) + (live ? shared_row(a, block.s, r) * D + c * 4 : 0);
+    *reinterpret_cast<float4*>(sq + r * LD + c * 4) =
+        live ? *reinterpret_cast<const float4*>(q) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  if (nt > 0) issue(sk, a.pool.k);
+
+  const int rg = tid >> 4, cg = tid & 15;
+  int pos[M];
+  float m[M], l[M];
+  uint64_t o[M][CP];
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    pos[i] = block.pos(a, rg * M + i);
+    m[i] = kNegInf;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CP; ++c) o[i][c] = 0ull;
+  }
+
+#pragma unroll 1
+  for (int j = 0; j < nt; ++j) {
+    const int k0 = block.at(j) * kKeys;
+    const bool hidden = k0 + kKeys - 1 > block.s.p_lo;
+    issue(sv, a.pool.v);
+    cp_async_wait<1>();
+    __syncthreads();
+    uint64_t s2[M][4];
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) s2[i][n] = 0ull;
+#pragma unroll (M == 4 ? 4 : 2)
+    for (int d = 0; d < D; d += 4) {
+      ulonglong2 y[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) y[n] = *reinterpret_cast<const ulonglong2*>(sk + (cg + 16 * n) * LD + d);
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sq + (rg * M + i) * LD + d);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          s2[i][n] = fma_pair(x.x, y[n].x, s2[i][n]);
+          s2[i][n] = fma_pair(x.y, y[n].y, s2[i][n]);
+        }
+      }
+    }
+    float w[M][4];
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      float top = kNegInf;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        float x, y;
+        unpair(s2[i][n], &x, &y);
+        w[i][n] = x + y;
+        if (hidden && k0 + cg + 16 * n > pos[i]) w[i][n] = kNegInf;
+        top = fmaxf(top, w[i][n]);
+      }
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      top = fmaxf(m[i], top * a.scale_log2);
+      const float mu = top == kNegInf ? 0.f : top;
+      const float f = ex2(m[i] - mu);
+      m[i] = top;
+      l[i] *= f;
+#pragma unroll
+      for (int c = 0; c < CP; ++c) o[i][c] = fma_pair(o[i][c], pair(f, f), 0ull);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        w[i][n] = ex2(fmaf(w[i][n], a.scale_log2, -mu));   // rounded as a difference, not at the logit's size
+        l[i] += w[i][n];
+      }
+    }
+    __syncthreads();   // K has been read
+    if (kOwnP && j + 1 < nt) {   // and the offsets, by the copies of V
+      look_up(j + 1);
+      __syncthreads();
+      issue(sk, a.pool.k);
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int i = 0; i < M; i += 4)
+        *reinterpret_cast<float4*>(sp + (cg + 16 * n) * LP + rg * M + i) =
+            make_float4(w[i][n], w[i + 1][n], w[i + 2][n], w[i + 3][n]);
+    if (!kOwnP && j + 1 < nt) look_up(j + 1);
+    if (kOwnP && j + 1 < nt) cp_async_wait<1>();   // V; K goes on
+    else cp_async_wait<0>();
+    __syncthreads();
+    // Where some row does not see some key of the tile, a weight of zero takes
+    // nothing of the value, which may hold anything there.
+    auto accumulate = [&](auto part) {
+#pragma unroll (M == 4 ? 8 : 2)
+      for (int k = 0; k < kKeys; ++k) {
+        float pi[M];
+#pragma unroll
+        for (int i = 0; i < M; i += 4) load16_f32(sp + k * LP + rg * M + i, pi + i);
+        uint64_t v[CP];
+#pragma unroll
+        for (int c = 0; c < CW; c += VW) {
+          const float* src = sv + k * LD + (c / VW) * 16 * VW + cg * VW;
+          if constexpr (VW == 4) {
+            const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(src);
+            v[c / 2] = t.x;
+            v[c / 2 + 1] = t.y;
+          } else if constexpr (VW == 2) {
+            v[0] = *reinterpret_cast<const uint64_t*>(src);
+          } else {
+            v[0] = pair(*src, 0.f);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          if (part.value && pi[i] == 0.f) continue;
+          const uint64_t pp = pair(pi[i], pi[i]);
+#pragma unroll
+          for (int c = 0; c < CP; ++c) o[i][c] = fma_pair(pp, v[c], o[i][c]);
+        }
+      }
+    };
+    if (hidden) accumulate(std::true_type{});
+    else accumulate(std::false_type{});
+    __syncthreads();   // P and V have been read
+    if (!kOwnP && j + 1 < nt) issue(sk, a.pool.k);
+  }
+
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    float ls = l[i];
+#pragma unroll
+    for (int x = 1; x < 16; x <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+    const int r = rg * M + i;
+    if (!block.live(a, r)) continue;
+    float* out = block.part<D>(a, r, m[i], ls, cg == 0);
+#pragma unroll
+    for (int c = 0; c < CP; ++c) {
+      float x, y;
+      unpair(o[i][c], &x, &y);
+      float* dst = out + (2 * c / VW) * 16 * VW + cg * VW + 2 * c % VW;
+      if constexpr (VW >= 2) *reinterpret_cast<float2*>(dst) = make_float2(x, y);
+      else *dst = x;
+    }
+  }
+  block.finish();
+}
 
 cudaError_t launch(const void* kernel, const PagedSharedArgs& a, int64_t grid, int threads, int smem,
                    std::atomic<uint64_t>& done, cudaStream_t stream) {
@@ -87,7 +475,7 @@ cudaError_t launch(const void* kernel, const PagedSharedArgs& a, int64_t grid, i
 template <int D>
 cudaError_t launch_mma(const PagedSharedArgs& a, int64_t grid, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  return launch(reinterpret_cast<const void*>(&paged_mma_kernel<SharedTask<kMmaThreads>, D>), a, grid, kMmaThreads,
+  return launch(reinterpret_cast<const void*>(&paged_shared_mma_kernel<D>), a, grid, kMmaThreads,
                 4 * kKeys * D * 2, done, stream);
 }
 
@@ -95,7 +483,7 @@ template <int D, int R, int M>
 cudaError_t launch_fma(const PagedSharedArgs& a, int64_t grid, cudaStream_t stream) {
   constexpr int kThreads = 16 * R / M;
   static std::atomic<uint64_t> done{0};
-  return launch(reinterpret_cast<const void*>(&paged_fma_kernel<SharedTask<kThreads>, D, R, M>), a, grid, kThreads,
+  return launch(reinterpret_cast<const void*>(&paged_shared_fma_kernel<D, R, M>), a, grid, kThreads,
                 fma_smem<D, R>(), done, stream);
 }
 

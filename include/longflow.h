@@ -477,8 +477,8 @@ int lf_paged_decode_workspace(const lf_pages* pages, int batch, int max_pages, i
  *   workspace    lf_paged_decode_shared_workspace bytes, as lf_paged_decode's
  * A sequence of no group, or with a longer prefix than its group's first, is reported (LF_DEVERR_STATE) and its rows of
  * out and lse are left as they are; group starts that decrease are reported too, and the outputs of the call are
- * unspecified then.  A bf16 cache's weights of values in the prefix are rounded as lf_paged_prompt's.  Three
- * launches.
+ * unspecified then.  A bf16 cache's weights of values in the prefix are rounded as lf_paged_prompt's.
+ * Refused where batch * kv_heads * (max_pages * page_size / 128 + 9) reaches 2^31.  Up to three launches.
  */
 int lf_paged_decode_shared(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
                            const int32_t* lens, int q_heads, const void* q, const int32_t* group_start, int groups,
