@@ -244,6 +244,10 @@ def test_refusals():
     for w, n in ((ws, need - 1), (None, need), (ws[8:], need)):
         with pytest.raises(lf.LFError, match="workspace"):
             lf.lf_paged_decode_shared(*args, w, n)
+    wide = lf.LFPages.from_buffer_copy(p)
+    wide.page_size = 2**30
+    with pytest.raises(lf.LFError, match="too large for one call"):
+        lf.lf_paged_decode_shared_workspace(wide, 4096, 1, 8, 4096)
     lf.lf_paged_decode_shared(*args, ws, need)
     assert torch.equal(out, f.decode(q)) and f.cache.check() == 0
 
