@@ -493,7 +493,7 @@ cudaError_t launch_fma(const PagedSharedArgs& a, int64_t grid, cudaStream_t stre
 // met it (lf_paged_decode.cu); the prefix's shares are rows that its blocks left.  Warps take a row of the group each, or
 // every so many of its shares, and join through shared memory, in order of position.  Bound by latency: what the call was given is
 // read while the kernel before drains, then come two reads that depend on each other, places and shares.
-constexpr int kJoinWarps = 8, kJoinBatch = 4;
+constexpr int kJoinBatch = 4;
 
 // Shares i = 0 .. n - 1 of a row (maximum and sum at ml(i), output at o(i)[D]) joined in their order, kJoinBatch of
 // them read at once: lane j holds columns E j .. E j + E - 1.
@@ -543,7 +543,7 @@ __device__ __forceinline__ void join_shares(int n, Ml ml, O o, int lane, float* 
   *l_out = l;
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs a,
                                                                             const __grid_constant__ PagedDecodeArgs d,
                                                                             int ctas) {
@@ -655,18 +655,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_shared_join_kernel(cons
   }
 }
 
-template <typename T, int D, int G>
-cudaError_t launch_join(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int ctas, cudaStream_t stream) {
+template <typename T, int D, int G, int W>
+cudaError_t launch_join_warps(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int ctas, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.pool.batch * a.pool.kv_heads), 1, 1);
-  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+  cfg.blockDim = dim3(W * 32, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_shared_join_kernel<T, D, G>, a, rest, ctas);
+  return cudaLaunchKernelEx(&cfg, paged_shared_join_kernel<T, D, G, W>, a, rest, ctas);
+}
+
+template <typename T, int D, int G>
+cudaError_t launch_join(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int ctas, cudaStream_t stream) {
+  // Few units: more warps for each.  (8 behind 2000, 64 units: 16 warps 17.0 us, 8 17.8, 4 19.1; 32 behind 60000, 256 units: 68.8,
+  // 70.5, 73.7; 64 behind 8192, 512: 53.1, 52.9, 52.4; 256 in 16 groups, 1944: 126, 117, 112.  A number that the
+  // kernel is told of and not built with costs registers: 114 and 72.8.)
+  if ((int64_t)a.pool.batch * a.pool.kv_heads <= 2 * (int64_t)ctas) return launch_join_warps<T, D, G, 16>(a, rest, ctas, stream);
+  return launch_join_warps<T, D, G, (G > 4 ? G : 4)>(a, rest, ctas, stream);
 }
 
 template <typename T, int D>
