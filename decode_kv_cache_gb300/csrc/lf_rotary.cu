@@ -412,7 +412,7 @@ int lf_rotary_turns(const double* frequency, int pairs, uint64_t* turns) {
   lf::clear_last_error();
   if (!frequency || !turns || pairs < 0) return fail(LF_ERR_ARG, "null frequency or turns, or pairs < 0");
   // 1 / (2 pi) in 2^-192, 32 bits at a time from the lowest.
-  static const uint32_t kInverse[6] = {0x4f10e410u, 0x36d8a566u, 0x4d4d3770u, 0x7f09d5f4u, 0x9391054au, 0x28be60dbu};
+  static const uint32_t kInverse[6] = {0x4f10e410u, 0x36d8a566u, 0x7d4d3770u, 0x7f09d5f4u, 0x9391054au, 0x28be60dbu};
   for (int i = 0; i < pairs; ++i) {
     if (!std::isfinite(frequency[i]) || std::fabs(frequency[i]) > 1024.0)
       return fail(LF_ERR_ARG, "frequency %d must be finite and at most 1024 radians per position", i);

@@ -72,6 +72,17 @@ def test_turns_are_the_nearest_64_bit_fractions(lib):
         assert min(off, 2**64 - off) <= Fraction(1, 2) + Fraction(1, 1000), f
 
 
+def test_turns_are_the_nearest_where_two_are_almost_as_near(lib):
+    """Within 2^-24 of halfway between two of them the fourth word of 1 / (2 pi) decides.  192 bits of it, cut, are off by up
+    to 2^-192; times up to 2^10 radians in units of 2^-64 of a turn that is 2^-118."""
+    inverse = Fraction(one_over_two_pi(), 1 << 260)
+    assert lf.lf_rotary_turns([512.0000040903037]) == [8989679718594790752]
+    near = [512.0000040903037, 512.0, 1023.9999999999999, 1.0, 3e-5] + rotary_oracle.frequencies(128, 1e6).tolist()
+    for f, got in zip(near, lf.lf_rotary_turns(near)):
+        off = (Fraction(got) - Fraction(f) * inverse * 2**64) % 2**64
+        assert min(off, 2**64 - off) <= Fraction(1, 2) + Fraction(1, 2**100), f
+
+
 def test_bad_frequencies_are_refused(lib):
     for f in (float("nan"), float("inf"), 1025.0, -1e9):
         with pytest.raises(lf.LFError, match="frequency 1"):
