@@ -8,8 +8,9 @@
 // The angle.  fp32 holds w to 2^-24 of itself, which at position 100000 is 0.006 of a radian.  Only w modulo a
 // turn counts, so a frequency is kept as a 64-bit fraction of a turn per position, and its
 // product with the position modulo 2^64 IS the fraction of the turn: one integer multiplication, off by 2^-65
-// of a turn for each position.  Its nearest quarter is taken off as an integer too, and sincospif gets the rest,
-// at most an eighth of a turn, rounded to 2^-25 of itself.
+// of a turn for each position.  Its nearest quarter is taken off as an integer too, and sincospif gets the rest, at
+// most an eighth of a turn, all 64 bits of it rounded once to a float, by 2^-24 of itself: sines of small angles are as
+// exact as large ones, and opposite positions turn by opposite angles.
 //
 // Work.  Two 16-byte chunks of a row make an item, which one thread reads, turns and writes: those that turn with
 // each other where pairs are half a row apart, so that a tensor may be rotated in place.  Neighbouring lanes take neighbouring
@@ -91,10 +92,10 @@ __device__ __forceinline__ int find_sequence(const RotaryArgs& a, int t, int lan
 
 // Cosine and sine of a position's angle, given as turns per position (2^-64 of a turn).
 __device__ __forceinline__ float2 turn_of(uint64_t per_position, int64_t position) {
-  const uint32_t w = (uint32_t)((per_position * (uint64_t)position) >> 32);   // modulo a turn, in 2^-32
-  const uint32_t quarter = (w + 0x20000000u) >> 30;
+  const uint64_t w = per_position * (uint64_t)position;   // modulo a turn
+  const uint64_t quarter = (w + (1ull << 61)) >> 62;
   float s, c;
-  sincospif((float)(int32_t)(w - (quarter << 30)) * 0x1p-31f, &s, &c);
+  sincospif((float)(int64_t)(w - (quarter << 62)) * 0x1p-63f, &s, &c);
   if (quarter & 1) {
     const float x = c;
     c = -s;

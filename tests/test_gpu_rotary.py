@@ -403,3 +403,29 @@ def test_rotated_prompt_and_step_attend_by_relative_positions():
         rel = 2 * (2 * 2.0 ** -8) * dots + 2.0 ** -8
         assert (np.abs(got - want) <= (rel[..., None] + 2.0 ** -8) * size + 2.0 ** -8 * np.abs(want)).all()
     assert p.cache.check() == 0
+
+
+# ---- small angles, and calls that could go wrong unseen ---------------------------------------------
+
+def test_small_angles_keep_their_sines():
+    """(x, 0) becomes (x cos w, x sin w): the sine of a small angle to its own size.  The angle is rounded by 2^-24 of itself
+    and, its frequency being held in 2^-64 of a turn, off by 2^-65 x 2 pi / frequency of itself; sincospif by two units, at most
+    2^-23 each, of the sine; the product by 2^-24 of it.  Opposite positions turn by opposite angles, and turning back is
+    turning by the opposite position: the same bits."""
+    freq = [1e-9, 1.1547e-6, 3e-5, 1e-3, -2e-8, 4.7e-5, 1e-12, 0.01]
+    r = lf.LFRotary(16, inv_freq=freq)
+    pos = np.array([1, 3, -1, -3, 17, -500])
+    x = values("f32", len(pos), 1, 16)
+    x[..., 8:] = 0
+    y = r.rotate(x, ints(pos))
+    f = np.array(freq)
+    want = f64(x)[..., :8] * np.sin(pos[:, None, None] * f)
+    rel = 2.0 ** -24 + 2.0 ** -65 * 2 * math.pi / np.abs(f) + 2 * 2.0 ** -23 + 2.0 ** -24 + 2.0 ** -40
+    assert (np.abs(f64(y)[..., 8:] - want) <= rel * np.abs(want)).all()
+    mirror = r.rotate(x, ints(-pos))
+    assert torch.equal(mirror[..., :8], y[..., :8]) and torch.equal(mirror[..., 8:], -y[..., 8:])
+    x = values("f32", 400, 2, 128, seed=1)
+    r = lf.LFRotary(128, base=1e6)
+    far = ints(position_set(np.random.default_rng(3), 400))
+    far[4] = -2**31 + 1                    # (the least number has no opposite)
+    assert torch.equal(r.rotate(x, far, inverse=True), r.rotate(x, -far))
