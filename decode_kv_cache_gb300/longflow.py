@@ -581,8 +581,17 @@ def _rows(x, y) -> LFRows:
     return LFRows(x.data_ptr(), y.data_ptr(), shape[2], *sx[:3], *sy[:3])
 
 
+def _no_gradients(*tensors):
+    """A call on raw memory gives its result no graph: a gradient would be lost unseen."""
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors):
+        raise LFError(LF_ERR_ARG, "a tensor requires a gradient, which rotations do not record: call them under "
+                                  "torch.no_grad(), or in an autograd function whose backward turns back (inverse)")
+
+
 class LFRotary:
     """Rotary positions of a model's heads: its frequencies, kept on the device, and the calls that rotate by them.
+
+    Rotations record no gradients: tensors that require one are refused while gradients are recorded.
 
     The first ``rotary_dim`` columns of a row are ``rotary_dim / 2`` pairs, columns ``(i, i + rotary_dim / 2)``, or
     ``(2 i, 2 i + 1)`` if ``adjacent``.  Pair i turns by ``inv_freq[i]`` radians per position; without ``inv_freq`` by
@@ -664,7 +673,8 @@ class LFRotary:
         """lf_rotate: rows q [tokens][heads][dim] or [sequences][tokens][heads][dim], in any order in memory with
         contiguous rows, and of k where it is given, by positions int32 [tokens] ([sequences][tokens]), or
         [axes][...].  Returns q_out (a new tensor if None; q rotates in place), or (q_out, k_out) with k.
-        ``inverse`` turns back: the transpose, which takes a gradient of the result to that of the rows."""
+        ``inverse`` turns back: the transpose, which takes a gradient of the result to that of the rows (the call
+        itself records none)."""
         shape = self._expect(q, "q")
         if q_out is not None:
             self._expect(q_out, "q_out", q.dtype, shape)
@@ -678,6 +688,7 @@ class LFRotary:
         elif k_out is not None:
             raise LFError(LF_ERR_ARG, "k_out without k")
         step = self._positions(positions, shape[:-2])
+        _no_gradients(q, k, q_out, k_out)
         return _run_on(self.device, self._index, stream, lambda: self._held, self._rotate, q, positions, k, q_out, k_out, step,
                        1 if inverse else 0)
 
@@ -853,6 +864,7 @@ class LFPagedCache:
                 self._expect(q_out, "q_out", self.dtype, q.shape)
         elif q_out is not None:
             raise LFError(LF_ERR_ARG, "q_out without q")
+        _no_gradients(k_new, v_new, q, q_out)
         return self._run(stream, self._append_rotated, pages, batch, width, page_table, lens, k_new, v_new, new_start,
                          n, rotary, *rotary._held, positions, step, q_heads, q, q_out)
 

@@ -429,3 +429,36 @@ def test_small_angles_keep_their_sines():
     far = ints(position_set(np.random.default_rng(3), 400))
     far[4] = -2**31 + 1                    # (the least number has no opposite)
     assert torch.equal(r.rotate(x, far, inverse=True), r.rotate(x, -far))
+
+
+def test_gradients_are_refused_where_they_are_recorded():
+    """Refused where a gradient would be lost; under no_grad, and inside an autograd function, the call runs."""
+    r = lf.LFRotary(64)
+    x, pos = values("f32", 6, 4, 64).requires_grad_(), ints([5, 0, -7, 300, 1, 2])
+    plain = x.detach().clone()
+    for call in (lambda: r.rotate(x, pos), lambda: r.rotate(x * 2, pos), lambda: r.rotate(plain, pos, k=x),
+                 lambda: r.rotate(plain, pos, q_out=x)):
+        with pytest.raises(lf.LFError, match="gradient"):
+            call()
+    assert torch.equal(x, plain)
+    p = Paged("f32", 4, 64, 16, [3, 3], seed=8)
+    for kw in (dict(k_new=x), dict(v_new=x), dict(q=x), dict(q=plain, q_out=x)):
+        with pytest.raises(lf.LFError, match="gradient"):
+            p.cache.append_rotated(0, **{**dict(k_new=plain, v_new=plain, page_table=p.table, lens=p.t_lens, rotary=r,
+                                                new_start=ints([0, 3, 6])), **kw})
+
+    class Rotate(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, pos):
+            ctx.save_for_backward(pos)
+            return r.rotate(x, pos)
+
+        @staticmethod
+        def backward(ctx, g):
+            return r.rotate(g, *ctx.saved_tensors, inverse=True), None
+
+    g = values("f32", 6, 4, 64, seed=1)
+    y = Rotate.apply(x, pos)
+    y.backward(g)
+    with torch.no_grad():
+        assert torch.equal(y, r.rotate(x, pos)) and torch.equal(x.grad, r.rotate(g, pos, inverse=True))

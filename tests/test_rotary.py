@@ -181,6 +181,22 @@ def test_rotary_refuses_what_is_none():
             lf.LFRotary(**{"rotary_dim": 64, **kw})
 
 
+def test_gradients_are_not_lost_unseen():
+    """A result without a graph is refused where gradients are recorded, before anything runs."""
+    r = object.__new__(lf.LFRotary)          # (a CPU tensor's index; no GPU)
+    r._index, r.device, r.axes = -1, torch.device("cpu"), 1
+    x, pos = torch.randn(4, 2, 16), torch.zeros(4, dtype=torch.int32)
+    leaf = torch.randn(4, 2, 16, requires_grad=True)
+    for kw in (dict(q=leaf), dict(q=x, k=leaf), dict(q=x, q_out=leaf), dict(q=x, k=x, k_out=leaf), dict(q=leaf * 2)):
+        with pytest.raises(lf.LFError, match="gradient"):
+            r.rotate(positions=pos, **kw)
+    ran = []
+    r._lib = type("Lib", (), {"lf_rotate": staticmethod(lambda *a: ran.append(a) or 0)})
+    r._table = table()
+    r._rotate(0, leaf.detach(), pos, None, None, None, 0, 0)
+    assert len(ran) == 1
+
+
 def test_structs_match_the_header(tmp_path):
     import os
     import shutil
