@@ -588,6 +588,13 @@ def _no_gradients(*tensors):
                                   "torch.no_grad(), or in an autograd function whose backward turns back (inverse)")
 
 
+def _will_change(*tensors):
+    """A call writes to these tensors of the caller's: autograd, which may have saved one for a backward pass, has to know."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 class LFRotary:
     """Rotary positions of a model's heads: its frequencies, kept on the device, and the calls that rotate by them.
 
@@ -689,6 +696,7 @@ class LFRotary:
             raise LFError(LF_ERR_ARG, "k_out without k")
         step = self._positions(positions, shape[:-2])
         _no_gradients(q, k, q_out, k_out)
+        _will_change(q_out, k_out)
         return _run_on(self.device, self._index, stream, lambda: self._held, self._rotate, q, positions, k, q_out, k_out, step,
                        1 if inverse else 0)
 
@@ -806,6 +814,7 @@ class LFPagedCache:
             self._expect(out, "out", self.dtype, q.shape)
         if lse is not None:
             self._expect(lse, "lse", torch.float32, q.shape[:2])
+        _will_change(out, lse)
 
     def _run(self, stream, call, *args):
         """call(stream handle, *args) with this cache's device and `stream` current, so that
@@ -865,6 +874,7 @@ class LFPagedCache:
         elif q_out is not None:
             raise LFError(LF_ERR_ARG, "q_out without q")
         _no_gradients(k_new, v_new, q, q_out)
+        _will_change(q_out)
         return self._run(stream, self._append_rotated, pages, batch, width, page_table, lens, k_new, v_new, new_start,
                          n, rotary, *rotary._held, positions, step, q_heads, q, q_out)
 

@@ -462,3 +462,30 @@ def test_gradients_are_refused_where_they_are_recorded():
     y.backward(g)
     with torch.no_grad():
         assert torch.equal(y, r.rotate(x, pos)) and torch.equal(x.grad, r.rotate(g, pos, inverse=True))
+
+
+def test_what_autograd_has_saved_is_not_overwritten_unseen():
+    """Outputs that the caller gives count as changed in place, in every call that writes to them; new ones do not matter."""
+    p = Paged("bf16", 2, 128, 16, [20, 9], seed=10)
+    r, kn, q, pos = lf.LFRotary(128), p.randn(2, 2, 128), p.randn(2, 4, 128), ints([3, 4])
+    lse = torch.zeros(2, 4, device="cuda")
+    start, none = ints([0, 1, 2]), ints([0, 0])
+    for call in (lambda o: r.rotate(q, pos, q_out=o), lambda o: r.rotate(o, pos, q_out=o), lambda o: r.rotate(kn, pos, k=o, k_out=o),
+                 lambda o: p.cache.append_rotated(0, kn, kn, p.table, p.t_lens, r, q=q, q_out=o),
+                 lambda o: p.cache.decode(0, q, p.table, p.t_lens, out=o, lse=lse),
+                 lambda o: p.cache.decode_shared(0, q, p.table, p.t_lens, start, none, out=o, lse=lse),
+                 lambda o: p.cache.prompt(0, q, p.table, p.t_lens, start, 1, out=o, lse=lse)):
+        out, w, before = q.clone(), torch.ones((), device="cuda", dtype=q.dtype, requires_grad=True), lse._version
+        y = (w * out).sum()
+        call(out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    assert lse._version == before + 1
+    w, x = torch.ones((), device="cuda", dtype=q.dtype, requires_grad=True), q.clone()
+    y = (w * x).sum()
+    r.rotate(x, pos)
+    y.backward()
+    with torch.inference_mode():
+        x = q.clone()
+        assert r.rotate(x, pos, q_out=x) is x
+    assert p.cache.check() == 0

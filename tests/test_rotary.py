@@ -197,6 +197,23 @@ def test_gradients_are_not_lost_unseen():
     assert len(ran) == 1
 
 
+def test_outputs_that_autograd_has_saved_are_known_to_have_changed(monkeypatch):
+    """A tensor that is rotated in place after autograd saved it: backward says so instead of using what it holds now."""
+    r = object.__new__(lf.LFRotary)
+    r._index, r.device, r.axes = -1, torch.device("cpu"), 1
+    monkeypatch.setattr(lf, "_run_on", lambda *a: None)
+    pos = torch.zeros(4, dtype=torch.int32)
+    for kw in (lambda x: dict(q=x, q_out=x), lambda x: dict(q=torch.zeros(4, 2, 16), k=x, k_out=x)):
+        x, w = torch.randn(4, 2, 16), torch.ones((), requires_grad=True)
+        y = (w * x).sum()
+        r.rotate(positions=pos, **kw(x))
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    with torch.inference_mode():
+        x = torch.randn(4, 2, 16)
+        r.rotate(x, pos, q_out=x)
+
+
 def test_structs_match_the_header(tmp_path):
     import os
     import shutil
