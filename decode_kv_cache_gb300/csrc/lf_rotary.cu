@@ -32,6 +32,7 @@
 #include <cmath>
 
 #include "lf_kernels.h"
+#include "lf_overlap.h"
 #include "lf_paged.cuh"
 #include "lf_paged_host.h"
 #include "longflow.h"
@@ -378,6 +379,35 @@ int rows_to_turn(const lf_rows* rows, const char* name, int elem, RotaryRows* ou
   return LF_OK;
 }
 
+// What a call writes, and all that it reads: rows are read a few steps ahead of the writes (the ring), so that an output
+// may be its own input and otherwise shares no memory with what is read or written.  A layout whose rows lie in each
+// other in no order of strides, and would take long to tell apart, counts as one that does.
+int apart(const RotaryArgs& a, int seqs, int tokens, int64_t row_bytes) {
+  const RotaryRows* rows[2] = {&a.q, &a.k};
+  static const char* const names[2] = {"q", "k"};
+  auto in = [&](const RotaryRows& r) {
+    return RowSet{reinterpret_cast<uintptr_t>(r.x), {seqs, tokens, r.heads}, {r.xs, r.xt, r.xh}, row_bytes};
+  };
+  auto out = [&](const RotaryRows& r) {
+    return RowSet{reinterpret_cast<uintptr_t>(r.y), {seqs, tokens, r.heads}, {r.ys, r.yt, r.yh}, row_bytes};
+  };
+  for (int i = 0; i < 2; ++i) {
+    if (rows[i]->heads == 0) continue;
+    const RowSet y = out(*rows[i]);
+    if (rows_overlap_themselves(y) != Overlap::kNo)
+      return fail(LF_ERR_ARG, "%s: rows of y overlap one another", names[i]);
+    for (int j = 0; j < 2; ++j) {
+      if (rows[j]->heads == 0) continue;
+      const RowSet x = in(*rows[j]);
+      if (rows_overlap(y, x) != Overlap::kNo && !(i == j && same_rows(y, x)))
+        return fail(LF_ERR_ARG, "%s: y overlaps %s's x, and is not the same rows", names[i], names[j]);
+    }
+  }
+  if (a.k.heads > 0 && rows_overlap(out(a.q), out(a.k)) != Overlap::kNo)
+    return fail(LF_ERR_ARG, "k: y overlaps q's y");
+  return LF_OK;
+}
+
 // How many warps a token gets, or how many tokens a warp: enough warps to fill the GPU, and then, where a token has
 // few steps, several tokens that look things up together (17 slab prompts of 1000 fp32 tokens, two steps each: four
 // tokens 12.1 us, one 14.2; two video prompts of 6000, eight steps: two tokens 37.5, one 37.9).
@@ -458,6 +488,7 @@ int lf_rotate(const lf_rotary* rotary, int dtype, int row_dim, int seqs, int tok
   if (seqs == 0 || tokens == 0) return LF_OK;
   if ((rc = lf::rows_to_turn(q, "q", elem, &a.q)) != LF_OK || (rc = lf::rows_to_turn(k, "k", elem, &a.k)) != LF_OK) return rc;
   if (!positions) return fail(LF_ERR_ARG, "null positions");
+  if ((rc = lf::apart(a, seqs, tokens, (int64_t)row_dim * elem)) != LF_OK) return rc;
   a.inverse = inverse;
   a.tokens = (int64_t)seqs * tokens;
   a.tokens_per_seq = tokens;
@@ -497,6 +528,16 @@ int lf_paged_append_rotated(const lf_pages* pages, int batch, const int32_t* pag
   a.new_start = new_start;
   a.tokens = total_new;
   a.tokens_per_seq = total_new;
+  if (q) {
+    const uintptr_t y = reinterpret_cast<uintptr_t>(q_out);
+    const uint64_t y_bytes = (uint64_t)row * q_heads * total_new, k_bytes = (uint64_t)row * pages->kv_heads * total_new;
+    auto overlaps = [&](const void* x, uint64_t bytes) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(x);
+      return at < y + y_bytes && y < at + bytes;
+    };
+    if ((q != q_out && overlaps(q, y_bytes)) || overlaps(k_new, k_bytes) || overlaps(v_new, k_bytes))
+      return fail(LF_ERR_ARG, "q_out may be q, and overlaps neither a part of it nor k_new and v_new");
+  }
   if ((rc = lf::take_slices(&a, a.q.heads + 2 * a.k.heads)) != LF_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = pages->dtype == LF_BF16 ? lf::launch<__nv_bfloat16, true>(a, rotary->adjacent, st)

@@ -548,7 +548,8 @@ int lf_rotary_turns(const double* frequency, int pairs, uint64_t* turns);
 
 /* Rows to rotate: row (s, t, h) of row_dim columns starts at element s * x_seq + t * x_token + h * x_head of x and goes
  * to the same of y.  16-byte aligned, strides multiples of 16 bytes.  y may be x, with its strides; otherwise what is
- * written overlaps nothing that is read. */
+ * written overlaps nothing that is read, nor anything else that is written (refused, as are layouts that a few
+ * thousand steps do not tell apart). */
 typedef struct lf_rows {
   const void* x;
   void* y;
@@ -568,7 +569,8 @@ int lf_rotate(const lf_rotary* rotary, int dtype, int row_dim, int seqs, int tok
 
 /*
  * lf_paged_append with the rotation on the way: k_new's rows are rotated, v_new's are copied.  Queries of the
- * same tokens, q [total_new][q_heads][head_dim], are rotated into q_out (which may be q); both NULL: none.  Rows that belong
+ * same tokens, q [total_new][q_heads][head_dim], are rotated into q_out (which may be q, and overlaps neither a part of it
+ * nor k_new and v_new); both NULL: none.  Rows that belong
  * to no sequence are neither stored nor written to q_out.
  *   positions    device [axes][total_new], axis_stride elements from axis to axis (0: one set); NULL: each token's
  *                position in the cache, on every axis

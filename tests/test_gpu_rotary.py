@@ -489,3 +489,31 @@ def test_what_autograd_has_saved_is_not_overwritten_unseen():
         x = q.clone()
         assert r.rotate(x, pos, q_out=x) is x
     assert p.cache.check() == 0
+
+
+def test_views_of_one_tensor_in_place_and_side_by_side():
+    """Queries and keys of one wide projection, rotated in place and into the values' columns; outputs that overlap are refused."""
+    r, pos = lf.LFRotary(64), ints(np.arange(50) * 7)
+    wide = values("bf16", 50, 4 + 2 + 4 + 2, 64)
+    q, k, q2, k2 = wide[:, :4], wide[:, 4:6], wide[:, 6:10], wide[:, 10:]
+    want_q, want_k = r.rotate(q.contiguous(), pos, k=k.contiguous())
+    r.rotate(q, pos, k=k, q_out=q2, k_out=k2)
+    assert torch.equal(q2, want_q) and torch.equal(k2, want_k)
+    r.rotate(q, pos, k=k, q_out=q, k_out=k)
+    assert torch.equal(q, want_q) and torch.equal(k, want_k)
+    keep = wide.clone()
+    one = torch.empty(1, 4, 64, dtype=torch.bfloat16, device="cuda").expand(50, 4, 64)
+    rolling = torch.empty(53 * 64, dtype=torch.bfloat16, device="cuda").as_strided((50, 4, 64), (64, 64, 1))
+    for args, kw, msg in [((q, pos), dict(q_out=one), "rows of y overlap"), ((q, pos), dict(q_out=rolling), "rows of y overlap"),
+                          ((q, pos), dict(q_out=wide[:, 1:5]), "q's x"), ((q[1:], pos[1:].contiguous()), dict(q_out=q[:-1]), "q's x"),
+                          ((q, pos), dict(k=k, k_out=q[:, 1:3]), "q's x"), ((q, pos), dict(k=k, q_out=wide[:, 2:6], k_out=k), "q's x"),
+                          ((q, pos), dict(k=k, q_out=q2, k_out=q2[:, :2]), "q's y"), ((q, pos), dict(k=k, q_out=wide[:, 5:9], k_out=k2), "k's x")]:
+        with pytest.raises(lf.LFError, match=msg):
+            r.rotate(*args, **kw)
+    p = Paged("bf16", 2, 128, 16, [30, 9], seed=11)
+    flat = p.randn(40, 4, 128)
+    with pytest.raises(lf.LFError, match="q_out may be q"):
+        p.cache.append_rotated(0, p.randn(30, 2, 128), p.randn(30, 2, 128), p.table, p.t_lens, lf.LFRotary(128), ints([0, 25, 30]),
+                               q=flat[:30], q_out=flat[1:31])
+    torch.cuda.synchronize()
+    assert torch.equal(wide, keep)

@@ -170,6 +170,94 @@ def test_bad_rotated_appends_are_refused(lib):
     assert append(lib, table(), total=0) == lf.LF_OK
 
 
+def test_outputs_that_overlap_are_refused(lib):
+    """Rows are read ahead of the writes: an output is its own input's rows or lies apart from everything."""
+    for kw, msg in [(dict(y_head=0), "rows of y overlap"), (dict(y_token=0), "rows of y overlap"), (dict(y_token=896), "rows of y overlap"),
+                    (dict(y_head=64), "rows of y overlap"), (dict(x_token=0, y_token=0, y=A), "rows of y overlap"),
+                    (dict(y=A + 16), "q's x"), (dict(y=A - 256), "q's x"), (dict(y=A + 256), "q's x"), (dict(y=A + 3 * 2048 + 1792), "q's x"),
+                    (dict(y=A, y_token=2048), "q's x"), (dict(y=A + 2048, x_token=2048, y_token=2048, y_head=136), "q's x")]:
+        assert rotate(lib, table(), q=rows(**kw)) == lf.LF_ERR_ARG, kw
+        assert msg in lf.lf_last_error(), (kw, lf.lf_last_error())
+    # in place, in sequences of more columns; keys in the queries' place, and keys' output in the queries'
+    assert rotate(lib, table(), q=rows(y=A), k=rows(x=C, y=C + 2 * 2048)) == lf.LF_ERR_ARG and "k's x" in lf.lf_last_error()
+    assert rotate(lib, table(), q=rows(y=A), k=rows(x=C, y=A + 2 * 2048)) == lf.LF_ERR_ARG and "q's x" in lf.lf_last_error()
+    assert rotate(lib, table(), q=rows(), k=rows(x=C, y=B + 2048)) == lf.LF_ERR_ARG and "k: y overlaps q's y" in lf.lf_last_error()
+    assert rotate(lib, table(), q=rows(y=C), k=rows(x=C + 4 * 2048 - 256, y=D)) == lf.LF_ERR_ARG and "k's x" in lf.lf_last_error()
+    # seven tokens of 32 heads of 256 bytes, 8 of keys
+    for kw in (dict(out=A + 16), dict(out=A + 7 * 32 * 256 - 16), dict(out=A - 7 * 32 * 256 + 16), dict(q=A, out=E), dict(q=A, k=D, out=D + 7 * 8 * 256 - 16),
+               dict(q=A, v=C, out=C + 16)):
+        assert append(lib, table(), **kw) == lf.LF_ERR_ARG, kw
+        assert "q_out may be q" in lf.lf_last_error(), kw
+
+
+OVERLAP = r"""
+#include <cstdio>
+#include "lf_overlap.h"
+using namespace lf;
+int main() {
+  RowSet a, b;
+  long long v[14];
+  for (;;) {
+    for (int i = 0; i < 14; ++i)
+      if (scanf("%lld", v + i) != 1) return 0;
+    a = RowSet{(uintptr_t)v[0], {v[1], v[2], v[3]}, {v[4], v[5], v[6]}, 2};
+    b = RowSet{(uintptr_t)v[7], {v[8], v[9], v[10]}, {v[11], v[12], v[13]}, 2};
+    printf("%d %d %d\n", (int)rows_overlap_themselves(a), (int)rows_overlap(a, b), (int)same_rows(a, b));
+  }
+}
+"""
+
+
+def test_overlaps_are_found_as_by_looking_at_every_byte(tmp_path):
+    """Every answer against the bytes that the rows have, over small layouts of all kinds; large ones that are views of a
+    tensor are told apart, and sizes times strides past 64 bits do no harm."""
+    import os
+    import random
+    import shutil
+    import subprocess
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no C++ compiler")
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "decode_kv_cache_gb300", "csrc")
+    src = tmp_path / "overlap.cpp"
+    src.write_text(OVERLAP)
+    subprocess.run([gxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-I", csrc, str(src), "-o", str(tmp_path / "x")], check=True)
+    rng, cases, want = random.Random(1), [], []
+
+    def row_starts(at, n, st):
+        return [at + i * st[0] + j * st[1] + k * st[2] for i in range(n[0]) for j in range(n[1]) for k in range(n[2])]
+
+    for _ in range(6000):
+        def layout(like=None):
+            n = [rng.choice((1, 1, 2, 3, 4)) for _ in range(3)]
+            if like and rng.random() < 0.6:
+                return rng.randrange(200, 260), (like[1] if rng.random() < 0.5 else n), like[2]
+            st = [rng.choice((0, 1, 2, 3, 4, 6, 8, 12, 16, 24, 48)) for _ in range(3)]
+            return rng.randrange(200, 260), n, st
+        a = layout()
+        b = layout(a)
+        if rng.random() < 0.2:
+            b = (a[0], *b[1:])
+        own = [x for s in row_starts(*a) for x in (s, s + 1)]
+        other = {x for s in row_starts(*b) for x in (s, s + 1)}
+        cases.append((a, b))
+        want.append((len(own) != len(set(own)), bool(other.intersection(own)),
+                     a[0] == b[0] and a[1] == b[1] and all(n == 1 or x == y for n, x, y in zip(a[1], a[2], b[2]))))
+    big = 2**31 - 1
+    views = [((10**9, [3, 70000, 32], [70000 * 96, 96, 2]), (10**9 + 64, [3, 70000, 8], [70000 * 96, 96, 2]), (0, 0, 0)),    # of one wide row
+             ((10**9, [3, 70000, 32], [70000 * 96, 96, 2]), (10**9 + 62, [3, 70000, 8], [70000 * 96, 96, 2]), (0, 1, 0)),
+             ((10**9, [8, 5000, 4], [40000, 2, 10000]), (10**9, [8, 5000, 4], [40000, 2, 10000]), (0, 1, 1)),                # a slab
+             ((10**9, [1, big, 65535], [0, 2**44, 2]), (10**9 + 2**20, [1, big, 65535], [0, 2**44, 2]), (0, 0, 0)),
+             ((10**9, [big, 1, 1], [2**44, 0, 0]), (10**9 + 2**44 * 1000 + 1, [big, 1, 1], [2**44, 0, 0]), (0, 1, 0))]
+    for a, b, w in views:
+        cases.append((a, b))
+        want.append(w)
+    text = "\n".join(" ".join(str(x) for s in c for x in (s[0], *s[1], *s[2])) for c in cases)
+    got = subprocess.run([str(tmp_path / "x")], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
+    for c, w, g in zip(cases, want, got):
+        assert tuple(int(x) for x in w) == tuple(int(x) for x in g.split()), (c, w, g)
+
+
 def test_rotary_refuses_what_is_none():
     for kw, msg in [(dict(rotary_dim=24), "multiple of 16"), (dict(rotary_dim=64.0), "multiple of 16"), (dict(rotary_dim=528), "multiple of 16"),
                     (dict(base=0), "base"), (dict(sections=[16, 15]), "sum to 32"), (dict(sections=[8, 8, 8, 4, 4]), "sections"),
