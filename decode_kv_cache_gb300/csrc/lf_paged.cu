@@ -303,7 +303,7 @@ int decode_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int wi
 struct SharedShape {
   DecodeShape rest;
   lf::SharedPlan plan;
-  size_t off_rest_o, off_rest_ml, off_part_o, off_part_ml, off_segments, off_first, off_ranges, bytes;
+  size_t off_rest_o, off_rest_ml, off_part_o, off_part_ml, off_segments, off_first, off_ranges, off_seen, bytes;
 };
 
 int shared_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int groups, SharedShape* s) {
@@ -322,7 +322,9 @@ int shared_shape(const lf_pages* p, const lf::PagedPool& pool, int group, int gr
   s->off_segments = s->off_part_ml + up((size_t)s->plan.part_rows * 2 * 4);
   s->off_first = s->off_segments + up((size_t)groups * 4);
   s->off_ranges = s->off_first + up((size_t)groups * 8);
-  s->bytes = s->off_ranges + up(3 * 4);
+  s->off_seen = s->off_ranges + up(3 * 4);
+  const size_t sets = groups > s->plan.table ? 1 : s->plan.kernel == lf::PromptPlan::kTensor ? s->rest.grid : 0;
+  s->bytes = s->off_seen + up(sets * groups * 4);
   return LF_OK;
 }
 
@@ -488,13 +490,15 @@ int lf_paged_decode_shared(const lf_pages* pages, int batch, const int32_t* page
   a.first_row = reinterpret_cast<int64_t*>(w + shape.off_first);
   a.ranges = reinterpret_cast<int32_t*>(w + shape.off_ranges);
   a.slot_rows = shape.plan.slot_rows;
+  a.seen = reinterpret_cast<int32_t*>(w + shape.off_seen);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int e = elem_bytes(pages);
   const int ctas = shape.rest.grid;
-  cudaError_t err;
-  if (shape.plan.kernel == lf::PromptPlan::kTensor) {
+  cudaError_t err = cudaSuccess;
+  if (groups > shape.plan.table) err = lf::paged_shared_seen_launch(a, st);
+  if (err == cudaSuccess && shape.plan.kernel == lf::PromptPlan::kTensor) {
     err = lf::paged_shared_tc_launch(a, d, pages->head_dim, ctas, st);
-  } else {
+  } else if (err == cudaSuccess) {
     err = lf::paged_decode_launch(d, e, pages->head_dim, ctas, st);
     if (err == cudaSuccess) err = lf::paged_shared_launch(a, shape.plan, pages->head_dim, st);
   }

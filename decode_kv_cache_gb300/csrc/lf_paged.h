@@ -102,6 +102,7 @@ struct PagedSharedArgs {
   int64_t* first_row;         // [groups]
   int32_t* ranges;            // [3]
   int slot_rows;
+  int32_t* seen;              // what a group's members see of its prefix: [groups], or, ranges of few groups, [CTAs][groups]
 };
 
 // Its kernel by type, heads and pages, and the rows of a piece.
@@ -109,8 +110,10 @@ struct SharedPlan {
   PromptPlan::Kernel kernel;
   int rows, keys, slots, rounds, least, slot_rows;
   int64_t grid, part_rows;
+  int table;                  // groups that the kernel looks at in its own memory; of more another launch comes ahead
   bool fits;                  // the kernels' numbers hold such a call
 };
+constexpr int kTableTensor = 2048, kTableOther = 512;
 SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int group, int groups, int sms);
 
 // Occupied tokens of sequence b, kept inside its row of the page table.
@@ -171,6 +174,9 @@ cudaError_t paged_prompt_launch(const PagedPromptArgs& a, const PromptPlan& plan
 bool paged_prompt_tc_takes(const PagedPool& pool, int head_dim);
 cudaError_t paged_prompt_tc_launch(const PagedPromptArgs& a, const PromptPlan& plan, int head_dim,
                                    cudaStream_t stream);
+
+// What the members of each group see of its prefix, to a.seen.
+cudaError_t paged_shared_seen_launch(const PagedSharedArgs& a, cudaStream_t stream);
 
 // A decode call behind prefixes, and the join of its shares; `ctas`: those that the rest's walk may have had.  On the
 // tensor cores prefixes and rest are one launch of `ctas` CTAs.  Otherwise the prefixes follow the rest's launch, placed while

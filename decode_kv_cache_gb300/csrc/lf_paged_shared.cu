@@ -27,7 +27,7 @@ struct Block {
   Segment s;
 
   template <int kThreads>
-  __device__ __forceinline__ bool take(const PagedSharedArgs& a);
+  __device__ __forceinline__ bool take(const PagedSharedArgs& a, void* smem);
   __device__ __forceinline__ int count() const { return s.last - s.first; }
   __device__ __forceinline__ int at(int j) const { return s.first + j; }
   __device__ __forceinline__ bool live(const PagedSharedArgs& a, int r) const { return r < s.members * a.group; }
@@ -52,9 +52,12 @@ struct Block {
 
 constexpr int kKeys = 64;
 
+// The groups that a block looks at together lie where its tiles will.
+using Families = FamilyTable<kTableOther>;
+
 template <int kThreads>
-__device__ __forceinline__ bool Block::take(const PagedSharedArgs& a) {
-  const bool ok = take_segment<kThreads>(a, kKeys, &s);
+__device__ __forceinline__ bool Block::take(const PagedSharedArgs& a, void* smem) {
+  const bool ok = take_segment<kThreads>(a, kKeys, *static_cast<Families*>(smem), &s);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!ok) finish();
   return ok;
@@ -80,7 +83,8 @@ __global__ void __launch_bounds__(kMmaThreads, D == 128 ? 3 : D >= 32 ? 4 : 5) p
   __shared__ int64_t s_off[2][kKeys];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Block block;
-  if (!block.take<kMmaThreads>(a)) return;
+  static_assert(sizeof(Families) <= 4 * kTileBytes, "the groups fit where the tiles will lie");
+  if (!block.take<kMmaThreads>(a, smem)) return;
   const int nt = block.count();
   const uint32_t ring = smem_u32(smem);
 
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(16 * R / M, D <= 64 ? 4 : 1) paged_shared_fma_
   __shared__ int64_t s_off[kKeys];
   const int tid = threadIdx.x;
   Block block;
-  if (!block.take<kThreads>(a)) return;
+  if (!block.take<kThreads>(a, sm)) return;
   const int nt = block.count();
 
   auto look_up = [&](int j) {
@@ -482,9 +486,31 @@ cudaError_t launch_mma(const PagedSharedArgs& a, int64_t grid, cudaStream_t stre
 template <int D, int R, int M>
 cudaError_t launch_fma(const PagedSharedArgs& a, int64_t grid, cudaStream_t stream) {
   constexpr int kThreads = 16 * R / M;
+  static_assert(sizeof(Families) <= fma_smem<D, R>(), "the groups fit where the tiles will lie");
   static std::atomic<uint64_t> done{0};
   return launch(reinterpret_cast<const void*>(&paged_shared_fma_kernel<D, R, M>), a, grid, kThreads,
                 fma_smem<D, R>(), done, stream);
+}
+
+// ---- many groups ---------------------------------------------------------------------
+//
+// What the members of each group see of its prefix, a warp for each group, where the groups are more than the kernels' own
+// tables hold.  Bound by its launch.
+
+constexpr int kSeenWarps = 8;
+
+__global__ void __launch_bounds__(kSeenWarps * 32) paged_shared_seen_kernel(const __grid_constant__ PagedSharedArgs a) {
+  const int lane = threadIdx.x & 31, i = blockIdx.x * kSeenWarps + (threadIdx.x >> 5);
+  if (i >= a.groups) return;
+  const int start = a.group_start[i], end = a.group_start[i + 1];
+  int most = 0;
+  if (start >= 0 && end > start && end <= a.pool.batch) {
+    for (int b = start + lane; b < end; b += 32)
+      most = max(most, shared_len(a.prefix_lens[b], paged_len(a.pool, b), a.fresh != 0));
+    most = __reduce_max_sync(0xffffffffu, most);
+    most = min(most, max(a.prefix_lens[start], 0));
+  }
+  if (lane == 0) a.seen[i] = most;
 }
 
 // ---- the join --------------------------------------------------------------------------
@@ -700,12 +726,19 @@ cudaError_t join_dim(const PagedSharedArgs& a, const PagedDecodeArgs& rest, int 
 
 }  // namespace
 
+cudaError_t paged_shared_seen_launch(const PagedSharedArgs& a, cudaStream_t stream) {
+  paged_shared_seen_kernel<<<(a.groups + kSeenWarps - 1) / kSeenWarps, kSeenWarps * 32, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
 SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int group, int groups, int sms) {
   SharedPlan p;
   p.keys = kKeys;
   p.least = 1;
+  p.table = kTableOther;
   if (elem == 2 && paged_prompt_tc_takes(pool, head_dim)) {
     p.kernel = PromptPlan::kTensor;
+    p.table = kTableTensor;
     p.rows = 256;
     p.keys = 128;
     p.slots = sms;

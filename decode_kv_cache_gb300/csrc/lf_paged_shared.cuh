@@ -14,28 +14,75 @@ struct Segment {
   int64_t row;               // of part_o
 };
 
-// What a group asks for: `pieces` pieces of `tiles` key tiles, of each KV head.
+// What a group asks for: `pieces` pieces of `tiles` key tiles, of each KV head.  Its prefix ends where its members' do: what
+// prefix_lens holds behind their lengths, or in padded rows, costs nothing (32 sequences behind 8192 and 32 empty groups whose
+// prefixes of 60000 are left from another step: 35 us, with those tiles planned for 847).
 struct Family {
   int start, members, prefix, tiles, pieces;
   bool right;
 };
 
-__device__ __forceinline__ Family family_of(const PagedSharedArgs& a, int i, int keys) {
+__device__ __forceinline__ Family family_from(const PagedSharedArgs& a, int start, int end, int prefix, int keys) {
   Family f;
-  f.start = a.group_start[i];
-  const int end = a.group_start[i + 1];
-  f.right = f.start >= 0 && end >= f.start && end <= a.pool.batch;
-  f.members = f.right ? end - f.start : 0;
+  f.start = start;
+  f.right = start >= 0 && end >= start && end <= a.pool.batch;
+  f.members = f.right ? end - start : 0;
   f.prefix = f.tiles = f.pieces = 0;
   if (f.members > 0) {
-    const int64_t most = (int64_t)a.pool.max_pages * a.pool.page_size;
-    f.prefix = (int)min((int64_t)max(a.prefix_lens[f.start], 0), most);
-    f.tiles = (f.prefix + keys - 1) / keys;
+    f.prefix = prefix;
+    f.tiles = (prefix + keys - 1) / keys;
     const int each = a.rows / a.group;
     f.pieces = (f.members + each - 1) / each;
   }
   return f;
 }
+
+// The groups of a call, kept in shared memory where there are up to kN: where they start, the prefix of their first sequence,
+// the most that a member sees of its own.  Of more groups a launch ahead has written what they see to a.seen.
+template <int kN>
+struct FamilyTable {
+  int start[kN + 1], lead[kN], most[kN];
+
+  // For the whole block together.
+  template <int kThreads>
+  __device__ __forceinline__ void fill(const PagedSharedArgs& a) {
+    const int tid = threadIdx.x, n = a.groups, batch = a.pool.batch;
+    if (n > kN) return;
+    const int64_t room = (int64_t)a.pool.max_pages * a.pool.page_size;
+    // (on their way together with the starts)
+    const int own_prefix = tid < batch ? a.prefix_lens[tid] : 0, own_len = tid < batch ? a.pool.lens[tid] : 0;
+    // (no loop of the plan is unrolled: code that runs once costs what it takes to fetch)
+#pragma unroll 1
+    for (int i = tid; i <= n; i += kThreads) {
+      start[i] = a.group_start[i];
+      if (i < n) lead[i] = most[i] = 0;
+    }
+    __syncthreads();
+    const int to = min(start[n], batch);
+#pragma unroll 1
+    for (int b = min(max(start[0], 0), batch) + tid; b < to; b += kThreads) {
+      int lo = 0, hi = n;   // the last group that starts at or before b
+#pragma unroll 1
+      while (lo + 1 < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= b) lo = mid;
+        else hi = mid;
+      }
+      const int first = start[lo], end = start[lo + 1];
+      if (first < 0 || b < first || b >= end || end > batch) continue;   // of no group
+      const int prefix = b == tid ? own_prefix : a.prefix_lens[b], len = b == tid ? own_len : a.pool.lens[b];
+      if (b == first) lead[lo] = (int)min((int64_t)max(prefix, 0), room);
+      const int mine = shared_len(prefix, (int)min((int64_t)max(len, 0), room), a.fresh != 0);
+      if (mine > 0) atomicMax(&most[lo], mine);
+    }
+    __syncthreads();
+  }
+
+  __device__ __forceinline__ Family at(const PagedSharedArgs& a, int i, int keys) const {
+    if (a.groups > kN) return family_from(a, a.group_start[i], a.group_start[i + 1], a.seen[i], keys);
+    return family_from(a, start[i], start[i + 1], min(lead[i], most[i]), keys);
+  }
+};
 
 // The last position that sequence b of a segment sees of its group's prefix, -1: none.
 __device__ __forceinline__ int last_seen(const PagedSharedArgs& a, int prefix, int b) {
@@ -63,182 +110,146 @@ __device__ __forceinline__ int segment_tiles(int slots, int rounds, int least, i
   return best;
 }
 
-// The segments of all groups, numbered group by group, piece by piece, head by head.  Every block goes through
-// the groups itself: a launch that did so for all would be one more to wait for.  Calls are for the whole block
-// together; a thread has a run of the groups.
-template <int kThreads>
-struct SegmentList {
-  static constexpr int kW = kThreads / 32;
-  int from, to, chunk;
-  int64_t seg, seg_to, row;   // segments before this thread's groups and with them, rows of part_o before them
-  int64_t segments;
+// Segment number blockIdx.x, where each block takes one; false: there is none.  The segments of all groups are numbered group
+// by group, piece by piece, head by head.  Every block goes through the groups itself: a launch that did so for all would be
+// one more to wait for.  Block 0 tells the join.  For the whole block together.
+template <int kThreads, int kN>
+__device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys, FamilyTable<kN>& table, Segment* out) {
+  constexpr int kW = kThreads / 32;
+  __shared__ int64_t s_all[2][kW], s_sum[2][kW];
+  __shared__ int s_max[kW], s_lo[kW], s_hi[kW];
+  __shared__ Segment s_seg;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int H = a.pool.kv_heads, id = blockIdx.x;
+  table.template fill<kThreads>(a);
+  const int per = (a.groups + kThreads - 1) / kThreads;
+  const int from = min(tid * per, a.groups), to = min(from + per, a.groups);   // this thread's groups
 
-  // Units, tiles and the longest unit's tiles of all groups, and the sum of every thread's `more`.
-  __device__ __forceinline__ void sum(const PagedSharedArgs& a, int keys, int64_t* units, int64_t* tiles, int* longest,
-                                      int64_t* more) {
-    __shared__ int64_t s_sum[3][kW];
-    __shared__ int s_max[kW];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.groups + kThreads - 1) / kThreads;
-    from = min(tid * per, a.groups);
-    to = min(from + per, a.groups);
-    int64_t u = 0, t = 0, x = *more;
-    int most = 0;
-    for (int i = from; i < to; ++i) {
-      const Family f = family_of(a, i, keys);
-      if (f.tiles > 0) {
-        u += (int64_t)f.pieces * a.pool.kv_heads;
-        t += (int64_t)f.pieces * a.pool.kv_heads * f.tiles;
-        most = max(most, f.tiles);
-      }
-      if (!f.right && blockIdx.x == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+  // Units, tiles and the longest unit's tiles of all groups.
+  int64_t units = 0, tiles = 0;
+  int longest = 0;
+#pragma unroll 1
+  for (int i = from; i < to; ++i) {
+    const Family f = table.at(a, i, keys);
+    if (f.tiles > 0) {
+      units += (int64_t)f.pieces * H;
+      tiles += (int64_t)f.pieces * H * f.tiles;
+      longest = max(longest, f.tiles);
     }
+    if (!f.right && blockIdx.x == 0 && a.pool.err) atomicOr(a.pool.err, LF_DEVERR_STATE);
+  }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      u += __shfl_xor_sync(0xffffffffu, u, o);
-      t += __shfl_xor_sync(0xffffffffu, t, o);
-      x += __shfl_xor_sync(0xffffffffu, x, o);
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) {
-      s_sum[0][warp] = u;
-      s_sum[1][warp] = t;
-      s_sum[2][warp] = x;
-      s_max[warp] = most;
-    }
-    __syncthreads();
-    *units = *tiles = *more = 0;
-    *longest = 0;
-    for (int w = 0; w < kW; ++w) {
-      *units += s_sum[0][w];
-      *tiles += s_sum[1][w];
-      *more += s_sum[2][w];
-      *longest = max(*longest, s_max[w]);
-    }
+  for (int o = 16; o > 0; o >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
   }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 0) {
+    s_all[0][warp] = units;
+    s_all[1][warp] = tiles;
+    s_max[warp] = longest;
+  }
+  if (tid == 0) s_seg.members = 0;
+  __syncthreads();
+  units = tiles = 0;
+  longest = 0;
+#pragma unroll 1
+  for (int w = 0; w < kW; ++w) {
+    units += s_all[0][w];
+    tiles += s_all[1][w];
+    longest = max(longest, s_max[w]);
+  }
+  const int chunk = units > 0 ? segment_tiles(a.slots, a.rounds, a.least, units, tiles, longest) : 1;
 
-  __device__ __forceinline__ int cuts(const Family& f) const { return (f.tiles + chunk - 1) / chunk; }
-
-  // Cut into segments of up to `tiles` tiles; block 0 tells the join.
-  __device__ __forceinline__ void cut(const PagedSharedArgs& a, int keys, int tiles) {
-    __shared__ int64_t s_sum[2][kW];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    chunk = tiles;
-    int64_t n = 0, r = 0;
-    for (int i = from; i < to; ++i) {
-      const Family f = family_of(a, i, keys);
-      n += (int64_t)f.pieces * a.pool.kv_heads * cuts(f);
-      r += (int64_t)f.members * a.q_heads * cuts(f);
-    }
-    seg_to = n;
-    row = r;
+  // Segments and their rows of part_o in front of each thread's groups.
+  auto cuts = [&](const Family& f) { return (f.tiles + chunk - 1) / chunk; };
+  int64_t own_seg = 0, own_row = 0;
+#pragma unroll 1
+  for (int i = from; i < to; ++i) {
+    const Family f = table.at(a, i, keys);
+    own_seg += (int64_t)f.pieces * H * cuts(f);
+    own_row += (int64_t)f.members * a.q_heads * cuts(f);
+  }
+  int64_t seg = own_seg, row = own_row;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, seg_to, o), y = __shfl_up_sync(0xffffffffu, row, o);
-      if (lane >= o) {
-        seg_to += x;
-        row += y;
-      }
-    }
-    if (lane == 31) {
-      s_sum[0][warp] = seg_to;
-      s_sum[1][warp] = row;
-    }
-    __syncthreads();
-    segments = 0;
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) {
-        seg_to += s_sum[0][w];
-        row += s_sum[1][w];
-      }
-      segments += s_sum[0][w];
-    }
-    seg = seg_to - n;
-    row -= r;
-    if (blockIdx.x == 0) {
-      int64_t at = row;
-      for (int i = from; i < to; ++i) {
-        const Family f = family_of(a, i, keys);
-        a.segments[i] = cuts(f);
-        a.first_row[i] = at;
-        at += (int64_t)f.members * a.q_heads * cuts(f);
-      }
-      if (threadIdx.x == 0) a.ranges[0] = 0;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, seg, o), y = __shfl_up_sync(0xffffffffu, row, o);
+    if (lane >= o) {
+      seg += x;
+      row += y;
     }
   }
-
-  // Segment number `id`; false: there is none.
-  __device__ __forceinline__ bool find(const PagedSharedArgs& a, int keys, int64_t id, Segment* out) const {
-    __shared__ Segment s_seg;
-    __shared__ int s_lo[kW], s_hi[kW];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int H = a.pool.kv_heads;
-    if (tid == 0) s_seg.members = 0;
-    __syncthreads();
-    if (id >= seg && id < seg_to) {
-      int64_t before = seg, r = row;
-      for (int i = from; i < to; ++i) {
-        const Family f = family_of(a, i, keys);
-        const int n = cuts(f);
-        const int64_t mine = (int64_t)f.pieces * H * n;
-        if (id >= before && id < before + mine) {
-          const int64_t unit = (id - before) / n;
-          const int j = (int)(id - before - unit * n), piece = (int)(unit / H), each = a.rows / a.group;
-          Segment s;
-          s.g = (int)(unit - (int64_t)piece * H);
-          s.b0 = f.start + piece * each;
-          s.members = min(each, f.members - piece * each);
-          s.leader = f.start;
-          s.first = (int)((int64_t)f.tiles * j / n);
-          s.last = (int)((int64_t)f.tiles * (j + 1) / n);
-          s.prefix = f.prefix;
-          s.p_lo = s.p_hi = -1;
-          s.row = r + (int64_t)piece * each * a.q_heads * n + ((int64_t)s.g * n + j) * s.members * a.group;
-          s_seg = s;
-        }
-        before += mine;
-        r += (int64_t)f.members * a.q_heads * n;
-      }
-    }
-    __syncthreads();
-    Segment s = s_seg;
-    // What its sequences see of the prefix.
-    int lo = INT_MAX, hi = -1;
-    for (int i = tid; i < s.members; i += kThreads) {
-      const int p = last_seen(a, s.prefix, s.b0 + i);
-      lo = min(lo, p);
-      hi = max(hi, p);
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-      s_lo[warp] = lo;
-      s_hi[warp] = hi;
-    }
-    __syncthreads();
-    // (Starts that decrease may ask for more than there is room for.)
-    if (s.members == 0 || s.row + (int64_t)s.members * a.group > a.part_rows) return false;
-    s.p_lo = s_lo[0];
-    s.p_hi = s_hi[0];
-    for (int w = 1; w < kW; ++w) {
-      s.p_lo = min(s.p_lo, s_lo[w]);
-      s.p_hi = max(s.p_hi, s_hi[w]);
-    }
-    s.last = max(s.first, min(s.last, s.p_hi < 0 ? 0 : s.p_hi / keys + 1));
-    *out = s;
-    return true;
+  if (lane == 31) {
+    s_sum[0][warp] = seg;
+    s_sum[1][warp] = row;
   }
-};
-
-// Segment number blockIdx.x, where each block takes one; false: there is none.
-template <int kThreads>
-__device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys, Segment* out) {
-  SegmentList<kThreads> list;
-  int64_t units, tiles, none = 0;
-  int longest;
-  list.sum(a, keys, &units, &tiles, &longest, &none);
-  list.cut(a, keys, units > 0 ? segment_tiles(a.slots, a.rounds, a.least, units, tiles, longest) : 1);
-  return blockIdx.x < list.segments && list.find(a, keys, blockIdx.x, out);
+  __syncthreads();
+  seg -= own_seg;
+  row -= own_row;
+#pragma unroll 1
+  for (int w = 0; w < warp; ++w) {
+    seg += s_sum[0][w];
+    row += s_sum[1][w];
+  }
+  if (id == 0 || (id >= seg && id < seg + own_seg)) {
+#pragma unroll 1
+    for (int i = from; i < to; ++i) {
+      const Family f = table.at(a, i, keys);
+      const int n = cuts(f);
+      const int64_t mine = (int64_t)f.pieces * H * n;
+      if (id >= seg && id < seg + mine) {
+        const int64_t unit = (id - seg) / n;
+        const int j = (int)(id - seg - unit * n), piece = (int)(unit / H), each = a.rows / a.group;
+        Segment s;
+        s.g = (int)(unit - (int64_t)piece * H);
+        s.b0 = f.start + piece * each;
+        s.members = min(each, f.members - piece * each);
+        s.leader = f.start;
+        s.first = (int)((int64_t)f.tiles * j / n);
+        s.last = (int)((int64_t)f.tiles * (j + 1) / n);
+        s.prefix = f.prefix;
+        s.p_lo = s.p_hi = -1;
+        s.row = row + (int64_t)piece * each * a.q_heads * n + ((int64_t)s.g * n + j) * s.members * a.group;
+        s_seg = s;
+      }
+      if (id == 0) {
+        a.segments[i] = n;
+        a.first_row[i] = row;
+      }
+      seg += mine;
+      row += (int64_t)f.members * a.q_heads * n;
+    }
+  }
+  if (id == 0 && tid == 0) a.ranges[0] = 0;
+  __syncthreads();
+  Segment s = s_seg;
+  // What its sequences see of the prefix.
+  int lo = INT_MAX, hi = -1;
+#pragma unroll 1
+  for (int i = tid; i < s.members; i += kThreads) {
+    const int p = last_seen(a, s.prefix, s.b0 + i);
+    lo = min(lo, p);
+    hi = max(hi, p);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    s_lo[warp] = lo;
+    s_hi[warp] = hi;
+  }
+  __syncthreads();
+  // (Starts that decrease may ask for more than there is room for.)
+  if (s.members == 0 || s.row + (int64_t)s.members * a.group > a.part_rows) return false;
+  s.p_lo = s_lo[0];
+  s.p_hi = s_hi[0];
+#pragma unroll 1
+  for (int w = 1; w < kW; ++w) {
+    s.p_lo = min(s.p_lo, s_lo[w]);
+    s.p_hi = max(s.p_hi, s_hi[w]);
+  }
+  s.last = max(s.first, min(s.last, s.p_hi < 0 ? 0 : s.p_hi / keys + 1));
+  *out = s;
+  return true;
 }
 
 // ---- ranges: prefixes and the rest in one launch ------------------------------------------
@@ -271,8 +282,10 @@ struct RangeList {
   unsigned places, start;      // in all, in front of a unit's tiles
   int ctas;                    // that take prefixes
 
-  // For the whole block together.  `rest`: this thread's share of the rest, in key tiles of a head.
-  __device__ __forceinline__ void plan(const PagedSharedArgs& a, int keys, float rest) {
+  // For the whole block together, with the table filled.  `rest`: this thread's share of the rest, in key tiles of a head; `keep`: room for what each
+  // group's members see, where there are few groups.
+  template <int kN>
+  __device__ __forceinline__ void plan(const PagedSharedArgs& a, int keys, float rest, FamilyTable<kN>& table, int32_t* keep) {
     constexpr int kW = kThreads / 32;
     __shared__ unsigned s_units[kW], s_tiles[kW], s_members[kW];
     __shared__ float s_rest[kW], s_mine[kW];
@@ -281,8 +294,10 @@ struct RangeList {
     const int from = min(tid * per, a.groups), to = min(from + per, a.groups);   // this thread's groups
     unsigned own_units = 0, own_tiles = 0, members = 0;
     float mine = 0.f;
+#pragma unroll 1
     for (int i = from; i < to; ++i) {
-      const Family f = family_of(a, i, keys);
+      const Family f = table.at(a, i, keys);
+      if (a.groups <= kN) keep[i] = f.prefix;
       members += f.members;
       const unsigned u = f.tiles > 0 ? f.pieces * a.pool.kv_heads : 0;
       own_units += u;
@@ -309,6 +324,7 @@ struct RangeList {
       s_rest[warp] = rest;
       s_mine[warp] = mine;
     }
+    fence_proxy_async_smem();   // (copies come in where the table was)
     __syncthreads();
     // Lane w of every warp has warp w's sums.
     const bool in = lane < kW;
@@ -341,8 +357,9 @@ struct RangeList {
     places = tiles + start * units;
     if (blockIdx.x == 0) {   // for the join
       unsigned at = before_tiles + start * before_units;
+#pragma unroll 1
       for (int i = from; i < to; ++i) {
-        const Family f = family_of(a, i, keys);
+        const Family f = table.at(a, i, keys);
         a.segments[i] = none ? 0 : f.tiles;
         a.first_row[i] = at;
         at += f.pieces * a.pool.kv_heads * (f.tiles > 0 ? f.tiles + start : 0);
@@ -352,21 +369,22 @@ struct RangeList {
         a.ranges[1] = (int)places;
         a.ranges[2] = (int)start;
       }
+      __syncthreads();   // the table has been read
     }
   }
 };
 
 // What the range that starts at place x and ends at `end` has of the unit at x: a segment, and in `next` where the unit ends.
-// members = 0: the range ends within the unit's start.  For one warp together; it goes through the groups again, 32 at
-// a time, so that no thread holds what it knew of them.
-__device__ __forceinline__ void find_segment(const PagedSharedArgs& a, int keys, unsigned start, unsigned x, unsigned end, int lane,
-                                             Segment* s, unsigned* next) {
+// members = 0: the range ends within the unit's start.  For one warp together; it goes through the groups again (`seen`: what
+// each one's members see), 32 at a time, so that no thread holds what it knew of them.
+__device__ __forceinline__ void find_segment(const PagedSharedArgs& a, int keys, const int32_t* seen, unsigned start, unsigned x,
+                                             unsigned end, int lane, Segment* s, unsigned* next) {
   unsigned before = 0;
 #pragma unroll 1
   for (int i0 = 0; i0 < a.groups; i0 += 32) {
     Family f;
     f.tiles = f.pieces = 0;
-    if (i0 + lane < a.groups) f = family_of(a, i0 + lane, keys);
+    if (i0 + lane < a.groups) f = family_from(a, a.group_start[i0 + lane], a.group_start[i0 + lane + 1], seen[i0 + lane], keys);
     const unsigned size = f.tiles + start, all = f.tiles > 0 ? f.pieces * a.pool.kv_heads * size : 0;
     unsigned at = all;
 #pragma unroll

@@ -52,6 +52,8 @@ struct SharedPlanTc {
   static constexpr int kSmem = kOffRing + kStages * kTileBytes + 1024;   // + alignment slack
 };
 
+constexpr int kKept = 56;   // groups whose numbers a CTA keeps in shared memory, from byte 544 to 768
+
 __device__ __forceinline__ void mbar_inval(uint64_t* bar) {
   asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -98,14 +100,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   unsigned char* ring = smem + P::kOffRing;
 
   // ---- who does what ------------------------------------------------------------------
+  using Families = FamilyTable<kTableTensor>;
+  static_assert(sizeof(Families) <= P::kSmem - 2048, "the groups' table lies where the tiles will");
+  // What each group's members see, for the segments: of few groups in front of kOffQ.
+  int32_t* const keep = a.groups > kTableTensor ? a.seen
+                        : a.groups <= kKept ? reinterpret_cast<int32_t*>(smem + 544)
+                                            : a.seen + (int64_t)blockIdx.x * a.groups;
+  Families& families = *reinterpret_cast<Families*>(smem + 1024);
+  families.fill<kThreadsTc>(a);
   RangeList<kThreadsTc> list;
   const int ctas = gridDim.x;
   float rest = 0.f;
+#pragma unroll 1
   for (int b = tid; b < a.pool.batch; b += kThreadsTc) {   // a unit costs about a tile of the walk's besides its own
     const int own = seen_of<C::kTokens>(ta.rest, b).tiles;
     if (own > 0) rest += (float)(own + 1);
   }
-  list.plan(a, kTile, rest * ((float)C::kTokens / kTile));
+  list.plan(a, kTile, rest * ((float)C::kTokens / kTile), families, keep);
   if ((int)blockIdx.x >= list.ctas) {
     if (warp < C::kWarps)
       decode_walk<C, D, G>(ta.rest, smem, blockIdx.x - list.ctas, ctas - list.ctas,
@@ -146,7 +157,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   }
   again = true;
   if (warp == kLoadWarp) {
-    find_segment(a, kTile, start, x, x_end, lane, s_seg, s_next);
+    find_segment(a, kTile, keep, start, x, x_end, lane, s_seg, s_next);
     Segment s = *s_seg;
     see_segment(a, kTile, s, lane);
     __syncwarp();

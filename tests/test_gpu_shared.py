@@ -454,3 +454,50 @@ def test_neighbours_of_the_call_keep_their_bits():
     f.decode(q, out=wide[1:4], lse=flat[1:4])
     assert (wide[[0, 4]] == 3).all() and (flat[[0, 4]] == 3).all()
     f.check(q, wide[1:4], flat[1:4])
+
+
+# ---- prefixes that no sequence sees to their end ----------------------------------------------------
+
+@pytest.mark.parametrize("fresh", [False, True])
+@pytest.mark.parametrize("kind,d,page", [("bf16", 128, 16), ("bf16", 64, 32), ("bf16", 32, 16), ("bf16", 128, 24), ("f32", 64, 16),
+                                         ("f32", 128, 16)])
+def test_prefixes_left_from_another_step_change_nothing(kind, d, page, fresh):
+    """Prefixes of padded rows, and prefixes above the lengths, under a wide table: work is laid out by what is seen, so that
+    every row has the bits that it has with prefixes of just that."""
+    shape = [[(500, 520), (500, 505), (300, 420)], [(333, 333), (200, 200)], [(0, 0)], [(0, 0), (0, 0)], [(0, 40)]] + [[(0, 0)]] * 9
+    f = Family(kind, 2, d, page, shape, seed=d, width=131072 // page)
+    batch = len(f.lens)
+    q = f.randn(batch, 8, d)
+    kn, vn = (f.randn(batch, 2, d), f.randn(batch, 2, d)) if fresh else (None, None)
+    top, lse = 2**31 - 1, torch.empty(batch, 8, device="cuda")
+    want = f.decode(q, kn, vn, lse=lse)
+    assert f.cache.check() == 0
+    for stale in ([500, 500, 300, top, top, 60000, 60000, 100, 0] + [60000] * 9,
+                  [500, 500, 300, 333, 200, top, top, top, 0] + [top, 1, 131072] * 3,
+                  [500, 500, 300, 100000, 400, 0, 1, 1, 0] + [0] * 8 + [120000]):
+        other = torch.empty_like(lse)
+        got = f.cache.decode_shared(0, q, f.table, f.t_lens, f.t_start, ints(stale), kn, vn, lse=other)
+        assert f.cache.check() == 0
+        assert torch.equal(got, want) and torch.equal(other, lse), stale
+    if not fresh:
+        f.check(q, want, lse)
+
+
+@pytest.mark.parametrize("kind,d,groups", [("bf16", 64, 2500), ("bf16", 128, 4200), ("bf16", 32, 1100), ("f32", 16, 600)])
+def test_more_groups_than_a_block_looks_at_together(kind, d, groups):
+    """Groups in several tables, their ends in the middle of a group of many; empty groups and rows without a sequence."""
+    rng = np.random.default_rng(groups)
+    shape = []
+    for i in range(groups):
+        p = int(rng.integers(1, 60))
+        n = 300 if i == groups // 2 else int(rng.integers(1, 3))
+        shape.append([(p, p + int(t)) if rng.random() < 0.9 else (p, 0) for t in rng.integers(0, 9, n)])
+    f = Family(kind, 1, d, 16, shape, seed=groups)
+    batch = len(f.lens)
+    q = f.randn(batch, 2, d)
+    out = f.decode(q)
+    assert f.cache.check() == 0
+    f.check(q, out, which=list(range(0, batch, 97)) + [batch - 1])
+    empty = np.sort(np.concatenate((f.start, rng.choice(f.start, min(batch - groups, 200)))))   # some groups of none
+    assert torch.equal(f.cache.decode_shared(0, q, f.table, f.t_lens, ints(empty), f.t_prefix), out)
+    assert f.cache.check() == 0
