@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kMmaThreads, D == 128 ? 3 : D >= 32 ? 4 : 5) p
 // ---- fp32: CUDA cores -----------------------------------------------------------------
 //
 // (A tf32 product drops 13 bits of each factor.)  Two floats per multiply-add instruction.  A thread holds an M x 4 piece of S
-// (sums over even and over odd columns of d) and M rows x d/16 columns of O.  V is on its way while S is computed.  Bound by
+// (sums over even and over odd columns of d, two columns' products at a time: a chain of d / 4 roundings at the sum's size,
+// where one product at a time has d / 2) and M rows x d/16 columns of O.  V is on its way while S is computed.  Bound by
 // the chain of a tile's steps: a tile of 64 keys takes about 6 us.  24 sequences behind 3000, 8 heads of 64, 30 us with
 // the rest and the join; 16 behind 4000, 32 / 8 heads of 128, 64 us; 64 behind 8192, 8 heads of 64, 57 us.
 
@@ -352,10 +353,7 @@ __global__ void __launch_bounds__(16 * R / M, D <= 64 ? 4 : 1) paged_shared_fma_
       for (int i = 0; i < M; ++i) {
         const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sq + (rg * M + i) * LD + d);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          s2[i][n] = fma_pair(x.x, y[n].x, s2[i][n]);
-          s2[i][n] = fma_pair(x.y, y[n].y, s2[i][n]);
-        }
+        for (int n = 0; n < 4; ++n) s2[i][n] = add_pair(s2[i][n], fma_pair(x.y, y[n].y, mul_pair(x.x, y[n].x)));
       }
     }
     float w[M][4];

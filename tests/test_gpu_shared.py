@@ -501,3 +501,22 @@ def test_more_groups_than_a_block_looks_at_together(kind, d, groups):
     empty = np.sort(np.concatenate((f.start, rng.choice(f.start, min(batch - groups, 200)))))   # some groups of none
     assert torch.equal(f.cache.decode_shared(0, q, f.table, f.t_lens, ints(empty), f.t_prefix), out)
     assert f.cache.check() == 0
+
+
+@pytest.mark.parametrize("d,members", [(16, 2), (32, 2), (64, 2), (128, 2), (128, 70)])
+def test_products_of_a_prefix_are_summed_in_short_chains(d, members):
+    """fp32: the log-sum-exp of a prefix of one key is its logit.  One large product first, all others just below half a unit of
+    its last place: each is lost where it is added alone.  Products are added in twos to two sums, d / 4 roundings each at
+    the sum's size, 2^-24 of it, with one of the twos; then the two sums' own, the scale, the product with it, and ln 2 and
+    the product with that."""
+    f = Family("f32", 1, d, 16, [[(1, 1)] * members], seed=d)
+    for small in (0.49, 0.245, 0.3, -0.24):
+        q, k = torch.ones(members, 1, d, device="cuda"), torch.full((d,), small * 2.0 ** -23, device="cuda")
+        k[0] = 1.0
+        f.k[int(f.np_table[0, 0]), 0, 0] = k
+        lse = torch.empty(members, 1, device="cuda")
+        f.decode(q, lse=lse)
+        want = float(k.double().sum()) / math.sqrt(d)
+        size = float(k.double().abs().sum()) / math.sqrt(d)
+        assert abs(lse.double() - want).max() <= (d / 4 + 1 + 1 + 4) * 2.0 ** -24 * size, small
+    assert f.cache.check() == 0
