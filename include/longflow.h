@@ -478,7 +478,8 @@ int lf_paged_decode_workspace(const lf_pages* pages, int batch, int max_pages, i
  * A sequence of no group, or with a longer prefix than its group's first, is reported (LF_DEVERR_STATE) and its rows of
  * out and lse are left as they are; group starts that decrease are reported too, and the outputs of the call are
  * unspecified then.  A bf16 cache's weights of values in the prefix are rounded as lf_paged_prompt's.
- * Refused where batch * kv_heads * (max_pages * page_size / 128 + 9) reaches 2^31.  Up to three launches, of more than 512 groups up to four.
+ * Where batch * kv_heads * (max_pages * page_size / 128 + 9) reaches 2^31 a call may be refused (LF_ERR_ARG: the kernel that
+ * would take it counts in 32 bits), below that none is.  Up to three launches, of more than 512 groups up to four.
  */
 int lf_paged_decode_shared(const lf_pages* pages, int batch, const int32_t* page_table, int max_pages,
                            const int32_t* lens, int q_heads, const void* q, const int32_t* group_start, int groups,

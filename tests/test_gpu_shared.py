@@ -520,3 +520,25 @@ def test_products_of_a_prefix_are_summed_in_short_chains(d, members):
         size = float(k.double().abs().sum()) / math.sqrt(d)
         assert abs(lse.double() - want).max() <= (d / 4 + 1 + 1 + 4) * 2.0 ** -24 * size, small
     assert f.cache.check() == 0
+
+
+@pytest.mark.parametrize("kind,d,page_size", [("bf16", 128, 16), ("bf16", 64, 2**30), ("bf16", 128, 24), ("bf16", 16, 16), ("f32", 64, 128)])
+def test_no_call_below_the_header_s_limit_is_refused(kind, d, page_size):
+    """batch * kv_heads * (max_pages * page_size / 128 + 9) below 2^31, at any number of groups; what the tensor cores' kernel
+    would have to count past 32 bits for is refused."""
+    f = Family(kind, 1, d, 16, [[(0, 1)]])
+    p = lf.LFPages.from_buffer_copy(f.cache._pages[0])
+    p.page_size = page_size
+    for tokens in (page_size, 2**20 // page_size * page_size, 2**28 // page_size * page_size, (2**31 - 257) // page_size * page_size):
+        if tokens == 0:
+            continue
+        for kv_heads in (1, 8, 64):
+            p.kv_heads = kv_heads
+            batch = min(65535, (2**31 - 1) * 128 // (kv_heads * (tokens + 9 * 128)))
+            assert batch * kv_heads * (tokens + 9 * 128) < 2**31 * 128
+            for groups in {1, max(1, batch // 3), batch} if batch else ():
+                assert lf.lf_paged_decode_shared_workspace(p, batch, tokens // page_size, kv_heads, groups) > 0
+    if kind == "bf16" and d >= 64 and page_size != 24:
+        p.kv_heads = 64
+        with pytest.raises(lf.LFError, match="too large for one call"):
+            lf.lf_paged_decode_shared_workspace(p, 65535, (2**31 - 257) // page_size, 64, 65535)
