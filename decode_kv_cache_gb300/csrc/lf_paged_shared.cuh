@@ -2,6 +2,7 @@
 #pragma once
 
 #include "lf_paged.cuh"
+#include "lf_ranges.h"
 
 namespace lf {
 
@@ -257,19 +258,6 @@ __device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys,
 // The units of all groups (group by group, piece by piece, head by head) lie one behind another, each `start` places, for what
 // a CTA spends on a unit besides its tiles, and then a place for each of its tiles.  The first `ctas` CTAs take equal ranges of the
 // list, the others the rest of the sequences.  Numbers are below 2^31 (the entry point sees to it).
-
-// CTA i's range starts at place floor(places * i / ctas).  (Products that 32 bits do not hold are rare, and their divisions slow.)
-struct Ranges {
-  unsigned places, ctas;
-  bool small;
-  __device__ __forceinline__ Ranges(unsigned p, unsigned c) : places(p), ctas(c), small(p < 0xffffffffu / (c + 1)) {}
-  __device__ __forceinline__ unsigned first(unsigned i) const {
-    return small ? places * i / ctas : (unsigned)((uint64_t)places * i / ctas);
-  }
-  __device__ __forceinline__ unsigned owner(unsigned x) const {   // the last i with first(i) <= x
-    return small ? ((x + 1) * ctas - 1) / places : (unsigned)((((uint64_t)x + 1) * ctas - 1) / places);
-  }
-};
 
 // What a prefix's tile costs, for one query tile and for two, and a unit's start, in tiles of the rest.  Beside
 // CTAs that take the rest, with memory as busy as it gets, a tile of theirs took 1.1 to 1.6 us, one of a prefix 1.5 to 1.9 and

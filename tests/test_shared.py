@@ -66,3 +66,52 @@ def test_bad_workspace_questions_are_refused(lib):
     assert call(ctypes.byref(pages()), 4, 10, 8, 0, ctypes.byref(n)) == lf.LF_ERR_ARG
     assert call(ctypes.byref(pages()), 4, 10, 8, 5, ctypes.byref(n)) == lf.LF_ERR_ARG
     assert call(ctypes.byref(pages()), 0, 10, 8, 1, ctypes.byref(n)) == lf.LF_ERR_ARG
+
+
+RANGES = r"""
+#define __device__
+#define __forceinline__ inline
+#include <cstdio>
+#include "lf_ranges.h"
+int main() {
+  unsigned p, c, i, x;
+  while (scanf("%u %u %u %u", &p, &c, &i, &x) == 4) {
+    const lf::Ranges r(p, c);
+    printf("%u %u %u %d\n", r.first(i), r.first(i + 1), r.owner(x), (int)r.small);
+  }
+}
+"""
+
+
+def test_ranges_are_exact_at_every_size(tmp_path):
+    """Where a CTA's range starts and whose a place is, against whole numbers of any size: on both sides of where products
+    leave 32 bits, up to the most places that a call may have."""
+    import os
+    import random
+    import shutil
+    import subprocess
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no C++ compiler")
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "decode_kv_cache_gb300", "csrc")
+    src = tmp_path / "ranges.cpp"
+    src.write_text(RANGES)
+    subprocess.run([gxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-I", csrc, str(src), "-o", str(tmp_path / "x")], check=True)
+    rng, cases = random.Random(1), []
+    for _ in range(20000):
+        c = rng.choice((1, 2, 7, 63, 128, 151, rng.randint(1, 303)))
+        edge = 0xffffffff // (c + 1)
+        p = rng.choice((rng.randint(c, 5000), rng.randint(c, 2**31 - 1), edge + rng.randint(-3, 3), 2**31 - 1 - rng.randint(0, 9)))
+        p = max(c, min(p, 2**31 - 1))
+        i = rng.choice((0, c - 1, rng.randrange(c)))
+        x = rng.choice((0, p - 1, rng.randrange(p), p * i // c, max(0, p * i // c - 1)))
+        cases.append((p, c, i, x))
+    text = "\n".join(" ".join(map(str, t)) for t in cases)
+    got = subprocess.run([str(tmp_path / "x")], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
+    sides = set()
+    for (p, c, i, x), line in zip(cases, got):
+        first, end, owner, small = map(int, line.split())
+        sides.add(small)
+        assert first == p * i // c and end == p * (i + 1) // c, (p, c, i)
+        assert 0 <= owner < c and p * owner // c <= x < p * (owner + 1) // c, (p, c, x)
+    assert sides == {0, 1}
