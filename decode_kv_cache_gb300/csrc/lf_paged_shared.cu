@@ -750,7 +750,11 @@ SharedPlan paged_shared_plan(const PagedPool& pool, int elem, int head_dim, int 
     p.slots = sms * (head_dim == 128 ? 3 : head_dim >= 32 ? 4 : 5);
   } else {
     p.kernel = PromptPlan::kFma;
-    p.rows = head_dim == 128 && pool.batch * group >= 64 ? 64 : 32;
+    // Blocks of 64 rows read a key half as often as those of 32 and take each tile longer: for groups of 256 rows on average
+    // (heads of 128; 8 KV heads, 256 rows behind 4000: 160 us, in blocks of 32 174; 2 KV heads behind 16000: 130, 142, but behind
+    // 2000: 47, 43).  Of fewer rows blocks of 32 are as fast or faster (8 KV heads behind 4000, 192 rows: 148 us, of 64 148; 128: 112,
+    // 110; 96: 91, 104; 64: 66, 68; one: 33, 48; 2 KV heads, 64 behind 2000: 29, 39).
+    p.rows = head_dim == 128 && (int64_t)pool.batch * group >= 256ll * groups ? 64 : 32;
     p.slots = sms * (head_dim == 128 ? 2 : 4);
   }
   // Pieces of groups that sum to the batch: the most there can be.

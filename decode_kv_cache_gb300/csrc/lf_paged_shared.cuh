@@ -261,7 +261,9 @@ __device__ __forceinline__ bool take_segment(const PagedSharedArgs& a, int keys,
 
 // What a prefix's tile costs, for one query tile and for two, and a unit's start, in tiles of the rest.  Beside
 // CTAs that take the rest, with memory as busy as it gets, a tile of theirs took 1.1 to 1.6 us, one of a prefix 1.5 to 1.9 and
-// 1.8 to 2.5, and a segment 8 to 10 us besides.
+// 1.8 to 2.5, and a segment 8 to 10 us besides: heads of 128.  Heads of 64 take the same numbers; of 0.75, 1.3 and 1.6 times these
+// none is better throughout (64 sequences, 8 heads a group, behind 8192: 43, 45 and 55 us, with these 42; 256 of 4 heads a group
+// behind 16384: 101, 86 and 85, 94; 32 behind 60000: 62, 60 and 58, 59).
 constexpr float kOneTile = 1.35f, kTwoTiles = 1.8f;
 constexpr int kUnitStart = 6;
 

@@ -13,7 +13,9 @@
 // that some row does not see all of (prefixes of other lengths, or the last tile).
 //
 // The rest's walk has twelve warps of two stages here, where lf_paged_decode.cu's kernel has eight of three: fewer SMs take it, and
-// more warps hide more of each other's steps (256 sequences in 16 groups: the walk 94 us, 85).
+// more warps hide more of each other's steps (256 sequences in 16 groups: the walk 94 us, 85).  Groups of eight heads take ten:
+// twelve do not fit beside each other in shared memory with heads of 128, and with heads of 64 they are no faster (64 sequences
+// behind 8192: 43 us, ten 42; 200 of up to 3000 behind 2000: 156, 147).
 //
 // Bound by HBM while a KV head has fewer than about 500 rows, by the key tiles' way in and the products above, and for short
 // calls by the steps before the first tile: 3 us until every CTA knows its part, 7 to 10 until a prefix's first products, 4 for its rows'
@@ -52,6 +54,9 @@ struct SharedPlanTc {
   static constexpr int kSmem = kOffRing + kStages * kTileBytes + 1024;   // + alignment slack
 };
 
+template <int D, int G>
+using Walk = MmaWalk<D, G, G == 8 ? 10 : 12, 2>;
+
 constexpr int kKept = 56;   // groups whose numbers a CTA keeps in shared memory, from byte 544 to 768
 
 __device__ __forceinline__ void mbar_inval(uint64_t* bar) {
@@ -71,7 +76,7 @@ __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_g
 template <int D, int G>
 __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __grid_constant__ SharedTcArgs ta) {
   using P = SharedPlanTc<D>;
-  using C = MmaWalk<D, G, G == 8 ? 10 : 12, 2>;
+  using C = Walk<D, G>;
   constexpr int S = P::kStages;
   const PagedSharedArgs& a = ta.a;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
 
 template <int D, int G>
 cudaError_t launch(const SharedTcArgs& ta, int64_t grid, cudaStream_t stream) {
-  using C = MmaWalk<D, G, G == 8 ? 10 : 12, 2>;
+  using C = Walk<D, G>;
   constexpr int kWalk = C::kWarps * warp_bytes<C, D, G>() + 1024;
   constexpr int kSmem = SharedPlanTc<D>::kSmem > kWalk ? SharedPlanTc<D>::kSmem : kWalk;
   static_assert(kSmem + 1024 <= 232448, "with the lists' own");

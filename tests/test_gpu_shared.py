@@ -503,7 +503,7 @@ def test_more_groups_than_a_block_looks_at_together(kind, d, groups):
     assert f.cache.check() == 0
 
 
-@pytest.mark.parametrize("d,members", [(16, 2), (32, 2), (64, 2), (128, 2), (128, 70)])
+@pytest.mark.parametrize("d,members", [(16, 2), (32, 2), (64, 2), (128, 2), (128, 70), (128, 300)])
 def test_products_of_a_prefix_are_summed_in_short_chains(d, members):
     """fp32: the log-sum-exp of a prefix of one key is its logit.  One large product first, all others just below half a unit of
     its last place: each is lost where it is added alone.  Products are added in twos to two sums, d / 4 roundings each at
@@ -542,3 +542,18 @@ def test_no_call_below_the_header_s_limit_is_refused(kind, d, page_size):
         p.kv_heads = 64
         with pytest.raises(lf.LFError, match="too large for one call"):
             lf.lf_paged_decode_shared_workspace(p, 65535, (2**31 - 257) // page_size, 64, 65535)
+
+
+@pytest.mark.parametrize("group,members,prefix", [(8, 32, 700), (8, 33, 130), (4, 100, 64), (1, 256, 1000), (2, 129, 63)])
+def test_fp32_groups_of_many_rows(group, members, prefix):
+    """Heads of 128, 256 rows and more of a KV head, where blocks take 64 rows; some leave the prefix early."""
+    rng = np.random.default_rng(members)
+    shape = [[(prefix, prefix + 20)] + [(int(p), int(p) + 1 + int(t)) for p, t in
+                                        zip(rng.integers(0, prefix + 1, members - 1), rng.integers(0, 40, members - 1))]]
+    f = Family("f32", 2, 128, 16, shape, seed=members)
+    q, kn, vn = f.randn(members, 2 * group, 128), f.randn(members, 2, 128), f.randn(members, 2, 128)
+    lse = torch.empty(members, 2 * group, device="cuda")
+    out = f.decode(q, kn, vn, lse=lse)
+    assert torch.equal(out, f.decode(q, kn, vn)) and f.cache.check() == 0
+    f.write_new(kn, vn)
+    f.check(q, out, lse, which=list(range(0, members, 13)) + [members - 1], fresh=True)
