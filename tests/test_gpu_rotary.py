@@ -517,3 +517,44 @@ def test_views_of_one_tensor_in_place_and_side_by_side():
                                q=flat[:30], q_out=flat[1:31])
     torch.cuda.synchronize()
     assert torch.equal(wide, keep)
+
+
+@pytest.mark.parametrize("kind,d,hkv,hq,axes", [("bf16", 16, 1, 2, 1), ("bf16", 128, 2, 1, 3), ("f32", 64, 1, 4, 1), ("f32", 16, 2, 2, 4),
+                                                ("f32", 128, 8, 32, 1)])
+def test_append_of_so_many_tokens_that_a_warp_takes_several(kind, d, hkv, hq, axes):
+    """Tokens of several sequences in one warp, empty ones between them, the last warp's not all there; fp32 prompts of 40
+    heads, where a token is several steps."""
+    rng = np.random.default_rng(d + axes)
+    n = 30 if hq == 32 else 1400
+    counts = rng.integers(0, 300 if hq == 32 else 17, n)
+    counts[rng.integers(0, n, n // 5)] = 0
+    counts[-1] = 3
+    sections = SECTIONS[axes] and SECTIONS[axes](d // 2)
+    axis = None if sections is None else np.repeat(np.arange(axes), sections)
+    r = lf.LFRotary(d, base=1e5, sections=sections)
+    p = Paged(kind, hkv, d, 16, (counts + rng.integers(0, 20, n)).tolist(), seed=d)
+    pos = None if axes == 1 else position_set(rng, axes, int(counts.sum()))
+    assert append_and_compare(p, r, rotary_oracle.frequencies(d, 1e5), counts.tolist(), pos, axis, q_heads=hq) == 0
+    if axes == 1 and hq < 32:      # a sequence with wrong starts among a warp's tokens: reported, and nothing of it stored
+        st = starts(counts.tolist())
+        b = n // 2
+        st[b] = st[b + 1] + 1
+        kn, q = p.randn(st[-1], hkv, d), p.randn(st[-1], hq, d)
+        out = torch.full_like(q, 3.0)
+        p.cache.append_rotated(0, kn, kn, p.table, p.t_lens, r, ints(st), q=q, q_out=out)
+        assert p.cache.check() == lf.LF_DEVERR_STATE
+
+
+def test_rows_of_slabs_so_many_that_a_warp_takes_several():
+    """Tokens of two sequences in one warp, the second's rows far from the first's; in place and back."""
+    r = lf.LFRotary(32, sections=[4, 6, 6], adjacent=True)
+    freq, axis = rotary_oracle.frequencies(32), np.repeat([0, 1, 2], [4, 6, 6])
+    pos = position_set(np.random.default_rng(1), 3, 33, 301)
+    for kind in ("bf16", "f32"):
+        slab = values(kind, 33, 2, 301, 64, seed=3)
+        before, x = f64(slab.transpose(1, 2)), slab.transpose(1, 2)
+        want, size = rotary_oracle.rotate(before, pos, freq, axis, True)
+        y = r.rotate(x, ints(pos))
+        close(kind, f64(y), want, size)
+        r.rotate(x, ints(pos), q_out=x)
+        assert torch.equal(x, y)

@@ -557,3 +557,18 @@ def test_fp32_groups_of_many_rows(group, members, prefix):
     assert torch.equal(out, f.decode(q, kn, vn)) and f.cache.check() == 0
     f.write_new(kn, vn)
     f.check(q, out, lse, which=list(range(0, members, 13)) + [members - 1], fresh=True)
+
+
+@pytest.mark.parametrize("kind,d,page,hkv,group,members,prefix", [("bf16", 64, 16, 8, 8, 64, 8192), ("bf16", 64, 64, 4, 4, 150, 4000),
+                                                                  ("bf16", 32, 16, 8, 4, 64, 3000), ("bf16", 128, 24, 8, 4, 32, 4000),
+                                                                  ("f32", 64, 16, 8, 1, 64, 3000)])
+def test_sizes_that_keep_every_block_busy(kind, d, page, hkv, group, members, prefix):
+    """Heads of 64 on the tensor cores, and the other kernels, with all blocks at work on several tiles each."""
+    rng = np.random.default_rng(members)
+    f = Family(kind, hkv, d, page, [[(prefix, prefix + int(t)) for t in rng.integers(1, 400, members)]], seed=members)
+    q, kn, vn = f.randn(members, hkv * group, d), f.randn(members, hkv, d), f.randn(members, hkv, d)
+    lse = torch.empty(members, hkv * group, device="cuda")
+    out = f.decode(q, kn, vn, lse=lse)
+    assert torch.equal(out, f.decode(q, kn, vn)) and f.cache.check() == 0
+    f.write_new(kn, vn)
+    f.check(q, out, lse, which=[0, members // 2, members - 1], fresh=True)
