@@ -68,6 +68,13 @@ inline Overlap rows_overlap_themselves(const RowSet& a) {
     if (a.stride[d] == 0) return Overlap::kYes;
     put(t, &n, Term{a.stride[d], -(Wide)(a.n[d] - 1), a.n[d] - 1});
   }
+  Wide reach = a.bytes;        // most often every stride reaches over all that lies inside it
+  int inside = n;
+  while (inside > 0 && t[inside - 1].stride >= reach) {
+    --inside;
+    reach += t[inside].hi * t[inside].stride;
+  }
+  if (inside == 0) return Overlap::kNo;
   return find(t, n, 0, a.bytes, false, &steps);
 }
 

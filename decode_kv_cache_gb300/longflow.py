@@ -583,9 +583,11 @@ def _rows(x, y) -> LFRows:
 
 def _no_gradients(*tensors):
     """A call on raw memory gives its result no graph: a gradient would be lost unseen."""
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors):
-        raise LFError(LF_ERR_ARG, "a tensor requires a gradient, which rotations do not record: call them under "
-                                  "torch.no_grad(), or in an autograd function whose backward turns back (inverse)")
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise LFError(LF_ERR_ARG, "a tensor requires a gradient, which rotations do not record: call them under "
+                                          "torch.no_grad(), or in an autograd function whose backward turns back (inverse)")
 
 
 def _will_change(*tensors):
@@ -696,7 +698,8 @@ class LFRotary:
             raise LFError(LF_ERR_ARG, "k_out without k")
         step = self._positions(positions, shape[:-2])
         _no_gradients(q, k, q_out, k_out)
-        _will_change(q_out, k_out)
+        if q_out is not None or k_out is not None:
+            _will_change(q_out, k_out)
         return _run_on(self.device, self._index, stream, lambda: self._held, self._rotate, q, positions, k, q_out, k_out, step,
                        1 if inverse else 0)
 
@@ -814,7 +817,8 @@ class LFPagedCache:
             self._expect(out, "out", self.dtype, q.shape)
         if lse is not None:
             self._expect(lse, "lse", torch.float32, q.shape[:2])
-        _will_change(out, lse)
+        if out is not None or lse is not None:
+            _will_change(out, lse)
 
     def _run(self, stream, call, *args):
         """call(stream handle, *args) with this cache's device and `stream` current, so that
@@ -874,7 +878,8 @@ class LFPagedCache:
         elif q_out is not None:
             raise LFError(LF_ERR_ARG, "q_out without q")
         _no_gradients(k_new, v_new, q, q_out)
-        _will_change(q_out)
+        if q_out is not None:
+            _will_change(q_out)
         return self._run(stream, self._append_rotated, pages, batch, width, page_table, lens, k_new, v_new, new_start,
                          n, rotary, *rotary._held, positions, step, q_heads, q, q_out)
 
