@@ -107,10 +107,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   // ---- who does what ------------------------------------------------------------------
   using Families = FamilyTable<kTableTensor>;
   static_assert(sizeof(Families) <= P::kSmem - 2048, "the groups' table lies where the tiles will");
-  // What each group's members see, for the segments: of few groups in front of kOffQ.
+  // What each group's members see, for the segments: of few groups in front of kOffQ.  (Where it lies is kept there too: a
+  // pointer that lives through the softmax takes registers that it has not to spare: 64 behind 8192 53.0 us, 51.2.)
   int32_t* const keep = a.groups > kTableTensor ? a.seen
                         : a.groups <= kKept ? reinterpret_cast<int32_t*>(smem + 544)
                                             : a.seen + (int64_t)blockIdx.x * a.groups;
+  int32_t* volatile* const s_keep = reinterpret_cast<int32_t* volatile*>(smem + 536);
+  if (tid == 0) *s_keep = keep;
   Families& families = *reinterpret_cast<Families*>(smem + 1024);
   families.fill<kThreadsTc>(a);
   RangeList<kThreadsTc> list;
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   }
   again = true;
   if (warp == kLoadWarp) {
-    find_segment(a, kTile, keep, start, x, x_end, lane, s_seg, s_next);
+    find_segment(a, kTile, *s_keep, start, x, x_end, lane, s_seg, s_next);
     Segment s = *s_seg;
     see_segment(a, kTile, s, lane);
     __syncwarp();

@@ -500,7 +500,15 @@ def test_more_groups_than_a_block_looks_at_together(kind, d, groups):
     f.check(q, out, which=list(range(0, batch, 97)) + [batch - 1])
     empty = np.sort(np.concatenate((f.start, rng.choice(f.start, min(batch - groups, 200)))))   # some groups of none
     assert torch.equal(f.cache.decode_shared(0, q, f.table, f.t_lens, ints(empty), f.t_prefix), out)
-    assert f.cache.check() == 0
+    graph = torch.cuda.CUDAGraph()              # captured, it follows its inputs: the launch that looks at the groups too
+    with torch.cuda.graph(graph):
+        got = f.decode(q)
+    graph.replay()
+    assert torch.equal(got, out)
+    f.t_prefix.copy_(torch.where(f.t_lens > 0, f.t_prefix, 2**31 - 1))
+    f.t_prefix[f.t_start[:-1].long()] = 2**31 - 1
+    graph.replay()
+    assert torch.equal(got, f.decode(q)) and f.cache.check() == 0
 
 
 @pytest.mark.parametrize("d,members", [(16, 2), (32, 2), (64, 2), (128, 2), (128, 70), (128, 300)])
