@@ -499,7 +499,7 @@ int lf_paged_decode_shared(const lf_pages* pages, int batch, const int32_t* page
   if (err == cudaSuccess && shape.plan.kernel == lf::PromptPlan::kTensor) {
     err = lf::paged_shared_tc_launch(a, d, pages->head_dim, ctas, st);
   } else if (err == cudaSuccess) {
-    err = lf::paged_decode_launch(d, e, pages->head_dim, ctas, st);
+    err = lf::paged_decode_behind_launch(d, e, pages->head_dim, ctas, st);
     if (err == cudaSuccess) err = lf::paged_shared_launch(a, shape.plan, pages->head_dim, st);
   }
   if (err == cudaSuccess) err = lf::paged_shared_join_launch(a, d, e, pages->head_dim, ctas, st);

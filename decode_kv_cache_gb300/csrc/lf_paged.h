@@ -168,6 +168,8 @@ cudaError_t paged_append_launch(const PagedAppendArgs& a, cudaStream_t stream);
 // elem: bytes of an element (2 bf16, 4 fp32).  `grid`: CTAs of the attention kernel.
 cudaError_t paged_decode_launch(const PagedDecodeArgs& a, int elem, int head_dim, int grid,
                                 cudaStream_t stream);
+// The same behind shared prefixes, whole units and parts left to paged_shared_join_launch.
+cudaError_t paged_decode_behind_launch(const PagedDecodeArgs& a, int elem, int head_dim, int grid, cudaStream_t stream);
 cudaError_t paged_prompt_launch(const PagedPromptArgs& a, const PromptPlan& plan, int elem, int head_dim,
                                 cudaStream_t stream);
 // Its tensor-core kernel: whether that takes such a cache, and its launch.

@@ -37,15 +37,6 @@ namespace lf {
 
 namespace {
 
-template <class C, int D, int G>
-__global__ void __launch_bounds__(C::kWarps * 32, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  // Everything below reads what earlier launches of the stream wrote.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  decode_walk<C, D, G>(a, smem, blockIdx.x, gridDim.x, [] { __syncthreads(); });
-}
-
 // ---- joining the CTAs' parts ---------------------------------------------------------
 //
 // Block (w, h) joins head h of the unit that CTA w + 1's range starts inside, if
@@ -92,55 +83,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_decode_join_kernel(cons
         min(n, kJoinWarps), [&](int i) { return s_ml[i]; }, [&](int i) { return s_o[i]; }, lane, &m,
         &l, acc);
     const int b = unit / a.pool.kv_heads;
-    write_row<T, D>(a, (int64_t)b * a.q_heads + (unit - b * a.pool.kv_heads) * G + h, lane, m, l, acc);
+    write_row<T, D, false>(a, (int64_t)b * a.q_heads + (unit - b * a.pool.kv_heads) * G + h, lane, m, l, acc);
   }
 }
 
-template <class C, int D, int G>
-cudaError_t launch(const PagedDecodeArgs& a, int grid, cudaStream_t stream) {
-  using T = typename C::T;
-  constexpr int kSmem = C::kWarps * warp_bytes<C, D, G>();
-  static_assert(kSmem + (2 * C::kWarps * (int)sizeof(Part) + 127) / 128 * 128 <= 232448, "shared memory of one CTA");
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(&paged_decode_kernel<C, D, G>), kSmem, done);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(C::kWarps * 32, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_decode_kernel<C, D, G>, a);
-  if (e != cudaSuccess || a.whole_units || grid < 2 || a.rest_o) return e;   // (a prefix's join takes the parts too)
-  cfg.gridDim = dim3(grid - 1, G, 1);
-  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_decode_join_kernel<T, D, G>, a, grid);
-}
-
-template <template <int, int> class C, int D>
-cudaError_t launch_group(const PagedDecodeArgs& a, int grid, cudaStream_t stream) {
-  switch (a.group) {
-    case 1: return launch<C<D, 1>, D, 1>(a, grid, stream);
-    case 2: return launch<C<D, 2>, D, 2>(a, grid, stream);
-    case 4: return launch<C<D, 4>, D, 4>(a, grid, stream);
-    default: return launch<C<D, 8>, D, 8>(a, grid, stream);
+struct Decode {
+  template <class C, int D, int G>
+  static cudaError_t launch(const PagedDecodeArgs& a, int grid, cudaStream_t stream) {
+    const cudaError_t e = launch_walk<C, D, G, false>(a, grid, stream);
+    if (e != cudaSuccess || a.whole_units || grid < 2) return e;
+    const DrainConfig c(dim3(grid - 1, G, 1), kJoinWarps * 32, 0, stream);
+    return cudaLaunchKernelEx(&c.cfg, paged_decode_join_kernel<typename C::T, D, G>, a, grid);
   }
-}
-
-template <template <int, int> class C>
-cudaError_t launch_dim(const PagedDecodeArgs& a, int head_dim, int grid, cudaStream_t stream) {
-  switch (head_dim) {
-    case 16: return launch_group<C, 16>(a, grid, stream);
-    case 32: return launch_group<C, 32>(a, grid, stream);
-    case 64: return launch_group<C, 64>(a, grid, stream);
-    default: return launch_group<C, 128>(a, grid, stream);
-  }
-}
+};
 
 template <template <int, int> class C>
 int sweep(int head_dim) {
@@ -156,8 +111,7 @@ int sweep(int head_dim) {
 
 cudaError_t paged_decode_launch(const PagedDecodeArgs& a, int elem, int head_dim, int grid,
                                 cudaStream_t stream) {
-  return elem == 2 ? launch_dim<MmaTile>(a, head_dim, grid, stream)
-                   : launch_dim<SimtTile>(a, head_dim, grid, stream);
+  return by_type<Decode>(a, elem, head_dim, grid, stream);
 }
 
 int paged_decode_sweep(int elem, int head_dim) {

@@ -121,13 +121,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1) paged_shared_tc_kernel(const __
   float rest = 0.f;
 #pragma unroll 1
   for (int b = tid; b < a.pool.batch; b += kThreadsTc) {   // a unit costs about a tile of the walk's besides its own
-    const int own = seen_of<C::kTokens>(ta.rest, b).tiles;
+    const int own = seen_of<C::kTokens, true>(ta.rest, b).tiles;
     if (own > 0) rest += (float)(own + 1);
   }
   list.plan(a, kTile, rest * ((float)C::kTokens / kTile), families, keep);
   if ((int)blockIdx.x >= list.ctas) {
     if (warp < C::kWarps)
-      decode_walk<C, D, G>(ta.rest, smem, blockIdx.x - list.ctas, ctas - list.ctas,
+      decode_walk<C, D, G, true>(ta.rest, smem, blockIdx.x - list.ctas, ctas - list.ctas,
                            [] { named_bar_sync(1, C::kWarps * 32); });
     return;
   }
