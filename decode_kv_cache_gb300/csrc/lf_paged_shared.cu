@@ -69,7 +69,7 @@ __device__ __forceinline__ bool Block::take(const PagedSharedArgs& a, void* smem
 // tiles of 64 tokens, 16-byte chunks gathered by page.  The queries stay in registers as A operands, S comes out as the C operand
 // whose layout is the A operand of P.V, so P (rounded to bf16: half a step is 2^-8 of a weight) never leaves the registers either.
 // Bound by these instructions' rate and the softmax between them, and with few tiles by the launches' starts: 32 sequences
-// behind 8192 in pages of 24, 32 / 8 heads of 128, 46 us with the rest and the join; four groups of eight behind 1000 to 2000, heads of
+// behind 8192 in pages of 24, 32 / 8 heads of 128, 43 us with the rest and the join; four groups of eight behind 1000 to 2000, heads of
 // 32, 16 us.
 
 constexpr int kMmaThreads = 128, kMmaRows = 64;
@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(kMmaThreads, D == 128 ? 3 : D >= 32 ? 4 : 5) p
 // (A tf32 product drops 13 bits of each factor.)  Two floats per multiply-add instruction.  A thread holds an M x 4 piece of S
 // (sums over even and over odd columns of d, two columns' products at a time: a chain of d / 4 roundings at the sum's size,
 // where one product at a time has d / 2) and M rows x d/16 columns of O.  V is on its way while S is computed.  Bound by
-// the chain of a tile's steps: a tile of 64 keys takes about 6 us.  24 sequences behind 3000, 8 heads of 64, 30 us with
-// the rest and the join; 16 behind 4000, 32 / 8 heads of 128, 64 us; 64 behind 8192, 8 heads of 64, 57 us.
+// the chain of a tile's steps: a tile of 64 keys takes about 6 us.  24 sequences behind 3000, 8 heads of 64, 29 us with
+// the rest and the join; 16 behind 4000, 32 / 8 heads of 128, 59 us; 64 behind 8192, 8 heads of 64, 60 us.
 
 // In blocks of 32 rows P has a place of its own, so that the next K can come in as soon
 // as S is done; in those of 64 it goes where K was, which leaves room for two blocks.

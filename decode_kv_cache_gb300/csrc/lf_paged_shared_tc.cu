@@ -20,11 +20,11 @@
 // Bound by HBM while a KV head has fewer than about 500 rows, by the key tiles' way in and the products above, and for short
 // calls by the steps before the first tile: 3 us until every CTA knows its part, 7 to 10 until a prefix's first products, 4 for its rows'
 // way out, and the join.  Measured with the join, bf16, 32 / 8 heads of 128, other inputs every time, against the bytes
-// at a plain copy's rate: 64 sequences of 100 to 1000 tokens behind 8192, 52 us, 25; 32 of 50 to 500 behind 60000, 69 us, 41; 256 in 16
-// groups behind 500 to 4000, 112 us, 76; 256 of 64 to 512 behind 16384, 113 us, 52 (36 by its products).  lf_paged_decode takes
-// 337, 1167, 375 and 2580 us for its bytes alone.  Two query tiles take 1.7 us a key tile where four CTAs read it, as the prompt
-// kernel does on such rows; 1.45 where sixteen do.  Not taken: the next tiles asked for into L2 ahead of their copies (64 behind 8192,
-// 52 us, 60).
+// at a plain copy's rate: 64 sequences of 100 to 1000 tokens behind 8192, 50 us, 25; 32 of 50 to 500 behind 60000, 67 us, 41; 256 in 16
+// groups behind 500 to 4000, 110 us, 76; 256 of 64 to 512 behind 16384, 110 us, 52 (36 by its products).  lf_paged_decode, which reads
+// each prefix for every sequence and most of it from L2, takes 261, 855, 296 and 1889 us.  Heads of 64: 38, 49, 94 and 96 us.  Two query tiles take 1.7 us a key tile where four CTAs read it, as the prompt
+// kernel does on such rows; 1.45 where sixteen do.  Not taken: the next tiles asked for into L2 ahead of their copies (64 behind 8192
+// 60 us instead of 52).
 #include <type_traits>
 
 #include "lf_paged_decode.cuh"

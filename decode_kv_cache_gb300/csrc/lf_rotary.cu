@@ -22,9 +22,9 @@
 // their lookups come one after another, those of fresh warps side by side.
 //
 // Bound by HBM: every row is read and written once.  Measured, other inputs every time, of a plain copy's 6.77 TB/s:
-// 32 prompts, 34 thousand tokens of 48 rows of 128 bf16 columns, 110 us, 97 %; 16000 video tokens of 40 rows 52.8 us, 92 %; 17
-// slab prompts of 1000 fp32 tokens 12.1 us, 85 %; two prompts of 6000 video tokens 37.5 us, 78 % (start and end of two waves of warps);
-// a step of 64 sequences 3.1 us.
+// 32 prompts, 34 thousand tokens of 48 rows of 128 bf16 columns, 110 us, 97 %, in fp32 215 us, 99 %; 16000 video tokens of 40 rows
+// 52.6 us, 92 %; 17 slab prompts of 1000 fp32 tokens 12.3 us, 84 %; two prompts of 6000 video tokens 37.8 us, 77 % (start and end of two
+// waves of warps); a step of 64 sequences 3.1 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
